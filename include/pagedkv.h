@@ -467,6 +467,152 @@ int paged_attention_decode_noalloc(const void *q, const void *k_cache, const voi
 
 
 /*
+ * The 4-bit cache. Pools whose K and V are held in 4 bits per channel, 5 bits
+ * with their scales: 5/16 of the bytes of a 16-bit pool. 32 neighbouring
+ * channels of one token and kv head are a group with a scale s and a middle m
+ * of the pool's 16-bit type (fp16 or bf16), and a channel's code c (0 .. 15)
+ * stands for
+ *
+ *     x = s * (c - 8) + m.
+ *
+ * A pool is uint8 [num_blocks][n_kv_heads][block_size * 5 * head_dim / 8]; the
+ * bytes of one (block, kv head) are
+ *
+ *     codes  [head_dim / 32 groups][block_size tokens][16 bytes], channel 2i
+ *            of the group in the low half of byte i, 2i + 1 in the high half
+ *     pairs  [block_size tokens][head_dim / 32 groups] of (s, m)
+ *
+ * and tokens, slots and block tables mean what they mean for 16-bit pools.
+ * Supported: `dtype` PAGEDKV_F16 or PAGEDKV_BF16 (the type of q, k, v, out and
+ * of the pools' s and m), head_dim 64 or 128, block_size 8, 16 or 32; else
+ * PAGEDKV_ERR_UNSUPPORTED. Whole blocks are copied and swapped as any other
+ * pool's: paged_kv_copy_blocks and paged_kv_swap_blocks with block_size,
+ * n_kv_heads, head_dim = 5/16 of this head_dim and a 16-bit dtype.
+ *
+ * These entry points read all their device inputs after the kernels before
+ * them on the stream have completed, so lengths, tables and slots may come
+ * from paged_kv_build_tables (or any other kernel) of the same step.
+ */
+
+/*
+ * paged_kv_append_q4 -- quantise new tokens' K and V rows into their slots.
+ *
+ * Per group of 32 channels x_i, with lo and hi the smallest and largest:
+ *
+ *     s = (hi - lo) / 15, rounded towards zero to dtype
+ *     m = lo / 2 + hi / 2 + s / 2, rounded to nearest (fp32 sums, then dtype)
+ *     c_i = clamp(round((x_i - m) / s), -8, 7) + 8, ties to even
+ *
+ * (s = 0: every c_i is 8.) A group with a NaN or an infinity in it, or whose
+ * hi - lo is not finite in fp32, reads back as NaN in all of its channels.
+ * Arguments as paged_kv_append's, with the pools as above; slot < 0 is
+ * padding, a slot past the pool is skipped and sets PAGEDKV_DEVERR_SLOT_RANGE.
+ * Two tokens with the same slot race; the caller must not do that.
+ */
+int paged_kv_append_q4(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache,
+                       void *v_cache, int num_tokens, int num_blocks, int block_size,
+                       int n_kv_heads, int head_dim, int dtype, void *stream);
+
+/*
+ * paged_kv_gather_q4 -- read rows back out of 4-bit pools.
+ *
+ * k[t] and v[t] (of dtype, [num_tokens][n_kv_heads][head_dim], written) are
+ * what slot slot_mapping[t]'s codes stand for, each channel rounded once. Rows
+ * with slot < 0 are left as they were, and so are rows whose slot lies past the
+ * pool (PAGEDKV_DEVERR_SLOT_RANGE). A slot may appear any number of times.
+ */
+int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *slot_mapping, void *k,
+                       void *v, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
+                       int head_dim, int dtype, void *stream);
+
+/*
+ * paged_attention_decode_q4 -- paged_attention_decode over 4-bit pools.
+ *
+ * The same attention with K_s[i] and V_s[i] the rows that the codes stand for;
+ * scores, softmax and the output sums are fp32, out is rounded once. Arguments,
+ * limits, splits and workspace (paged_attention_workspace_bytes) as
+ * paged_attention_decode's, except that partition_tokens > 0 must be a
+ * multiple of 32. No q, K or V is expected to hold an infinity or a NaN: a
+ * sequence whose rows do gets NaN outputs; what lies in a block past a
+ * sequence's context never matters.
+ */
+int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, float scale,
+                              void *out, int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                              int num_blocks, int block_size, int max_blocks_per_seq,
+                              int partition_tokens, void *workspace, size_t workspace_bytes,
+                              int dtype, void *stream);
+
+/*
+ * paged_attention_prefill_q4 -- paged_attention_prefill_split over 4-bit pools.
+ *
+ * The same causal attention of each sequence's chunk of query rows, with K and
+ * V the rows that the codes stand for. Arguments and limits as
+ * paged_attention_prefill_split's.
+ */
+int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *query_start,
+                               const int32_t *context_lens, float scale, void *out, int num_seqs,
+                               int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads,
+                               int head_dim, int num_blocks, int block_size, int max_blocks_per_seq,
+                               int dtype, int key_parts, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * paged_kv_build_tables -- a step's block tables, token lists and slots, on
+ * the GPU.
+ *
+ * Page "How a serving engine actually works", sections "Three allocators, one
+ * workload" (a sequence of L tokens holds ceil(L / block_size) blocks and grows
+ * a block at a time from a free list) and "The one formula". Request s holds
+ * context_lens[s] tokens and asks for new_lens[s] more, which opens
+ *
+ *     need_s = ceil((context + new) / block_size) - ceil(context / block_size)
+ *
+ * blocks. Requests are granted in order, first come, first served: s is granted
+ * when it opens no block or requests 0 .. s together open at most as many as
+ * are free, and when it asks for no token or requests 0 .. s together ask for
+ * at most token_capacity tokens. (A request that does not fit therefore waits,
+ * and so does every later one that needs what it waited for.) For each granted
+ * request, in order, its blocks come off the top of the free stack (the j-th
+ * block opened by the call is free_blocks[free_count - 1 - j]) into its row of
+ * block_tables behind those it holds, and its tokens into the token lists.
+ *
+ *   new_lens        int32 [num_seqs], device, >= 0
+ *   context_lens    int32 [num_seqs], device: tokens held before the call
+ *   block_tables    int32 [num_seqs][max_blocks_per_seq], device, updated: the
+ *                   opened entries alone are written
+ *   free_blocks     int32 [free_capacity], device: a stack, not written
+ *   free_count      int32 [1], device: blocks on the stack
+ *   query_start     int32 [num_seqs + 1], device, written: each request's first
+ *                   row in the token lists; a request was granted when
+ *                   query_start[s + 1] - query_start[s] == new_lens[s]
+ *   token_seq       int32 [token_capacity], device, written: the token's request
+ *   token_pos       int32 [token_capacity], device, written: its position
+ *   slot_mapping    int64 [token_capacity], device, written: its slot; may be NULL
+ *   context_lens_out int32 [num_seqs], device, written: tokens held after the
+ *                   call (unchanged where a request was not granted); may be
+ *                   context_lens itself
+ *   free_count_out  int32 [1], device, written: blocks left; may be free_count
+ *
+ * Entries of the token lists past the last granted token are padding: seq 0,
+ * pos -1, slot -1. A negative length sets PAGEDKV_DEVERR_CONTEXT_LEN, a request
+ * past its table's width (or a free_count outside [0, free_capacity], which is
+ * clamped) PAGEDKV_DEVERR_POSITION; such a request asks for nothing and is not
+ * granted. A block id outside [0, num_blocks), taken from the stack or found in
+ * the table for a token's partly filled block, sets PAGEDKV_DEVERR_BLOCK_ID and
+ * its tokens' slots are -1. num_seqs <= 4096; outputs other than the two named
+ * must not overlap inputs.
+ */
+int paged_kv_build_tables(const int32_t *new_lens, const int32_t *context_lens,
+                          int32_t *block_tables, const int32_t *free_blocks,
+                          const int32_t *free_count, int32_t *query_start, int32_t *token_seq,
+                          int32_t *token_pos, int64_t *slot_mapping, int32_t *context_lens_out,
+                          int32_t *free_count_out, int num_seqs, int max_blocks_per_seq,
+                          int free_capacity, int token_capacity, int block_size, int num_blocks,
+                          void *stream);
+
+/*
  * pagedkv_device_errors -- read (and optionally clear) the sticky device
  * error word of the current device. Synchronises the device first, so it
  * sees every kernel enqueued before the call. *flags receives the PAGEDKV_DEVERR_*

@@ -16,6 +16,15 @@ The entry points keep the C names:
                            partition_tokens=0, workspace=None)
     paged_attention_workspace_bytes(num_seqs, n_q_heads, head_dim, max_blocks_per_seq,
                                     block_size, partition_tokens)
+    paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, free_count, block_size,
+                          num_blocks, query_start, token_seq, token_pos, slot_mapping=None,
+                          context_lens_out=None, free_count_out=None)
+    paged_kv_append_q4(k, v, slot_mapping, k_cache, v_cache)
+    paged_kv_gather_q4(k_cache, v_cache, slot_mapping, k, v)
+    paged_attention_decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                              partition_tokens=0, workspace=None)
+    paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
+                               out, max_query_len=None, workspace=None, key_parts=1)
 
 All tensors live on the current CUDA device; work is enqueued on the current
 torch stream (or the stream passed) and the calls return without waiting.
@@ -35,6 +44,8 @@ __all__ = [
     "paged_kv_copy_blocks", "paged_attention_decode_shared_prefix", "paged_kv_swap_blocks",
     "paged_attention_prefill", "paged_kv_append_tokens", "check_bounded_wait", "DEVERR_TIMEOUT",
     "prefill_workspace_bytes", "prefill_workspace",
+    "paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
+    "paged_attention_decode_q4", "paged_attention_prefill_q4", "new_q4_pool",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,7 +63,8 @@ EXPORTS = ("paged_kv_slot_mapping", "paged_kv_append", "paged_attention_decode",
            "pagedkv_abi_version", "paged_attention_decode_noalloc", "paged_kv_copy_blocks",
            "paged_attention_decode_shared_prefix", "paged_kv_append_tokens",
            "pagedkv_check_bounded_wait", "paged_attention_prefill_split",
-           "paged_attention_prefill_workspace_bytes")
+           "paged_attention_prefill_workspace_bytes", "paged_kv_build_tables", "paged_kv_append_q4",
+           "paged_kv_gather_q4", "paged_attention_decode_q4", "paged_attention_prefill_q4")
 
 
 class PagedKVError(RuntimeError):
@@ -104,6 +116,13 @@ def load():
     lib.paged_attention_prefill_split.restype = i32
     lib.paged_attention_prefill_workspace_bytes.argtypes = [i32]
     lib.paged_attention_prefill_workspace_bytes.restype = sz
+    lib.paged_kv_build_tables.argtypes = [vp] * 11 + [i32] * 6 + [vp]
+    lib.paged_kv_append_q4.argtypes = [vp] * 5 + [i32] * 6 + [vp]
+    lib.paged_kv_gather_q4.argtypes = [vp] * 5 + [i32] * 6 + [vp]
+    lib.paged_attention_decode_q4.argtypes = lib.paged_attention_decode.argtypes
+    lib.paged_attention_prefill_q4.argtypes = lib.paged_attention_prefill_split.argtypes
+    for name in EXPORTS[-5:]:
+        getattr(lib, name).restype = i32
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
     lib.pagedkv_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
@@ -233,17 +252,26 @@ def paged_kv_append_tokens(k, v, block_tables, token_seq, token_pos, k_cache, v_
     _check(st, "paged_kv_append_tokens")
 
 
+def _block_shape(pool):
+    """(num_blocks, block_size, heads, head_dim, dtype code) that give a pool's
+    bytes per block; a 4-bit pool's bytes count as pairs."""
+    if pool.dtype is torch.uint8:
+        return pool.shape[0], pool.shape[2], pool.shape[1], pool.shape[3] // 2, DTYPE_CODES[torch.float16]
+    return (*pool.shape, _code(pool))
+
+
 def paged_kv_copy_blocks(k_cache, v_cache, block_pairs, stream=None):
-    """Copy-on-write: copy whole blocks block_pairs[i][0] -> block_pairs[i][1] in both pools."""
+    """Copy-on-write: copy whole blocks block_pairs[i][0] -> block_pairs[i][1] in both pools
+    (of 16- or 32-bit elements, or 4-bit pools as new_q4_pool makes them)."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
         raise PagedKVError("expected pools [NB][B][Hkv][D] of one element type")
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise PagedKVError("block_pairs must be [n][2]")
-    NB, B, Hkv, D = k_cache.shape
+    NB, B, Hkv, D, code = _block_shape(k_cache)
     st = load().paged_kv_copy_blocks(
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _dev(block_pairs, "block_pairs", torch.int32), block_pairs.shape[0], NB, B, Hkv, D,
-        _code(k_cache), _stream(stream))
+        code, _stream(stream))
     _check(st, "paged_kv_copy_blocks")
 
 
@@ -264,7 +292,7 @@ def paged_kv_swap_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
     """Copy whole blocks block_pairs[i][0] of the source pools to block_pairs[i][1]
     of the destination pools (swap-out to pinned host pools, or swap-in back).
 
-    Pools are [NB][B][Hkv][D] of one element type; source and destination may
+    Pools are [NB][B][Hkv][D] of one element type (or 4-bit pools); source and destination may
     hold different numbers of blocks. Any argument may live in CUDA memory or in
     pinned host memory; the copy runs on the GPU, asynchronously on `stream`.
     """
@@ -275,12 +303,12 @@ def paged_kv_swap_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
         raise PagedKVError("source and destination blocks differ in shape or element type")
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise PagedKVError("block_pairs must be [n][2]")
-    _, B, Hkv, D = src_k.shape
+    _, B, Hkv, D, code = _block_shape(src_k)
     st = load().paged_kv_swap_blocks(
         _reachable(src_k, "src_k"), _reachable(src_v, "src_v"), src_k.shape[0],
         _reachable(dst_k, "dst_k"), _reachable(dst_v, "dst_v"), dst_k.shape[0],
         _reachable(block_pairs, "block_pairs", torch.int32), block_pairs.shape[0], B, Hkv, D,
-        _code(src_k), _stream(stream))
+        code, _stream(stream))
     _check(st, "paged_kv_swap_blocks")
 
 
@@ -425,6 +453,160 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, block_tables, context_le
         _dev(context_lens, "context_lens", torch.int32), float(scale), _dev(out, "out"), S, Hq, Hkv,
         D, NB, B, MB, int(partition_tokens), _code(q), _stream(stream))
     _check(st, "paged_attention_decode_noalloc")
+
+
+def new_q4_pool(num_blocks, n_kv_heads, block_size, head_dim, device="cuda"):
+    """An empty 4-bit pool: uint8 [num_blocks][n_kv_heads][block_size][5 * head_dim / 8]
+    (the last two dimensions are one run of bytes, laid out as pagedkv.h says)."""
+    if head_dim % 32:
+        raise PagedKVError("a 4-bit pool's head_dim must be a multiple of 32")
+    return torch.empty(num_blocks, n_kv_heads, block_size, head_dim * 5 // 8, dtype=torch.uint8, device=device)
+
+
+def _q4_pools(k_cache, v_cache, D):
+    """(NB, Hkv, B) of a pair of 4-bit pools for head_dim D, checked."""
+    cs = k_cache.shape
+    if len(cs) != 4 or v_cache.shape != cs or cs[3] * 8 != 5 * D:
+        raise PagedKVError("expected 4-bit pools [NB][Hkv][B][5 D / 8] for head_dim D")
+    return cs[0], cs[1], cs[2]
+
+
+def _on(dev, t, name, dtype):
+    """The address of a contiguous tensor of `dtype` on CUDA device `dev`, checked."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise PagedKVError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
+    if t.dtype is not dtype:
+        raise PagedKVError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise PagedKVError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _current_device(t):
+    if not t.is_cuda:
+        raise PagedKVError("expected CUDA tensors (the paged-KV path has no CPU fallback)")
+    return torch.cuda.current_device()
+
+
+def paged_kv_append_q4(k, v, slot_mapping, k_cache, v_cache, stream=None):
+    """Quantise k/v [T][Hkv][D] (fp16 or bf16) into 4-bit pools at slot_mapping[T]
+    (int64; -1 is padding)."""
+    ks, dt = k.shape, k.dtype
+    if len(ks) != 3 or v.shape != ks or slot_mapping.numel() != ks[0]:
+        raise PagedKVError("expected k, v [T][Hkv][D] and one slot per token")
+    NB, Hkv, B = _q4_pools(k_cache, v_cache, ks[2])
+    if ks[1] != Hkv:
+        raise PagedKVError("token rows do not match the pools' kv heads")
+    d = _current_device(k)
+    st = load().paged_kv_append_q4(
+        _on(d, k, "k", dt), _on(d, v, "v", dt), _on(d, slot_mapping, "slot_mapping", torch.int64),
+        _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8), ks[0], NB, B,
+        Hkv, ks[2], _code(k), _stream(stream))
+    _check(st, "paged_kv_append_q4")
+
+
+def paged_kv_gather_q4(k_cache, v_cache, slot_mapping, k, v, stream=None):
+    """Rows slot_mapping[T] of 4-bit pools as k/v [T][Hkv][D] (fp16 or bf16, the
+    type they were appended in); rows of a negative slot are left as they were."""
+    ks, dt = k.shape, k.dtype
+    if len(ks) != 3 or v.shape != ks or slot_mapping.numel() != ks[0]:
+        raise PagedKVError("expected k, v [T][Hkv][D] and one slot per token")
+    NB, Hkv, B = _q4_pools(k_cache, v_cache, ks[2])
+    if ks[1] != Hkv:
+        raise PagedKVError("token rows do not match the pools' kv heads")
+    d = _current_device(k)
+    st = load().paged_kv_gather_q4(
+        _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8),
+        _on(d, slot_mapping, "slot_mapping", torch.int64), _on(d, k, "k", dt), _on(d, v, "v", dt), ks[0],
+        NB, B, Hkv, ks[2], _code(k), _stream(stream))
+    _check(st, "paged_kv_gather_q4")
+
+
+def paged_attention_decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                              partition_tokens=0, workspace=None, stream=None):
+    """paged_attention_decode over 4-bit pools (fixed partitions: multiples of 32
+    tokens; workspace from new_workspace)."""
+    qs, bs, dt = q.shape, block_tables.shape, q.dtype
+    if len(qs) != 3 or out.shape != qs or len(bs) != 2 or bs[0] != qs[0] or context_lens.numel() != qs[0]:
+        raise PagedKVError("expected q/out [S][Hq][D], block_tables [S][max_blocks] and context_lens [S]")
+    NB, Hkv, B = _q4_pools(k_cache, v_cache, qs[2])
+    d = _current_device(q)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _on(d, workspace, "workspace", workspace.dtype), workspace.nbytes
+    st = load().paged_attention_decode_q4(
+        _on(d, q, "q", dt), _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8),
+        _on(d, block_tables, "block_tables", torch.int32), _on(d, context_lens, "context_lens", torch.int32),
+        float(scale), _on(d, out, "out", dt), qs[0], qs[1], Hkv, qs[2], NB, B, bs[1], int(partition_tokens),
+        ws_ptr, ws_bytes, _code(q), _stream(stream))
+    _check(st, "paged_attention_decode_q4")
+
+
+def paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
+                               out, max_query_len=None, stream=None, workspace=None, key_parts=1):
+    """paged_attention_prefill over 4-bit pools, with its arguments. With key_parts
+    other than 1 the workspace (see prefill_workspace) is taken from torch's
+    allocator when none is given."""
+    qs, dt, S = q.shape, q.dtype, context_lens.shape[0]
+    if len(qs) != 3 or out.shape != qs:
+        raise PagedKVError("q and out must be [num_tokens][n_q_heads][head_dim]")
+    if query_start.shape[0] != S + 1 or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise PagedKVError("query_start must hold num_seqs + 1 offsets, block_tables num_seqs rows")
+    NB, Hkv, B = _q4_pools(k_cache, v_cache, qs[2])
+    d = _current_device(q)
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
+    if workspace is None and key_parts != 1:
+        workspace = prefill_workspace(q)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _on(d, workspace, "workspace", workspace.dtype), workspace.nbytes
+    st = load().paged_attention_prefill_q4(
+        _on(d, q, "q", dt), _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8),
+        _on(d, block_tables, "block_tables", torch.int32), _on(d, query_start, "query_start", torch.int32),
+        _on(d, context_lens, "context_lens", torch.int32), float(scale), _on(d, out, "out", dt), S, qs[0],
+        int(max_query_len), qs[1], Hkv, qs[2], NB, B, block_tables.shape[1], _code(q), int(key_parts), ws_ptr,
+        ws_bytes, _stream(stream))
+    _check(st, "paged_attention_prefill_q4")
+
+
+def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, free_count, block_size,
+                          num_blocks, query_start, token_seq, token_pos, slot_mapping=None,
+                          context_lens_out=None, free_count_out=None, stream=None):
+    """A step's block tables, token lists and slots from the requests' lengths.
+
+    Request s holds context_lens[s] tokens and asks for new_lens[s] more. Granted
+    requests, in order, take the blocks they open off the top of free_blocks (a
+    stack of free_count[0] ids) into block_tables and get a run of the token
+    lists (token_seq, token_pos, slot_mapping; query_start[s] is its first row).
+    The lengths and the count after the step go to context_lens_out and
+    free_count_out, by default the inputs themselves. query_start[s + 1] -
+    query_start[s] tells whether s was granted its new_lens[s] tokens; entries
+    past the last token are padding (pos and slot -1)."""
+    S, T = new_lens.numel(), token_seq.numel()
+    if context_lens_out is None:
+        context_lens_out = context_lens
+    if free_count_out is None:
+        free_count_out = free_count
+    if (context_lens.numel() != S or context_lens_out.numel() != S or query_start.numel() != S + 1 or
+            block_tables.dim() != 2 or block_tables.shape[0] != S):
+        raise PagedKVError("lengths, query_start and block_tables differ in their number of requests")
+    if token_pos.numel() != T or (slot_mapping is not None and slot_mapping.numel() != T):
+        raise PagedKVError("token_seq, token_pos and slot_mapping differ in length")
+    if free_count.numel() != 1 or free_count_out.numel() != 1:
+        raise PagedKVError("free_count must hold one number")
+    i32, d = torch.int32, _current_device(new_lens)
+    st = load().paged_kv_build_tables(
+        _on(d, new_lens, "new_lens", i32), _on(d, context_lens, "context_lens", i32),
+        _on(d, block_tables, "block_tables", i32), _on(d, free_blocks, "free_blocks", i32),
+        _on(d, free_count, "free_count", i32), _on(d, query_start, "query_start", i32),
+        _on(d, token_seq, "token_seq", i32), _on(d, token_pos, "token_pos", i32),
+        None if slot_mapping is None else _on(d, slot_mapping, "slot_mapping", torch.int64),
+        _on(d, context_lens_out, "context_lens_out", i32), _on(d, free_count_out, "free_count_out", i32), S,
+        block_tables.shape[1], free_blocks.numel(), T, int(block_size), int(num_blocks), _stream(stream))
+    _check(st, "paged_kv_build_tables")
 
 
 def check_bounded_wait(stream=None):

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/pagedkv.h"
+#include "api_common.h"
 #include "context_id.h"
 #include "decode_launch.h"
 #include "prefill.h"
@@ -228,6 +229,12 @@ long long max_parts_for(int max_blocks, int block_size, int part_tokens) {
 }
 
 }  // namespace
+
+namespace pkv {
+
+int api_device_state(unsigned int **err, int *sms) { return device_state(err, sms); }
+
+}  // namespace pkv
 
 extern "C" {
 

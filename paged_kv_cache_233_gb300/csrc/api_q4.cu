@@ -1,0 +1,246 @@
+// api_q4.cu -- the C ABI of the 4-bit paged cache and of the tables a step
+// builds on the GPU (declared in include/pagedkv.h): host-side checks and
+// launches.
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/pagedkv.h"
+#include "api_common.h"
+#include "decode_launch.h"
+#include "q4.h"
+
+namespace {
+
+using pkv::api_aligned;
+using pkv::api_device_state;
+
+constexpr int kMaxSeqs = 4096;
+constexpr int kMaxCount = (1 << 30) - 1;   // free blocks and tokens of a step
+
+int done(cudaError_t e) { return e == cudaSuccess ? PAGEDKV_OK : PAGEDKV_ERR_CUDA; }
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The checks that every call on 4-bit pools shares.
+int check_pool(int num_blocks, int block_size, int n_kv_heads, int head_dim, int dtype) {
+    if (num_blocks < 1 || block_size < 1 || n_kv_heads < 1 || head_dim < 1 ||
+        (dtype != PAGEDKV_F32 && dtype != PAGEDKV_F16 && dtype != PAGEDKV_BF16))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (dtype == PAGEDKV_F32) return PAGEDKV_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PAGEDKV_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PAGEDKV_ERR_UNSUPPORTED;
+    if (n_kv_heads > 65535) return PAGEDKV_ERR_UNSUPPORTED;
+    return PAGEDKV_OK;
+}
+
+bool finite(float x) { return x == x && x != INFINITY && x != -INFINITY; }
+
+template <typename Launch>
+int move_rows(const void *k, const void *v, const int64_t *slot_mapping, const void *k_cache,
+              const void *v_cache, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
+              int head_dim, int dtype, Launch launch) {
+    if (num_tokens < 0) return PAGEDKV_ERR_INVALID_ARG;
+    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
+    if (st != PAGEDKV_OK) return st;
+    if (num_tokens == 0) return PAGEDKV_OK;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache) return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(k, 16) || !api_aligned(v, 16) || !api_aligned(k_cache, 16) ||
+        !api_aligned(v_cache, 16) || !api_aligned(slot_mapping, 8))
+        return PAGEDKV_ERR_INVALID_ARG;
+    unsigned int *err = nullptr;
+    int sms = 0;
+    st = api_device_state(&err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    return done(launch((long long)num_blocks * block_size, sms, err));
+}
+
+}  // namespace
+
+extern "C" {
+
+int paged_kv_build_tables(const int32_t *new_lens, const int32_t *context_lens, int32_t *block_tables,
+                          const int32_t *free_blocks, const int32_t *free_count, int32_t *query_start,
+                          int32_t *token_seq, int32_t *token_pos, int64_t *slot_mapping,
+                          int32_t *context_lens_out, int32_t *free_count_out, int num_seqs,
+                          int max_blocks_per_seq, int free_capacity, int token_capacity, int block_size,
+                          int num_blocks, void *stream) {
+    if (num_seqs < 0 || max_blocks_per_seq < 1 || free_capacity < 0 || token_capacity < 0 ||
+        block_size < 1 || num_blocks < 1)
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (num_seqs > kMaxSeqs || free_capacity > kMaxCount || token_capacity > kMaxCount ||
+        (long long)max_blocks_per_seq * block_size > INT_MAX / 2)
+        return PAGEDKV_ERR_UNSUPPORTED;
+    if (!free_count || !query_start || !free_count_out) return PAGEDKV_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!new_lens || !context_lens || !block_tables || !context_lens_out))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if ((free_capacity > 0 && !free_blocks) || (token_capacity > 0 && (!token_seq || !token_pos)))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(new_lens, 4) || !api_aligned(context_lens, 4) || !api_aligned(block_tables, 4) ||
+        !api_aligned(free_blocks, 4) || !api_aligned(free_count, 4) || !api_aligned(query_start, 4) ||
+        !api_aligned(token_seq, 4) || !api_aligned(token_pos, 4) || !api_aligned(slot_mapping, 8) ||
+        !api_aligned(context_lens_out, 4) || !api_aligned(free_count_out, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    pkv::TablesParams p{};
+    int sms = 0;
+    const int st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.new_lens = new_lens;
+    p.context_lens = context_lens;
+    p.block_tables = block_tables;
+    p.free_blocks = free_blocks;
+    p.free_count = free_count;
+    p.query_start = query_start;
+    p.token_seq = token_seq;
+    p.token_pos = token_pos;
+    p.slot_mapping = slot_mapping;
+    p.context_lens_out = context_lens_out;
+    p.free_count_out = free_count_out;
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.free_capacity = free_capacity;
+    p.token_capacity = token_capacity;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    return done(pkv::launch_build_tables(p, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_kv_append_q4(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache,
+                       void *v_cache, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
+                       int head_dim, int dtype, void *stream) {
+    return move_rows(k, v, slot_mapping, k_cache, v_cache, num_tokens, num_blocks, block_size, n_kv_heads,
+                     head_dim, dtype, [&](long long num_slots, int sms, unsigned int *err) {
+                         return pkv::launch_append_q4(k, v, slot_mapping, static_cast<uint8_t *>(k_cache),
+                                                      static_cast<uint8_t *>(v_cache), num_tokens, n_kv_heads,
+                                                      head_dim, block_size, num_slots, dtype, sms, err,
+                                                      static_cast<cudaStream_t>(stream));
+                     });
+}
+
+int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *slot_mapping, void *k,
+                       void *v, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
+                       int head_dim, int dtype, void *stream) {
+    return move_rows(k, v, slot_mapping, k_cache, v_cache, num_tokens, num_blocks, block_size, n_kv_heads,
+                     head_dim, dtype, [&](long long num_slots, int sms, unsigned int *err) {
+                         return pkv::launch_gather_q4(static_cast<const uint8_t *>(k_cache),
+                                                      static_cast<const uint8_t *>(v_cache), slot_mapping, k, v,
+                                                      num_tokens, n_kv_heads, head_dim, block_size, num_slots,
+                                                      dtype, sms, err, static_cast<cudaStream_t>(stream));
+                     });
+}
+
+int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, float scale,
+                              void *out, int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                              int num_blocks, int block_size, int max_blocks_per_seq, int partition_tokens,
+                              void *workspace, size_t workspace_bytes, int dtype, void *stream) {
+    if (num_seqs < 0 || n_q_heads < 1 || max_blocks_per_seq < 1 ||
+        (partition_tokens < 0 && partition_tokens != PAGEDKV_PARTITION_BALANCED))
+        return PAGEDKV_ERR_INVALID_ARG;
+    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
+    if (st == PAGEDKV_ERR_INVALID_ARG) return st;
+    if (n_q_heads % n_kv_heads != 0 || !finite(scale)) return PAGEDKV_ERR_INVALID_ARG;
+    if (partition_tokens > 0 && partition_tokens % 32 != 0) return PAGEDKV_ERR_INVALID_ARG;
+    if (st != PAGEDKV_OK) return st;
+    const int group = n_q_heads / n_kv_heads;
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    if (group > 8 || num_seqs > kMaxSeqs || cap > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PAGEDKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(q, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
+        !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(context_lens, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (partition_tokens != 0) {
+        const size_t need = paged_attention_workspace_bytes(num_seqs, n_q_heads, head_dim, max_blocks_per_seq,
+                                                            block_size, partition_tokens);
+        if (need == 0 || !workspace || workspace_bytes < need || !api_aligned(workspace, 256))
+            return PAGEDKV_ERR_WORKSPACE;
+    }
+    pkv::Q4AttnParams p{};
+    int sms = 0;
+    st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.out = out;
+    p.scale_log2 = scale * pkv::kLog2e;
+    p.num_seqs = num_seqs;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = group;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    while ((1 << p.log2_block) < block_size) ++p.log2_block;
+    p.max_blocks = max_blocks_per_seq;
+    p.part_tokens = partition_tokens > 0 ? partition_tokens : 0;
+    p.max_parts = p.part_tokens ? int((cap + p.part_tokens - 1) / p.part_tokens) : 1;
+    if (p.part_tokens) {
+        const size_t rows = size_t(num_seqs) * n_q_heads * size_t(p.max_parts);
+        uint8_t *w = static_cast<uint8_t *>(workspace);
+        p.ws_o = reinterpret_cast<float *>(w);
+        p.ws_m = reinterpret_cast<float *>(w + round256(rows * head_dim * 4));
+        p.ws_l = reinterpret_cast<float *>(w + round256(rows * head_dim * 4) + round256(rows * 4));
+    }
+    cudaError_t e = pkv::launch_attn_q4(dtype, head_dim, p, num_seqs, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && p.part_tokens)
+        e = pkv::launch_lse_merge(dtype, head_dim, p.ws_o, p.ws_m, p.ws_l, context_lens, out, num_seqs, n_q_heads,
+                                  p.part_tokens, p.max_parts, int(cap), p.err, static_cast<cudaStream_t>(stream));
+    return done(e);
+}
+
+int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *query_start,
+                               const int32_t *context_lens, float scale, void *out, int num_seqs,
+                               int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads, int head_dim,
+                               int num_blocks, int block_size, int max_blocks_per_seq, int dtype,
+                               int key_parts, void *workspace, size_t workspace_bytes, void *stream) {
+    (void)workspace;
+    (void)workspace_bytes;
+    if (key_parts < 0 || key_parts > 32 || num_seqs < 0 || num_tokens < 0 || max_query_len < 0 ||
+        n_q_heads < 1 || max_blocks_per_seq < 1)
+        return PAGEDKV_ERR_INVALID_ARG;
+    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
+    if (st == PAGEDKV_ERR_INVALID_ARG) return st;
+    if (n_q_heads % n_kv_heads != 0 || !finite(scale)) return PAGEDKV_ERR_INVALID_ARG;
+    if (st != PAGEDKV_OK) return st;
+    const int group = n_q_heads / n_kv_heads;
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    if (group > 64 || num_seqs > 65535 || cap > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PAGEDKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !query_start || !context_lens || !out)
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(q, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
+        !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(query_start, 4) ||
+        !api_aligned(context_lens, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    pkv::Q4AttnParams p{};
+    int sms = 0;
+    st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.block_tables = block_tables;
+    p.query_start = query_start;
+    p.context_lens = context_lens;
+    p.out = out;
+    p.scale_log2 = scale * pkv::kLog2e;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.max_query_len = max_query_len;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = group;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    while ((1 << p.log2_block) < block_size) ++p.log2_block;
+    p.max_blocks = max_blocks_per_seq;
+    p.max_parts = 1;
+    return done(pkv::launch_attn_q4(dtype, head_dim, p, num_tokens, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
