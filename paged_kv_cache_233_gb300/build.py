@@ -18,7 +18,7 @@ LIBRARY = os.path.join(HERE, "libpagedkv.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "api_q4.cu", "append.cu", "attn_q4.cu", "cache_q4.cu", "tables.cu", "swap.cu",
            "merge.cu", "prefill.cu", "prefill_tc.cu", "decode_f32.cu", "decode_f16.cu",
-           "decode_bf16.cu", "decode_noalloc.cu"]
+           "decode_bf16.cu", "decode_q4_f16.cu", "decode_q4_bf16.cu", "decode_noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -176,17 +176,28 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
     p.block_size = block_size;
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.max_blocks = max_blocks_per_seq;
-    p.part_tokens = partition_tokens > 0 ? partition_tokens : 0;
-    p.max_parts = p.part_tokens ? int((cap + p.part_tokens - 1) / p.part_tokens) : 1;
-    if (p.part_tokens) {
-        const size_t rows = size_t(num_seqs) * n_q_heads * size_t(p.max_parts);
+    p.balanced = partition_tokens == PAGEDKV_PARTITION_BALANCED ? 1 : 0;
+    p.log2_hpu = n_kv_heads % 4 == 0 ? 2 : (n_kv_heads % 2 == 0 ? 1 : 0);
+    // (unsplit: one partition of the tables' whole width)
+    p.part_tokens = partition_tokens > 0 ? partition_tokens : int((cap + 31) / 32 * 32);
+    p.max_parts = int((cap + p.part_tokens - 1) / p.part_tokens);
+    // the kernel counts units and tiles in ints
+    const long long units = (long long)num_seqs * (n_kv_heads >> p.log2_hpu) *
+                            (p.balanced ? (cap + 31) / 32 : p.max_parts);
+    if (units > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
+    if (partition_tokens != 0) {
+        // rows of partition states, or of pieces: two per CTA, as paged_attention_workspace_bytes sizes them
+        const size_t rows = p.balanced ? size_t(16) * sms * size_t(n_q_heads < 32 ? n_q_heads : 32)
+                                       : size_t(num_seqs) * n_q_heads * size_t(p.max_parts);
         uint8_t *w = static_cast<uint8_t *>(workspace);
         p.ws_o = reinterpret_cast<float *>(w);
         p.ws_m = reinterpret_cast<float *>(w + round256(rows * head_dim * 4));
         p.ws_l = reinterpret_cast<float *>(w + round256(rows * head_dim * 4) + round256(rows * 4));
     }
-    cudaError_t e = pkv::launch_attn_q4(dtype, head_dim, p, num_seqs, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess && p.part_tokens)
+    cudaError_t e = dtype == PAGEDKV_BF16
+                        ? pkv::launch_decode_q4_bf16(head_dim, p, sms, static_cast<cudaStream_t>(stream))
+                        : pkv::launch_decode_q4_f16(head_dim, p, sms, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && partition_tokens > 0)
         e = pkv::launch_lse_merge(dtype, head_dim, p.ws_o, p.ws_m, p.ws_l, context_lens, out, num_seqs, n_q_heads,
                                   p.part_tokens, p.max_parts, int(cap), p.err, static_cast<cudaStream_t>(stream));
     return done(e);

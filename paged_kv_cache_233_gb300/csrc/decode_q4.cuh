@@ -1,0 +1,851 @@
+// decode_q4.cuh -- fused paged-attention decode over the 4-bit cache (q4.h).
+//
+// Arithmetic. With c a code minus 8, s and m its group's scale and middle, a
+// key's score and the output split into sums over the codes and sums over the
+// pairs, so that no channel is ever multiplied by a scale:
+//     q . K_t   = sum_g s_tg (q_g . c_tg)  +  sum_g m_tg (sum of q_g)
+//     O[ch]     = sum_t (p_t s_tg) c_t[ch] +  sum_t p_t m_tg
+// Codes are small integers, exact in fp16, and both contractions run on
+// m16n8k16 tensor-core MMAs with fp32 sums: keys (or channels) are the 16 rows
+// and the up to 8 query heads of the kv head the 8 columns. One 32-bit word
+// from shared memory is 8 codes and one MMA operand pair; two and-or's, a
+// shift and four fp16 adds or multiply-adds turn it into four operand
+// registers. (Scaling each channel would cost as many instructions again, and
+// a warp's instructions, not memory, are what bounds this kernel.)
+//   K   an 8x8 matrix load gives lane (r, c) word c of token r's group: its
+//       eight channels 8c .. 8c + 7. The MMA's k order is free as long as both
+//       operands agree, so q is laid out once per unit to match. A group's two
+//       MMAs accumulate q_g . c_tg, one packed multiply-add per row applies
+//       s_tg, and one more MMA adds the m part: its rows are the stored (s, m)
+//       pairs as they are, its columns zeros for s and the q sums (in two
+//       16-bit parts) for m.
+//   V   the transposed 8x8 load gives lane (r, c) four channels 4r .. 4r + 3 of
+//       tokens 2c and 2c + 1: two MMAs' rows. Probabilities are multiplied by
+//       s_tg in fp32 and rounded once, to fp16, as the other operand; the m
+//       part is summed in fp32.
+// q is scaled by a power of two per row and taken as fp16, which holds every
+// 8- or 11-bit significand: the MMAs are fp16 ones in bf16 caches too.
+//
+// Softmax reference. p = 2^(z - ref), and ref moves only when it must: when a
+// p times the largest scale beside it passes 2^14 (fp16 ends at 2^16). Then
+// ref becomes the tile's largest score plus the exponent of its largest scale
+// minus 4, so that p * s sits in the upper part of fp16's range whatever V's
+// size, and the sums are rescaled. ref never goes down. Everything is relative
+// to it, so no result depends on when it moved beyond rounding.
+//
+// Work. A unit is (sequence, group of H kv heads, range of keys), split whole,
+// in fixed partitions or in equal shares of the call's 32-key tiles per CTA.
+// Per CTA one producer warp copies each tile's blocks with untiled bulk copies
+// (a block's bytes of neighbouring kv heads are one run), through a ring of
+// stages; four consumer warps own a kv head each (H = 4) or share one (H = 2,
+// 1: every (4/H)-th tile each, joined at the unit's end).
+#pragma once
+
+#include "decode_params.h"
+#include "launch_cache.h"
+#include "q4.cuh"
+
+namespace pkv {
+
+constexpr int kQ4Tile = 32;            // keys per stage
+constexpr int kQ4Consumers = 4;
+constexpr int kQ4Threads = 32 * (1 + kQ4Consumers);
+constexpr int kQ4CtasPerSm = 3;
+constexpr unsigned kQ4All = 0xffffffffu;
+
+// Equal shares of `total` tiles over `grid` CTAs.
+__host__ __device__ inline long long q4_share(long long total, int c, int grid) { return total * c / grid; }
+
+struct Q4Smem {
+    int stage_bytes, stages, seqs, head_dim, shared_heads;   // shared_heads: warps of one kv head join states
+    __host__ __device__ int bars() const { return stages * stage_bytes; }
+    __host__ __device__ int flag() const { return bars() + 16 * stages; }
+    __host__ __device__ int scan() const { return flag() + 16; }                 // a word per warp
+    __host__ __device__ int base() const { return scan() + 32; }                 // seqs + 1
+    __host__ __device__ int len() const { return base() + 4 * (seqs + 1); }      // seqs
+    __host__ __device__ int join() const { return (len() + 4 * seqs + 15) & ~15; }
+    __host__ __device__ int row() const { return head_dim + 4; }                 // floats of a joined row
+    __host__ __device__ int total() const {
+        return join() + (shared_heads ? kQ4Consumers * 8 * (row() + 2) * 4 : 0);
+    }
+};
+
+struct Q4Unit {
+    int s, hg, L, t0, t1, part, slot;
+    bool partial;
+};
+
+// This CTA's units in order; the producer and every consumer warp walk a copy.
+struct Q4Walk {
+    const int *base, *len;
+    int S, groups, P, balanced, s, pos, end, stride, count;
+
+    __device__ void init(const int *base_, const int *len_, const Q4AttnParams &p) {
+        base = base_;
+        len = len_;
+        S = p.num_seqs;
+        groups = p.n_kv_heads >> p.log2_hpu;
+        P = p.part_tokens;
+        balanced = p.balanced;
+        s = count = 0;
+        const int total = base[S];
+        if (balanced) {
+            pos = int(q4_share(total, blockIdx.x, gridDim.x));
+            end = int(q4_share(total, blockIdx.x + 1, gridDim.x));
+            stride = 0;
+        } else {
+            pos = blockIdx.x;
+            end = total;
+            stride = gridDim.x;
+        }
+    }
+
+    __device__ bool next(Q4Unit &x) {
+        if (pos >= end) return false;
+        const int lane = threadIdx.x & 31;
+        for (;;) {   // the sequence that holds pos, 32 candidates at a time
+            const int c = s + 1 + lane;
+            const unsigned m = __ballot_sync(kQ4All, c > S || base[c] > pos);
+            if (m) {
+                s += __ffs(m) - 1;
+                break;
+            }
+            s += 32;
+        }
+        x.s = s;
+        x.L = len[s];
+        const int r = pos - base[s];
+        if (balanced) {
+            const int nt = (x.L + kQ4Tile - 1) / kQ4Tile;
+            x.hg = r / nt;
+            const int a = r - x.hg * nt, b = min(nt, a + (end - pos));
+            x.t0 = a * kQ4Tile;
+            x.t1 = min(x.L, b * kQ4Tile);
+            x.part = 0;
+            x.partial = !(a == 0 && b == nt);
+            x.slot = count == 0 ? 0 : 1;
+            pos += b - a;
+        } else {
+            x.part = r / groups;
+            x.hg = r - x.part * groups;
+            x.t0 = x.part * P;
+            x.t1 = min(x.L, x.t0 + P);
+            x.partial = x.L > P;
+            x.slot = 0;
+            pos += stride;
+        }
+        ++count;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint4 q4_lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 q4_lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t q4_lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// G (s, m) words of one token.
+template <int G>
+__device__ __forceinline__ void load_pairs(uint32_t a, uint32_t (&w)[G]) {
+    if constexpr (G == 4) {
+        const uint4 v = q4_lds128(a);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+        const uint2 v = q4_lds64(a);
+        w[0] = v.x; w[1] = v.y;
+    }
+}
+
+// Two fp32 lanes of work in one instruction: (a0, a1) = (x0, x1) * s + (a0, a1), and (x0, x1) * s.
+__device__ __forceinline__ void fma2_by(float &a0, float &a1, float x0, float x1, float s) {
+    asm("{\n\t.reg .b64 a, x, s;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+        "fma.rn.f32x2 a, x, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1) : "f"(x0), "f"(x1), "f"(s));
+}
+__device__ __forceinline__ float2 mul2_by(float x0, float x1, float s) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, s;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+        "mul.rn.f32x2 x, x, s;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x0), "f"(x1), "f"(s));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) { return Elem<__half>::pack2(lo, hi); }
+
+// The scale (low half) of an (s, m) word, and the middle, as floats.
+template <typename T>
+__device__ __forceinline__ float scale_of(uint32_t w) {
+    if constexpr (Elem<T>::kBf16) return __uint_as_float(w << 16);
+    else return __half2float(__ushort_as_half(uint16_t(w)));
+}
+template <typename T>
+__device__ __forceinline__ float middle_of(uint32_t w) {
+    if constexpr (Elem<T>::kBf16) return __uint_as_float(w & 0xffff0000u);
+    else return __half2float(__ushort_as_half(uint16_t(w >> 16)));
+}
+
+// One consumer warp's state for a unit's kv head.
+template <typename T, int D>
+struct Q4Consumer {
+    static constexpr int G = D / kQ4Group;
+    static constexpr float kMost = 16384.f;    // largest p * s that may pass without moving ref
+    static constexpr float kAbove = 4.f;       // log2: a tile that moves ref puts its largest p * s here
+    static constexpr float kLeast = 0x1p-80f;  // scales count as at least this, so that sums of p stay finite
+
+    uint32_t qb[G][4];     // q in the MMA's k order
+    uint32_t qs0, qs1;     // the q sums' column words
+    float kh[2];           // score scale of heads 2c, 2c + 1 (with the inverse of q's power of two)
+    float o[G][2][4];
+    float corr[G][2];      // this lane's part of sum p m
+    float l[2];            // this lane's part of sum p
+    float ref[2];
+    int grp, c, mi, r8;
+
+    __device__ void init(int lane) {
+        grp = lane >> 2;
+        c = lane & 3;
+        mi = lane >> 3;
+        r8 = lane & 7;
+    }
+
+    // Query rows qh0 .. qh0 + g - 1 of sequence s; column grp of the MMAs is head qh0 + grp.
+    __device__ void begin(const T *q, size_t row0, int g, float scale_log2) {
+        float x[G][8];
+        float top = 0.f;
+        const bool live = grp < g;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live) w = __ldg(reinterpret_cast<const uint4 *>(q + (row0 + grp) * D + 32 * i) + c);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = Elem<T>::unpack2(ww[j]);
+                x[i][2 * j] = f.x;
+                x[i][2 * j + 1] = f.y;
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        }
+        top = fmaxf(top, __shfl_xor_sync(kQ4All, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kQ4All, top, 2));
+        // a power of two that brings the row's largest value to [2^7, 2^8)
+        const int ex = min(max(int((__float_as_uint(top) >> 23) & 255u), 30), 240);
+        const float mult = __uint_as_float(uint32_t(7 + 127 + 127 - ex) << 23);
+        const float inv = __uint_as_float(uint32_t(ex - 7) << 23);   // 1 / mult
+        float sums[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            sums[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                qb[i][j] = pack_f16(x[i][j] * mult, x[i][j + 4] * mult);
+                const float2 f = Elem<__half>::unpack2(qb[i][j]);
+                sums[i] += f.x + f.y;
+            }
+            sums[i] += __shfl_xor_sync(kQ4All, sums[i], 1);
+            sums[i] += __shfl_xor_sync(kQ4All, sums[i], 2);
+        }
+        // the sums in two parts of the cache's type, under the pairs' m half;
+        // the first MMA half takes lane c's group, and so does the second with
+        // four groups, while with two groups lanes 2 and 3 hold the low parts
+        float mine = sums[0];
+#pragma unroll
+        for (int i = 1; i < G; ++i)
+            if ((c & (G - 1)) == i) mine = sums[i];
+        const float hi = Elem<T>::to_float(Elem<T>::from_float(mine));
+        const uint32_t whi = Elem<T>::pack2(0.f, mine), wlo = Elem<T>::pack2(0.f, mine - hi);
+        qs0 = G == 4 || c < 2 ? whi : wlo;
+        qs1 = G == 4 ? wlo : 0u;
+        const float k = scale_log2 * inv;
+        kh[0] = __shfl_sync(kQ4All, k, 8 * c);
+        kh[1] = __shfl_sync(kQ4All, k, 8 * c + 4);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            corr[i][0] = corr[i][1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][0][e] = o[i][1][e] = 0.f;
+        }
+        l[0] = l[1] = 0.f;
+        ref[0] = ref[1] = -INFINITY;
+    }
+
+    // Move the reference: z[u][h] the tile's scores (-inf where masked), top this
+    // lane's largest scale.
+    __device__ __forceinline__ void move(const float (&z)[4][2], float top) {
+        // (positive floats order as their bits)
+        const uint32_t all = __reduce_max_sync(kQ4All, __float_as_uint(top));
+        const float e = float(int(all >> 23) - 126);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float zm = fmaxf(fmaxf(z[0][h], z[1][h]), fmaxf(z[2][h], z[3][h]));
+#pragma unroll
+            for (int mask = 4; mask <= 16; mask <<= 1) zm = fmaxf(zm, __shfl_xor_sync(kQ4All, zm, mask));
+            const float nref = fmaxf(ref[h], zm + (e - kAbove));
+            const float alpha = ref[h] == -INFINITY ? 0.f : fast_exp2(ref[h] - nref);
+            ref[h] = nref;
+            l[h] *= alpha;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                corr[i][h] *= alpha;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    o[i][mt][h] *= alpha;
+                    o[i][mt][2 + h] *= alpha;
+                }
+            }
+        }
+    }
+
+    // kc, vc: shared addresses of this head's codes of octet o at kc + off[o]
+    // (stride `panel` bytes between groups); pairs at kp + poff[o].
+    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, const int (&off)[4], const int (&poff)[4],
+                                         int panel, int nvalid) {
+        const bool tail = nvalid < kQ4Tile;
+        // ---- scores
+        float z[4][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            // words of octets 2t and 2t + 1, all groups
+            uint32_t w[2][G];
+            if constexpr (G == 4) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t r[4];
+                    ldmatrix_x4(kbase + off[2 * t + u] + mi * panel + r8 * 16, r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[u][i] = r[i];
+                }
+            } else {
+                uint32_t r[4];
+                const int a = mi >= 2 ? off[2 * t + 1] : off[2 * t];
+                ldmatrix_x4(kbase + a + (mi & 1) * panel + r8 * 16, r);
+                w[0][0] = r[0]; w[0][1] = r[1]; w[1][0] = r[2]; w[1][1] = r[3];
+            }
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            {
+                // the m part: rows are the stored pairs
+                uint32_t a[4];
+                a[0] = q4_lds32(kbase + poff[2 * t] + grp * 4 * G + (c & (G - 1)) * 4);
+                a[1] = q4_lds32(kbase + poff[2 * t + 1] + grp * 4 * G + (c & (G - 1)) * 4);
+                a[2] = G == 4 ? a[0] : 0u;
+                a[3] = G == 4 ? a[1] : 0u;
+                mma_m16n8k16<Elem<T>::kBf16>(sc, a, qs0, qs1);
+            }
+            uint32_t p0[G], p1[G];
+            load_pairs<G>(kbase + poff[2 * t] + grp * 4 * G, p0);
+            load_pairs<G>(kbase + poff[2 * t + 1] + grp * 4 * G, p1);
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                uint32_t x[4], y[4];
+                q4_codes(w[0][i], x);
+                q4_codes(w[1][i], y);
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint32_t a0[4] = {x[0], y[0], x[1], y[1]};
+                const uint32_t a1[4] = {x[2], y[2], x[3], y[3]};
+                mma_m16n8k16<false>(acc, a0, qb[i][0], qb[i][1]);
+                mma_m16n8k16<false>(acc, a1, qb[i][2], qb[i][3]);
+                fma2_by(sc[0], sc[1], acc[0], acc[1], scale_of<T>(p0[i]));
+                fma2_by(sc[2], sc[3], acc[2], acc[3], scale_of<T>(p1[i]));
+            }
+            z[2 * t][0] = sc[0] * kh[0];
+            z[2 * t][1] = sc[1] * kh[1];
+            z[2 * t + 1][0] = sc[2] * kh[0];
+            z[2 * t + 1][1] = sc[3] * kh[1];
+        }
+        if (tail) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (8 * u + grp >= nvalid) z[u][0] = z[u][1] = -INFINITY;
+        }
+        // ---- the values' pairs, and this lane's largest scale
+        uint32_t pw[4][G], most = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            load_pairs<G>(vbase + poff[u] + grp * 4 * G, pw[u]);
+            if (tail && 8 * u + grp >= nvalid) {
+#pragma unroll
+                for (int i = 0; i < G; ++i) pw[u][i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < G; ++i) most = __vmaxu2(most, pw[u][i]);
+        }
+        const float top = fmaxf(scale_of<T>(most & 0xffffu), kLeast);
+        // ---- probabilities; where one times the scale is too large (or no
+        // reference is set), they are computed again against a new reference
+        float pr[4][2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            pr[u][0] = fast_exp2(z[u][0] - ref[0]);
+            pr[u][1] = fast_exp2(z[u][1] - ref[1]);
+        }
+        const float pm = fmaxf(fmaxf(fmaxf(pr[0][0], pr[0][1]), fmaxf(pr[1][0], pr[1][1])),
+                               fmaxf(fmaxf(pr[2][0], pr[2][1]), fmaxf(pr[3][0], pr[3][1])));
+        if (__any_sync(kQ4All, !(pm * top <= kMost) || ref[0] == -INFINITY)) {
+            move(z, top);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                pr[u][0] = fast_exp2(z[u][0] - ref[0]);
+                pr[u][1] = fast_exp2(z[u][1] - ref[1]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            l[0] += pr[u][0];
+            l[1] += pr[u][1];
+        }
+        // ---- output
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            uint32_t b[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                fma2_by(corr[i][0], corr[i][1], pr[u][0], pr[u][1], middle_of<T>(pw[u][i]));
+                const float2 v = mul2_by(pr[u][0], pr[u][1], scale_of<T>(pw[u][i]));
+                b[u] = movmatrix_trans(pack_f16(v.x, v.y));
+            }
+            uint32_t r[4];
+            const int a = mi >= 2 ? (mi == 3 ? off[3] : off[2]) : (mi == 1 ? off[1] : off[0]);
+            ldmatrix_x4_trans(vbase + a + i * panel + r8 * 16, r);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t x[4], y[4];
+                q4_codes(r[2 * t], x);
+                q4_codes(r[2 * t + 1], y);
+                const uint32_t a0[4] = {x[0], x[1], y[0], y[1]};
+                const uint32_t a1[4] = {x[2], x[3], y[2], y[3]};
+                mma_m16n8k16<false>(o[i][0], a0, b[2 * t], b[2 * t + 1]);
+                mma_m16n8k16<false>(o[i][1], a1, b[2 * t], b[2 * t + 1]);
+            }
+        }
+    }
+
+    // Sum the lanes' parts; afterwards o holds whole sums and l agrees in lanes of equal c.
+    __device__ void finish() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int mask = 4; mask <= 16; mask <<= 1) l[h] += __shfl_xor_sync(kQ4All, l[h], mask);
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+#pragma unroll
+                for (int mask = 4; mask <= 16; mask <<= 1) corr[i][h] += __shfl_xor_sync(kQ4All, corr[i][h], mask);
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    o[i][mt][h] += corr[i][h];
+                    o[i][mt][2 + h] += corr[i][h];
+                }
+            }
+        }
+    }
+
+    // Four neighbouring channels of head 2c + h: 32 i + 4 grp ..
+    __device__ float4 quad(int i, int h) const {
+        return make_float4(o[i][0][h], o[i][0][2 + h], o[i][1][h], o[i][1][2 + h]);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_quad(T *dst, float4 v, float inv) {
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(Elem<T>::pack2(v.x * inv, v.y * inv), Elem<T>::pack2(v.z * inv, v.w * inv));
+}
+
+// 1 / l for a row's sum; 0 for a row without keys (a NaN sum stays NaN).
+__device__ __forceinline__ float q4_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(const __grid_constant__ Q4AttnParams p) {
+    constexpr int G = D / kQ4Group;
+    extern __shared__ __align__(128) uint8_t sm[];
+    const uint32_t base = smem_addr(sm);
+    const int S = p.num_seqs, H = 1 << p.log2_hpu, B = p.block_size, NS = p.stages;
+    const int TL = kQ4Consumers >> p.log2_hpu;          // warps per kv head
+    const int head_bytes = q4_head_bytes(B, D), run = H * head_bytes;
+    const int half = run * (kQ4Tile / B);               // K (or V) of a stage
+    const Q4Smem lay{2 * half, NS, S, D, TL > 1 ? 1 : 0};
+    const uint32_t full0 = base + lay.bars(), empty0 = full0 + 8 * NS;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + lay.flag());
+    int *scan = reinterpret_cast<int *>(sm + lay.scan());
+    int *seq_base = reinterpret_cast<int *>(sm + lay.base());
+    int *seq_len = reinterpret_cast<int *>(sm + lay.len());
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < NS; ++k) {
+            mbar_init(full0 + 8 * k, 1);
+            mbar_init(empty0 + 8 * k, kQ4Consumers);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    // lengths, tables and pools as the kernels before this one left them
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // ---- per sequence: length, and units (or tiles) before it
+    {
+        const int cap = p.max_blocks * B, groups = p.n_kv_heads >> p.log2_hpu;
+        const int per = (S + kQ4Threads - 1) / kQ4Threads;
+        const int s0 = min(int(threadIdx.x) * per, S), s1 = min(s0 + per, S);
+        int sum = 0;
+        for (int s = s0; s < s1; ++s) {
+            const int L = __ldg(p.context_lens + s), Lc = min(max(L, 0), cap);
+            if (L != Lc && blockIdx.x == 0) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
+            seq_len[s] = Lc;
+            const int n = p.balanced ? (Lc + kQ4Tile - 1) / kQ4Tile
+                                     : (Lc > 0 ? (Lc + p.part_tokens - 1) / p.part_tokens : 1);
+            sum += n * groups;
+            seq_base[s + 1] = sum;
+        }
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kQ4All, incl, d);
+            if (lane >= d) incl += y;
+        }
+        if (lane == 31) scan[warp] = incl;
+        if (threadIdx.x == 0) seq_base[0] = 0;
+        __syncthreads();
+        int before = incl - sum;
+        for (int w = 0; w < warp; ++w) before += scan[w];
+        for (int s = s0; s < s1; ++s) seq_base[s + 1] += before;
+        __syncthreads();
+    }
+    Q4Walk walk;
+    walk.init(seq_base, seq_len, p);
+
+    if (warp == 0) {
+        // -------------------------------------------------------- producer
+        int stage = 0, armed = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        Q4Unit u;
+        const int blk = lane >> 1, operand = lane & 1;     // this lane's copy of a tile
+        const uint8_t *pool = operand ? p.v_cache : p.k_cache;
+        const int lanes = 2 * (kQ4Tile / B);
+        while (ok && walk.next(u)) {
+            const int32_t *table = p.block_tables + size_t(u.s) * p.max_blocks;
+            const int h0 = u.hg << p.log2_hpu;
+            // block ids of the next 32 blocks, one per lane
+            int win = u.t0 >> p.log2_block;
+            const int nblk = (u.t1 + B - 1) >> p.log2_block;
+            int ids = win + lane < nblk ? __ldg(table + win + lane) : 0;
+            for (int tok = u.t0; tok < u.t1; tok += kQ4Tile) {
+                const int j0 = tok >> p.log2_block;
+                if (j0 + (kQ4Tile >> p.log2_block) > win + 32) {
+                    win = j0;
+                    ids = win + lane < nblk ? __ldg(table + win + lane) : 0;
+                }
+                int pb = __shfl_sync(kQ4All, ids, (j0 - win + blk) & 31);
+                const int present = (min(kQ4Tile, u.t1 - tok) + B - 1) >> p.log2_block;
+                if (lane == 0) {
+                    ok = !*abort_flag && mbar_wait(empty0 + 8 * stage, phase ^ 1u, p.err);
+                    if (ok) mbar_arrive_expect_tx(full0 + 8 * stage, uint32_t(2 * present * run));
+                }
+                ok = __shfl_sync(kQ4All, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                if (lane < lanes && blk < present) {
+                    if (pb < 0 || pb >= p.num_blocks) {
+                        atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+                        pb = 0;
+                    }
+                    bulk_load(base + stage * 2 * half + operand * half + blk * run,
+                              pool + (size_t(pb) * p.n_kv_heads + h0) * head_bytes, uint32_t(run), full0 + 8 * stage);
+                }
+                ++armed;
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // stop everyone, then wait (bounded) for this CTA's copies in flight
+            *abort_flag = 1;
+            for (int k = max(0, armed - NS); k < armed; ++k)
+                mbar_wait(full0 + 8 * (k % NS), uint32_t((k / NS) & 1), p.err);
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------ consumers
+    const int cw = warp - 1, hh = cw & (H - 1), tw = cw >> p.log2_hpu, g = p.group;
+    Q4Consumer<T, D> st;
+    st.init(lane);
+    // octet u of a stage: its block's run, this head, its rows
+    int off[4], poff[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int at = ((8 * u) >> p.log2_block) * run + hh * head_bytes, row = (8 * u) & (B - 1);
+        off[u] = at + row * 16;
+        poff[u] = at + q4_pairs_at(B, D) + row * 4 * G;
+    }
+    const int panel = B * 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    const T *q = reinterpret_cast<const T *>(p.q);
+    T *out = reinterpret_cast<T *>(p.out);
+    Q4Unit u;
+    while (walk.next(u)) {
+        const int qh0 = ((u.hg << p.log2_hpu) + hh) * g;
+        st.begin(q, size_t(u.s) * p.n_q_heads + qh0, g, p.scale_log2);
+        int i = 0;
+        for (int tok = u.t0; tok < u.t1; tok += kQ4Tile, ++i) {
+            int good = mbar_try_wait(full0 + 8 * stage, phase);
+            if (!good) good = !*abort_flag && mbar_wait(full0 + 8 * stage, phase, p.err);
+            if (!__all_sync(kQ4All, good)) {
+                *abort_flag = 1;
+            } else if ((i & (TL - 1)) == tw) {
+                const uint32_t k = base + stage * 2 * half;
+                st.tile(k, k + half, off, poff, panel, min(kQ4Tile, u.t1 - tok));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+            if (++stage == NS) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        st.finish();
+        // row of head j: workspace rows [seq][q head][partition], or [CTA][slot][head of unit][j]
+        auto ws_row = [&](int h, int j) {
+            return p.balanced ? ((size_t(blockIdx.x) * 2 + u.slot) * H + h) * g + j
+                              : (size_t(u.s) * p.n_q_heads + size_t((u.hg << p.log2_hpu) + h) * g + j) * p.max_parts + u.part;
+        };
+        if (TL == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 2 * st.c + h;
+                if (j >= g) continue;
+                if (u.partial) {
+                    const size_t row = ws_row(hh, j);
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+                        *reinterpret_cast<float4 *>(p.ws_o + row * D + 32 * i + 4 * st.grp) = st.quad(i, h);
+                    if (st.grp == 0) {
+                        p.ws_m[row] = st.ref[h] * kLn2;
+                        p.ws_l[row] = st.l[h];
+                    }
+                } else {
+                    const float inv = q4_inverse(st.l[h]);
+                    T *dst = out + (size_t(u.s) * p.n_q_heads + qh0 + j) * D + 4 * st.grp;
+#pragma unroll
+                    for (int i = 0; i < G; ++i) store_quad(dst + 32 * i, st.quad(i, h), inv);
+                }
+            }
+        } else {
+            // the warps of a kv head join their states
+            const int rowf = lay.row();
+            float *jo = reinterpret_cast<float *>(sm + lay.join());
+            float *jm = jo + kQ4Consumers * 8 * rowf, *jl = jm + kQ4Consumers * 8;
+            named_barrier(1, 32 * kQ4Consumers);      // the previous unit's readers are done
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 2 * st.c + h;
+                if (j >= g) continue;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    *reinterpret_cast<float4 *>(jo + (cw * 8 + j) * rowf + 32 * i + 4 * st.grp) = st.quad(i, h);
+                if (st.grp == 0) {
+                    jm[cw * 8 + j] = st.ref[h];
+                    jl[cw * 8 + j] = st.l[h];
+                }
+            }
+            named_barrier(1, 32 * kQ4Consumers);
+            for (int x = threadIdx.x - 32; x < H * g * (D / 4); x += 32 * kQ4Consumers) {
+                const int h = x / (g * (D / 4)), rem = x - h * g * (D / 4), j = rem / (D / 4), d = 4 * (rem - j * (D / 4));
+                float M = -INFINITY;
+                for (int t = 0; t < TL; ++t) M = fmaxf(M, jm[(t * H + h) * 8 + j]);
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+                float den = 0.f;
+                for (int t = 0; t < TL; ++t) {
+                    const int w = (t * H + h) * 8 + j;
+                    if (jm[w] == -INFINITY) continue;     // no tile of the unit was this warp's
+                    const float f = fast_exp2(jm[w] - M);
+                    const float4 v = *reinterpret_cast<const float4 *>(jo + w * rowf + d);
+                    num.x = fmaf(f, v.x, num.x);
+                    num.y = fmaf(f, v.y, num.y);
+                    num.z = fmaf(f, v.z, num.z);
+                    num.w = fmaf(f, v.w, num.w);
+                    den = fmaf(f, jl[w], den);
+                }
+                if (u.partial) {
+                    const size_t row = ws_row(h, j);
+                    *reinterpret_cast<float4 *>(p.ws_o + row * D + d) = num;
+                    if (d == 0) {
+                        p.ws_m[row] = M * kLn2;
+                        p.ws_l[row] = den;
+                    }
+                } else {
+                    store_quad(out + (size_t(u.s) * p.n_q_heads + size_t((u.hg << p.log2_hpu) + h) * g + j) * D + d, num,
+                               q4_inverse(den));
+                }
+            }
+        }
+    }
+}
+
+// Balanced split: the pieces of each (sequence, head group) that spans shares,
+// joined by the softmax identity. A warp per row of the pair; zero rows for
+// empty sequences. Where a pair's tiles lie follows from the lengths alone.
+constexpr int kQ4MergeWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __grid_constant__ Q4AttnParams p, int grid) {
+    constexpr int E = D / 32, kBatch = 8;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int H = 1 << p.log2_hpu, groups = p.n_kv_heads >> p.log2_hpu, rows = H * p.group;
+    const int s = blockIdx.x / groups, hg = blockIdx.x - s * groups;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * kQ4MergeWarps + warp;
+    const int cap = p.max_blocks * p.block_size;
+    __shared__ int part[2][kQ4MergeWarps];
+    int before = 0, total = 0, nt = 0;
+    for (int t = threadIdx.x; t < p.num_seqs; t += blockDim.x) {
+        const int n = (min(max(__ldg(p.context_lens + t), 0), cap) + kQ4Tile - 1) / kQ4Tile * groups;
+        total += n;
+        if (t < s) before += n;
+    }
+    before = __reduce_add_sync(kQ4All, before);
+    total = __reduce_add_sync(kQ4All, total);
+    if (lane == 0) {
+        part[0][warp] = before;
+        part[1][warp] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int w = 0; w < kQ4MergeWarps; ++w) {
+        before += part[0][w];
+        total += part[1][w];
+    }
+    nt = (min(max(__ldg(p.context_lens + s), 0), cap) + kQ4Tile - 1) / kQ4Tile;
+    if (r >= rows) return;
+    T *dst = reinterpret_cast<T *>(p.out) + (size_t(s) * p.n_q_heads + hg * rows + r) * D + lane * E;
+    float acc[E] = {};
+    float den = 0.f;
+    if (nt > 0) {
+        const long long Tt = total, A = (long long)before + (long long)hg * nt, Z = A + nt - 1;
+        auto share_of = [&](long long t) {
+            long long c = t * grid / Tt;
+            while (c + 1 < grid && q4_share(Tt, int(c + 1), grid) <= t) ++c;
+            while (c > 0 && q4_share(Tt, int(c), grid) > t) --c;
+            return int(c);
+        };
+        const int c0 = share_of(A), c1 = share_of(Z);
+        if (c0 == c1) return;                       // one share: written by the decode itself
+        const int np = c1 - c0 + 1;
+        const int slot0 = A != q4_share(Tt, c0, grid) ? 1 : 0;
+        auto row_of = [&](int i) { return (size_t(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * rows + r; };
+        // shares without tiles (fewer tiles than CTAs) left no piece
+        auto has = [&](int i) { return i < np && q4_share(Tt, c0 + i, grid) != q4_share(Tt, c0 + i + 1, grid); };
+        float M = -INFINITY;
+        for (int b = 0; b < np; b += 32)
+            if (has(b + lane)) M = fmaxf(M, __ldcg(p.ws_m + row_of(b + lane)));
+#pragma unroll
+        for (int mask = 16; mask >= 1; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(kQ4All, M, mask));
+        for (int b = 0; b < np; b += 32) {
+            float w = 0.f;
+            if (has(b + lane)) {
+                w = fast_exp2((__ldcg(p.ws_m + row_of(b + lane)) - M) * kLog2e);
+                den = fmaf(w, __ldcg(p.ws_l + row_of(b + lane)), den);
+            }
+            const int n = min(32, np - b);
+            for (int k0 = 0; k0 < n; k0 += kBatch) {
+                float x[kBatch][E];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (!has(b + k0 + k)) continue;
+                    const float *src = p.ws_o + row_of(b + k0 + k) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                        x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
+                    } else {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                        x[k][0] = v.x; x[k][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float wk = __shfl_sync(kQ4All, w, (k0 + k) & 31);
+                    if (!has(b + k0 + k)) continue;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[k][e], acc[e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int mask = 16; mask >= 1; mask >>= 1) den += __shfl_xor_sync(kQ4All, den, mask);
+    }
+    const float inv = q4_inverse(den);
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(dst + e) = Elem<T>::pack2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <typename T, int D>
+cudaError_t launch_decode_q4_typed(Q4AttnParams p, int sms, cudaStream_t st) {
+    auto kernel = decode_q4_kernel<T, D>;
+    const int H = 1 << p.log2_hpu, stage = 2 * H * kQ4Tile * D * 5 / 8;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // as many stages as kQ4CtasPerSm CTAs leave room for on an SM of 228 KB
+    Q4Smem lay{stage, 2, p.num_seqs, D, H < 4 ? 1 : 0};
+    while (lay.stages < 8) {
+        Q4Smem more = lay;
+        ++more.stages;
+        if (more.total() > 74 * 1024) break;
+        lay = more;
+    }
+    p.stages = lay.stages;
+    static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
+    e = open_dynamic_smem(opened, dev, kernel, lay.total());
+    if (e != cudaSuccess) return e;
+    static std::atomic<long long> fits[kLaunchCacheDevices];
+    int per_sm = 0;
+    e = occupancy_per_sm(fits, dev, kernel, kQ4Threads, lay.total(), &per_sm);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    if (per_sm > kQ4CtasPerSm) per_sm = kQ4CtasPerSm;
+    const long long cap = (long long)p.max_blocks * p.block_size;
+    const long long groups = p.n_kv_heads >> p.log2_hpu;
+    const long long most = p.balanced ? groups * p.num_seqs * ((cap + kQ4Tile - 1) / kQ4Tile)
+                                      : groups * p.num_seqs * ((cap + p.part_tokens - 1) / p.part_tokens);
+    const long long want = (long long)per_sm * sms;
+    const int grid = int(most < want ? most : want);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kQ4Threads);
+    cfg.dynamicSmemBytes = size_t(lay.total());
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess || !p.balanced) return e;
+    cfg.gridDim = dim3(unsigned(p.num_seqs * groups), unsigned((H * p.group + kQ4MergeWarps - 1) / kQ4MergeWarps));
+    cfg.blockDim = dim3(32 * kQ4MergeWarps);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D>, p, grid);
+}
+
+}  // namespace pkv

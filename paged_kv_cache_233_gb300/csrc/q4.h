@@ -72,7 +72,14 @@ struct Q4AttnParams {
     int num_blocks, block_size, log2_block, max_blocks;
     int part_tokens;              // tokens per partition; 0: whole contexts
     int max_parts;
+    // decode
+    int balanced;                 // equal shares of the call's tiles per CTA, pieces joined
+    int log2_hpu;                 // kv heads per unit: 4, 2 or 1
+    int stages;
 };
+// Decode, with the balanced split's merge (fixed partitions: the caller merges).
+cudaError_t launch_decode_q4_f16(int head_dim, const Q4AttnParams &p, int sms, cudaStream_t st);
+cudaError_t launch_decode_q4_bf16(int head_dim, const Q4AttnParams &p, int sms, cudaStream_t st);
 cudaError_t launch_attn_q4(int dtype, int head_dim, const Q4AttnParams &p, int rows, cudaStream_t st);
 
 }  // namespace pkv
