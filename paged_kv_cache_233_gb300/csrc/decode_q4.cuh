@@ -27,11 +27,13 @@
 // 8- or 11-bit significand: the MMAs are fp16 ones in bf16 caches too.
 //
 // Softmax reference. p = 2^(z - ref), and ref moves only when it must: when a
-// p times the largest scale beside it passes 2^14 (fp16 ends at 2^16). Then
-// ref becomes the tile's largest score plus the exponent of its largest scale
-// minus 4, so that p * s sits in the upper part of fp16's range whatever V's
-// size, and the sums are rescaled. ref never goes down. Everything is relative
-// to it, so no result depends on when it moved beyond rounding.
+// p or a scale passes the bounds set with ref, whose product is 2^14 (fp16
+// ends at 2^16). Then, with 2^e above the tile's largest scale, the bounds
+// become 2^(12 - e) for p and 2^(e + 2) for scales, ref becomes the tile's
+// largest score plus e - 4, if that is more, so that p * s sits in the upper
+// part of fp16's range whatever V's size, and the sums are rescaled.
+// Everything is relative to ref, so no result depends on when it moved beyond
+// rounding.
 //
 // Work. A unit is (sequence, group of H kv heads, range of keys), split whole,
 // in fixed partitions or in equal shares of the call's 32-key tiles per CTA.
@@ -53,8 +55,12 @@ constexpr int kQ4Threads = 32 * (1 + kQ4Consumers);
 constexpr int kQ4CtasPerSm = 3;
 constexpr unsigned kQ4All = 0xffffffffu;
 
-// Equal shares of `total` tiles over `grid` CTAs.
-__host__ __device__ inline long long q4_share(long long total, int c, int grid) { return total * c / grid; }
+// Balanced split: the CTAs that get a share of `total` tiles, none of them
+// empty, and share c's first tile.
+__device__ __forceinline__ int q4_sharers(int total, int grid) { return max(1, min(grid, total)); }
+__device__ __forceinline__ int q4_share(int total, int c, int sharers) {
+    return int((long long)total * c / sharers);
+}
 
 struct Q4Smem {
     int stage_bytes, stages, seqs, head_dim, shared_heads;   // shared_heads: warps of one kv head join states
@@ -90,8 +96,9 @@ struct Q4Walk {
         s = count = 0;
         const int total = base[S];
         if (balanced) {
-            pos = int(q4_share(total, blockIdx.x, gridDim.x));
-            end = int(q4_share(total, blockIdx.x + 1, gridDim.x));
+            const int n = q4_sharers(total, gridDim.x), c = blockIdx.x;
+            pos = c < n ? q4_share(total, c, n) : total;
+            end = c < n ? q4_share(total, c + 1, n) : total;
             stride = 0;
         } else {
             pos = blockIdx.x;
@@ -200,13 +207,19 @@ __device__ __forceinline__ float middle_of(uint32_t w) {
     else return __half2float(__ushort_as_half(uint16_t(w >> 16)));
 }
 
+__device__ __forceinline__ float fmax3_q4(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // One consumer warp's state for a unit's kv head.
-template <typename T, int D>
+template <typename T, int D, int B>
 struct Q4Consumer {
     static constexpr int G = D / kQ4Group;
-    static constexpr float kMost = 16384.f;    // largest p * s that may pass without moving ref
-    static constexpr float kAbove = 4.f;       // log2: a tile that moves ref puts its largest p * s here
-    static constexpr float kLeast = 0x1p-80f;  // scales count as at least this, so that sums of p stay finite
+    static constexpr int kPanel = B * 16;              // bytes between groups
+    static constexpr int kPairs = B * D / 2;           // offset of the pairs in a (block, head)
+    static constexpr int kHead = B * D * 5 / 8;
 
     uint32_t qb[G][4];     // q in the MMA's k order
     uint32_t qs0, qs1;     // the q sums' column words
@@ -215,14 +228,29 @@ struct Q4Consumer {
     float corr[G][2];      // this lane's part of sum p m
     float l[2];            // this lane's part of sum p
     float ref[2];
-    int grp, c, mi, r8;
+    float plim;            // the bounds: p, and scales as bits of T
+    uint32_t slim;
+    int grp, c;
+    // this lane's offsets into a stage's K or V: its row of the matrix loads, of
+    // the transposed ones, and the pairs of its rows, of its matrix row's word
+    // and of token `lane`
+    uint32_t at_codes, at_trans, at_pairs, at_word, at_token;
 
-    __device__ void init(int lane) {
+    __device__ void init(int lane, int hh, int run) {
         grp = lane >> 2;
         c = lane & 3;
-        mi = lane >> 3;
-        r8 = lane & 7;
+        const int mi = lane >> 3, r8 = lane & 7;
+        const uint32_t head = uint32_t(hh * kHead);
+        at_codes = head + (G == 4 ? mi * kPanel : (mi & 1) * kPanel + octet(mi >> 1, run)) + r8 * 16;
+        at_trans = head + octet(mi, run) + r8 * 16;
+        at_pairs = head + kPairs + grp * 4 * G;
+        at_word = at_pairs + (c & (G - 1)) * 4;
+        at_token = head + (lane / B) * run + kPairs + (lane % B) * 4 * G;
     }
+
+    // Octet u of a tile (tokens 8u ..): its block's run and its row of codes, or pairs.
+    __device__ static uint32_t octet(int u, int run) { return uint32_t((8 * u / B) * run + (8 * u % B) * 16); }
+    __device__ static uint32_t octet_pairs(int u, int run) { return uint32_t((8 * u / B) * run + (8 * u % B) * 4 * G); }
 
     // Query rows qh0 .. qh0 + g - 1 of sequence s; column grp of the MMAs is head qh0 + grp.
     __device__ void begin(const T *q, size_t row0, int g, float scale_log2) {
@@ -283,20 +311,25 @@ struct Q4Consumer {
         }
         l[0] = l[1] = 0.f;
         ref[0] = ref[1] = -INFINITY;
+        plim = -1.f;
+        slim = 0;
     }
 
-    // Move the reference: z[u][h] the tile's scores (-inf where masked), top this
-    // lane's largest scale.
-    __device__ __forceinline__ void move(const float (&z)[4][2], float top) {
-        // (positive floats order as their bits)
-        const uint32_t all = __reduce_max_sync(kQ4All, __float_as_uint(top));
-        const float e = float(int(all >> 23) - 126);
+    // Move the reference and the bounds: sc the tile's sums of products, most the
+    // bits of this lane's token's largest scale.
+    __device__ __forceinline__ void move(const float (&sc)[4][2], uint32_t most, int nvalid) {
+        // (bits of values >= 0 order as the values; scales count as at least
+        // 2^-80, so that sums of p stay finite)
+        const float top = fmaxf(scale_of<T>(__reduce_max_sync(kQ4All, most)), 0x1p-80f);
+        const int e = int(__float_as_uint(top) >> 23) - 126;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float zm = fmaxf(fmaxf(z[0][h], z[1][h]), fmaxf(z[2][h], z[3][h]));
+            float zm = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) zm = fmaxf(zm, 8 * u + grp < nvalid ? sc[u][h] * kh[h] : -INFINITY);
 #pragma unroll
             for (int mask = 4; mask <= 16; mask <<= 1) zm = fmaxf(zm, __shfl_xor_sync(kQ4All, zm, mask));
-            const float nref = fmaxf(ref[h], zm + (e - kAbove));
+            const float nref = fmaxf(ref[h], zm + float(e - 4));
             const float alpha = ref[h] == -INFINITY ? 0.f : fast_exp2(ref[h] - nref);
             ref[h] = nref;
             l[h] *= alpha;
@@ -310,15 +343,17 @@ struct Q4Consumer {
                 }
             }
         }
+        plim = __uint_as_float(uint32_t(127 + 12 - e) << 23);
+        const int f = e + 2;
+        if constexpr (Elem<T>::kBf16) slim = f > 127 ? 0x7f7fu : uint32_t(f + 127) << 7;
+        else slim = f > 15 ? 0x7bffu : f < -14 ? 0x0400u : uint32_t(f + 15) << 10;
     }
 
-    // kc, vc: shared addresses of this head's codes of octet o at kc + off[o]
-    // (stride `panel` bytes between groups); pairs at kp + poff[o].
-    __device__ __forceinline__ void tile(uint32_t kbase, uint32_t vbase, const int (&off)[4], const int (&poff)[4],
-                                         int panel, int nvalid) {
+    // One tile: ks, vs the stage's K and V in shared memory, run the bytes between blocks.
+    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, int run, int nvalid) {
         const bool tail = nvalid < kQ4Tile;
         // ---- scores
-        float z[4][2];
+        float sc[4][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             // words of octets 2t and 2t + 1, all groups
@@ -327,89 +362,88 @@ struct Q4Consumer {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t r[4];
-                    ldmatrix_x4(kbase + off[2 * t + u] + mi * panel + r8 * 16, r);
+                    ldmatrix_x4(ks + at_codes + octet(2 * t + u, run), r);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[u][i] = r[i];
                 }
             } else {
+                // (octets 2t and 2t + 1 lie as far apart as octets 0 and 1)
                 uint32_t r[4];
-                const int a = mi >= 2 ? off[2 * t + 1] : off[2 * t];
-                ldmatrix_x4(kbase + a + (mi & 1) * panel + r8 * 16, r);
+                ldmatrix_x4(ks + at_codes + octet(2 * t, run), r);
                 w[0][0] = r[0]; w[0][1] = r[1]; w[1][0] = r[2]; w[1][1] = r[3];
             }
-            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
             {
                 // the m part: rows are the stored pairs
                 uint32_t a[4];
-                a[0] = q4_lds32(kbase + poff[2 * t] + grp * 4 * G + (c & (G - 1)) * 4);
-                a[1] = q4_lds32(kbase + poff[2 * t + 1] + grp * 4 * G + (c & (G - 1)) * 4);
+                a[0] = q4_lds32(ks + at_word + octet_pairs(2 * t, run));
+                a[1] = q4_lds32(ks + at_word + octet_pairs(2 * t + 1, run));
                 a[2] = G == 4 ? a[0] : 0u;
                 a[3] = G == 4 ? a[1] : 0u;
-                mma_m16n8k16<Elem<T>::kBf16>(sc, a, qs0, qs1);
+                mma_m16n8k16<Elem<T>::kBf16>(s4, a, qs0, qs1);
             }
             uint32_t p0[G], p1[G];
-            load_pairs<G>(kbase + poff[2 * t] + grp * 4 * G, p0);
-            load_pairs<G>(kbase + poff[2 * t + 1] + grp * 4 * G, p1);
+            load_pairs<G>(ks + at_pairs + octet_pairs(2 * t, run), p0);
+            load_pairs<G>(ks + at_pairs + octet_pairs(2 * t + 1, run), p1);
 #pragma unroll
             for (int i = 0; i < G; ++i) {
                 uint32_t x[4], y[4];
                 q4_codes(w[0][i], x);
                 q4_codes(w[1][i], y);
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                float acc[4];
                 const uint32_t a0[4] = {x[0], y[0], x[1], y[1]};
                 const uint32_t a1[4] = {x[2], y[2], x[3], y[3]};
-                mma_m16n8k16<false>(acc, a0, qb[i][0], qb[i][1]);
+                mma_f16_first(acc, a0, qb[i][0], qb[i][1]);
                 mma_m16n8k16<false>(acc, a1, qb[i][2], qb[i][3]);
-                fma2_by(sc[0], sc[1], acc[0], acc[1], scale_of<T>(p0[i]));
-                fma2_by(sc[2], sc[3], acc[2], acc[3], scale_of<T>(p1[i]));
+                fma2_by(s4[0], s4[1], acc[0], acc[1], scale_of<T>(p0[i]));
+                fma2_by(s4[2], s4[3], acc[2], acc[3], scale_of<T>(p1[i]));
             }
-            z[2 * t][0] = sc[0] * kh[0];
-            z[2 * t][1] = sc[1] * kh[1];
-            z[2 * t + 1][0] = sc[2] * kh[0];
-            z[2 * t + 1][1] = sc[3] * kh[1];
+            sc[2 * t][0] = s4[0];
+            sc[2 * t][1] = s4[1];
+            sc[2 * t + 1][0] = s4[2];
+            sc[2 * t + 1][1] = s4[3];
         }
-        if (tail) {
+        // ---- probabilities, and whether the reference has to move
+        uint32_t most;   // the largest scale of token `lane`'s groups
+        {
+            uint32_t w[G];
+            load_pairs<G>(vs + at_token, w);
+            most = __vmaxu2(w[0], w[1]);
+            if constexpr (G == 4) most = __vmaxu2(most, __vmaxu2(w[2], w[3]));
+            most &= 0xffffu;
+            if (tail && int(threadIdx.x & 31) >= nvalid) most = 0;
+        }
+        float pr[4][2];
+        auto probabilities = [&]() {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (8 * u + grp >= nvalid) z[u][0] = z[u][1] = -INFINITY;
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float t = fmaf(sc[u][h], kh[h], -ref[h]);
+                    if (tail && 8 * u + grp >= nvalid) t = -INFINITY;
+                    pr[u][h] = fast_exp2(t);
+                }
+            }
+        };
+        probabilities();
+        const float pm = fmax3_q4(fmax3_q4(pr[0][0], pr[0][1], pr[1][0]), fmax3_q4(pr[1][1], pr[2][0], pr[2][1]),
+                                  fmaxf(pr[3][0], pr[3][1]));
+        if (__any_sync(kQ4All, !(pm <= plim) || most > slim)) {
+            move(sc, most, nvalid);
+            probabilities();
         }
-        // ---- the values' pairs, and this lane's largest scale
-        uint32_t pw[4][G], most = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) fma2_by(l[0], l[1], pr[u][0], pr[u][1], 1.f);
+        // ---- output
+        uint32_t pw[4][G];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            load_pairs<G>(vbase + poff[u] + grp * 4 * G, pw[u]);
+            load_pairs<G>(vs + at_pairs + octet_pairs(u, run), pw[u]);
             if (tail && 8 * u + grp >= nvalid) {
 #pragma unroll
                 for (int i = 0; i < G; ++i) pw[u][i] = 0;
             }
-#pragma unroll
-            for (int i = 0; i < G; ++i) most = __vmaxu2(most, pw[u][i]);
         }
-        const float top = fmaxf(scale_of<T>(most & 0xffffu), kLeast);
-        // ---- probabilities; where one times the scale is too large (or no
-        // reference is set), they are computed again against a new reference
-        float pr[4][2];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            pr[u][0] = fast_exp2(z[u][0] - ref[0]);
-            pr[u][1] = fast_exp2(z[u][1] - ref[1]);
-        }
-        const float pm = fmaxf(fmaxf(fmaxf(pr[0][0], pr[0][1]), fmaxf(pr[1][0], pr[1][1])),
-                               fmaxf(fmaxf(pr[2][0], pr[2][1]), fmaxf(pr[3][0], pr[3][1])));
-        if (__any_sync(kQ4All, !(pm * top <= kMost) || ref[0] == -INFINITY)) {
-            move(z, top);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                pr[u][0] = fast_exp2(z[u][0] - ref[0]);
-                pr[u][1] = fast_exp2(z[u][1] - ref[1]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            l[0] += pr[u][0];
-            l[1] += pr[u][1];
-        }
-        // ---- output
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             uint32_t b[4];
@@ -420,8 +454,7 @@ struct Q4Consumer {
                 b[u] = movmatrix_trans(pack_f16(v.x, v.y));
             }
             uint32_t r[4];
-            const int a = mi >= 2 ? (mi == 3 ? off[3] : off[2]) : (mi == 1 ? off[1] : off[0]);
-            ldmatrix_x4_trans(vbase + a + i * panel + r8 * 16, r);
+            ldmatrix_x4_trans(vs + at_trans + i * kPanel, r);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 uint32_t x[4], y[4];
@@ -469,12 +502,12 @@ __device__ __forceinline__ void store_quad(T *dst, float4 v, float inv) {
 // 1 / l for a row's sum; 0 for a row without keys (a NaN sum stays NaN).
 __device__ __forceinline__ float q4_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-template <typename T, int D>
+template <typename T, int D, int B>
 __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(const __grid_constant__ Q4AttnParams p) {
     constexpr int G = D / kQ4Group;
     extern __shared__ __align__(128) uint8_t sm[];
     const uint32_t base = smem_addr(sm);
-    const int S = p.num_seqs, H = 1 << p.log2_hpu, B = p.block_size, NS = p.stages;
+    const int S = p.num_seqs, H = 1 << p.log2_hpu, NS = p.stages;
     const int TL = kQ4Consumers >> p.log2_hpu;          // warps per kv head
     const int head_bytes = q4_head_bytes(B, D), run = H * head_bytes;
     const int half = run * (kQ4Tile / B);               // K (or V) of a stage
@@ -542,17 +575,17 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
             const int32_t *table = p.block_tables + size_t(u.s) * p.max_blocks;
             const int h0 = u.hg << p.log2_hpu;
             // block ids of the next 32 blocks, one per lane
-            int win = u.t0 >> p.log2_block;
-            const int nblk = (u.t1 + B - 1) >> p.log2_block;
+            int win = u.t0 / B;
+            const int nblk = (u.t1 + B - 1) / B;
             int ids = win + lane < nblk ? __ldg(table + win + lane) : 0;
             for (int tok = u.t0; tok < u.t1; tok += kQ4Tile) {
-                const int j0 = tok >> p.log2_block;
-                if (j0 + (kQ4Tile >> p.log2_block) > win + 32) {
+                const int j0 = tok / B;
+                if (j0 + kQ4Tile / B > win + 32) {
                     win = j0;
                     ids = win + lane < nblk ? __ldg(table + win + lane) : 0;
                 }
                 int pb = __shfl_sync(kQ4All, ids, (j0 - win + blk) & 31);
-                const int present = (min(kQ4Tile, u.t1 - tok) + B - 1) >> p.log2_block;
+                const int present = (min(kQ4Tile, u.t1 - tok) + B - 1) / B;
                 if (lane == 0) {
                     ok = !*abort_flag && mbar_wait(empty0 + 8 * stage, phase ^ 1u, p.err);
                     if (ok) mbar_arrive_expect_tx(full0 + 8 * stage, uint32_t(2 * present * run));
@@ -585,17 +618,8 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
 
     // ------------------------------------------------------------ consumers
     const int cw = warp - 1, hh = cw & (H - 1), tw = cw >> p.log2_hpu, g = p.group;
-    Q4Consumer<T, D> st;
-    st.init(lane);
-    // octet u of a stage: its block's run, this head, its rows
-    int off[4], poff[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int at = ((8 * u) >> p.log2_block) * run + hh * head_bytes, row = (8 * u) & (B - 1);
-        off[u] = at + row * 16;
-        poff[u] = at + q4_pairs_at(B, D) + row * 4 * G;
-    }
-    const int panel = B * 16;
+    Q4Consumer<T, D, B> st;
+    st.init(lane, hh, run);
     int stage = 0;
     uint32_t phase = 0;
     const T *q = reinterpret_cast<const T *>(p.q);
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
                 *abort_flag = 1;
             } else if ((i & (TL - 1)) == tw) {
                 const uint32_t k = base + stage * 2 * half;
-                st.tile(k, k + half, off, poff, panel, min(kQ4Tile, u.t1 - tok));
+                st.tile(k, k + half, run, min(kQ4Tile, u.t1 - tok));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * stage);
@@ -741,28 +765,27 @@ __global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __gr
     float acc[E] = {};
     float den = 0.f;
     if (nt > 0) {
-        const long long Tt = total, A = (long long)before + (long long)hg * nt, Z = A + nt - 1;
-        auto share_of = [&](long long t) {
-            long long c = t * grid / Tt;
-            while (c + 1 < grid && q4_share(Tt, int(c + 1), grid) <= t) ++c;
-            while (c > 0 && q4_share(Tt, int(c), grid) > t) --c;
-            return int(c);
+        const int n_shares = q4_sharers(total, grid);
+        const int A = before + hg * nt, Z = A + nt - 1;   // the pair's first and last tile
+        auto share_of = [&](int t) {
+            int c = int((long long)t * n_shares / total);
+            while (c + 1 < n_shares && q4_share(total, c + 1, n_shares) <= t) ++c;
+            while (c > 0 && q4_share(total, c, n_shares) > t) --c;
+            return c;
         };
         const int c0 = share_of(A), c1 = share_of(Z);
         if (c0 == c1) return;                       // one share: written by the decode itself
         const int np = c1 - c0 + 1;
-        const int slot0 = A != q4_share(Tt, c0, grid) ? 1 : 0;
+        const int slot0 = A != q4_share(total, c0, n_shares) ? 1 : 0;
         auto row_of = [&](int i) { return (size_t(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * rows + r; };
-        // shares without tiles (fewer tiles than CTAs) left no piece
-        auto has = [&](int i) { return i < np && q4_share(Tt, c0 + i, grid) != q4_share(Tt, c0 + i + 1, grid); };
         float M = -INFINITY;
         for (int b = 0; b < np; b += 32)
-            if (has(b + lane)) M = fmaxf(M, __ldcg(p.ws_m + row_of(b + lane)));
+            if (b + lane < np) M = fmaxf(M, __ldcg(p.ws_m + row_of(b + lane)));
 #pragma unroll
         for (int mask = 16; mask >= 1; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(kQ4All, M, mask));
         for (int b = 0; b < np; b += 32) {
             float w = 0.f;
-            if (has(b + lane)) {
+            if (b + lane < np) {
                 w = fast_exp2((__ldcg(p.ws_m + row_of(b + lane)) - M) * kLog2e);
                 den = fmaf(w, __ldcg(p.ws_l + row_of(b + lane)), den);
             }
@@ -771,7 +794,7 @@ __global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __gr
                 float x[kBatch][E];
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    if (!has(b + k0 + k)) continue;
+                    if (k0 + k >= n) continue;
                     const float *src = p.ws_o + row_of(b + k0 + k) * D + lane * E;
                     if constexpr (E == 4) {
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
@@ -784,7 +807,7 @@ __global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __gr
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
                     const float wk = __shfl_sync(kQ4All, w, (k0 + k) & 31);
-                    if (!has(b + k0 + k)) continue;
+                    if (k0 + k >= n) continue;
 #pragma unroll
                     for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[k][e], acc[e]);
                 }
@@ -799,9 +822,9 @@ __global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __gr
         *reinterpret_cast<uint32_t *>(dst + e) = Elem<T>::pack2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <typename T, int D>
-cudaError_t launch_decode_q4_typed(Q4AttnParams p, int sms, cudaStream_t st) {
-    auto kernel = decode_q4_kernel<T, D>;
+template <typename T, int D, int B>
+cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
+    auto kernel = decode_q4_kernel<T, D, B>;
     const int H = 1 << p.log2_hpu, stage = 2 * H * kQ4Tile * D * 5 / 8;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -846,6 +869,13 @@ cudaError_t launch_decode_q4_typed(Q4AttnParams p, int sms, cudaStream_t st) {
     cfg.blockDim = dim3(32 * kQ4MergeWarps);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D>, p, grid);
+}
+
+template <typename T, int D>
+cudaError_t launch_decode_q4_typed(const Q4AttnParams &p, int sms, cudaStream_t st) {
+    return p.block_size == 8    ? launch_decode_q4_sized<T, D, 8>(p, sms, st)
+           : p.block_size == 16 ? launch_decode_q4_sized<T, D, 16>(p, sms, st)
+                                : launch_decode_q4_sized<T, D, 32>(p, sms, st);
 }
 
 }  // namespace pkv
