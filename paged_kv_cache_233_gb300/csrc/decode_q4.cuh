@@ -15,14 +15,18 @@
 //   K   an 8x8 matrix load gives lane (r, c) word c of token r's group: its
 //       eight channels 8c .. 8c + 7. The MMA's k order is free as long as both
 //       operands agree, so q is laid out once per unit to match. A group's two
-//       MMAs accumulate q_g . c_tg, one packed multiply-add per row applies
-//       s_tg, and one more MMA adds the m part: its rows are the stored (s, m)
-//       pairs as they are, its columns zeros for s and the q sums (in two
-//       16-bit parts) for m.
+//       MMAs accumulate q_g . (64 + code), which takes no arithmetic to make
+//       from a code, one packed multiply-add per row applies s_tg, and one more
+//       MMA adds sum_g m_tg Q_g - 72 s_tg Q_g with Q_g the sum of q_g: its rows
+//       are the stored (s, m) pairs as they are, its columns Q_g and -72 Q_g in
+//       two 16-bit parts. (An offset of 64 costs the fp32 sums 4 of their bits;
+//       1024, which would save three more shifts, cost scores too many.)
 //   V   the transposed 8x8 load gives lane (r, c) four channels 4r .. 4r + 3 of
 //       tokens 2c and 2c + 1: two MMAs' rows. Probabilities are multiplied by
-//       s_tg in fp32 and rounded once, to fp16, as the other operand; the m
-//       part is summed in fp32.
+//       s_tg in fp32 and rounded once, to fp16, as the other operand. The m
+//       part is summed in fp32; in bf16 caches with four groups, whose output
+//       is rounded far more coarsely, it takes one more MMA instead: the
+//       probabilities rounded to bf16, the pairs as stored.
 // q is scaled by a power of two per row and taken as fp16, which holds every
 // 8- or 11-bit significand: the MMAs are fp16 ones in bf16 caches too.
 //
@@ -77,42 +81,42 @@ struct Q4Smem {
 };
 
 struct Q4Unit {
-    int s, hg, L, t0, t1, part, slot;
-    bool partial;
+    int s, hg, t0, t1;
+    int part;         // its partition; balanced split: its piece slot of the CTA
+    bool partial;     // the result is a state for the merge
 };
 
 // This CTA's units in order; the producer and every consumer warp walk a copy.
 struct Q4Walk {
-    const int *base, *len;
-    int S, groups, P, balanced, s, pos, end, stride, count;
+    uint32_t base;   // shared address: [S + 1] units (or tiles) before each sequence, then [S] lengths
+    int s, pos, end, count;
 
-    __device__ void init(const int *base_, const int *len_, const Q4AttnParams &p) {
+    __device__ static int at(uint32_t a) {
+        int v;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+        return v;
+    }
+
+    __device__ void init(uint32_t base_, const Q4AttnParams &p) {
         base = base_;
-        len = len_;
-        S = p.num_seqs;
-        groups = p.n_kv_heads >> p.log2_hpu;
-        P = p.part_tokens;
-        balanced = p.balanced;
         s = count = 0;
-        const int total = base[S];
-        if (balanced) {
+        const int total = at(base + 4 * p.num_seqs);
+        if (p.balanced) {
             const int n = q4_sharers(total, gridDim.x), c = blockIdx.x;
             pos = c < n ? q4_share(total, c, n) : total;
             end = c < n ? q4_share(total, c + 1, n) : total;
-            stride = 0;
         } else {
             pos = blockIdx.x;
             end = total;
-            stride = gridDim.x;
         }
     }
 
-    __device__ bool next(Q4Unit &x) {
+    __device__ bool next(Q4Unit &x, const Q4AttnParams &p) {
         if (pos >= end) return false;
-        const int lane = threadIdx.x & 31;
+        const int lane = threadIdx.x & 31, S = p.num_seqs, groups = p.n_kv_heads >> p.log2_hpu;
         for (;;) {   // the sequence that holds pos, 32 candidates at a time
             const int c = s + 1 + lane;
-            const unsigned m = __ballot_sync(kQ4All, c > S || base[c] > pos);
+            const unsigned m = __ballot_sync(kQ4All, c > S || at(base + 4 * c) > pos);
             if (m) {
                 s += __ffs(m) - 1;
                 break;
@@ -120,26 +124,24 @@ struct Q4Walk {
             s += 32;
         }
         x.s = s;
-        x.L = len[s];
-        const int r = pos - base[s];
-        if (balanced) {
-            const int nt = (x.L + kQ4Tile - 1) / kQ4Tile;
+        const int L = at(base + 4 * (S + 1 + s));
+        const int r = pos - at(base + 4 * s);
+        if (p.balanced) {
+            const int nt = (L + kQ4Tile - 1) / kQ4Tile;
             x.hg = r / nt;
             const int a = r - x.hg * nt, b = min(nt, a + (end - pos));
             x.t0 = a * kQ4Tile;
-            x.t1 = min(x.L, b * kQ4Tile);
-            x.part = 0;
+            x.t1 = min(L, b * kQ4Tile);
+            x.part = count == 0 ? 0 : 1;
             x.partial = !(a == 0 && b == nt);
-            x.slot = count == 0 ? 0 : 1;
             pos += b - a;
         } else {
             x.part = r / groups;
             x.hg = r - x.part * groups;
-            x.t0 = x.part * P;
-            x.t1 = min(x.L, x.t0 + P);
-            x.partial = x.L > P;
-            x.slot = 0;
-            pos += stride;
+            x.t0 = x.part * p.part_tokens;
+            x.t1 = min(L, x.t0 + p.part_tokens);
+            x.partial = L > p.part_tokens;
+            pos += gridDim.x;
         }
         ++count;
         return true;
@@ -225,16 +227,19 @@ struct Q4Consumer {
     uint32_t qs0, qs1;     // the q sums' column words
     float kh[2];           // score scale of heads 2c, 2c + 1 (with the inverse of q's power of two)
     float o[G][2][4];
-    float corr[G][2];      // this lane's part of sum p m
+    // sum p m: this lane's part of it for each group, or (kMmaMiddle) the whole
+    // sum of row grp of the pairs' halves (s0, m0, s1, ..) in [0][0], [0][1]
+    static constexpr bool kMmaMiddle = Elem<T>::kBf16 && G == 4;
+    float corr[kMmaMiddle ? 2 : G][2];
     float l[2];            // this lane's part of sum p
     float ref[2];
     float plim;            // the bounds: p, and scales as bits of T
     uint32_t slim;
     int grp, c;
     // this lane's offsets into a stage's K or V: its row of the matrix loads, of
-    // the transposed ones, and the pairs of its rows, of its matrix row's word
-    // and of token `lane`
-    uint32_t at_codes, at_trans, at_pairs, at_word, at_token;
+    // the transposed ones, and the pairs of its rows, of its matrix row's word,
+    // of token `lane`, and its row of the pairs' transposed loads
+    uint32_t at_codes, at_trans, at_pairs, at_word, at_token, at_middle;
 
     __device__ void init(int lane, int hh, int run) {
         grp = lane >> 2;
@@ -245,6 +250,7 @@ struct Q4Consumer {
         at_trans = head + octet(mi, run) + r8 * 16;
         at_pairs = head + kPairs + grp * 4 * G;
         at_word = at_pairs + (c & (G - 1)) * 4;
+        at_middle = head + kPairs + octet_pairs(mi, run) + r8 * 4 * G;
         at_token = head + (lane / B) * run + kPairs + (lane % B) * 4 * G;
     }
 
@@ -272,10 +278,11 @@ struct Q4Consumer {
         }
         top = fmaxf(top, __shfl_xor_sync(kQ4All, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kQ4All, top, 2));
-        // a power of two that brings the row's largest value to [2^7, 2^8)
+        // a power of two that brings the row's largest value to [8, 16): 72
+        // times a group's sum stays in fp16's range
         const int ex = min(max(int((__float_as_uint(top) >> 23) & 255u), 30), 240);
-        const float mult = __uint_as_float(uint32_t(7 + 127 + 127 - ex) << 23);
-        const float inv = __uint_as_float(uint32_t(ex - 7) << 23);   // 1 / mult
+        const float mult = __uint_as_float(uint32_t(3 + 127 + 127 - ex) << 23);
+        const float inv = __uint_as_float(uint32_t(ex - 3) << 23);   // 1 / mult
         float sums[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -289,23 +296,26 @@ struct Q4Consumer {
             sums[i] += __shfl_xor_sync(kQ4All, sums[i], 1);
             sums[i] += __shfl_xor_sync(kQ4All, sums[i], 2);
         }
-        // the sums in two parts of the cache's type, under the pairs' m half;
+        // the sums in two parts of the cache's type, under the pairs' halves;
         // the first MMA half takes lane c's group, and so does the second with
         // four groups, while with two groups lanes 2 and 3 hold the low parts
         float mine = sums[0];
 #pragma unroll
         for (int i = 1; i < G; ++i)
             if ((c & (G - 1)) == i) mine = sums[i];
-        const float hi = Elem<T>::to_float(Elem<T>::from_float(mine));
-        const uint32_t whi = Elem<T>::pack2(0.f, mine), wlo = Elem<T>::pack2(0.f, mine - hi);
+        const float off = -72.f * mine;
+        const uint32_t whi = Elem<T>::pack2(off, mine);
+        const float2 top2 = Elem<T>::unpack2(whi);
+        const uint32_t wlo = Elem<T>::pack2(off - top2.x, mine - top2.y);
         qs0 = G == 4 || c < 2 ? whi : wlo;
         qs1 = G == 4 ? wlo : 0u;
         const float k = scale_log2 * inv;
         kh[0] = __shfl_sync(kQ4All, k, 8 * c);
         kh[1] = __shfl_sync(kQ4All, k, 8 * c + 4);
 #pragma unroll
+        for (auto &x : corr) x[0] = x[1] = 0.f;
+#pragma unroll
         for (int i = 0; i < G; ++i) {
-            corr[i][0] = corr[i][1] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][0][e] = o[i][1][e] = 0.f;
         }
@@ -334,8 +344,9 @@ struct Q4Consumer {
             ref[h] = nref;
             l[h] *= alpha;
 #pragma unroll
+            for (auto &x : corr) x[h] *= alpha;
+#pragma unroll
             for (int i = 0; i < G; ++i) {
-                corr[i][h] *= alpha;
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     o[i][mt][h] *= alpha;
@@ -350,8 +361,8 @@ struct Q4Consumer {
     }
 
     // One tile: ks, vs the stage's K and V in shared memory, run the bytes between blocks.
+    template <bool tail>
     __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, int run, int nvalid) {
-        const bool tail = nvalid < kQ4Tile;
         // ---- scores
         float sc[4][2];
 #pragma unroll
@@ -372,7 +383,7 @@ struct Q4Consumer {
                 ldmatrix_x4(ks + at_codes + octet(2 * t, run), r);
                 w[0][0] = r[0]; w[0][1] = r[1]; w[1][0] = r[2]; w[1][1] = r[3];
             }
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+            float s4[4];
             {
                 // the m part: rows are the stored pairs
                 uint32_t a[4];
@@ -380,7 +391,7 @@ struct Q4Consumer {
                 a[1] = q4_lds32(ks + at_word + octet_pairs(2 * t + 1, run));
                 a[2] = G == 4 ? a[0] : 0u;
                 a[3] = G == 4 ? a[1] : 0u;
-                mma_m16n8k16<Elem<T>::kBf16>(s4, a, qs0, qs1);
+                mma_first<Elem<T>::kBf16>(s4, a, qs0, qs1);
             }
             uint32_t p0[G], p1[G];
             load_pairs<G>(ks + at_pairs + octet_pairs(2 * t, run), p0);
@@ -388,12 +399,12 @@ struct Q4Consumer {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
                 uint32_t x[4], y[4];
-                q4_codes(w[0][i], x);
-                q4_codes(w[1][i], y);
+                q4_codes_64(w[0][i], x);
+                q4_codes_64(w[1][i], y);
                 float acc[4];
                 const uint32_t a0[4] = {x[0], y[0], x[1], y[1]};
                 const uint32_t a1[4] = {x[2], y[2], x[3], y[3]};
-                mma_f16_first(acc, a0, qb[i][0], qb[i][1]);
+                mma_first<false>(acc, a0, qb[i][0], qb[i][1]);
                 mma_m16n8k16<false>(acc, a1, qb[i][2], qb[i][3]);
                 fma2_by(s4[0], s4[1], acc[0], acc[1], scale_of<T>(p0[i]));
                 fma2_by(s4[2], s4[3], acc[2], acc[3], scale_of<T>(p1[i]));
@@ -435,6 +446,23 @@ struct Q4Consumer {
 #pragma unroll
         for (int u = 0; u < 4; ++u) fma2_by(l[0], l[1], pr[u][0], pr[u][1], 1.f);
         // ---- output
+        if constexpr (kMmaMiddle) {
+            // rows: the pairs' eight halves, two tokens a word (a row past them is not used)
+            uint32_t r[4];
+            ldmatrix_x4_trans(vs + at_middle, r);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if constexpr (tail) {
+                    const int k0 = 16 * t + 2 * c;
+                    r[2 * t] &= (k0 < nvalid ? 0xffffu : 0u) | (k0 + 1 < nvalid ? 0xffff0000u : 0u);
+                    r[2 * t + 1] &= (k0 + 8 < nvalid ? 0xffffu : 0u) | (k0 + 9 < nvalid ? 0xffff0000u : 0u);
+                }
+                const uint32_t a[4] = {r[2 * t], 0u, r[2 * t + 1], 0u};
+                float (&d)[4] = *reinterpret_cast<float(*)[4]>(&corr[0][0]);
+                mma_m16n8k16<true>(d, a, movmatrix_trans(Elem<T>::pack2(pr[2 * t][0], pr[2 * t][1])),
+                                   movmatrix_trans(Elem<T>::pack2(pr[2 * t + 1][0], pr[2 * t + 1][1])));
+            }
+        }
         uint32_t pw[4][G];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -449,7 +477,8 @@ struct Q4Consumer {
             uint32_t b[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                fma2_by(corr[i][0], corr[i][1], pr[u][0], pr[u][1], middle_of<T>(pw[u][i]));
+                if constexpr (!kMmaMiddle)
+                    fma2_by(corr[i][0], corr[i][1], pr[u][0], pr[u][1], middle_of<T>(pw[u][i]));
                 const float2 v = mul2_by(pr[u][0], pr[u][1], scale_of<T>(pw[u][i]));
                 b[u] = movmatrix_trans(pack_f16(v.x, v.y));
             }
@@ -476,12 +505,18 @@ struct Q4Consumer {
             for (int mask = 4; mask <= 16; mask <<= 1) l[h] += __shfl_xor_sync(kQ4All, l[h], mask);
 #pragma unroll
             for (int i = 0; i < G; ++i) {
+                float x;
+                if constexpr (kMmaMiddle) {
+                    x = __shfl_sync(kQ4All, corr[0][h], 4 * (2 * i + 1) + c);   // row 2i + 1: group i's m
+                } else {
+                    x = corr[i][h];
 #pragma unroll
-                for (int mask = 4; mask <= 16; mask <<= 1) corr[i][h] += __shfl_xor_sync(kQ4All, corr[i][h], mask);
+                    for (int mask = 4; mask <= 16; mask <<= 1) x += __shfl_xor_sync(kQ4All, x, mask);
+                }
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
-                    o[i][mt][h] += corr[i][h];
-                    o[i][mt][2 + h] += corr[i][h];
+                    o[i][mt][h] += x;
+                    o[i][mt][2 + h] += x;
                 }
             }
         }
@@ -560,7 +595,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         __syncthreads();
     }
     Q4Walk walk;
-    walk.init(seq_base, seq_len, p);
+    walk.init(base + lay.base(), p);
 
     if (warp == 0) {
         // -------------------------------------------------------- producer
@@ -571,7 +606,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         const int blk = lane >> 1, operand = lane & 1;     // this lane's copy of a tile
         const uint8_t *pool = operand ? p.v_cache : p.k_cache;
         const int lanes = 2 * (kQ4Tile / B);
-        while (ok && walk.next(u)) {
+        while (ok && walk.next(u, p)) {
             const int32_t *table = p.block_tables + size_t(u.s) * p.max_blocks;
             const int h0 = u.hg << p.log2_hpu;
             // block ids of the next 32 blocks, one per lane
@@ -625,7 +660,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     const T *q = reinterpret_cast<const T *>(p.q);
     T *out = reinterpret_cast<T *>(p.out);
     Q4Unit u;
-    while (walk.next(u)) {
+    while (walk.next(u, p)) {
         const int qh0 = ((u.hg << p.log2_hpu) + hh) * g;
         st.begin(q, size_t(u.s) * p.n_q_heads + qh0, g, p.scale_log2);
         int i = 0;
@@ -636,7 +671,8 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
                 *abort_flag = 1;
             } else if ((i & (TL - 1)) == tw) {
                 const uint32_t k = base + stage * 2 * half;
-                st.tile(k, k + half, run, min(kQ4Tile, u.t1 - tok));
+                if (u.t1 - tok >= kQ4Tile) st.template tile<false>(k, k + half, run, kQ4Tile);
+                else st.template tile<true>(k, k + half, run, u.t1 - tok);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * stage);
@@ -648,7 +684,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         st.finish();
         // row of head j: workspace rows [seq][q head][partition], or [CTA][slot][head of unit][j]
         auto ws_row = [&](int h, int j) {
-            return p.balanced ? ((size_t(blockIdx.x) * 2 + u.slot) * H + h) * g + j
+            return p.balanced ? ((size_t(blockIdx.x) * 2 + u.part) * H + h) * g + j
                               : (size_t(u.s) * p.n_q_heads + size_t((u.hg << p.log2_hpu) + h) * g + j) * p.max_parts + u.part;
         };
         if (TL == 1) {

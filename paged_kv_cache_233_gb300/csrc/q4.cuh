@@ -41,13 +41,31 @@ __device__ __forceinline__ void q4_codes(uint32_t w, uint32_t (&out)[4]) {
     out[3] = hfma2_u(d, 0x2c002c00u, 0xd480d480u);
 }
 
-// D = A (16x16) * B (16x8), fp16 operands, fp32 sums from zero.
-__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+// The same codes as fp16 values 64 + c: a nibble at mantissa bits 4-7 under 2^6.
+// Three shifts and four and-or's, for a product whose offset is taken off its sum.
+__device__ __forceinline__ void q4_codes_64(uint32_t w, uint32_t (&out)[4]) {
+    out[0] = and_or(w << 4, 0x00f000f0u, 0x54005400u);
+    out[1] = and_or(w, 0x00f000f0u, 0x54005400u);
+    out[2] = and_or(w >> 4, 0x00f000f0u, 0x54005400u);
+    out[3] = and_or(w >> 8, 0x00f000f0u, 0x54005400u);
+}
+
+// D = A (16x16) * B (16x8), fp32 sums from zero.
+template <bool kBf16>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kBf16) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    } else {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    }
 }
 
 // One (s, m) word as two floats.
