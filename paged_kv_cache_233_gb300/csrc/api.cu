@@ -234,6 +234,11 @@ namespace pkv {
 
 int api_device_state(unsigned int **err, int *sms) { return device_state(err, sms); }
 
+int api_encode_q_map(CUtensorMap *map, const void *q, int dtype, int head_dim, int n_q_heads, int num_tokens,
+                     int group) {
+    return encode_q_map(map, q, dtype, head_dim, n_q_heads, num_tokens, group);
+}
+
 }  // namespace pkv
 
 extern "C" {
@@ -492,6 +497,44 @@ size_t prefill_split_bytes(int head_dim, int ctas) {
            2 * round256(rows * 4);
 }
 
+}  // namespace
+
+}  // extern "C"
+
+// Key split (tcgen05 kernel only): the call's key tiles in equal ranges, one
+// per SM. 0 takes it when the items leave SMs idle and the workspace holds it
+// (no item then in more than kMaxKeyParts ranges); an explicit count needs the
+// workspace. Calls of more than kPfMaxSplitItems items, or whose key tiles
+// could pass the plan's ints, run whole items.
+int pkv::api_plan_key_split(PrefillParams &p, int key_parts, void *workspace, size_t workspace_bytes, int head_dim,
+                            int max_query_len, int sms) {
+    const long long cap = (long long)p.max_blocks * p.block_size;
+    const long long tiles = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens;
+    const long long items = tiles * p.n_kv_heads * p.num_seqs;
+    const long long tile_cap = (cap + 63) / 64;   // key tiles of one item at most
+    const bool splittable = items <= kPfMaxSplitItems && items * tile_cap <= INT_MAX / 2;
+    const size_t split_bytes = prefill_split_bytes(head_dim, sms);
+    int parts = splittable ? key_parts : 1;
+    if (parts == 0)
+        parts = items < sms && workspace && split_bytes <= workspace_bytes ? kMaxKeyParts : 1;
+    if (parts > 1) {
+        if (!workspace || split_bytes > workspace_bytes) return PAGEDKV_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return PAGEDKV_ERR_INVALID_ARG;
+        const size_t rows = size_t(2) * size_t(sms) * 256;
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.ws_plan = reinterpret_cast<int *>(ws);
+        p.ws_o = reinterpret_cast<float *>(ws + round256(size_t(kPfMaxSplitItems) * 4));
+        p.ws_m = p.ws_o + round256(rows * size_t(head_dim) * 4) / 4;
+        p.ws_l = p.ws_m + round256(rows * 4) / 4;
+    }
+    p.key_parts = parts;
+    return PAGEDKV_OK;
+}
+
+extern "C" {
+
+namespace {
+
 int prefill_impl(const void *q, const void *k_cache, const void *v_cache,
                  const int32_t *block_tables, const int32_t *query_start,
                  const int32_t *context_lens, float scale, void *out, int num_seqs, int num_tokens,
@@ -556,41 +599,25 @@ int prefill_impl(const void *q, const void *k_cache, const void *v_cache,
     // chunk tokens per item: the tcgen05 kernel's two Q tiles hold 128 / group
     // whole tokens each
     p.tile_tokens = tc ? 2 * (128 / group) : pkv::kPfRows / group;
-    // key split (tcgen05 kernel only): the call's key tiles in equal ranges,
-    // one per SM. 0 takes it when the items leave SMs idle and the workspace
-    // holds it (no item then in more than kMaxKeyParts ranges); an explicit
-    // count needs the workspace. Calls of more than kPfMaxSplitItems items,
-    // or whose key tiles could pass the plan's ints, run whole items.
-    const long long tiles = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens;
-    const long long items = tiles * n_kv_heads * num_seqs;
-    const long long tile_cap = (cap + 63) / 64;   // key tiles of one item at most
-    const bool splittable = tc && items <= pkv::kPfMaxSplitItems && items * tile_cap <= INT_MAX / 2;
-    const size_t split_bytes = prefill_split_bytes(head_dim, sms);
-    int parts = splittable ? key_parts : 1;
-    if (parts == 0)
-        parts = items < sms && workspace && split_bytes <= workspace_bytes ? kMaxKeyParts : 1;
-    if (parts > 1) {
-        if (!workspace || split_bytes > workspace_bytes) return PAGEDKV_ERR_WORKSPACE;
-        if (!aligned(workspace, 256)) return PAGEDKV_ERR_INVALID_ARG;
-        const size_t rows = size_t(2) * size_t(sms) * 256;
-        uint8_t *ws = static_cast<uint8_t *>(workspace);
-        p.ws_plan = reinterpret_cast<int *>(ws);
-        p.ws_o = reinterpret_cast<float *>(ws + round256(size_t(pkv::kPfMaxSplitItems) * 4));
-        p.ws_m = p.ws_o + round256(rows * size_t(head_dim) * 4) / 4;
-        p.ws_l = p.ws_m + round256(rows * 4) / 4;
+    p.max_blocks = max_blocks_per_seq;
+    p.block_size = block_size;
+    if (tc) {
+        st = pkv::api_plan_key_split(p, key_parts, workspace, workspace_bytes, head_dim, max_query_len, sms);
+        if (st != PAGEDKV_OK) return st;
+    } else {
+        p.key_parts = 1;
     }
-    p.key_parts = parts;
+    const int parts = p.key_parts;
+    const long long tiles = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens;
     if (tc) {
         // the persistent kernel counts its work items in ints
         const long long per_seq = tiles * n_kv_heads;
         if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
     }
     p.num_blocks = num_blocks;
-    p.block_size = block_size;
     int log2_block = 0;
     while ((1 << log2_block) < block_size) ++log2_block;
     p.log2_block = log2_block;
-    p.max_blocks = max_blocks_per_seq;
     cudaError_t e =
         tc ? pkv::launch_prefill_tc(dtype, head_dim, kmap, vmap, qmap, p, max_query_len, sms,
                                     static_cast<cudaStream_t>(stream))

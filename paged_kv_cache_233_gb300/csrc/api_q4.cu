@@ -9,6 +9,7 @@
 #include "../../include/pagedkv.h"
 #include "api_common.h"
 #include "decode_launch.h"
+#include "prefill.h"
 #include "q4.h"
 
 namespace {
@@ -209,8 +210,6 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
                                int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads, int head_dim,
                                int num_blocks, int block_size, int max_blocks_per_seq, int dtype,
                                int key_parts, void *workspace, size_t workspace_bytes, void *stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     if (key_parts < 0 || key_parts > 32 || num_seqs < 0 || num_tokens < 0 || max_query_len < 0 ||
         n_q_heads < 1 || max_blocks_per_seq < 1)
         return PAGEDKV_ERR_INVALID_ARG;
@@ -228,13 +227,13 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
         !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(query_start, 4) ||
         !api_aligned(context_lens, 4))
         return PAGEDKV_ERR_INVALID_ARG;
-    pkv::Q4AttnParams p{};
+    pkv::PrefillParams p{};
     int sms = 0;
     st = api_device_state(&p.err, &sms);
     if (st != PAGEDKV_OK) return st;
     p.q = q;
-    p.k_cache = static_cast<const uint8_t *>(k_cache);
-    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.k_q4 = static_cast<const uint8_t *>(k_cache);
+    p.v_q4 = static_cast<const uint8_t *>(v_cache);
     p.block_tables = block_tables;
     p.query_start = query_start;
     p.context_lens = context_lens;
@@ -242,16 +241,27 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
     p.scale_log2 = scale * pkv::kLog2e;
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
-    p.max_query_len = max_query_len;
     p.n_q_heads = n_q_heads;
     p.n_kv_heads = n_kv_heads;
     p.group = group;
+    p.tile_tokens = 2 * (128 / group);
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.max_blocks = max_blocks_per_seq;
-    p.max_parts = 1;
-    return done(pkv::launch_attn_q4(dtype, head_dim, p, num_tokens, static_cast<cudaStream_t>(stream)));
+    // the persistent kernel counts its work items in ints
+    const long long per_seq = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens * n_kv_heads;
+    if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
+    st = pkv::api_plan_key_split(p, key_parts, workspace, workspace_bytes, head_dim, max_query_len, sms);
+    if (st != PAGEDKV_OK) return st;
+    CUtensorMap qmap;
+    st = pkv::api_encode_q_map(&qmap, q, dtype, head_dim, n_q_heads, num_tokens, group);
+    if (st != PAGEDKV_OK) return st;
+    cudaError_t e = pkv::launch_prefill_q4_tc(dtype, head_dim, qmap, p, max_query_len, sms,
+                                              static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && p.key_parts > 1)
+        e = pkv::launch_prefill_merge(dtype, head_dim, p, max_query_len, sms, static_cast<cudaStream_t>(stream));
+    return done(e);
 }
 
 }  // extern "C"

@@ -42,6 +42,9 @@ struct PrefillParams {
     // launch_prefill_merge; an item within one range writes `out` itself.
     // key_parts == 1: whole items
     int key_parts;
+    // 4-bit pools (q4.h; launch_prefill_q4_tc alone reads them)
+    const uint8_t *k_q4;
+    const uint8_t *v_q4;
     int *ws_plan;
     float *ws_o;
     float *ws_m;
@@ -66,6 +69,11 @@ cudaError_t launch_prefill_tc(int dtype, int head_dim, const CUtensorMap &kmap,
                               const PrefillParams &p, int max_query_len, int num_sms,
                               cudaStream_t stream);
 int prefill_tc_smem_bytes(int head_dim);
+
+// The tcgen05 kernel over 4-bit pools (p.k_q4, p.v_q4).
+cudaError_t launch_prefill_q4_tc(int dtype, int head_dim, const CUtensorMap &qmap,
+                                 const PrefillParams &p, int max_query_len, int num_sms,
+                                 cudaStream_t stream);
 
 // Key split limits: items per call (the plan lives in the kernel's shared
 // memory) and ranges per item (a merge lane each).

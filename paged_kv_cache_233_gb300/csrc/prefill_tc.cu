@@ -55,12 +55,22 @@
 // A Q tile skips the key tiles that lie wholly past its last row. Every
 // mbarrier wait is bounded in time; on a timeout the CTA stops, waits for its
 // copies and MMAs in flight, frees its tensor memory and exits.
+//
+// 4-bit pools (kQ4, layout in q4.h) take the same kernel with four more warps.
+// The producer copies a key tile's blocks as they lie (a bulk copy per block
+// and operand) into a ring of raw tiles of their own; warps 12-15 turn each raw
+// tile into a stage, 32 keys of one operand each: a word of eight codes becomes eight
+// channels s * (c - 8) + m, rounded once to the 16-bit type, which are one
+// 16-byte chunk of the swizzled row. Rows past the context are written as
+// zeros, so the tail's detour is not needed. A stage is then complete when all
+// four warps have arrived.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "launch_cache.h"
 #include "prefill.h"
 #include "ptx.cuh"
+#include "q4.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -78,6 +88,11 @@ constexpr int kTcStages = 4;
 constexpr int kIssuer1Warp = 2 + kTcTiles * kTcRows / 32;
 constexpr int kZeroWarp = kIssuer1Warp + 1;
 constexpr int kTcThreads = 32 * (kZeroWarp + 1);
+// 4-bit pools: four more warps, and a ring of raw key tiles
+constexpr int kDqWarp0 = kZeroWarp + 1;
+constexpr int kDqWarps = 4;
+constexpr int kRawStages = 2;
+template <bool kQ4> constexpr int tc_threads() { return kTcThreads + (kQ4 ? 32 * kDqWarps : 0); }
 constexpr int kTmemTile = 256;   // tensor-memory columns per Q tile: S, S, O
 constexpr float kRescaleLog2 = 8.f;  // the reference maximum moves past 2^8
 
@@ -139,6 +154,11 @@ struct TcLayout {
     static constexpr int kOutRow = kOrder + 8 * kMaxRankedSeqs;
     static constexpr int kRefRow = kOutRow + 8 * kTcTiles * kTcRows;
     static constexpr int kTotal = kRefRow + 4 * kTcTiles * kTcRows;
+    // 4-bit pools: the raw ring's barriers (full, empty), then its tiles: K's blocks, V's
+    static constexpr int kRawBars = (kTotal + 15) & ~15;
+    static constexpr int kRaw = kRawBars + 16 * kRawStages;
+    static constexpr int kRawHalf = kTcKeys * D * 5 / 8;
+    static constexpr int kTotalQ4 = kRaw + kRawStages * 2 * kRawHalf;
     static_assert(2 * kTcKeys + D <= kTmemTile, "S buffers and O must fit a Q tile's columns");
     static_assert(kMaxSplitItems < kPlanRange && 4 * (kPlanRange + 6) <= 8 * kMaxRankedSeqs,
                   "the key split's plan must fit the item-order region");
@@ -155,6 +175,13 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
+}
+
+__device__ __forceinline__ uint4 lds128_u4(uint32_t addr) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
+    return r;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
@@ -393,8 +420,8 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
 
 }  // namespace
 
-template <typename T, int D, bool kSplit>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <typename T, int D, bool kSplit, bool kQ4>
+__global__ void __launch_bounds__(tc_threads<kQ4>(), 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ CUtensorMap qmap, const PrefillParams p, int tiles) {
@@ -413,11 +440,19 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const int B = p.block_size;
     const int g = p.group;
     const int all_items = p.num_seqs * tiles * p.n_kv_heads;
+    // (with 4-bit pools the lengths and offsets may be the kernel's before this one)
+    if (kQ4) grid_dependency_wait();
 
     if (threadIdx.x == 0) {
         for (int k = 0; k < kTcStages; ++k) {
-            mbar_init(bar(kKvFull + k), 1);
+            mbar_init(bar(kKvFull + k), kQ4 ? kDqWarps : 1);
             mbar_init(bar(kKvEmpty + k), kTcTiles);   // one commit per issuer and key tile
+        }
+        if (kQ4) {
+            for (int k = 0; k < kRawStages; ++k) {
+                mbar_init(base + Ly::kRawBars + 16 * k, 1);
+                mbar_init(base + Ly::kRawBars + 16 * k + 8, kDqWarps);
+            }
         }
         for (int t = 0; t < kTcTiles; ++t) {
             for (int b = 0; b < 2; ++b) {
@@ -478,7 +513,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // each, most of a key tile's period at D = 128). Stages run on across
         // the CTA's items, so the next item's first tiles load while the
         // current one finishes.
-        if (lane == 0) {
+        if (!kQ4 && lane == 0) {
             tma_prefetch_descriptor(&kmap);
             tma_prefetch_descriptor(&vmap);
         }
@@ -517,7 +552,39 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             PfItem it;
             if (!pf_item<kSplit>(p, order, tiles, k, lane == 0, it)) continue;
             const int32_t *table = p.block_tables + size_t(it.s) * p.max_blocks;
-            for (int j = 0; j < it.nkt; ++j) {
+            if constexpr (kQ4) {
+                // a tile's blocks, K and V, a lane per copy
+                const int hb = q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
+                const uint8_t *pool = op ? p.v_q4 : p.k_q4;
+                for (int j = 0; j < it.nkt; ++j) {
+                    const int gk = kt + j;
+                    const int st = gk % kRawStages;
+                    const int k0 = (it.kb + j) * kTcKeys;
+                    const int blocks = (min(kTcKeys, it.L - k0) + B - 1) >> p.log2_block;
+                    const bool mine = blk < blocks;
+                    int pb = mine ? __ldg(table + (k0 >> p.log2_block) + blk) : 0;
+                    const uint32_t full = base + Ly::kRawBars + 16 * st;
+                    bool got = true;
+                    if (lane == 0) {
+                        got = !aborted() && mbar_wait(full + 8, uint32_t((gk / kRawStages) & 1) ^ 1u, p.err);
+                        if (got) mbar_arrive_expect_tx(full, uint32_t(2 * blocks * hb));
+                    }
+                    __syncwarp();
+                    if (!__shfl_sync(kAll, got ? 1 : 0, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (mine) {
+                        if (pb < 0 || pb >= p.num_blocks) {
+                            atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+                            pb = 0;
+                        }
+                        bulk_load(base + Ly::kRaw + st * 2 * Ly::kRawHalf + op * Ly::kRawHalf + blk * hb,
+                                  pool + (size_t(pb) * p.n_kv_heads + it.h) * hb, uint32_t(hb), full);
+                    }
+                    ++armed;
+                }
+            } else for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
                 const int st = gk % kTcStages;
                 const int k0 = (it.kb + j) * kTcKeys;
@@ -568,9 +635,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // (a tail stage completes only with the zeroing warp's arrival: when that
             // warp stopped too, the wait ends at its time limit, its copies long done)
             sts32(flag, 1);
-            const int first = armed > kTcStages ? armed - kTcStages : 0;
+            constexpr int kRing = kQ4 ? kRawStages : kTcStages;
+            const int first = armed > kRing ? armed - kRing : 0;
             for (int x = first; x < armed; ++x)
-                mbar_wait(bar(kKvFull + x % kTcStages), uint32_t((x / kTcStages) & 1), p.err);
+                mbar_wait(kQ4 ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kTcStages),
+                          uint32_t((x / kRing) & 1), p.err);
         }
         __syncwarp();
     } else if (warp == kZeroWarp) {
@@ -638,7 +707,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     break;
                 }
             }
-            if (it.tail) {
+            if (!kQ4 && it.tail) {
                 const int st = (kt + it.nkt - 1) % kTcStages;
                 const int present = it.L - (it.kb + it.nkt - 1) * kTcKeys;
                 bool got = true;
@@ -670,6 +739,81 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             for (int t = 0; t < kTcTiles; ++t)
                 if (qlast[t] >= 0) mbar_wait(bar(bar_qfull(t)), uint32_t(qlast[t] & 1), p.err);
         }
+        __syncwarp();
+    } else if (kQ4 && warp >= kDqWarp0) {
+        // -------------------------------------- 4-bit pools: raw tiles to stages
+        // A lane owns a key row of K or V: its pairs, then per group 16 bytes of
+        // codes, each word of which is one 16-byte chunk of the stage's row.
+        constexpr int G = D / kQ4Group;
+        constexpr uint32_t kOne = kBf16 ? 0x43004300u : 0x64006400u;    // 128 or 1024: a code's unit is one ulp
+        constexpr uint32_t kBack = kBf16 ? 0xc308c308u : 0xe408e408u;   // minus that and 8
+        const int row = 32 * (warp & 1) + lane, op = (warp - kDqWarp0) >> 1;
+        const int hb = q4_head_bytes(B, D), blk = row >> p.log2_block, off = row & (B - 1);
+        const uint32_t src = base + Ly::kRaw + uint32_t(blk * hb + off * 16);
+        const uint32_t pairs = base + Ly::kRaw + uint32_t(blk * hb + q4_pairs_at(B, D) + off * 4 * G);
+        const uint32_t dst = base + Ly::kKv + uint32_t(row * 128);
+        int kt = 0;
+        bool ok = true;
+        for (int m = 0; ok; ++m) {
+            const int k = pf_item_index<kSplit>(m);
+            if (k >= num_items) break;
+            PfItem it;
+            if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
+            for (int j = 0; j < it.nkt; ++j) {
+                const int gk = kt + j;
+                const int st = gk % kTcStages, rs = gk % kRawStages;
+                const uint32_t rfull = base + Ly::kRawBars + 16 * rs;
+                const bool live = (it.kb + j) * kTcKeys + row < it.L;
+                // the raw tile is there, and the stage's last readers are done
+                bool got = mbar_try_wait(rfull, uint32_t((gk / kRawStages) & 1)) ||
+                           (!aborted() && mbar_wait(rfull, uint32_t((gk / kRawStages) & 1), p.err));
+                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u) ||
+                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err)));
+                if (!__all_sync(kAll, got)) {
+                    ok = false;
+                    break;
+                }
+                {
+                    const uint32_t from = uint32_t(rs * 2 * Ly::kRawHalf + op * Ly::kRawHalf);
+                    const uint32_t to = dst + uint32_t(st * Ly::kStage + op * Ly::kHalf);
+                    uint32_t pw[G];
+                    uint4 cw[G];
+#pragma unroll
+                    for (int i = 0; i < G; ++i) cw[i] = lds128_u4(src + from + uint32_t(i * B * 16));
+#pragma unroll
+                    for (int i = 0; i < G; ++i) pw[i] = uint32_t(lds32(pairs + from + 4 * i));
+#pragma unroll
+                    for (int i = 0; i < G; ++i) {
+                        const uint32_t s2 = __byte_perm(pw[i], 0, 0x1010), m2 = __byte_perm(pw[i], 0, 0x3232);
+                        const uint32_t w4[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // bytes of the codes at even channels (low half) and odd ones (high)
+                            const uint32_t lo = w4[c], hi = lo >> 4;
+                            uint32_t x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t two = __byte_perm(lo, hi, uint32_t(e | ((4 + e) << 8)));
+                                const uint32_t v = and_or(two, 0x000f000fu, kOne);
+                                x[e] = q4_fma<T>(q4_add<T>(v, kBack), s2, m2);
+                                x[e] = live ? x[e] : 0u;
+                            }
+                            const uint32_t chunk = uint32_t((i & 1) * 4 + c);
+                            sts128(to + uint32_t((i >> 1) * Ly::kKvSlab) + ((chunk ^ uint32_t(row & 7)) << 4),
+                                   make_uint4(x[0], x[1], x[2], x[3]));
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(kKvFull + st));
+                    mbar_arrive(rfull + 8);
+                }
+            }
+            kt += it.nkt;
+        }
+        if (lane == 0 && !ok) sts32(flag, 1);
         __syncwarp();
     } else if (warp == 1 || warp == kIssuer1Warp) {
         // ------------------------------------------------------- MMA issuers
@@ -1094,12 +1238,12 @@ int prefill_tc_smem_bytes(int head_dim) {
     return (head_dim == 64 ? TcLayout<64>::kTotal : TcLayout<128>::kTotal) + 1024;
 }
 
-template <typename T, int D, bool kSplit>
+template <typename T, int D, bool kSplit, bool kQ4 = false>
 static cudaError_t launch_tc_instance(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                       const CUtensorMap &qmap, const PrefillParams &p, int max_query_len, int num_sms,
                                       cudaStream_t stream) {
-    auto kernel = paged_prefill_tc_kernel<T, D, kSplit>;
-    const int smem = TcLayout<D>::kTotal + 1024;
+    auto kernel = paged_prefill_tc_kernel<T, D, kSplit, kQ4>;
+    const int smem = (kQ4 ? TcLayout<D>::kTotalQ4 : TcLayout<D>::kTotal) + 1024;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1124,7 +1268,7 @@ static cudaError_t launch_tc_instance(const CUtensorMap &kmap, const CUtensorMap
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(tc_threads<kQ4>());
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1184,6 +1328,24 @@ cudaError_t launch_prefill_tc(int dtype, int head_dim, const CUtensorMap &kmap,
                     : launch_tc_instance<__half, 64, false>(kmap, vmap, qmap, p, max_query_len, num_sms, stream);
     return bf16 ? launch_tc_instance<__nv_bfloat16, 128, false>(kmap, vmap, qmap, p, max_query_len, num_sms, stream)
                 : launch_tc_instance<__half, 128, false>(kmap, vmap, qmap, p, max_query_len, num_sms, stream);
+}
+
+template <typename T, int D>
+static cudaError_t launch_q4_instance(const CUtensorMap &qmap, const PrefillParams &p, int max_query_len,
+                                      int num_sms, cudaStream_t stream) {
+    return p.key_parts > 1
+               ? launch_tc_instance<T, D, true, true>(qmap, qmap, qmap, p, max_query_len, num_sms, stream)
+               : launch_tc_instance<T, D, false, true>(qmap, qmap, qmap, p, max_query_len, num_sms, stream);
+}
+
+cudaError_t launch_prefill_q4_tc(int dtype, int head_dim, const CUtensorMap &qmap, const PrefillParams &p,
+                                 int max_query_len, int num_sms, cudaStream_t stream) {
+    const bool bf16 = dtype == PAGEDKV_BF16;
+    if (head_dim == 64)
+        return bf16 ? launch_q4_instance<__nv_bfloat16, 64>(qmap, p, max_query_len, num_sms, stream)
+                    : launch_q4_instance<__half, 64>(qmap, p, max_query_len, num_sms, stream);
+    return bf16 ? launch_q4_instance<__nv_bfloat16, 128>(qmap, p, max_query_len, num_sms, stream)
+                : launch_q4_instance<__half, 128>(qmap, p, max_query_len, num_sms, stream);
 }
 
 }  // namespace pkv

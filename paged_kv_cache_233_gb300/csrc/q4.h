@@ -55,24 +55,21 @@ struct TablesParams {
 };
 cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t st);
 
-// One query row attends to the first `limit` keys of its sequence: decode has
-// a row per sequence, prefill a row per chunk token.
+// Decode over the 4-bit cache.
 struct Q4AttnParams {
-    const void *q;                // [rows][n_q_heads][head_dim]
+    const void *q;                // [num_seqs][n_q_heads][head_dim]
     const uint8_t *k_cache;
     const uint8_t *v_cache;
     const int32_t *block_tables;  // [num_seqs][max_blocks]
-    const int32_t *query_start;   // [num_seqs + 1], or null: row s is sequence s's
     const int32_t *context_lens;  // [num_seqs]
     void *out;
     float *ws_o, *ws_m, *ws_l;
     unsigned int *err;
     float scale_log2;
-    int num_seqs, num_tokens, max_query_len, n_q_heads, n_kv_heads, group;
+    int num_seqs, n_q_heads, n_kv_heads, group;
     int num_blocks, block_size, log2_block, max_blocks;
-    int part_tokens;              // tokens per partition; 0: whole contexts
+    int part_tokens;              // tokens per partition (unsplit: the tables' whole width)
     int max_parts;
-    // decode
     int balanced;                 // equal shares of the call's tiles per CTA, pieces joined
     int log2_hpu;                 // kv heads per unit: 4, 2 or 1
     int stages;
@@ -80,6 +77,5 @@ struct Q4AttnParams {
 // Decode, with the balanced split's merge (fixed partitions: the caller merges).
 cudaError_t launch_decode_q4_f16(int head_dim, const Q4AttnParams &p, int sms, cudaStream_t st);
 cudaError_t launch_decode_q4_bf16(int head_dim, const Q4AttnParams &p, int sms, cudaStream_t st);
-cudaError_t launch_attn_q4(int dtype, int head_dim, const Q4AttnParams &p, int rows, cudaStream_t st);
 
 }  // namespace pkv
