@@ -54,7 +54,7 @@ int move_rows(const void *k, const void *v, const int64_t *slot_mapping, const v
     int sms = 0;
     st = api_device_state(&err, &sms);
     if (st != PAGEDKV_OK) return st;
-    return done(launch((long long)num_blocks * block_size, sms, err));
+    return done(launch((long long)num_blocks * block_size, err));
 }
 
 }  // namespace
@@ -111,10 +111,10 @@ int paged_kv_append_q4(const void *k, const void *v, const int64_t *slot_mapping
                        void *v_cache, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
                        int head_dim, int dtype, void *stream) {
     return move_rows(k, v, slot_mapping, k_cache, v_cache, num_tokens, num_blocks, block_size, n_kv_heads,
-                     head_dim, dtype, [&](long long num_slots, int sms, unsigned int *err) {
+                     head_dim, dtype, [&](long long num_slots, unsigned int *err) {
                          return pkv::launch_append_q4(k, v, slot_mapping, static_cast<uint8_t *>(k_cache),
                                                       static_cast<uint8_t *>(v_cache), num_tokens, n_kv_heads,
-                                                      head_dim, block_size, num_slots, dtype, sms, err,
+                                                      head_dim, block_size, num_slots, dtype, err,
                                                       static_cast<cudaStream_t>(stream));
                      });
 }
@@ -123,11 +123,11 @@ int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *
                        void *v, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
                        int head_dim, int dtype, void *stream) {
     return move_rows(k, v, slot_mapping, k_cache, v_cache, num_tokens, num_blocks, block_size, n_kv_heads,
-                     head_dim, dtype, [&](long long num_slots, int sms, unsigned int *err) {
+                     head_dim, dtype, [&](long long num_slots, unsigned int *err) {
                          return pkv::launch_gather_q4(static_cast<const uint8_t *>(k_cache),
                                                       static_cast<const uint8_t *>(v_cache), slot_mapping, k, v,
                                                       num_tokens, n_kv_heads, head_dim, block_size, num_slots,
-                                                      dtype, sms, err, static_cast<cudaStream_t>(stream));
+                                                      dtype, err, static_cast<cudaStream_t>(stream));
                      });
 }
 

@@ -756,22 +756,26 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
 }
 
 // Balanced split: the pieces of each (sequence, head group) that spans shares,
-// joined by the softmax identity. A warp per row of the pair; zero rows for
-// empty sequences. Where a pair's tiles lie follows from the lengths alone.
-constexpr int kQ4MergeWarps = 4;
+// joined by the softmax identity; zero rows for empty sequences. Where a
+// pair's tiles lie follows from the lengths alone. A row is kWarps warps' work
+// (the launcher takes four where a pair can have many pieces): each joins
+// every kWarps-th piece, all loads of eight pieces in one round trip, against
+// a running maximum of its own, and the warps' sums meet in shared memory.
+constexpr int kQ4MergeThreads = 128;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __grid_constant__ Q4AttnParams p, int grid) {
-    constexpr int E = D / 32, kBatch = 8;
+template <typename T, int D, int kWarps>
+__global__ void __launch_bounds__(kQ4MergeThreads) merge_q4_kernel(const __grid_constant__ Q4AttnParams p, int grid) {
+    constexpr int E = D / 32, kBatch = 8, kRows = kQ4MergeThreads / 32 / kWarps;
     grid_dependency_wait();
     grid_launch_dependents();
     const int H = 1 << p.log2_hpu, groups = p.n_kv_heads >> p.log2_hpu, rows = H * p.group;
     const int s = blockIdx.x / groups, hg = blockIdx.x - s * groups;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kQ4MergeWarps + warp;
+    const int r = blockIdx.y * kRows + warp / kWarps, first = warp % kWarps;
     const int cap = p.max_blocks * p.block_size;
-    __shared__ int part[2][kQ4MergeWarps];
-    int before = 0, total = 0, nt = 0;
+    __shared__ int part[2][kQ4MergeThreads / 32];
+    __shared__ float joined[kQ4MergeThreads / 32][D + 2];
+    int before = 0, total = 0;
     for (int t = threadIdx.x; t < p.num_seqs; t += blockDim.x) {
         const int n = (min(max(__ldg(p.context_lens + t), 0), cap) + kQ4Tile - 1) / kQ4Tile * groups;
         total += n;
@@ -783,18 +787,15 @@ __global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __gr
         part[0][warp] = before;
         part[1][warp] = total;
     }
+    const int nt = (min(max(__ldg(p.context_lens + s), 0), cap) + kQ4Tile - 1) / kQ4Tile;
     __syncthreads();
     before = total = 0;
 #pragma unroll
-    for (int w = 0; w < kQ4MergeWarps; ++w) {
+    for (int w = 0; w < kQ4MergeThreads / 32; ++w) {
         before += part[0][w];
         total += part[1][w];
     }
-    nt = (min(max(__ldg(p.context_lens + s), 0), cap) + kQ4Tile - 1) / kQ4Tile;
-    if (r >= rows) return;
-    T *dst = reinterpret_cast<T *>(p.out) + (size_t(s) * p.n_q_heads + hg * rows + r) * D + lane * E;
-    float acc[E] = {};
-    float den = 0.f;
+    int c0 = 0, np = 0, slot0 = 0;
     if (nt > 0) {
         const int n_shares = q4_sharers(total, grid);
         const int A = before + hg * nt, Z = A + nt - 1;   // the pair's first and last tile
@@ -804,49 +805,77 @@ __global__ void __launch_bounds__(32 * kQ4MergeWarps) merge_q4_kernel(const __gr
             while (c > 0 && q4_share(total, c, n_shares) > t) --c;
             return c;
         };
-        const int c0 = share_of(A), c1 = share_of(Z);
-        if (c0 == c1) return;                       // one share: written by the decode itself
-        const int np = c1 - c0 + 1;
-        const int slot0 = A != q4_share(total, c0, n_shares) ? 1 : 0;
-        auto row_of = [&](int i) { return (size_t(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * rows + r; };
-        float M = -INFINITY;
-        for (int b = 0; b < np; b += 32)
-            if (b + lane < np) M = fmaxf(M, __ldcg(p.ws_m + row_of(b + lane)));
+        c0 = share_of(A);
+        np = share_of(Z) - c0 + 1;
+        if (np == 1) return;                        // one share: written by the decode itself
+        slot0 = A != q4_share(total, c0, n_shares) ? 1 : 0;
+    }
+    if (kWarps == 1 && r >= rows) return;
+    float acc[E] = {}, M = -INFINITY, den = 0.f;
+    if (r < rows) {
+        for (int b = first; b < np; b += kBatch * kWarps) {
+            float x[kBatch][E], m[kBatch], l[kBatch];
 #pragma unroll
-        for (int mask = 16; mask >= 1; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(kQ4All, M, mask));
-        for (int b = 0; b < np; b += 32) {
-            float w = 0.f;
-            if (b + lane < np) {
-                w = fast_exp2((__ldcg(p.ws_m + row_of(b + lane)) - M) * kLog2e);
-                den = fmaf(w, __ldcg(p.ws_l + row_of(b + lane)), den);
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = b + k * kWarps;
+                m[k] = -INFINITY;
+                l[k] = 0.f;
+                if (i >= np) continue;
+                const size_t row = (size_t(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * rows + r;
+                m[k] = __ldcg(p.ws_m + row) * kLog2e;
+                l[k] = __ldcg(p.ws_l + row);
+                const float *src = p.ws_o + row * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    x[k][0] = v.x; x[k][1] = v.y;
+                }
             }
-            const int n = min(32, np - b);
-            for (int k0 = 0; k0 < n; k0 += kBatch) {
-                float x[kBatch][E];
+            float top = M;
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    if (k0 + k >= n) continue;
-                    const float *src = p.ws_o + row_of(b + k0 + k) * D + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                        x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
-                    } else {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                        x[k][0] = v.x; x[k][1] = v.y;
-                    }
-                }
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, m[k]);
+            const float alpha = M == -INFINITY ? 0.f : fast_exp2(M - top);
+            M = top;
+            den *= alpha;
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const float wk = __shfl_sync(kQ4All, w, (k0 + k) & 31);
-                    if (k0 + k >= n) continue;
+            for (int e = 0; e < E; ++e) acc[e] *= alpha;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[k][e], acc[e]);
-                }
+            for (int k = 0; k < kBatch; ++k) {
+                if (b + k * kWarps >= np) continue;
+                const float w = fast_exp2(m[k] - M);
+                den = fmaf(w, l[k], den);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[k][e], acc[e]);
             }
         }
-#pragma unroll
-        for (int mask = 16; mask >= 1; mask >>= 1) den += __shfl_xor_sync(kQ4All, den, mask);
     }
+    if constexpr (kWarps > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) joined[warp][lane * E + e] = acc[e];
+        if (lane == 0) {
+            joined[warp][D] = M;
+            joined[warp][D + 1] = den;
+        }
+        __syncthreads();
+        if (first != 0 || r >= rows) return;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, joined[warp + w][D]);
+        den = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w >= np) continue;                  // this warp had no piece
+            const float f = fast_exp2(joined[warp + w][D] - top);
+            den = fmaf(f, joined[warp + w][D + 1], den);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, joined[warp + w][lane * E + e], acc[e]);
+        }
+    }
+    T *dst = reinterpret_cast<T *>(p.out) + (size_t(s) * p.n_q_heads + hg * rows + r) * D + lane * E;
     const float inv = q4_inverse(den);
 #pragma unroll
     for (int e = 0; e < E; e += 2)
@@ -896,10 +925,17 @@ cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess || !p.balanced) return e;
-    cfg.gridDim = dim3(unsigned(p.num_seqs * groups), unsigned((H * p.group + kQ4MergeWarps - 1) / kQ4MergeWarps));
-    cfg.blockDim = dim3(32 * kQ4MergeWarps);
+    // four warps per row where the pairs are few enough to have more than eight pieces each
+    const int rows = H * p.group;
+    const long long pairs = groups * p.num_seqs;
+    cfg.blockDim = dim3(kQ4MergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D>, p, grid);
+    if (pairs * 8 <= grid) {
+        cfg.gridDim = dim3(unsigned(pairs), unsigned(rows));
+        return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D, 4>, p, grid);
+    }
+    cfg.gridDim = dim3(unsigned(pairs), unsigned((rows + 3) / 4));
+    return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D, 1>, p, grid);
 }
 
 template <typename T, int D>

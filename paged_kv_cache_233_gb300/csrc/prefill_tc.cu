@@ -745,8 +745,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // A lane owns a key row of K or V: its pairs, then per group 16 bytes of
         // codes, each word of which is one 16-byte chunk of the stage's row.
         constexpr int G = D / kQ4Group;
-        constexpr uint32_t kOne = kBf16 ? 0x43004300u : 0x64006400u;    // 128 or 1024: a code's unit is one ulp
-        constexpr uint32_t kBack = kBf16 ? 0xc308c308u : 0xe408e408u;   // minus that and 8
         const int row = 32 * (warp & 1) + lane, op = (warp - kDqWarp0) >> 1;
         const int hb = q4_head_bytes(B, D), blk = row >> p.log2_block, off = row & (B - 1);
         const uint32_t src = base + Ly::kRaw + uint32_t(blk * hb + off * 16);
@@ -788,16 +786,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const uint32_t w4[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            // bytes of the codes at even channels (low half) and odd ones (high)
-                            const uint32_t lo = w4[c], hi = lo >> 4;
                             uint32_t x[4];
+                            q4_values<T>(w4[c], s2, m2, x);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t two = __byte_perm(lo, hi, uint32_t(e | ((4 + e) << 8)));
-                                const uint32_t v = and_or(two, 0x000f000fu, kOne);
-                                x[e] = q4_fma<T>(q4_add<T>(v, kBack), s2, m2);
-                                x[e] = live ? x[e] : 0u;
-                            }
+                            for (int e = 0; e < 4; ++e) x[e] = live ? x[e] : 0u;
                             const uint32_t chunk = uint32_t((i & 1) * 4 + c);
                             sts128(to + uint32_t((i >> 1) * Ly::kKvSlab) + ((chunk ^ uint32_t(row & 7)) << 4),
                                    make_uint4(x[0], x[1], x[2], x[3]));

@@ -46,6 +46,22 @@ __device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) 
     return d;
 }
 
+// A word of eight codes -> the eight channels they stand for, in order, two to a
+// register: s * (c - 8) + m in one rounding. A code at mantissa bits 0-3 under
+// 2^10 (2^7 in bf16) reads 1024 + c (128 + c); s2 and m2 hold s and m twice.
+template <typename T>
+__device__ __forceinline__ void q4_values(uint32_t w, uint32_t s2, uint32_t m2, uint32_t (&out)[4]) {
+    constexpr uint32_t kOne = Elem<T>::kBf16 ? 0x43004300u : 0x64006400u;
+    constexpr uint32_t kBack = Elem<T>::kBf16 ? 0xc308c308u : 0xe408e408u;   // minus that and 8
+    const uint32_t up = w >> 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        // byte e: its low half to the low 16 bits, its high half to the high 16
+        const uint32_t two = __byte_perm(w, up, uint32_t(e | ((4 + e) << 8)));
+        out[e] = q4_fma<T>(q4_add<T>(and_or(two, 0x000f000fu, kOne), kBack), s2, m2);
+    }
+}
+
 // The four codes in each 16-bit half of w, as fp16 values c - 8 (exact): out[i]
 // holds nibble i of the low half in its low half and nibble i of the high
 // half in its high half. Two exponents cover four nibbles with one shift: a

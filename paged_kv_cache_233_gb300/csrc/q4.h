@@ -31,11 +31,11 @@ __host__ __device__ constexpr int q4_pairs_at(int block_size, int head_dim) {
 
 cudaError_t launch_append_q4(const void *k, const void *v, const int64_t *slots, uint8_t *k_cache,
                              uint8_t *v_cache, int num_tokens, int n_kv_heads, int head_dim,
-                             int block_size, long long num_slots, int dtype, int num_sms,
+                             int block_size, long long num_slots, int dtype,
                              unsigned int *err, cudaStream_t st);
 cudaError_t launch_gather_q4(const uint8_t *k_cache, const uint8_t *v_cache, const int64_t *slots,
                              void *k, void *v, int num_tokens, int n_kv_heads, int head_dim,
-                             int block_size, long long num_slots, int dtype, int num_sms,
+                             int block_size, long long num_slots, int dtype,
                              unsigned int *err, cudaStream_t st);
 
 struct TablesParams {

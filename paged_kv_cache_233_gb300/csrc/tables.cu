@@ -30,6 +30,7 @@ namespace cg = cooperative_groups;
 constexpr unsigned kAllLanes = 0xffffffffu;
 constexpr int kMaxThreads = 1024;
 constexpr int kPerThread = 4;          // requests per thread: 4096 requests at most
+constexpr int kTokens = 4;             // tokens per lane at a time
 constexpr unsigned kFull30 = 1u << 30; // sums saturate here: past every capacity
 
 __device__ __forceinline__ unsigned add_sat(unsigned a, unsigned b) { return min(a + b, kFull30); }
@@ -87,6 +88,9 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const TablesP
     __shared__ uint2 warp_sums[32];
     cg::cluster_group cluster = cg::this_cluster();
     const int S = p.num_seqs, B = p.block_size;
+    // x / B (x >= 0): a shift where B is a power of two
+    const int shift = (B & (B - 1)) == 0 ? 31 - __clz(B) : -1;
+    auto divide = [&](int x) { return shift >= 0 ? x >> shift : x / B; };
     int *tok0 = arrays, *blk0 = arrays + S + 1, *held_tokens = blk0 + S + 1;
     const unsigned rank = cluster.block_rank(), blocks = cluster.num_blocks();
 
@@ -184,25 +188,48 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const TablesP
         const int s = last_at_or_before(blk0, S, x);
         const int id = __ldg(p.free_blocks + (free_count - 1 - x));
         if (id < 0 || id >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-        p.block_tables[size_t(s) * p.max_blocks + (held_tokens[s] + B - 1) / B + (x - blk0[s])] = id;
+        p.block_tables[size_t(s) * p.max_blocks + divide(held_tokens[s] + B - 1) + (x - blk0[s])] = id;
     }
-    for (int t = first; t < p.token_capacity; t += stride) {
-        int s = 0, pos = -1;
-        long long slot = -1;
-        if (t < tokens) {
-            s = last_at_or_before(tok0, S, t);
-            const int held = held_tokens[s];
-            pos = held + (t - tok0[s]);
-            const int j = pos / B;
-            const int nth = j - (held + B - 1) / B;   // which of the request's opened blocks, if any
-            const int id = nth < 0 ? p.block_tables[size_t(s) * p.max_blocks + j]
-                                   : __ldg(p.free_blocks + (free_count - 1 - (blk0[s] + nth)));
-            if (id < 0 || id >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-            else slot = (long long)id * B + (pos - j * B);
+    // A warp takes runs of 32 kTokens neighbouring tokens: a lane searches its
+    // first one's request, walks on from it to the others', and has their table
+    // entries in flight together.
+    const int lane = threadIdx.x & 31;
+    for (int t0 = (first - lane) * kTokens; t0 < p.token_capacity; t0 += stride * kTokens) {
+        int s[kTokens], pos[kTokens], j[kTokens], id[kTokens];
+        int at = t0 + lane < tokens ? last_at_or_before(tok0, S, t0 + lane) : 0;
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            const int t = t0 + 32 * k + lane;
+            s[k] = 0;
+            pos[k] = -1;
+            id[k] = -1;
+            if (t < tokens) {
+                if (k > 0 && tok0[at + 1] <= t) {
+                    // the next request, or one further on
+                    at = tok0[at + 2 < S ? at + 2 : S] > t ? at + 1 : last_at_or_before(tok0, S, t);
+                }
+                const int held = held_tokens[at];
+                s[k] = at;
+                pos[k] = held + (t - tok0[at]);
+                j[k] = divide(pos[k]);
+                const int nth = j[k] - divide(held + B - 1);   // which of the request's opened blocks, if any
+                id[k] = nth < 0 ? p.block_tables[size_t(at) * p.max_blocks + j[k]]
+                                : __ldg(p.free_blocks + (free_count - 1 - (blk0[at] + nth)));
+            }
         }
-        p.token_seq[t] = s;
-        p.token_pos[t] = pos;
-        if (p.slot_mapping) p.slot_mapping[t] = slot;
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            const int t = t0 + 32 * k + lane;
+            if (t >= p.token_capacity) break;
+            long long slot = -1;
+            if (t < tokens) {
+                if (id[k] < 0 || id[k] >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+                else slot = (long long)id[k] * B + (pos[k] - j[k] * B);
+            }
+            p.token_seq[t] = s[k];
+            p.token_pos[t] = pos[k];
+            if (p.slot_mapping) p.slot_mapping[t] = slot;
+        }
     }
     // The kernel after this one may be a programmatic dependent that reads the
     // tables and lengths before its grid dependency wait, which it may start
