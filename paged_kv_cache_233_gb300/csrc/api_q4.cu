@@ -38,6 +38,16 @@ int check_pool(int num_blocks, int block_size, int n_kv_heads, int head_dim, int
 
 bool finite(float x) { return x == x && x != INFINITY && x != -INFINITY; }
 
+// Whether a prefill call of `items` items of about `tiles` key tiles each is
+// faster with its keys shared out over the SMs: whole items take
+// ceil(items / SMs) rounds of `tiles`, shared keys their even share, the extra
+// pieces and a merge.
+bool split_pays(long long items, long long tiles, int sms) {
+    const long long rounds = (items + sms - 1) / sms;
+    const double gain = double(rounds * tiles) - double(items * tiles) / sms;
+    return gain > 10.0 + 0.2 * double(items);
+}
+
 template <typename Launch>
 int move_rows(const void *k, const void *v, const int64_t *slot_mapping, const void *k_cache,
               const void *v_cache, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
@@ -252,6 +262,11 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
     // the persistent kernel counts its work items in ints
     const long long per_seq = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens * n_kv_heads;
     if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
+    if (key_parts == 0)
+        key_parts = workspace && workspace_bytes >= paged_attention_prefill_workspace_bytes(head_dim) &&
+                            split_pays(per_seq * num_seqs, (cap + 63) / 64, sms)
+                        ? 32
+                        : 1;
     st = pkv::api_plan_key_split(p, key_parts, workspace, workspace_bytes, head_dim, max_query_len, sms);
     if (st != PAGEDKV_OK) return st;
     CUtensorMap qmap;

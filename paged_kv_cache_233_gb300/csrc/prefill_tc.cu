@@ -125,6 +125,8 @@ constexpr int kNumBars = kTailV + kTcStages;
 // merely to reach every SM; a piece is an item's tiles within one range, and
 // an item cut into several pieces leaves per-row states for the merge
 constexpr int kMinPartTiles = 16;
+constexpr int kMinPartTilesQ4 = 6;
+template <bool kQ4> constexpr int min_part_tiles() { return kQ4 ? kMinPartTilesQ4 : kMinPartTiles; }
 constexpr int kMaxSplitParts = kPfMaxSplitParts;   // pieces of one item (a merge lane each)
 // the split's plan in the item-order region: off[i] = key tiles of items
 // before i (i = 0 .. items), then this CTA's range
@@ -326,6 +328,7 @@ __device__ __forceinline__ int pf_item_index(int m) {
 // Every thread of the CTA calls it.
 constexpr int kPieceCost = 4;   // a piece's fixed cost (Q copy, epilogue, merge) in key tiles
 constexpr int kMaxItemParts = 16;  // CTAs per item in the parts layout at most
+template <bool kQ4>
 __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles, int items, int *off,
                                               bool report) {
     for (int i = int(threadIdx.x); i < items; i += int(blockDim.x)) {
@@ -349,7 +352,7 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
             sum += n;
             mx = max(mx, n);
             if (pp > 0) {
-                const int eff = min(pp, max(1, (n + kMinPartTiles - 1) / kMinPartTiles));
+                const int eff = min(pp, max(1, (n + min_part_tiles<kQ4>() - 1) / min_part_tiles<kQ4>()));
                 part_mx = max(part_mx, (n + eff - 1) / eff);
             }
         }
@@ -372,7 +375,7 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
             off[0] = 0;
             int r = (T + G - 1) / G;
             if (mx > 1) r = max(r, (mx - 2) / (p.key_parts - 1) + 1);
-            r = max(r, max(min(kMinPartTiles, mx), 1));
+            r = max(r, max(min(min_part_tiles<kQ4>(), mx), 1));
             const int c = int(blockIdx.x);
             long long start, end;
             int first, count;
@@ -382,7 +385,7 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
             if (parts_layout) {
                 const int i = c / pp, q = c - i * pp;
                 const int n = i < items ? off[i + 1] - off[i] : 0;
-                const int eff = min(pp, max(1, (n + kMinPartTiles - 1) / kMinPartTiles));
+                const int eff = min(pp, max(1, (n + min_part_tiles<kQ4>() - 1) / min_part_tiles<kQ4>()));
                 first = i;
                 count = n > 0 && q < eff ? 1 : 0;
                 start = count ? off[i] + (long long)n * q / eff : 0;
@@ -496,7 +499,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     if (kSplit) {
         // (the launcher keeps the split to at most kMaxSplitItems items)
         order = base + Ly::kOrder;
-        pf_split_plan(p, tiles, all_items, reinterpret_cast<int *>(sm + Ly::kOrder), blockIdx.x == 0);
+        pf_split_plan<kQ4>(p, tiles, all_items, reinterpret_cast<int *>(sm + Ly::kOrder), blockIdx.x == 0);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -531,7 +534,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 int c0 = 0, pieces = 0;
                 if (n > 0 && pp > 0) {
                     c0 = i * pp;
-                    pieces = min(pp, max(1, (n + kMinPartTiles - 1) / kMinPartTiles));
+                    pieces = min(pp, max(1, (n + min_part_tiles<kQ4>() - 1) / min_part_tiles<kQ4>()));
                 } else if (n > 0) {
                     c0 = o / r;
                     pieces = (o + n - 1) / r - c0 + 1;
@@ -749,7 +752,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const int hb = q4_head_bytes(B, D), blk = row >> p.log2_block, off = row & (B - 1);
         const uint32_t src = base + Ly::kRaw + uint32_t(blk * hb + off * 16);
         const uint32_t pairs = base + Ly::kRaw + uint32_t(blk * hb + q4_pairs_at(B, D) + off * 4 * G);
-        const uint32_t dst = base + Ly::kKv + uint32_t(row * 128);
+        const uint32_t dst = base + Ly::kKv + uint32_t(row * 128 + ((row & 7) << 4));
         int kt = 0;
         bool ok = true;
         for (int m = 0; ok; ++m) {
@@ -780,6 +783,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     for (int i = 0; i < G; ++i) cw[i] = lds128_u4(src + from + uint32_t(i * B * 16));
 #pragma unroll
                     for (int i = 0; i < G; ++i) pw[i] = uint32_t(lds32(pairs + from + 4 * i));
+                    // (a row past the context: 0 * (c - 8) + 0)
+#pragma unroll
+                    for (int i = 0; i < G; ++i) pw[i] = live ? pw[i] : 0u;
 #pragma unroll
                     for (int i = 0; i < G; ++i) {
                         const uint32_t s2 = __byte_perm(pw[i], 0, 0x1010), m2 = __byte_perm(pw[i], 0, 0x3232);
@@ -788,10 +794,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[4];
                             q4_values<T>(w4[c], s2, m2, x);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] = live ? x[e] : 0u;
-                            const uint32_t chunk = uint32_t((i & 1) * 4 + c);
-                            sts128(to + uint32_t((i >> 1) * Ly::kKvSlab) + ((chunk ^ uint32_t(row & 7)) << 4),
+                            // chunk (i & 1) * 4 + c of the row, swizzled by the row's low bits
+                            sts128((to ^ uint32_t(((i & 1) * 4 + c) << 4)) + uint32_t((i >> 1) * Ly::kKvSlab),
                                    make_uint4(x[0], x[1], x[2], x[3]));
                         }
                     }
