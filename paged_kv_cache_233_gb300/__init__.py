@@ -1,6 +1,7 @@
 """GB300-native paged KV cache: append and fused paged-attention decode.
 
-A thin ctypes binding over ``libpagedkv.so`` (C ABI in ``include/pagedkv.h``).
+A thin binding over ``libpagedkv.so`` (C ABI in ``include/pagedkv.h``): ctypes,
+and for the 4-bit cache and the step's tables a small C++ module, ``_binding.so``.
 It only marshals torch tensors into pointers and sizes: every step of the
 path runs in the library's CUDA kernels, and there is no CPU fallback. If the
 library has not been built, the first call raises ``PagedKVError`` (build it
@@ -30,6 +31,7 @@ All tensors live on the current CUDA device; work is enqueued on the current
 torch stream (or the stream passed) and the calls return without waiting.
 """
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -463,113 +465,57 @@ def new_q4_pool(num_blocks, n_kv_heads, block_size, head_dim, device="cuda"):
     return torch.empty(num_blocks, n_kv_heads, block_size, head_dim * 5 // 8, dtype=torch.uint8, device=device)
 
 
-def _q4_pools(k_cache, v_cache, D):
-    """(NB, Hkv, B) of a pair of 4-bit pools for head_dim D, checked."""
-    cs = k_cache.shape
-    if len(cs) != 4 or v_cache.shape != cs or cs[3] * 8 != 5 * D:
-        raise PagedKVError("expected 4-bit pools [NB][Hkv][B][5 D / 8] for head_dim D")
-    return cs[0], cs[1], cs[2]
+_fast = None   # the C++ binding of the entry points below
 
 
-def _on(dev, t, name, dtype):
-    """The address of a contiguous tensor of `dtype` on CUDA device `dev`, checked."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != dev:
-        raise PagedKVError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
-    if t.dtype is not dtype:
-        raise PagedKVError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise PagedKVError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _current_device(t):
-    if not t.is_cuda:
-        raise PagedKVError("expected CUDA tensors (the paged-KV path has no CPU fallback)")
-    return torch.cuda.current_device()
+def _binding():
+    """Load the C++ binding (once). Raises PagedKVError when it is missing."""
+    global _fast
+    if _fast is None:
+        load()
+        path = os.path.join(_HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise PagedKVError(f"{path} is not built: run `python -m paged_kv_cache_233_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(PagedKVError)
+        _fast = module
+    return _fast
 
 
 def paged_kv_append_q4(k, v, slot_mapping, k_cache, v_cache, stream=None):
     """Quantise k/v [T][Hkv][D] (fp16 or bf16) into 4-bit pools at slot_mapping[T]
     (int64; -1 is padding)."""
-    ks, dt = k.shape, k.dtype
-    if len(ks) != 3 or v.shape != ks or slot_mapping.numel() != ks[0]:
-        raise PagedKVError("expected k, v [T][Hkv][D] and one slot per token")
-    NB, Hkv, B = _q4_pools(k_cache, v_cache, ks[2])
-    if ks[1] != Hkv:
-        raise PagedKVError("token rows do not match the pools' kv heads")
-    d = _current_device(k)
-    st = load().paged_kv_append_q4(
-        _on(d, k, "k", dt), _on(d, v, "v", dt), _on(d, slot_mapping, "slot_mapping", torch.int64),
-        _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8), ks[0], NB, B,
-        Hkv, ks[2], _code(k), _stream(stream))
-    _check(st, "paged_kv_append_q4")
+    (_fast or _binding()).append_q4(k, v, slot_mapping, k_cache, v_cache, stream)
 
 
 def paged_kv_gather_q4(k_cache, v_cache, slot_mapping, k, v, stream=None):
     """Rows slot_mapping[T] of 4-bit pools as k/v [T][Hkv][D] (fp16 or bf16, the
     type they were appended in); rows of a negative slot are left as they were."""
-    ks, dt = k.shape, k.dtype
-    if len(ks) != 3 or v.shape != ks or slot_mapping.numel() != ks[0]:
-        raise PagedKVError("expected k, v [T][Hkv][D] and one slot per token")
-    NB, Hkv, B = _q4_pools(k_cache, v_cache, ks[2])
-    if ks[1] != Hkv:
-        raise PagedKVError("token rows do not match the pools' kv heads")
-    d = _current_device(k)
-    st = load().paged_kv_gather_q4(
-        _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8),
-        _on(d, slot_mapping, "slot_mapping", torch.int64), _on(d, k, "k", dt), _on(d, v, "v", dt), ks[0],
-        NB, B, Hkv, ks[2], _code(k), _stream(stream))
-    _check(st, "paged_kv_gather_q4")
+    (_fast or _binding()).gather_q4(k, v, slot_mapping, k_cache, v_cache, stream)
 
 
 def paged_attention_decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out,
                               partition_tokens=0, workspace=None, stream=None):
     """paged_attention_decode over 4-bit pools (fixed partitions: multiples of 32
     tokens; workspace from new_workspace)."""
-    qs, bs, dt = q.shape, block_tables.shape, q.dtype
-    if len(qs) != 3 or out.shape != qs or len(bs) != 2 or bs[0] != qs[0] or context_lens.numel() != qs[0]:
-        raise PagedKVError("expected q/out [S][Hq][D], block_tables [S][max_blocks] and context_lens [S]")
-    NB, Hkv, B = _q4_pools(k_cache, v_cache, qs[2])
-    d = _current_device(q)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr, ws_bytes = _on(d, workspace, "workspace", workspace.dtype), workspace.nbytes
-    st = load().paged_attention_decode_q4(
-        _on(d, q, "q", dt), _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8),
-        _on(d, block_tables, "block_tables", torch.int32), _on(d, context_lens, "context_lens", torch.int32),
-        float(scale), _on(d, out, "out", dt), qs[0], qs[1], Hkv, qs[2], NB, B, bs[1], int(partition_tokens),
-        ws_ptr, ws_bytes, _code(q), _stream(stream))
-    _check(st, "paged_attention_decode_q4")
+    (_fast or _binding()).decode_q4(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                                    partition_tokens, workspace, stream)
 
 
 def paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
                                out, max_query_len=None, stream=None, workspace=None, key_parts=1):
-    """paged_attention_prefill over 4-bit pools, with its arguments. With key_parts
+    """paged_attention_prefill over 4-bit pools, with its arguments; key_parts 0
+    lets the call decide from the items and the tables' width. With key_parts
     other than 1 the workspace (see prefill_workspace) is taken from torch's
     allocator when none is given."""
-    qs, dt, S = q.shape, q.dtype, context_lens.shape[0]
-    if len(qs) != 3 or out.shape != qs:
-        raise PagedKVError("q and out must be [num_tokens][n_q_heads][head_dim]")
-    if query_start.shape[0] != S + 1 or block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise PagedKVError("query_start must hold num_seqs + 1 offsets, block_tables num_seqs rows")
-    NB, Hkv, B = _q4_pools(k_cache, v_cache, qs[2])
-    d = _current_device(q)
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if context_lens.numel() else 0
     if workspace is None and key_parts != 1:
         workspace = prefill_workspace(q)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr, ws_bytes = _on(d, workspace, "workspace", workspace.dtype), workspace.nbytes
-    st = load().paged_attention_prefill_q4(
-        _on(d, q, "q", dt), _on(d, k_cache, "k_cache", torch.uint8), _on(d, v_cache, "v_cache", torch.uint8),
-        _on(d, block_tables, "block_tables", torch.int32), _on(d, query_start, "query_start", torch.int32),
-        _on(d, context_lens, "context_lens", torch.int32), float(scale), _on(d, out, "out", dt), S, qs[0],
-        int(max_query_len), qs[1], Hkv, qs[2], NB, B, block_tables.shape[1], _code(q), int(key_parts), ws_ptr,
-        ws_bytes, _stream(stream))
-    _check(st, "paged_attention_prefill_q4")
+    (_fast or _binding()).prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
+                                     out, max_query_len, workspace, key_parts, stream)
 
 
 def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, free_count, block_size,
@@ -585,28 +531,9 @@ def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, fre
     free_count_out, by default the inputs themselves. query_start[s + 1] -
     query_start[s] tells whether s was granted its new_lens[s] tokens; entries
     past the last token are padding (pos and slot -1)."""
-    S, T = new_lens.numel(), token_seq.numel()
-    if context_lens_out is None:
-        context_lens_out = context_lens
-    if free_count_out is None:
-        free_count_out = free_count
-    if (context_lens.numel() != S or context_lens_out.numel() != S or query_start.numel() != S + 1 or
-            block_tables.dim() != 2 or block_tables.shape[0] != S):
-        raise PagedKVError("lengths, query_start and block_tables differ in their number of requests")
-    if token_pos.numel() != T or (slot_mapping is not None and slot_mapping.numel() != T):
-        raise PagedKVError("token_seq, token_pos and slot_mapping differ in length")
-    if free_count.numel() != 1 or free_count_out.numel() != 1:
-        raise PagedKVError("free_count must hold one number")
-    i32, d = torch.int32, _current_device(new_lens)
-    st = load().paged_kv_build_tables(
-        _on(d, new_lens, "new_lens", i32), _on(d, context_lens, "context_lens", i32),
-        _on(d, block_tables, "block_tables", i32), _on(d, free_blocks, "free_blocks", i32),
-        _on(d, free_count, "free_count", i32), _on(d, query_start, "query_start", i32),
-        _on(d, token_seq, "token_seq", i32), _on(d, token_pos, "token_pos", i32),
-        None if slot_mapping is None else _on(d, slot_mapping, "slot_mapping", torch.int64),
-        _on(d, context_lens_out, "context_lens_out", i32), _on(d, free_count_out, "free_count_out", i32), S,
-        block_tables.shape[1], free_blocks.numel(), T, int(block_size), int(num_blocks), _stream(stream))
-    _check(st, "paged_kv_build_tables")
+    (_fast or _binding()).build_tables(new_lens, context_lens, block_tables, free_blocks, free_count,
+                                       block_size, num_blocks, query_start, token_seq, token_pos,
+                                       slot_mapping, context_lens_out, free_count_out, stream)
 
 
 def check_bounded_wait(stream=None):

@@ -114,7 +114,7 @@ int paged_kv_build_tables(const int32_t *new_lens, const int32_t *context_lens, 
     p.token_capacity = token_capacity;
     p.block_size = block_size;
     p.num_blocks = num_blocks;
-    return done(pkv::launch_build_tables(p, static_cast<cudaStream_t>(stream)));
+    return done(pkv::launch_build_tables(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int paged_kv_append_q4(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache,

@@ -53,7 +53,7 @@ struct TablesParams {
     unsigned int *err;
     int num_seqs, max_blocks, free_capacity, token_capacity, block_size, num_blocks;
 };
-cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t st);
+cudaError_t launch_build_tables(const TablesParams &p, int num_sms, cudaStream_t st);
 
 // Decode over the 4-bit cache.
 struct Q4AttnParams {

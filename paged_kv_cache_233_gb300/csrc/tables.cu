@@ -10,11 +10,11 @@
 // lists. A second prefix sum over the granted ones places their tokens and
 // their blocks, which come off the top of the free stack.
 //
-// The sums run over the whole call in one block of threads, and every block of
-// a cluster runs them for itself: the cluster's blocks then share out the
-// tokens and the opened blocks, and its barrier keeps the outputs that may be
-// the inputs' own memory (lengths, free count) from being written before every
-// block has read them. One launch, whatever the sizes.
+// The sums run over the whole call in one block of threads, and every block
+// runs them for itself, then takes its part of the tokens and the opened
+// blocks: one launch, whatever the sizes. Where the lengths or the free count
+// are updated in place the blocks are one cluster, whose barrier keeps them
+// from being written before every block has read them.
 #include <cooperative_groups.h>
 
 #include "launch_cache.h"
@@ -30,7 +30,6 @@ namespace cg = cooperative_groups;
 constexpr unsigned kAllLanes = 0xffffffffu;
 constexpr int kMaxThreads = 1024;
 constexpr int kPerThread = 4;          // requests per thread: 4096 requests at most
-constexpr int kTokens = 4;             // tokens per lane at a time
 constexpr unsigned kFull30 = 1u << 30; // sums saturate here: past every capacity
 
 __device__ __forceinline__ unsigned add_sat(unsigned a, unsigned b) { return min(a + b, kFull30); }
@@ -82,17 +81,18 @@ __device__ __forceinline__ int last_at_or_before(const int *start, int n, int x)
     return lo;
 }
 
-__global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const TablesParams p) {
+// kTokens: tokens per lane at a time.
+template <int kTokens>
+__global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_constant__ TablesParams p, bool cluster) {
     // [S + 1] each: first token, first opened block; then tokens held
     extern __shared__ int arrays[];
     __shared__ uint2 warp_sums[32];
-    cg::cluster_group cluster = cg::this_cluster();
     const int S = p.num_seqs, B = p.block_size;
     // x / B (x >= 0): a shift where B is a power of two
     const int shift = (B & (B - 1)) == 0 ? 31 - __clz(B) : -1;
     auto divide = [&](int x) { return shift >= 0 ? x >> shift : x / B; };
     int *tok0 = arrays, *blk0 = arrays + S + 1, *held_tokens = blk0 + S + 1;
-    const unsigned rank = cluster.block_rank(), blocks = cluster.num_blocks();
+    const unsigned rank = blockIdx.x, blocks = gridDim.x;
 
     int free_count = __ldg(p.free_count);
     if (free_count < 0 || free_count > p.free_capacity) {
@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const TablesP
         tok0[S] = tokens;
         blk0[S] = opened;
     }
-    // every block has read the lengths and the count before any block writes
-    // them, and this block's arrays are complete
-    if (blocks > 1) cluster.sync();
+    // this block's arrays are complete, and (in place) every block has read the
+    // lengths and the count before any writes them
+    if (cluster) cg::this_cluster().sync();
     else __syncthreads();
 
     if (rank == 0) {
@@ -239,20 +239,29 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const TablesP
 
 }  // namespace
 
-cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t st) {
-    // One block up to a few tokens per thread, then a cluster of up to 8.
+cudaError_t launch_build_tables(const TablesParams &p, int num_sms, cudaStream_t st) {
+    // A block up to a token per thread, then four tokens per lane: in a cluster
+    // of up to 8 blocks where an output is an input, else up to a block per SM.
     const long long work = p.token_capacity > p.num_seqs ? p.token_capacity : p.num_seqs;
     int threads = 128;
     while (threads < kMaxThreads && (threads < work || threads * kPerThread < p.num_seqs)) threads <<= 1;
+    const bool in_place = p.context_lens_out == p.context_lens || p.free_count_out == p.free_count;
+    const bool many = work > threads;
     int blocks = 1;
-    while (blocks < 8 && (long long)blocks * threads * 2 < work) blocks <<= 1;
+    if (many) {
+        const long long want = (work + 4ll * threads - 1) / (4ll * threads);
+        if (in_place) while (blocks < 8 && blocks < want) blocks <<= 1;
+        else blocks = int(want < num_sms ? want : num_sms);
+    }
+    const bool cluster = in_place && blocks > 1;
     const int smem = int(sizeof(int)) * (3 * p.num_seqs + 2);
+    auto kernel = many ? build_tables_kernel<4> : build_tables_kernel<1>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
+    static std::atomic<unsigned long long> opened[2][kLaunchCacheDevices];
     if (smem > 40 * 1024) {
-        e = open_dynamic_smem(opened, dev, build_tables_kernel, smem);
+        e = open_dynamic_smem(opened[many ? 1 : 0], dev, kernel, smem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute attr[1];
@@ -266,8 +275,8 @@ cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t st) {
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+    cfg.numAttrs = cluster ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
 }
 
 }  // namespace pkv
