@@ -56,7 +56,7 @@ namespace pkv {
 constexpr int kQ4Tile = 32;            // keys per stage
 constexpr int kQ4Consumers = 4;
 constexpr int kQ4Threads = 32 * (1 + kQ4Consumers);
-constexpr int kQ4CtasPerSm = 3;
+template <int D> constexpr int q4_ctas_per_sm() { return D == 64 ? 3 : 3; }
 constexpr unsigned kQ4All = 0xffffffffu;
 
 // Balanced split: the CTAs that get a share of `total` tiles, none of them
@@ -64,6 +64,14 @@ constexpr unsigned kQ4All = 0xffffffffu;
 __device__ __forceinline__ int q4_sharers(int total, int grid) { return max(1, min(grid, total)); }
 __device__ __forceinline__ int q4_share(int total, int c, int sharers) {
     return int((long long)total * c / sharers);
+}
+
+// The share that holds tile t.
+__device__ __forceinline__ int q4_share_of(int total, int t, int sharers) {
+    int c = int((long long)t * sharers / total);
+    while (c + 1 < sharers && q4_share(total, c + 1, sharers) <= t) ++c;
+    while (c > 0 && q4_share(total, c, sharers) > t) --c;
+    return c;
 }
 
 struct Q4Smem {
@@ -84,6 +92,7 @@ struct Q4Unit {
     int s, hg, t0, t1;
     int part;         // its partition; balanced split: its piece slot of the CTA
     bool partial;     // the result is a state for the merge
+    int last;         // balanced split: the pair's last tile where this CTA has its first, else -1
 };
 
 // This CTA's units in order; the producer and every consumer warp walk a copy.
@@ -134,6 +143,7 @@ struct Q4Walk {
             x.t1 = min(L, b * kQ4Tile);
             x.part = count == 0 ? 0 : 1;
             x.partial = !(a == 0 && b == nt);
+            x.last = a == 0 ? pos + nt - 1 : -1;
             pos += b - a;
         } else {
             x.part = r / groups;
@@ -141,6 +151,7 @@ struct Q4Walk {
             x.t0 = x.part * p.part_tokens;
             x.t1 = min(L, x.t0 + p.part_tokens);
             x.partial = L > p.part_tokens;
+            x.last = -1;
             pos += gridDim.x;
         }
         ++count;
@@ -533,7 +544,7 @@ __device__ __forceinline__ void store_quad(T *dst, float4 v, float inv) {
 __device__ __forceinline__ float q4_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(const __grid_constant__ Q4AttnParams p) {
+__global__ void __launch_bounds__(kQ4Threads, q4_ctas_per_sm<D>()) decode_q4_kernel(const __grid_constant__ Q4AttnParams p) {
     constexpr int G = D / kQ4Group;
     extern __shared__ __align__(128) uint8_t sm[];
     const uint32_t base = smem_addr(sm);
@@ -591,6 +602,17 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     }
     Q4Walk walk;
     walk.init(base + lay.base(), p);
+    if (p.balanced) {
+        // empty sequences have no unit: their rows are zeros
+        for (int s = blockIdx.x; s < S; s += gridDim.x) {
+            if (seq_len[s] != 0) continue;
+            if (p.cuts_by_pair)
+                for (int x = threadIdx.x; x < p.n_kv_heads >> p.log2_hpu; x += kQ4Threads)
+                    p.ws_cuts[s * (p.n_kv_heads >> p.log2_hpu) + x] = make_int4(-1, 0, 0, 0);
+            uint32_t *dst = reinterpret_cast<uint32_t *>(p.out) + size_t(s) * p.n_q_heads * (D / 2);
+            for (int x = threadIdx.x; x < p.n_q_heads * (D / 2); x += kQ4Threads) dst[x] = 0u;
+        }
+    }
 
     if (warp == 0) {
         // -------------------------------------------------------- producer
@@ -601,6 +623,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         const int blk = lane >> 1, operand = lane & 1;     // this lane's copy of a tile
         const uint8_t *pool = operand ? p.v_cache : p.k_cache;
         const int lanes = 2 * (kQ4Tile / B);
+        int4 cut = make_int4(-1, 0, 0, 0);
         while (ok && walk.next(u, p)) {
             const int32_t *table = p.block_tables + size_t(u.s) * p.max_blocks;
             const int h0 = u.hg << p.log2_hpu;
@@ -636,7 +659,20 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
                     phase ^= 1u;
                 }
             }
+            if (p.balanced && u.last >= 0) {
+                // for the merge: the pair, its first and last share, and the slot of its first piece
+                const int total = Q4Walk::at(base + lay.base() + 4 * S), n = q4_sharers(total, gridDim.x);
+                const int pair = u.s * (p.n_kv_heads >> p.log2_hpu) + u.hg;
+                const int4 mine = make_int4(u.partial ? pair : -1, blockIdx.x,
+                                            u.partial ? q4_share_of(total, u.last, n) : 0, u.part);
+                if (p.cuts_by_pair) {
+                    if (lane == 0) p.ws_cuts[pair] = mine;
+                } else if (u.partial) {
+                    cut = mine;
+                }
+            }
         }
+        if (p.balanced && !p.cuts_by_pair && lane == 0) p.ws_cuts[blockIdx.x] = cut;
         if (!ok && lane == 0) {
             // stop everyone, then wait (bounded) for this CTA's copies in flight
             *abort_flag = 1;
@@ -756,60 +792,28 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
 }
 
 // Balanced split: the pieces of each (sequence, head group) that spans shares,
-// joined by the softmax identity; zero rows for empty sequences. Where a
-// pair's tiles lie follows from the lengths alone. A row is kWarps warps' work
-// (the launcher takes four where a pair can have many pieces): each joins
-// every kWarps-th piece, all loads of eight pieces in one round trip, against
-// a running maximum of its own, and the warps' sums meet in shared memory.
-constexpr int kQ4MergeThreads = 128;
+// joined by the softmax identity. Block x takes pair x, or, where the pairs
+// outnumber the decode's CTAs, the pair that CTA x starts and does not end, of
+// which there is at most one (ws_cuts, written by the decode). A
+// row is kWarps warps' work (the launcher takes eight where a pair can have many
+// pieces): each joins every kWarps-th piece, all loads of eight pieces in one
+// round trip, against a running maximum of its own, and the warps' sums meet in
+// shared memory.
+template <int kWarps> constexpr int q4_merge_threads() { return kWarps > 4 ? 32 * kWarps : 128; }
 
 template <typename T, int D, int kWarps>
-__global__ void __launch_bounds__(kQ4MergeThreads) merge_q4_kernel(const __grid_constant__ Q4AttnParams p, int grid) {
-    constexpr int E = D / 32, kBatch = 8, kRows = kQ4MergeThreads / 32 / kWarps;
+__global__ void __launch_bounds__(q4_merge_threads<kWarps>()) merge_q4_kernel(const __grid_constant__ Q4AttnParams p) {
+    constexpr int E = D / 32, kBatch = 8, kRows = q4_merge_threads<kWarps>() / 32 / kWarps;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int H = 1 << p.log2_hpu, groups = p.n_kv_heads >> p.log2_hpu, rows = H * p.group;
-    const int s = blockIdx.x / groups, hg = blockIdx.x - s * groups;
+    const int H = 1 << p.log2_hpu, rows = H * p.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.y * kRows + warp / kWarps, first = warp % kWarps;
-    const int cap = p.max_blocks * p.block_size;
-    __shared__ int part[2][kQ4MergeThreads / 32];
-    __shared__ float joined[kQ4MergeThreads / 32][D + 2];
-    int before = 0, total = 0;
-    for (int t = threadIdx.x; t < p.num_seqs; t += blockDim.x) {
-        const int n = (min(max(__ldg(p.context_lens + t), 0), cap) + kQ4Tile - 1) / kQ4Tile * groups;
-        total += n;
-        if (t < s) before += n;
-    }
-    before = __reduce_add_sync(kQ4All, before);
-    total = __reduce_add_sync(kQ4All, total);
-    if (lane == 0) {
-        part[0][warp] = before;
-        part[1][warp] = total;
-    }
-    const int nt = (min(max(__ldg(p.context_lens + s), 0), cap) + kQ4Tile - 1) / kQ4Tile;
-    __syncthreads();
-    before = total = 0;
-#pragma unroll
-    for (int w = 0; w < kQ4MergeThreads / 32; ++w) {
-        before += part[0][w];
-        total += part[1][w];
-    }
-    int c0 = 0, np = 0, slot0 = 0;
-    if (nt > 0) {
-        const int n_shares = q4_sharers(total, grid);
-        const int A = before + hg * nt, Z = A + nt - 1;   // the pair's first and last tile
-        auto share_of = [&](int t) {
-            int c = int((long long)t * n_shares / total);
-            while (c + 1 < n_shares && q4_share(total, c + 1, n_shares) <= t) ++c;
-            while (c > 0 && q4_share(total, c, n_shares) > t) --c;
-            return c;
-        };
-        c0 = share_of(A);
-        np = share_of(Z) - c0 + 1;
-        if (np == 1) return;                        // one share: written by the decode itself
-        slot0 = A != q4_share(total, c0, n_shares) ? 1 : 0;
-    }
+    __shared__ float joined[q4_merge_threads<kWarps>() / 32][D + 2];
+    const int4 cut = __ldcg(p.ws_cuts + blockIdx.x);
+    if (cut.x < 0) return;
+    const int groups = p.n_kv_heads >> p.log2_hpu, s = cut.x / groups, hg = cut.x - s * groups;
+    const int c0 = cut.y, np = cut.z - c0 + 1, slot0 = cut.w;
     if (kWarps == 1 && r >= rows) return;
     float acc[E] = {}, M = -INFINITY, den = 0.f;
     if (r < rows) {
@@ -889,12 +893,13 @@ cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // as many stages as kQ4CtasPerSm CTAs leave room for on an SM of 228 KB
+    // as many stages as the CTAs of an SM leave room for in its 228 KB
+    constexpr int kCtas = q4_ctas_per_sm<D>();
     Q4Smem lay{stage, 2, p.num_seqs, D, H < 4 ? 1 : 0};
     while (lay.stages < 8) {
         Q4Smem more = lay;
         ++more.stages;
-        if (more.total() > 74 * 1024) break;
+        if (more.total() > 222 * 1024 / kCtas) break;
         lay = more;
     }
     p.stages = lay.stages;
@@ -906,13 +911,17 @@ cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
     e = occupancy_per_sm(fits, dev, kernel, kQ4Threads, lay.total(), &per_sm);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    if (per_sm > kQ4CtasPerSm) per_sm = kQ4CtasPerSm;
+    if (per_sm > kCtas) per_sm = kCtas;
     const long long cap = (long long)p.max_blocks * p.block_size;
     const long long groups = p.n_kv_heads >> p.log2_hpu;
     const long long most = p.balanced ? groups * p.num_seqs * ((cap + kQ4Tile - 1) / kQ4Tile)
                                       : groups * p.num_seqs * ((cap + p.part_tokens - 1) / p.part_tokens);
     const long long want = (long long)per_sm * sms;
     const int grid = int(most < want ? most : want);
+    // (the pieces take at most 3 of the workspace's 8 CTAs per SM; the cuts lie behind them)
+    const long long pairs = groups * p.num_seqs;
+    p.cuts_by_pair = pairs <= grid ? 1 : 0;
+    if (p.balanced) p.ws_cuts = reinterpret_cast<int4 *>(p.ws_o + size_t(grid) * 2 * (H * p.group) * D);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -925,17 +934,18 @@ cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess || !p.balanced) return e;
-    // four warps per row where the pairs are few enough to have more than eight pieces each
+    // eight warps per row where the pairs are few enough to have more than eight pieces each
     const int rows = H * p.group;
-    const long long pairs = groups * p.num_seqs;
-    cfg.blockDim = dim3(kQ4MergeThreads);
+    const unsigned blocks = unsigned(p.cuts_by_pair ? pairs : grid);
     cfg.dynamicSmemBytes = 0;
     if (pairs * 8 <= grid) {
-        cfg.gridDim = dim3(unsigned(pairs), unsigned(rows));
-        return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D, 4>, p, grid);
+        cfg.blockDim = dim3(q4_merge_threads<8>());
+        cfg.gridDim = dim3(blocks, unsigned(rows));
+        return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D, 8>, p);
     }
-    cfg.gridDim = dim3(unsigned(pairs), unsigned((rows + 3) / 4));
-    return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D, 1>, p, grid);
+    cfg.blockDim = dim3(q4_merge_threads<1>());
+    cfg.gridDim = dim3(blocks, unsigned((rows + 3) / 4));
+    return cudaLaunchKernelEx(&cfg, merge_q4_kernel<T, D, 1>, p);
 }
 
 template <typename T, int D>

@@ -64,6 +64,8 @@ struct Q4AttnParams {
     const int32_t *context_lens;  // [num_seqs]
     void *out;
     float *ws_o, *ws_m, *ws_l;
+    int4 *ws_cuts;                // balanced split: where pairs are cut, by pair or by CTA (decode_q4.cuh)
+    int cuts_by_pair;
     unsigned int *err;
     float scale_log2;
     int num_seqs, n_q_heads, n_kv_heads, group;
