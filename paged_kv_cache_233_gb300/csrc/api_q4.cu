@@ -188,6 +188,7 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.max_blocks = max_blocks_per_seq;
     p.balanced = partition_tokens == PAGEDKV_PARTITION_BALANCED ? 1 : 0;
+    p.merged = partition_tokens != 0 ? 1 : 0;
     p.log2_hpu = n_kv_heads % 4 == 0 ? 2 : (n_kv_heads % 2 == 0 ? 1 : 0);
     // (unsplit: one partition of the tables' whole width)
     p.part_tokens = partition_tokens > 0 ? partition_tokens : int((cap + 31) / 32 * 32);

@@ -570,7 +570,9 @@ __global__ void __launch_bounds__(kQ4Threads, q4_ctas_per_sm<D>()) decode_q4_ker
     }
     // lengths, tables and pools as the kernels before this one left them
     grid_dependency_wait();
-    grid_launch_dependents();
+    // the merge may start its launch; without one the next kernel may not (it
+    // could be one that reads its queries, these outputs, before it waits)
+    if (p.merged) grid_launch_dependents();
     // ---- per sequence: length, and units (or tiles) before it
     {
         const int cap = p.max_blocks * B, groups = p.n_kv_heads >> p.log2_hpu;
@@ -805,7 +807,6 @@ template <typename T, int D, int kWarps>
 __global__ void __launch_bounds__(q4_merge_threads<kWarps>()) merge_q4_kernel(const __grid_constant__ Q4AttnParams p) {
     constexpr int E = D / 32, kBatch = 8, kRows = q4_merge_threads<kWarps>() / 32 / kWarps;
     grid_dependency_wait();
-    grid_launch_dependents();
     const int H = 1 << p.log2_hpu, rows = H * p.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.y * kRows + warp / kWarps, first = warp % kWarps;

@@ -72,6 +72,7 @@ struct Q4AttnParams {
     int num_blocks, block_size, log2_block, max_blocks;
     int part_tokens;              // tokens per partition (unsplit: the tables' whole width)
     int max_parts;
+    int merged;                   // a merge kernel follows
     int balanced;                 // equal shares of the call's tiles per CTA, pieces joined
     int log2_hpu;                 // kv heads per unit: 4, 2 or 1
     int stages;

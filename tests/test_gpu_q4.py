@@ -372,3 +372,116 @@ def test_serving_loop(dtype, graph):
     held = t[t >= 0].tolist()
     assert len(set(held)) == len(held)
     assert int(count) == nb - len(held)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gather_into_a_16_bit_pool(dtype):
+    """A 4-bit sequence moved into 16-bit pools: paged_kv_append_tokens right behind
+    the gather that makes its rows, many times over."""
+    n, heads, dim, block = 3000, 8, 128, 16
+    kc, vc, tables = q4.filled([n], heads, block, dim, dtype, 5)
+    slots = q4.sequence_slots(tables, 0, n, block).cuda()
+    gk, gv, gt = kc.cuda(), vc.cuda(), tables.cuda()
+    seq, pos = torch.zeros(n, dtype=torch.int32).cuda(), torch.arange(n, dtype=torch.int32).cuda()
+    want = [q4.read(p, slots.cpu(), dim, dtype) for p in (kc, vc)]
+    for i in range(5):
+        k, v = (torch.full((n, heads, dim), float(i), dtype=dtype, device="cuda") for _ in range(2))
+        k16, v16 = (torch.zeros(kc.shape[0], block, heads, dim, dtype=dtype, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        pk.paged_kv_gather_q4(gk, gv, slots, k, v)
+        pk.paged_kv_append_tokens(k, v, gt, seq, pos, k16, v16)
+        torch.cuda.synchronize()
+        for pool, ref in ((k16, want[0]), (v16, want[1])):
+            err = (pool.flatten(0, 1)[slots].cpu().double() - ref).abs()
+            assert bool((err <= ref.abs() * (q4.HALF_STEP[dtype] + 2.0 ** -24) + q4.TINY[dtype]).all())
+
+
+def test_pools_past_4_gib():
+    """Blocks whose bytes lie past 2^32 in their pool."""
+    heads, dim, block, dtype = 8, 128, 32, BF16
+    head_bytes = block * dim * 5 // 8
+    nb = (1 << 32) // (heads * head_bytes) + 40
+    pools = [pk.new_q4_pool(nb, heads, block, dim) for _ in range(2)]
+    lens = [300, 70]
+    tables = torch.tensor([[nb - 1 - 2 * j for j in range(10)], [nb - 2 - 2 * j if j < 3 else -1 for j in range(10)]],
+                          dtype=torch.int32)
+    small = [q4.new_pool(40, heads, block, dim, i) for i in range(2)]      # the pools' last 40 blocks
+    near = torch.where(tables >= 0, tables - (nb - 40), tables)
+    slots = torch.cat([q4.sequence_slots(tables, s, n, block) for s, n in enumerate(lens)])
+    near_slots = torch.cat([q4.sequence_slots(near, s, n, block) for s, n in enumerate(lens)])
+    k, v = rows((370, heads, dim), dtype, 1), rows((370, heads, dim), dtype, 2)
+    for pool, x in zip(small, (k, v)):
+        q4.write_fast(pool, near_slots, x)
+    for pool in pools:
+        pool[nb - 40:] = 255
+    pk.paged_kv_append_q4(k.cuda(), v.cuda(), slots.cuda(), *pools)
+    back = [torch.zeros(370, heads, dim, dtype=dtype, device="cuda") for _ in range(2)]
+    pk.paged_kv_gather_q4(*pools, slots.cuda(), *back)
+    for got, pool in zip(back, small):
+        ref = q4.read(pool, near_slots, dim, dtype)
+        assert bool(((got.cpu().double() - ref).abs() <= ref.abs() * 2.0 ** -8 * 1.01).all())
+    q = rows((2, heads * 4, dim), dtype, 3)
+    ref = q4.attention(q, small, near, range(3), lens, 0.09, dim, dtype)
+    for part in (0, pk.PARTITION_BALANCED):
+        q4.assert_near(decode(q, pools[0], pools[1], tables, lens, 0.09, part), ref, dtype, 2)
+    qp = rows((370, heads * 4, dim), dtype, 4)
+    starts = torch.tensor([0, 300, 370], dtype=torch.int32)
+    out = torch.zeros_like(qp).cuda()
+    pk.paged_attention_prefill_q4(qp.cuda(), *pools, tables.cuda(), starts.cuda(),
+                                  torch.tensor(lens, dtype=torch.int32).cuda(), 0.09, out, 300)
+    q4.assert_near(out, q4.attention(qp, small, near, starts, lens, 0.09, dim, dtype), dtype, 4)
+    assert pk.device_errors() == 0
+
+
+def test_decode_4096_sequences():
+    rng = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 40, (4096,), generator=rng).tolist()
+    for heads, group, dim in ((4, 2, 128), (1, 1, 64)):
+        kc, vc, tables = q4.filled(lens, heads, 8, dim, BF16, 6)
+        q = rows((4096, heads * group, dim), BF16, 7)
+        ref = q4.attention(q, (kc, vc), tables, range(4097), lens, dim ** -0.5, dim, BF16)
+        for part in (0, 32, pk.PARTITION_BALANCED):
+            q4.assert_near(decode(q, kc, vc, tables, lens, dim ** -0.5, part), ref, BF16, 2)
+        assert pk.device_errors() == 0
+
+
+def test_two_streams_with_a_workspace_each():
+    lens, heads, dim, block = [2000, 700, 31], 4, 128, 16
+    kc, vc, tables = q4.filled(lens, heads, block, dim, BF16, 4)
+    gk, gv, gt = kc.cuda(), vc.cuda(), tables.cuda()
+    L = torch.tensor(lens, dtype=torch.int32).cuda()
+    qs = [rows((3, heads * 2, dim), BF16, 20 + i).cuda() for i in range(2)]
+    outs = [torch.zeros_like(q) for q in qs]
+    ws = [pk.new_workspace(q, gt, block, pk.PARTITION_BALANCED) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(40):
+        s = i % 2
+        pk.paged_attention_decode_q4(qs[s], gk, gv, gt, L, 0.09, outs[s], pk.PARTITION_BALANCED, ws[s], stream=streams[s])
+    torch.cuda.synchronize()
+    for q, out in zip(qs, outs):
+        q4.assert_near(out, q4.attention(q.cpu(), (kc, vc), tables, range(4), lens, 0.09, dim, BF16), BF16, 2)
+
+
+def test_refusals_on_the_gpu():
+    kc, vc, tables = (t.cuda() for t in q4.filled([20], 2, 16, 64, F16, 1))
+    q, L = torch.zeros(1, 4, 64, dtype=F16, device="cuda"), torch.tensor([20], dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    with pytest.raises(pk.PagedKVError, match="contiguous"):
+        pk.paged_attention_decode_q4(q.transpose(1, 2).contiguous().transpose(1, 2), kc, vc, tables, L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="out must be"):
+        pk.paged_attention_decode_q4(q, kc, vc, tables, L, 0.1, out.bfloat16())
+    with pytest.raises(pk.PagedKVError, match="current device"):
+        pk.paged_attention_decode_q4(q, kc, vc, tables.cpu(), L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="block_tables must be"):
+        pk.paged_attention_decode_q4(q, kc, vc, tables.long(), L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="unsupported"):
+        pk.paged_attention_decode_q4(q.float(), kc, vc, tables, L, 0.1, out.float())
+    with pytest.raises(pk.PagedKVError, match="workspace"):
+        pk.paged_attention_decode_q4(q, kc, vc, tables, L, 0.1, out, 32)
+    with pytest.raises(TypeError):
+        pk.paged_attention_decode_q4(q, kc, vc, tables, [20], 0.1, out)
+    pk.paged_attention_decode_q4(q[:0], kc, vc, tables[:0], L[:0], 0.1, out[:0])
+    with pytest.raises(pk.PagedKVError, match="workspace"):
+        pk.paged_attention_prefill_q4(q, kc, vc, tables, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), L, 0.1,
+                                      out, 1, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"), key_parts=4)
