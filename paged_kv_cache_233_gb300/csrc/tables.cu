@@ -93,8 +93,11 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
     auto divide = [&](int x) { return shift >= 0 ? x >> shift : x / B; };
     int *tok0 = arrays, *blk0 = arrays + S + 1, *held_tokens = blk0 + S + 1;
     const unsigned rank = blockIdx.x, blocks = gridDim.x;
+    // lengths, tables and the free stack as the kernels before this one left
+    // them, and those kernels done with what is written here
+    grid_dependency_wait();
 
-    int free_count = __ldg(p.free_count);
+    int free_count = __ldcg(p.free_count);
     if (free_count < 0 || free_count > p.free_capacity) {
         if (rank == 0 && threadIdx.x == 0) atomicOr(p.err, PAGEDKV_DEVERR_POSITION);
         free_count = min(max(free_count, 0), p.free_capacity);
@@ -108,8 +111,8 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
     for (int i = 0; i < kPerThread; ++i) {
         c[i] = n[i] = need[i] = 0;
         if (i < per && s0 + i < S) {
-            c[i] = __ldg(p.context_lens + s0 + i);
-            n[i] = __ldg(p.new_lens + s0 + i);
+            c[i] = __ldcg(p.context_lens + s0 + i);
+            n[i] = __ldcg(p.new_lens + s0 + i);
         }
     }
     bool ok[kPerThread];
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
     const int first = int(rank * blockDim.x + threadIdx.x);
     for (int x = first; x < opened; x += stride) {
         const int s = last_at_or_before(blk0, S, x);
-        const int id = __ldg(p.free_blocks + (free_count - 1 - x));
+        const int id = __ldcg(p.free_blocks + (free_count - 1 - x));
         if (id < 0 || id >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
         p.block_tables[size_t(s) * p.max_blocks + divide(held_tokens[s] + B - 1) + (x - blk0[s])] = id;
     }
@@ -213,8 +216,8 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
                 pos[k] = held + (t - tok0[at]);
                 j[k] = divide(pos[k]);
                 const int nth = j[k] - divide(held + B - 1);   // which of the request's opened blocks, if any
-                id[k] = nth < 0 ? p.block_tables[size_t(at) * p.max_blocks + j[k]]
-                                : __ldg(p.free_blocks + (free_count - 1 - (blk0[at] + nth)));
+                id[k] = nth < 0 ? __ldcg(p.block_tables + size_t(at) * p.max_blocks + j[k])
+                                : __ldcg(p.free_blocks + (free_count - 1 - (blk0[at] + nth)));
             }
         }
 #pragma unroll
@@ -232,9 +235,12 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
         }
     }
     // The kernel after this one may be a programmatic dependent that reads the
-    // tables and lengths before its grid dependency wait, which it may start
-    // on once every block here has exited: the writes are performed first.
+    // tables and lengths before its grid dependency wait: it may start once
+    // every thread here has performed its writes. (Everything is read past L1,
+    // so that no SM keeps an old line of them for that kernel to find.)
     __threadfence();
+    __syncthreads();
+    grid_launch_dependents();
 }
 
 }  // namespace
@@ -264,18 +270,20 @@ cudaError_t launch_build_tables(const TablesParams &p, int num_sms, cudaStream_t
         e = open_dynamic_smem(opened[many ? 1 : 0], dev, kernel, smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(blocks);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(blocks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 1 : 0;
+    cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
 }
 

@@ -170,3 +170,47 @@ def test_side_stream_and_graph_evolve_the_state():
     assert np.array_equal(tab.cpu().numpy(), h_tab) and c.tolist() == h_ctx.tolist() and int(cnt) == h_cnt
     assert slots.tolist() == w[6]
     assert pk.device_errors() == 0
+
+
+def test_the_16_bit_path_right_behind():
+    """paged_kv_append_tokens and paged_attention_decode on tables, lengths and token
+    lists that the kernel before them writes, step after step in one graph."""
+    S, heads, dim, block = 96, 4, 64, 16
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, 50, (S,), generator=g)
+    held = -(-lens // block)
+    blocks, width, steps = int(held.sum()) + S * 3, 8, 30
+    ids = torch.randperm(blocks, generator=g).to(torch.int32)
+    tables = torch.full((S, width), -1, dtype=torch.int32)
+    tables[torch.arange(width)[None] < held[:, None]] = ids[:int(held.sum())]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bt, ctx, free = tables.cuda(), lens.to(torch.int32).cuda(), ids[int(held.sum()):].cuda()
+    count, new = torch.tensor([len(free)], **i32), torch.ones(S, **i32)
+    starts, seq, pos = torch.zeros(S + 1, **i32), torch.zeros(S, **i32), torch.zeros(S, **i32)
+    kc, vc = (torch.zeros(blocks, block, heads, dim, dtype=torch.float16, device="cuda") for _ in range(2))
+    # every earlier token's rows are zero, so a step's output is its own V row times its weight
+    k = torch.zeros(S, heads, dim, dtype=torch.float16, device="cuda")
+    v = torch.ones(S, heads, dim, dtype=torch.float16, device="cuda")
+    q = torch.zeros(S, heads, dim, dtype=torch.float16, device="cuda")
+    out = torch.zeros(steps, S, heads, dim, dtype=torch.float16, device="cuda")
+
+    def step(i):
+        pk.paged_kv_build_tables(new, ctx, bt, free, count, block, blocks, starts, seq, pos)
+        pk.paged_kv_append_tokens(k, v, bt, seq, pos, kc, vc)
+        pk.paged_attention_decode(q, kc, vc, bt, ctx, 1.0, out[i])
+
+    step(0)                                   # (first calls look up addresses: not in a capture)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(1, steps):
+            step(i)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert pk.device_errors() == 0
+    for i in range(steps):
+        # i + 1 ones among lens + i + 1 tokens of equal weight, in fp16 (2^-11, and P's own)
+        want = ((i + 1) / (lens + i + 1).double())[:, None, None]
+        got = out[i].cpu().double()
+        assert bool(((got - want).abs() <= want * 2.0 ** -9).all()), f"step {i}"
+    assert ctx.tolist() == (lens + steps).tolist()
