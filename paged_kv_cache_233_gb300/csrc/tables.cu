@@ -12,11 +12,8 @@
 //
 // The sums run over the whole call in one block of threads, and every block
 // runs them for itself, then takes its part of the tokens and the opened
-// blocks: one launch, whatever the sizes. Where the lengths or the free count
-// are updated in place the blocks are one cluster, whose barrier keeps them
-// from being written before every block has read them.
-#include <cooperative_groups.h>
-
+// blocks. One launch, unless several blocks read lengths or a count that are
+// updated in place: those are then written by a second one.
 #include "launch_cache.h"
 #include "ptx.cuh"
 #include "q4.h"
@@ -24,8 +21,6 @@
 namespace pkv {
 
 namespace {
-
-namespace cg = cooperative_groups;
 
 constexpr unsigned kAllLanes = 0xffffffffu;
 constexpr int kMaxThreads = 1024;
@@ -81,9 +76,8 @@ __device__ __forceinline__ int last_at_or_before(const int *start, int n, int x)
     return lo;
 }
 
-// kTokens: tokens per lane at a time.
-template <int kTokens>
-__global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_constant__ TablesParams p, bool cluster) {
+// `totals`: write the lengths and the count after the step too.
+__global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_constant__ TablesParams p, bool totals) {
     // [S + 1] each: first token, first opened block; then tokens held
     extern __shared__ int arrays[];
     __shared__ uint2 warp_sums[32];
@@ -167,22 +161,21 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
         tok0[S] = tokens;
         blk0[S] = opened;
     }
-    // this block's arrays are complete, and (in place) every block has read the
-    // lengths and the count before any writes them
-    if (cluster) cg::this_cluster().sync();
-    else __syncthreads();
+    // this block's arrays are complete, and (a single one) it has read the
+    // lengths and the count that it may now overwrite
+    __syncthreads();
 
     if (rank == 0) {
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
             if (i < per && s0 + i < S) {
-                p.context_lens_out[s0 + i] = c[i] + n[i];
+                if (totals) p.context_lens_out[s0 + i] = c[i] + n[i];
                 p.query_start[s0 + i] = tok0[s0 + i];
             }
         }
         if (threadIdx.x == 0) {
             p.query_start[S] = tokens;
-            *p.free_count_out = free_count - opened;
+            if (totals) *p.free_count_out = free_count - opened;
         }
     }
     const int stride = int(blocks * blockDim.x);
@@ -193,46 +186,23 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
         if (id < 0 || id >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
         p.block_tables[size_t(s) * p.max_blocks + divide(held_tokens[s] + B - 1) + (x - blk0[s])] = id;
     }
-    // A warp takes runs of 32 kTokens neighbouring tokens: a lane searches its
-    // first one's request, walks on from it to the others', and has their table
-    // entries in flight together.
-    const int lane = threadIdx.x & 31;
-    for (int t0 = (first - lane) * kTokens; t0 < p.token_capacity; t0 += stride * kTokens) {
-        int s[kTokens], pos[kTokens], j[kTokens], id[kTokens];
-        int at = t0 + lane < tokens ? last_at_or_before(tok0, S, t0 + lane) : 0;
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-            const int t = t0 + 32 * k + lane;
-            s[k] = 0;
-            pos[k] = -1;
-            id[k] = -1;
-            if (t < tokens) {
-                if (k > 0 && tok0[at + 1] <= t) {
-                    // the next request, or one further on
-                    at = tok0[at + 2 < S ? at + 2 : S] > t ? at + 1 : last_at_or_before(tok0, S, t);
-                }
-                const int held = held_tokens[at];
-                s[k] = at;
-                pos[k] = held + (t - tok0[at]);
-                j[k] = divide(pos[k]);
-                const int nth = j[k] - divide(held + B - 1);   // which of the request's opened blocks, if any
-                id[k] = nth < 0 ? __ldcg(p.block_tables + size_t(at) * p.max_blocks + j[k])
-                                : __ldcg(p.free_blocks + (free_count - 1 - (blk0[at] + nth)));
-            }
+    for (int t = first; t < p.token_capacity; t += stride) {
+        int s = 0, pos = -1;
+        long long slot = -1;
+        if (t < tokens) {
+            s = last_at_or_before(tok0, S, t);
+            const int held = held_tokens[s];
+            pos = held + (t - tok0[s]);
+            const int j = divide(pos);
+            const int nth = j - divide(held + B - 1);   // which of the request's opened blocks, if any
+            const int id = nth < 0 ? __ldcg(p.block_tables + size_t(s) * p.max_blocks + j)
+                                   : __ldcg(p.free_blocks + (free_count - 1 - (blk0[s] + nth)));
+            if (id < 0 || id >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+            else slot = (long long)id * B + (pos - j * B);
         }
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-            const int t = t0 + 32 * k + lane;
-            if (t >= p.token_capacity) break;
-            long long slot = -1;
-            if (t < tokens) {
-                if (id[k] < 0 || id[k] >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-                else slot = (long long)id[k] * B + (pos[k] - j[k] * B);
-            }
-            p.token_seq[t] = s[k];
-            p.token_pos[t] = pos[k];
-            if (p.slot_mapping) p.slot_mapping[t] = slot;
-        }
+        p.token_seq[t] = s;
+        p.token_pos[t] = pos;
+        if (p.slot_mapping) p.slot_mapping[t] = slot;
     }
     // The kernel after this one may be a programmatic dependent that reads the
     // tables and lengths before its grid dependency wait: it may start once
@@ -243,48 +213,68 @@ __global__ void __launch_bounds__(kMaxThreads) build_tables_kernel(const __grid_
     grid_launch_dependents();
 }
 
+// The lengths and the count after a step, in place: query_start holds what each
+// request was granted.
+__global__ void __launch_bounds__(kMaxThreads) tables_totals_kernel(const __grid_constant__ TablesParams p) {
+    __shared__ int sums[32];
+    grid_dependency_wait();
+    const int B = p.block_size;
+    int opened = 0;
+    for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
+        const int c = __ldcg(p.context_lens + s);
+        const int n = __ldcg(p.query_start + s + 1) - __ldcg(p.query_start + s);
+        p.context_lens_out[s] = c + n;
+        if (n > 0) opened += int(((long long)c + n + B - 1) / B) - (c + B - 1) / B;
+    }
+    opened = __reduce_add_sync(kAllLanes, opened);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = opened;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < int(blockDim.x >> 5); ++w) opened += sums[w];
+        *p.free_count_out = min(max(__ldcg(p.free_count), 0), p.free_capacity) - opened;
+    }
+    // (as above)
+    __threadfence();
+    __syncthreads();
+    grid_launch_dependents();
+}
+
 }  // namespace
 
 cudaError_t launch_build_tables(const TablesParams &p, int num_sms, cudaStream_t st) {
-    // A block up to a token per thread, then four tokens per lane: in a cluster
-    // of up to 8 blocks where an output is an input, else up to a block per SM.
+    // a token per thread, up to a block per SM
     const long long work = p.token_capacity > p.num_seqs ? p.token_capacity : p.num_seqs;
     int threads = 128;
     while (threads < kMaxThreads && (threads < work || threads * kPerThread < p.num_seqs)) threads <<= 1;
+    const long long want = (work + threads - 1) / threads;
+    const int blocks = want < 1 ? 1 : int(want < num_sms ? want : num_sms);
     const bool in_place = p.context_lens_out == p.context_lens || p.free_count_out == p.free_count;
-    const bool many = work > threads;
-    int blocks = 1;
-    if (many) {
-        const long long want = (work + 4ll * threads - 1) / (4ll * threads);
-        if (in_place) while (blocks < 8 && blocks < want) blocks <<= 1;
-        else blocks = int(want < num_sms ? want : num_sms);
-    }
-    const bool cluster = in_place && blocks > 1;
+    const bool totals = blocks == 1 || !in_place;
     const int smem = int(sizeof(int)) * (3 * p.num_seqs + 2);
-    auto kernel = many ? build_tables_kernel<4> : build_tables_kernel<1>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static std::atomic<unsigned long long> opened[2][kLaunchCacheDevices];
+    static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
     if (smem > 40 * 1024) {
-        e = open_dynamic_smem(opened[many ? 1 : 0], dev, kernel, smem);
+        e = open_dynamic_smem(opened, dev, build_tables_kernel, smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(blocks);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, build_tables_kernel, p, totals);
+    if (e != cudaSuccess || totals) return e;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(p.num_seqs > 256 ? kMaxThreads : 256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, tables_totals_kernel, p);
 }
 
 }  // namespace pkv
