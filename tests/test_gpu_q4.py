@@ -485,3 +485,19 @@ def test_refusals_on_the_gpu():
     with pytest.raises(pk.PagedKVError, match="workspace"):
         pk.paged_attention_prefill_q4(q, kc, vc, tables, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), L, 0.1,
                                       out, 1, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"), key_parts=4)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_decode_shared_prefixes_in_a_call_past_l2(dtype):
+    """Sequences that hold the same blocks, in their order or another, in a call that
+    reads more than the L2 holds."""
+    heads, dim, block, n, S = 8, 128, 16, 30000, 4
+    kc, vc, tables = q4.filled([n], heads, block, dim, dtype, 9)
+    tables = tables.repeat(S, 1)
+    tables[3] = tables[3].flip(0)
+    q = rows((S, heads, dim), dtype, 2)
+    lens = [n, n - 7, 12345, n]
+    ref = q4.attention(q, (kc, vc), tables, range(S + 1), lens, dim ** -0.5, dim, dtype)
+    for part in (0, 2048, pk.PARTITION_BALANCED):
+        q4.assert_near(decode(q, kc, vc, tables, lens, dim ** -0.5, part), ref, dtype, 2, f"part {part}")
+    assert pk.device_errors() == 0
