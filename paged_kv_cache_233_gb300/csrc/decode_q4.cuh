@@ -688,9 +688,10 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
             }
         }
         if (p.balanced && !p.cuts_by_pair && lane == 0) p.ws_cuts[blockIdx.x] = cut;
-        if (!ok && lane == 0) {
-            // stop everyone, then wait (bounded) for this CTA's copies in flight
-            *abort_flag = 1;
+        if (lane == 0) {
+            // stop everyone if a wait ran out; then wait (bounded) for this CTA's
+            // copies in flight, which consumers that stopped do not
+            if (!ok) *abort_flag = 1;
             for (int k = max(0, armed - NS); k < armed; ++k)
                 mbar_wait(full0 + 8 * (k % NS), uint32_t((k / NS) & 1), p.err);
         }
@@ -825,8 +826,10 @@ __global__ void __launch_bounds__(q4_merge_threads<kWarps>()) merge_q4_kernel(co
     const int r = blockIdx.y * kRows + warp / kWarps, first = warp % kWarps;
     __shared__ float joined[q4_merge_threads<kWarps>() / 32][D + 2];
     const int4 cut = __ldcg(p.ws_cuts + blockIdx.x);
-    if (cut.x < 0) return;
-    const int groups = p.n_kv_heads >> p.log2_hpu, s = cut.x / groups, hg = cut.x - s * groups;
+    const int groups = p.n_kv_heads >> p.log2_hpu;
+    // none; or no cut at all, where a CTA of the decode stopped before it wrote one
+    if (cut.x < 0 || cut.x >= groups * p.num_seqs || cut.y < 0 || cut.z >= p.decode_ctas || (cut.w & ~1) != 0) return;
+    const int s = cut.x / groups, hg = cut.x - s * groups;
     const int c0 = cut.y, np = cut.z - c0 + 1, slot0 = cut.w;
     if (kWarps == 1 && r >= rows) return;
     float acc[E] = {}, M = -INFINITY, den = 0.f;
@@ -935,6 +938,7 @@ cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
     // (the pieces take at most 3 of the workspace's 8 CTAs per SM; the cuts lie behind them)
     const long long pairs = groups * p.num_seqs;
     p.cuts_by_pair = pairs <= grid ? 1 : 0;
+    p.decode_ctas = grid;
     if (p.balanced) p.ws_cuts = reinterpret_cast<int4 *>(p.ws_o + size_t(grid) * 2 * (H * p.group) * D);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -66,6 +66,7 @@ struct Q4AttnParams {
     float *ws_o, *ws_m, *ws_l;
     int4 *ws_cuts;                // balanced split: where pairs are cut, by pair or by CTA (decode_q4.cuh)
     int cuts_by_pair;
+    int decode_ctas;              // the decode's grid (its launcher fills both)
     unsigned int *err;
     float scale_log2;
     int num_seqs, n_q_heads, n_kv_heads, group;
