@@ -547,8 +547,13 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
  * paged_attention_prefill_q4 -- paged_attention_prefill_split over 4-bit pools.
  *
  * The same causal attention of each sequence's chunk of query rows, with K and
- * V the rows that the codes stand for. Arguments and limits as
- * paged_attention_prefill_split's.
+ * V the rows that the codes stand for, each channel rounded once to dtype, as
+ * paged_kv_gather_q4 reads them. Arguments, limits and workspace as
+ * paged_attention_prefill_split's, and 1 <= key_parts means the same; a split's
+ * ranges hold at least 6 key tiles here, not 16. key_parts 0 splits when the
+ * workspace holds it and the items (counted from max_query_len) and the tables'
+ * width say that the SMs' even share of the key tiles saves more than the extra
+ * pieces and the merge cost, which may be so past a round of items too.
  */
 int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v_cache,
                                const int32_t *block_tables, const int32_t *query_start,
