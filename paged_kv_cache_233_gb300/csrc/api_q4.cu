@@ -195,7 +195,7 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
     p.max_parts = int((cap + p.part_tokens - 1) / p.part_tokens);
     // the kernel counts units and tiles in ints
     const long long units = (long long)num_seqs * (n_kv_heads >> p.log2_hpu) *
-                            (p.balanced ? (cap + 31) / 32 : p.max_parts);
+                            (p.balanced ? (cap + 31) / 32 + pkv::kQ4UnitCost : p.max_parts);
     if (units > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
     if (partition_tokens != 0) {
         // rows of partition states, or of pieces: two per CTA, as paged_attention_workspace_bytes sizes them

@@ -40,7 +40,12 @@
 // rounding.
 //
 // Work. A unit is (sequence, group of H kv heads, range of keys), split whole,
-// in fixed partitions or in equal shares of the call's 32-key tiles per CTA.
+// in fixed partitions or in equal shares of the call's work per CTA: its 32-key
+// tiles, and two tiles' worth (kQ4UnitCost) for each (sequence, head group),
+// whose queries, sums and stores cost about that. (Counting tiles alone, the
+// CTAs that got many short sequences ended last: 64 sequences of 1 to 2048
+// tokens, 32 heads of 64, 45.7 us against 42.5, 256 of 1 to 512 59.1 against
+// 48.3; with one tile's worth 42.3 and 51.6, with three 43.4 and 50.1.)
 // Per CTA one producer warp copies each tile's blocks with untiled bulk copies
 // (a block's bytes of neighbouring kv heads are one run), through a ring of
 // stages; four consumer warps own a kv head each (H = 4) or share one (H = 2,
@@ -51,9 +56,11 @@
 //
 // Measured (GB300, tables and lengths of a serving step; of a copy's 6.71 TB/s):
 // 8 requests of 65536 tokens, 8 kv heads of 128, 64 query heads: 671 MB in
-// 117 us, 5.73 TB/s (85%); the same bytes with head size 64 and 32 kv heads of
-// one query head each 129 us (77%); 64 requests of 1 to 2048 tokens, 32 heads
-// of 64: 168 MB in 46 us (55%: about 10 us are launch, ramp, pieces and merge).
+// 117 us, 5.74 TB/s (86%); the same bytes with head size 64 and 32 kv heads of
+// one query head each 129 us (78%); 64 requests of 1 to 2048 tokens, 32 heads
+// of 64: 168 MB in 42.5 us (59%: about 10 us are launch, ramp, pieces and
+// merge); 256 requests of 200 to 4000 tokens, 8 kv heads of 128, 32 query
+// heads, bf16: 692 MB in 122.5 us (84%).
 // The copies alone, without arithmetic, reach 94%: the consumers' instructions
 // are the bound, then that fixed part.
 #pragma once
@@ -70,14 +77,14 @@ constexpr int kQ4Threads = 32 * (1 + kQ4Consumers);
 constexpr int kQ4CtasPerSm = 3;
 constexpr unsigned kQ4All = 0xffffffffu;
 
-// Balanced split: the CTAs that get a share of `total` tiles, none of them
-// empty, and share c's first tile.
+// Balanced split: the CTAs that get a share of `total` positions (tiles and unit
+// costs), none of them empty, and share c's first position.
 __device__ __forceinline__ int q4_sharers(int total, int grid) { return max(1, min(grid, total)); }
 __device__ __forceinline__ int q4_share(int total, int c, int sharers) {
     return int((long long)total * c / sharers);
 }
 
-// The share that holds tile t.
+// The share that holds position t.
 __device__ __forceinline__ int q4_share_of(int total, int t, int sharers) {
     int c = int((long long)t * sharers / total);
     while (c + 1 < sharers && q4_share(total, c + 1, sharers) <= t) ++c;
@@ -103,12 +110,12 @@ struct Q4Unit {
     int s, hg, t0, t1;
     int part;         // its partition; balanced split: its piece slot of the CTA
     bool partial;     // the result is a state for the merge
-    int last;         // balanced split: the pair's last tile where this CTA has its first, else -1
+    int last;         // balanced split: the position of the pair's last tile where this CTA has its first, else -1
 };
 
 // This CTA's units in order; the producer and every consumer warp walk a copy.
 struct Q4Walk {
-    uint32_t base;   // shared address: [S + 1] units (or tiles) before each sequence, then [S] lengths
+    uint32_t base;   // shared address: [S + 1] units (or positions) before each sequence, then [S] lengths
     int s, pos, end, count;
 
     __device__ static int at(uint32_t a) {
@@ -147,15 +154,17 @@ struct Q4Walk {
         const int L = at(base + 4 * (S + 1 + s));
         const int r = pos - at(base + 4 * s);
         if (p.balanced) {
-            const int nt = (L + kQ4Tile - 1) / kQ4Tile;
-            x.hg = r / nt;
-            const int a = r - x.hg * nt, b = min(nt, a + (end - pos));
+            const int nt = (L + kQ4Tile - 1) / kQ4Tile, w = kQ4UnitCost + nt;
+            x.hg = r / w;
+            const int from = r - x.hg * w, n = min(w - from, end - pos);
+            const int a = max(from - kQ4UnitCost, 0), b = from + n - kQ4UnitCost;
+            if (b <= a) return false;    // the share ends before the pair's first tile
             x.t0 = a * kQ4Tile;
             x.t1 = min(L, b * kQ4Tile);
             x.part = count == 0 ? 0 : 1;
             x.partial = !(a == 0 && b == nt);
-            x.last = a == 0 ? pos + nt - 1 : -1;
-            pos += b - a;
+            x.last = a == 0 ? pos - from + w - 1 : -1;
+            pos += n;
         } else {
             x.part = r / groups;
             x.hg = r - x.part * groups;
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     // the merge may start its launch; without one the next kernel may not (it
     // could be one that reads its queries, these outputs, before it waits)
     if (p.merged) grid_launch_dependents();
-    // ---- per sequence: length, and units (or tiles) before it
+    // ---- per sequence: length, and units (or positions) before it
     {
         const int cap = p.max_blocks * B, groups = p.n_kv_heads >> p.log2_hpu;
         const int per = (S + kQ4Threads - 1) / kQ4Threads;
@@ -594,7 +603,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
             const int L = __ldg(p.context_lens + s), Lc = min(max(L, 0), cap);
             if (L != Lc && blockIdx.x == 0) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
             seq_len[s] = Lc;
-            const int n = p.balanced ? (Lc + kQ4Tile - 1) / kQ4Tile
+            const int n = p.balanced ? (Lc > 0 ? (Lc + kQ4Tile - 1) / kQ4Tile + kQ4UnitCost : 0)
                                      : (Lc > 0 ? (Lc + p.part_tokens - 1) / p.part_tokens : 1);
             sum += n * groups;
             seq_base[s + 1] = sum;
@@ -629,7 +638,7 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
 
     if (warp == 0) {
         // -------------------------------------------------------- producer
-        int stage = 0, armed = 0;
+        int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         Q4Unit u;
@@ -668,7 +677,6 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
                                    pool + (size_t(pb) * p.n_kv_heads + h0) * head_bytes, uint32_t(run),
                                    full0 + 8 * stage, once);
                 }
-                ++armed;
                 if (++stage == NS) {
                     stage = 0;
                     phase ^= 1u;
@@ -690,10 +698,16 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
         if (p.balanced && !p.cuts_by_pair && lane == 0) p.ws_cuts[blockIdx.x] = cut;
         if (lane == 0) {
             // stop everyone if a wait ran out; then wait (bounded) for this CTA's
-            // copies in flight, which consumers that stopped do not
+            // copies in flight, which consumers that stopped do not: each stage's
+            // last use (the phase before a stage's first counts as done)
             if (!ok) *abort_flag = 1;
-            for (int k = max(0, armed - NS); k < armed; ++k)
-                mbar_wait(full0 + 8 * (k % NS), uint32_t((k / NS) & 1), p.err);
+            for (int k = 0; k < NS; ++k) {
+                mbar_wait(full0 + 8 * stage, phase ^ 1u, p.err);
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
         }
         return;
     }
@@ -827,8 +841,11 @@ __global__ void __launch_bounds__(q4_merge_threads<kWarps>()) merge_q4_kernel(co
     __shared__ float joined[q4_merge_threads<kWarps>() / 32][D + 2];
     const int4 cut = __ldcg(p.ws_cuts + blockIdx.x);
     const int groups = p.n_kv_heads >> p.log2_hpu;
-    // none; or no cut at all, where a CTA of the decode stopped before it wrote one
-    if (cut.x < 0 || cut.x >= groups * p.num_seqs || cut.y < 0 || cut.z >= p.decode_ctas || (cut.w & ~1) != 0) return;
+    if (cut.x < 0) return;
+    // no cut at all, where a CTA of the decode stopped before it wrote one (a test
+    // of its own: in one with the other it costs the merge 1 us)
+    const bool bad = cut.x >= groups * p.num_seqs || cut.y < 0 || cut.z >= p.decode_ctas || (cut.w & ~1) != 0;
+    if (bad) return;
     const int s = cut.x / groups, hg = cut.x - s * groups;
     const int c0 = cut.y, np = cut.z - c0 + 1, slot0 = cut.w;
     if (kWarps == 1 && r >= rows) return;
@@ -931,7 +948,7 @@ cudaError_t launch_decode_q4_sized(Q4AttnParams p, int sms, cudaStream_t st) {
     if (per_sm > kCtas) per_sm = kCtas;
     const long long cap = (long long)p.max_blocks * p.block_size;
     const long long groups = p.n_kv_heads >> p.log2_hpu;
-    const long long most = p.balanced ? groups * p.num_seqs * ((cap + kQ4Tile - 1) / kQ4Tile)
+    const long long most = p.balanced ? groups * p.num_seqs * ((cap + kQ4Tile - 1) / kQ4Tile + kQ4UnitCost)
                                       : groups * p.num_seqs * ((cap + p.part_tokens - 1) / p.part_tokens);
     const long long want = (long long)per_sm * sms;
     const int grid = int(most < want ? most : want);

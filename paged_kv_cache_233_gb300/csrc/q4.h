@@ -66,7 +66,7 @@ struct Q4AttnParams {
     float *ws_o, *ws_m, *ws_l;
     int4 *ws_cuts;                // balanced split: where pairs are cut, by pair or by CTA (decode_q4.cuh)
     int cuts_by_pair;
-    int decode_ctas;              // the decode's grid (its launcher fills both)
+    int decode_ctas;              // the decode's grid (its launcher fills the three)
     unsigned int *err;
     float scale_log2;
     int num_seqs, n_q_heads, n_kv_heads, group;
@@ -74,10 +74,14 @@ struct Q4AttnParams {
     int part_tokens;              // tokens per partition (unsplit: the tables' whole width)
     int max_parts;
     int merged;                   // a merge kernel follows
-    int balanced;                 // equal shares of the call's tiles per CTA, pieces joined
+    int balanced;                 // equal shares of the call's work per CTA, pieces joined
     int log2_hpu;                 // kv heads per unit: 4, 2 or 1
     int stages;
 };
+
+// Balanced split: what a (sequence, head group) costs beside its 32-key tiles, in tiles.
+constexpr int kQ4UnitCost = 2;
+
 // Decode, with the balanced split's merge (fixed partitions: the caller merges).
 cudaError_t launch_decode_q4_f16(int head_dim, const Q4AttnParams &p, int sms, cudaStream_t st);
 cudaError_t launch_decode_q4_bf16(int head_dim, const Q4AttnParams &p, int sms, cudaStream_t st);

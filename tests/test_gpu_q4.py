@@ -501,3 +501,15 @@ def test_decode_shared_prefixes_in_a_call_past_l2(dtype):
     for part in (0, 2048, pk.PARTITION_BALANCED):
         q4.assert_near(decode(q, kc, vc, tables, lens, dim ** -0.5, part), ref, dtype, 2, f"part {part}")
     assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("heads, dim, block", [(32, 64, 8), (2, 128, 32), (3, 64, 16)])
+def test_decode_short_sequences_beside_long_ones(heads, dim, block):
+    """A balanced split over sequences of one or two tiles, empty ones and a few long
+    ones, in an order that ends shares inside, before and behind each of them."""
+    lens = [(5000, 0, 1, 32, 33, 64, 700, 31)[(3 * i + i // 8) % 8] for i in range(150)]
+    kc, vc, tables = q4.filled(lens, heads, block, dim, F16, 4)
+    q = rows((len(lens), heads, dim), F16, 6)
+    ref = q4.attention(q, (kc, vc), tables, range(len(lens) + 1), lens, dim ** -0.5, dim, F16)
+    q4.assert_near(decode(q, kc, vc, tables, lens, dim ** -0.5, pk.PARTITION_BALANCED), ref, F16, 2, "short and long")
+    assert pk.device_errors() == 0
