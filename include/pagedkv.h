@@ -532,7 +532,8 @@ int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *
  * scores, softmax and the output sums are fp32, out is rounded once. Arguments,
  * limits, splits and workspace (paged_attention_workspace_bytes) as
  * paged_attention_decode's, except that partition_tokens > 0 must be a
- * multiple of 32. No q, K or V is expected to hold an infinity or a NaN: a
+ * multiple of 32 and a balanced split's shares are of 32-token tiles and a fixed
+ * cost per sequence and head. No q, K or V is expected to hold an infinity or a NaN: a
  * sequence whose rows do gets NaN outputs; what lies in a block past a
  * sequence's context never matters.
  */
@@ -553,7 +554,8 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
  * ranges hold at least 6 key tiles here, not 16. key_parts 0 splits when the
  * workspace holds it and the items (counted from max_query_len) and the tables'
  * width say that the SMs' even share of the key tiles saves more than the extra
- * pieces and the merge cost, which may be so past a round of items too.
+ * pieces and the merge cost: with few items, or with one sequence whose items
+ * leave SMs without any in their last round.
  */
 int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v_cache,
                                const int32_t *block_tables, const int32_t *query_start,

@@ -38,12 +38,21 @@ int check_pool(int num_blocks, int block_size, int n_kv_heads, int head_dim, int
 
 bool finite(float x) { return x == x && x != INFINITY && x != -INFINITY; }
 
-// Whether a prefill call of `items` items of about `tiles` key tiles each is
+// Whether a prefill call of `items` items of up to `tiles` key tiles each is
 // faster with its keys shared out over the SMs: whole items take
 // ceil(items / SMs) rounds of `tiles`, shared keys their even share, the extra
-// pieces and a merge.
-bool split_pays(long long items, long long tiles, int sms) {
-    const long long rounds = (items + sms - 1) / sms;
+// pieces and a merge, which come to about 10 tiles and 0.2 per item. Items of
+// several sequences count as one round: their lengths differ, which the host
+// does not see, and whole items taken longest first then fill the SMs.
+// Measured (us, whole / shared; 8 kv heads of 128, 32 query heads, 152 SMs):
+//   one sequence      rows 33, cached 1000: 25 / 19; 33, 6001: 114 / 24;
+//                     1216, 8192 (152 items): 167 / 192; 1280, 8192 (160):
+//                     294 / 200; 2048, 2048 (256): 112 / 142; 2048, 16384: 599 / 542
+//   4 of 64 rows      up to 500 cached: 17 / 19; 4000: 78 / 43
+//   20 of 64 rows     up to 1000 cached (160 items): 25 / 59; 4000: 76 / 128
+// and the same choices with heads of 64.
+bool split_pays(long long items, long long tiles, int seqs, int sms) {
+    const long long rounds = seqs > 1 ? 1 : (items + sms - 1) / sms;
     const double gain = double(rounds * tiles) - double(items * tiles) / sms;
     return gain > 10.0 + 0.2 * double(items);
 }
@@ -265,7 +274,7 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
     if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
     if (key_parts == 0)
         key_parts = workspace && workspace_bytes >= paged_attention_prefill_workspace_bytes(head_dim) &&
-                            split_pays(per_seq * num_seqs, (cap + 63) / 64, sms)
+                            split_pays(per_seq * num_seqs, (cap + 63) / 64, num_seqs, sms)
                         ? 32
                         : 1;
     st = pkv::api_plan_key_split(p, key_parts, workspace, workspace_bytes, head_dim, max_query_len, sms);
