@@ -17,8 +17,7 @@
 //
 // Bound by latency: a launch, the lengths, a table entry or a free block. 256
 // requests of a token each: 4.0 us; 2048 requests, 67,000 tokens: 7.4 us, in
-// place 9.8 (one block for everything 12.6; a cluster of 16 blocks that share
-// the sums over distributed shared memory 12.6 in place).
+// place 9.8 (by a cluster of blocks over distributed shared memory 12.6).
 #include "launch_cache.h"
 #include "ptx.cuh"
 #include "q4.h"
