@@ -60,7 +60,7 @@
 // one query head each 129 us (78%); 64 requests of 1 to 2048 tokens, 32 heads
 // of 64: 168 MB in 42.5 us (59%: about 10 us are launch, ramp, pieces and
 // merge); 256 requests of 200 to 4000 tokens, 8 kv heads of 128, 32 query
-// heads, bf16: 692 MB in 122.5 us (84%).
+// heads, bf16: 692 MB in 121.5 us (85%).
 // The copies alone, without arithmetic, reach 94%: the consumers' instructions
 // are the bound, then that fixed part.
 #pragma once
