@@ -354,9 +354,12 @@ struct Q4Consumer {
     // Move the reference and the bounds: sc the tile's sums of products, most the
     // bits of this lane's token's largest scale.
     __device__ __forceinline__ void move(const float (&sc)[4][2], uint32_t most, int nvalid) {
-        // (bits of values >= 0 order as the values; scales count as at least
-        // 2^-80, so that sums of p stay finite)
-        const float top = fmaxf(scale_of<T>(__reduce_max_sync(kQ4All, most)), 0x1p-80f);
+        // (bits of values >= 0 order as the values; scales count as at least the
+        // smallest that a bound of type T can hold: 2^-16 in fp16, whose bound
+        // 2^(e + 2) is then a normal number, and 2^-80 in bf16, so that sums of p
+        // stay finite)
+        constexpr float kLeast = Elem<T>::kBf16 ? 0x1p-80f : 0x1p-16f;
+        const float top = fmaxf(scale_of<T>(__reduce_max_sync(kQ4All, most)), kLeast);
         const int e = int(__float_as_uint(top) >> 23) - 126;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -383,7 +386,7 @@ struct Q4Consumer {
         plim = __uint_as_float(uint32_t(127 + 12 - e) << 23);
         const int f = e + 2;
         if constexpr (Elem<T>::kBf16) slim = f > 127 ? 0x7f7fu : uint32_t(f + 127) << 7;
-        else slim = f > 15 ? 0x7bffu : f < -14 ? 0x0400u : uint32_t(f + 15) << 10;
+        else slim = f > 15 ? 0x7bffu : uint32_t(f + 15) << 10;
     }
 
     // One tile: ks, vs the stage's K and V in shared memory, run the bytes between blocks.

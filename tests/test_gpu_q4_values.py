@@ -1,0 +1,86 @@
+"""The 4-bit decode on values at the ends of what its arithmetic takes."""
+import pytest
+import torch
+
+import paged_kv_cache_233_gb300 as pk
+import q4_support as q4
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+SPLITS = [0, 32, 64, pk.PARTITION_BALANCED]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pk.load()
+    torch.cuda.set_device(0)
+    pk.device_errors()
+
+
+def rows(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+def pools(k, v, block, seed=1):
+    """One sequence's K and V [n][Hkv][D] in 4-bit pools of stale bytes, and its table."""
+    n, heads, dim = k.shape
+    tables, nb = q4.tables_for([n], block, seed)
+    out = []
+    for i, x in enumerate((k, v)):
+        pool = q4.new_pool(nb, heads, block, dim, seed + i)
+        q4.write_fast(pool, q4.sequence_slots(tables, 0, n, block), x)
+        out.append(pool)
+    return out[0], out[1], tables
+
+
+def decode(q, kc, vc, tables, lens, scale, part):
+    out = torch.full_like(q, 7.0).cuda()
+    q, tables = q.cuda(), tables.cuda()
+    ws = pk.new_workspace(q, tables, kc.shape[2], part)
+    if ws is not None:
+        ws.fill_(255)                          # NaN
+    pk.paged_attention_decode_q4(q, kc.cuda(), vc.cuda(), tables, torch.tensor(lens, dtype=torch.int32).cuda(), scale, out,
+                                 part, ws)
+    return out.cpu()
+
+
+def check(q, k, v, block, scale, what):
+    dtype, dim = q.dtype, q.shape[2]
+    kc, vc, tables = pools(k, v, block)
+    n = k.shape[0]
+    ref = q4.attention(q, (kc, vc), tables, [0, 1], [n], scale, dim, dtype)
+    for part in SPLITS:
+        got = decode(q, kc, vc, tables, [n], scale, part)
+        # the output is rounded, and so are the probabilities (times a scale)
+        q4.assert_near(got, ref, dtype, 2, f"{what} part {part}")
+    assert pk.device_errors() == 0
+
+
+# ------------------------------------------- scales of the values, small and none
+@pytest.mark.parametrize("heads,dim,block", [(4, 128, 16), (2, 64, 8), (1, 128, 32)])
+@pytest.mark.parametrize("flat", [0.0, 0.5, 1e-4])
+def test_fp16_flat_values_before_small_ones(flat, heads, dim, block):
+    """Tiles whose groups have no spread (scale 0), then tiles of size 1e-4."""
+    n = 200
+    v = (rows((n, heads, dim), 3) * 1e-4).to(F16)
+    v[:64] = flat
+    v[130:140] = flat
+    check(rows((1, heads * 2, dim), 1).to(F16), rows((n, heads, dim), 2).to(F16), v, block, dim ** -0.5, f"flat {flat}")
+
+
+@pytest.mark.parametrize("heads,dim,block", [(4, 128, 16), (2, 64, 8), (1, 128, 32)])
+@pytest.mark.parametrize("rise", [20.0, -20.0])
+def test_fp16_scales_from_the_smallest_with_moving_scores(rise, heads, dim, block):
+    """Values from 15 steps of 2^-24 to a spread of 15 * 2^-13, over tiles of 32 tokens,
+    while the scores rise or fall by `rise` in all."""
+    n = 32 * 8
+    step = 2.0 ** (-24 + (torch.arange(n) // 32 * 1.5).round())           # 2^-24 .. 2^-14 (or -13)
+    code = torch.randint(0, 16, (n, heads, dim), generator=torch.Generator().manual_seed(4))
+    v = (code * step[:, None, None]).to(F16)
+    k = rows((n, heads, dim), 2) * 0.3
+    k[..., 0] += torch.linspace(0, rise / 8, n)[:, None]
+    q = rows((1, heads * 2, dim), 1) * 0.5
+    q[..., 0] = 8.0
+    check(q.to(F16), k.to(F16), v, block, 1.0, f"rise {rise}")
