@@ -799,7 +799,9 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
                 float den = 0.f;
                 for (int t = 0; t < TL; ++t) {
                     const int w = (t * H + h) * 8 + j;
-                    if (jm[w] == -INFINITY) continue;     // no tile of the unit was this warp's
+                    // no tile of the unit was this warp's (a warp whose scores were all
+                    // NaN has no reference either, and its NaN sums have to go through)
+                    if (t >= i) continue;
                     const float f = fast_exp2(jm[w] - M);
                     const float4 v = *reinterpret_cast<const float4 *>(jo + w * rowf + d);
                     num.x = fmaf(f, v.x, num.x);

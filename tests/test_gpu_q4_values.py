@@ -84,3 +84,37 @@ def test_fp16_scales_from_the_smallest_with_moving_scores(rise, heads, dim, bloc
     q = rows((1, heads * 2, dim), 1) * 0.5
     q[..., 0] = 8.0
     check(q.to(F16), k.to(F16), v, block, 1.0, f"rise {rise}")
+
+
+# --------------------------------------------------------------- NaN goes through
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads", [1, 2, 3, 4])
+@pytest.mark.parametrize("what", ["query", "key", "key tile", "first key tile", "value", "value tile", "all keys"])
+def test_nan_reaches_the_outputs(what, heads, dtype):
+    """A NaN in a query, in one key or value, or in a whole tile of them beside clean
+    ones makes the rows that attend to it NaN (a value's: its group's channels; the
+    rest of that head may be), and no others."""
+    n, dim, block, group = 160, 64, 16, 3
+    k, v = rows((n, heads, dim), 2).to(dtype), rows((n, heads, dim), 3).to(dtype)
+    q = rows((1, heads * group, dim), 1).to(dtype)
+    h = heads - 1
+    bad = torch.zeros(heads * group, dtype=torch.bool)
+    bad[h * group:] = True
+    sure = bad
+    if what == "query":
+        q[0, -1, 5] = float("nan")
+        bad[:-1] = False
+    else:
+        x = v if what.startswith("value") else k
+        at = {"tile": slice(64, 96), "keys": slice(0, n)}.get(what.split()[-1], slice(70, 71))
+        if what.startswith("first"):
+            at = slice(0, 32)
+        x[at, h, 40] = float("nan")
+        if what.startswith("value"):
+            sure = bad[:, None] & (torch.arange(dim) >= 32)
+    kc, vc, tables = pools(k, v, block)
+    for part in SPLITS:
+        got = decode(q, kc, vc, tables, [n], dim ** -0.5, part)[0]
+        assert bool(got[sure].isnan().all()), f"part {part}"
+        assert bool(torch.isfinite(got[~bad]).all()), f"part {part}"
+    assert pk.device_errors() == 0
