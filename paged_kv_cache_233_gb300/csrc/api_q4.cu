@@ -197,11 +197,11 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.max_blocks = max_blocks_per_seq;
     p.balanced = partition_tokens == PAGEDKV_PARTITION_BALANCED ? 1 : 0;
-    p.merged = partition_tokens != 0 ? 1 : 0;
     p.log2_hpu = n_kv_heads % 4 == 0 ? 2 : (n_kv_heads % 2 == 0 ? 1 : 0);
     // (unsplit: one partition of the tables' whole width)
     p.part_tokens = partition_tokens > 0 ? partition_tokens : int((cap + 31) / 32 * 32);
     p.max_parts = int((cap + p.part_tokens - 1) / p.part_tokens);
+    p.merged = p.balanced || p.max_parts > 1 ? 1 : 0;
     // the kernel counts units and tiles in ints
     const long long units = (long long)num_seqs * (n_kv_heads >> p.log2_hpu) *
                             (p.balanced ? (cap + 31) / 32 + pkv::kQ4UnitCost : p.max_parts);
@@ -218,7 +218,7 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
     cudaError_t e = dtype == PAGEDKV_BF16
                         ? pkv::launch_decode_q4_bf16(head_dim, p, sms, static_cast<cudaStream_t>(stream))
                         : pkv::launch_decode_q4_f16(head_dim, p, sms, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess && partition_tokens > 0)
+    if (e == cudaSuccess && p.merged && !p.balanced)
         e = pkv::launch_lse_merge(dtype, head_dim, p.ws_o, p.ws_m, p.ws_l, context_lens, out, num_seqs, n_q_heads,
                                   p.part_tokens, p.max_parts, int(cap), p.err, static_cast<cudaStream_t>(stream));
     return done(e);

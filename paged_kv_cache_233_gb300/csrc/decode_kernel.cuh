@@ -825,7 +825,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     Walk walk;
     walk.init(seq_base, seq_len, S, groups, P, p.split, p.balanced, prefix ? seq_p0 : nullptr,
               prefix ? seq_pu : nullptr, p.seq_group, p.max_members);
-    if (!walk.has_work()) return;
+    if (!walk.has_work()) {
+        // (a call of empty sequences alone must not end before the kernels
+        // ahead of it: the kernel behind it waits for this grid only)
+        if (blockIdx.x == 0) grid_dependency_wait();
+        return;
+    }
     // a dependent merge launch may start once every CTA got here or exited;
     // it waits on this grid's completion before reading the partition states
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

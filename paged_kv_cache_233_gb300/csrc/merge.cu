@@ -79,8 +79,11 @@ lse_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_m,
     const int s = row / n_q_heads;
     const int L = min(max(__ldg(lens + s), 0), cap);
     const int np = L > 0 ? (L + part_tokens - 1) / part_tokens : 1;
-    if (np <= 1) return;  // written directly by the partition kernel
+    // (row 0 waits even with nothing to merge: a kernel that comes after this
+    // one waits for this grid alone, which must not end before the decode)
+    if (np <= 1 && row != 0) return;  // written directly by the partition kernel
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (np <= 1) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const size_t row0 = size_t(row) * max_parts;
     const bool keep = np <= kMaxParts;
@@ -157,8 +160,11 @@ lse_merge_rows_kernel(const float *__restrict__ ws_o, const float *__restrict__ 
     const int s = row / n_q_heads;
     const int L = min(max(__ldg(lens + s), 0), cap);
     const int np = L > 0 ? (L + part_tokens - 1) / part_tokens : 1;
-    if (np <= 1) return;  // written directly by the partition kernel
+    // (row 0 waits even with nothing to merge: a kernel that comes after this
+    // one waits for this grid alone, which must not end before the decode)
+    if (np <= 1 && row != 0) return;  // written directly by the partition kernel
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (np <= 1) return;
     const size_t row0 = size_t(row) * max_parts;
     const float mp = lane < np ? __ldcg(ws_m + row0 + lane) : -INFINITY;
     const float lp = lane < np ? __ldcg(ws_l + row0 + lane) : 0.f;
@@ -321,7 +327,12 @@ lse_merge_pieces_kernel(const float *__restrict__ ws_o, const float *__restrict_
         return c;
     };
     const long long c0 = nt > 0 ? share_of(A) : 0, c1 = nt > 0 ? share_of(Z) : 0;
-    if (nt > 0 && c0 == c1) return;   // the decode wrote this pair's rows itself
+    if (nt > 0 && c0 == c1) {   // the decode wrote this pair's rows itself
+        // (a kernel that comes after this one waits for this grid alone, which
+        // must not end before the decode)
+        if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int np = int(c1 - c0 + 1);
     const int slot0 = nt > 0 && A != share_start(c0) ? 1 : 0;
     // piece i of a row comes from share c0 + i: the first share's piece sits in

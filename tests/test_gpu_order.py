@@ -1,0 +1,150 @@
+"""Calls right behind one another on a stream and in a graph, each reading what the
+one before it wrote: the kernels are chained by programmatic dependent launch, so a
+kernel that may start early has to wait before it reads that. Every chain's results
+are compared with those of the same calls with a synchronisation between them."""
+import pytest
+import torch
+
+import paged_kv_cache_233_gb300 as pk
+
+pytestmark = pytest.mark.gpu
+F16 = torch.float16
+TIMES = 6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pk.load()
+    torch.cuda.set_device(0)
+    pk.device_errors()
+
+
+class Cache:
+    """S sequences of n tokens in shuffled blocks, 16-bit and 4-bit pools of the same rows."""
+
+    def __init__(self, S, n, heads, dim=128, block=16, seed=1):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.heads, self.dim, self.block = heads, dim, block
+        per = -(-n // block)
+        self.blocks = S * per
+        self.tables = torch.randperm(self.blocks, generator=g, device="cuda").to(torch.int32).view(S, per)
+        self.lens = torch.full((S,), n, dtype=torch.int32, device="cuda")
+        self.kc, self.vc = (torch.randn(self.blocks, block, heads, dim, generator=g, device="cuda", dtype=F16) for _ in range(2))
+        self.k4, self.v4 = (pk.new_q4_pool(self.blocks, heads, block, dim) for _ in range(2))
+        slots = torch.arange(self.blocks * block, device="cuda")
+        pk.paged_kv_append_q4(self.kc.flatten(0, 1), self.vc.flatten(0, 1), slots, self.k4, self.v4)
+        torch.cuda.synchronize()
+
+    def decode(self, bits, q, out, part, ws, lens=None):
+        f = pk.paged_attention_decode_q4 if bits == 4 else pk.paged_attention_decode
+        k, v = (self.k4, self.v4) if bits == 4 else (self.kc, self.vc)
+        f(q, k, v, self.tables, self.lens if lens is None else lens, self.dim ** -0.5, out, part, ws)
+
+
+def queries(S, heads, dim, seed):
+    return torch.randn(S, heads, dim, generator=torch.Generator().manual_seed(seed)).to(F16).cuda()
+
+
+def same_as_apart(steps, reset, results, graph):
+    """steps: calls in order. The results of a run with a synchronisation after each,
+    and of runs without any, are the same bits."""
+    reset()
+    for s in steps:
+        s()
+        torch.cuda.synchronize()
+    want = [r.clone() for r in results]
+    torch.cuda.synchronize()
+    g = None
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for s in steps:
+                s()
+    for _ in range(TIMES):
+        reset()
+        torch.cuda.synchronize()
+        if graph:
+            g.replay()
+        else:
+            for s in steps:
+                s()
+        torch.cuda.synchronize()
+        for r, w in zip(results, want):
+            assert torch.equal(r, w)
+    assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("bits,part,S,n,heads", [
+    (4, 512, 400, 500, 8), (16, 512, 400, 500, 8),      # every row within one partition
+    (4, 2048, 30, 2000, 8), (16, 2048, 30, 2000, 8),
+    (4, 32, 600, 32, 8),                                 # more than 32 partitions in the tables' width
+    (16, pk.PARTITION_BALANCED, 38, 1024, 32),           # every pair within one share of 304
+    (4, pk.PARTITION_BALANCED, 57, 1024, 32), (4, 512, 40, 1500, 8)])
+def test_rows_taken_right_behind_a_decode(bits, part, S, n, heads, graph):
+    """A decode whose merge has nothing to do for any row, and an append of its
+    outputs, which waits for the merge alone."""
+    c = Cache(S, n, heads)
+    if part == 32:
+        c.tables = torch.cat([c.tables, c.tables.repeat(1, 40)], 1).contiguous()
+    q = queries(S, heads, c.dim, 2)
+    out = torch.empty_like(q)
+    ws = pk.new_workspace(q, c.tables, c.block, part)
+    k4, v4 = (pk.new_q4_pool(-(-S // c.block), heads, c.block, c.dim) for _ in range(2))
+    kc, vc = (torch.empty(-(-S // c.block), c.block, heads, c.dim, dtype=F16, device="cuda") for _ in range(2))
+    slots = torch.arange(S, device="cuda")
+
+    def reset():
+        for x in (out, kc, vc):
+            x.fill_(-1)
+        for x in (k4, v4):
+            x.fill_(0)
+
+    for take, pools in ((lambda: pk.paged_kv_append_q4(out, out, slots, k4, v4), (k4, v4)),
+                        (lambda: pk.paged_kv_append(out, out, slots, kc, vc), (kc, vc))):
+        same_as_apart([lambda: c.decode(bits, q, out, part, ws), take], reset, [out, *pools], graph)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_lengths_moved_on_right_behind_a_decode(graph):
+    """paged_kv_build_tables moves the lengths on in place behind a decode whose merge
+    has nothing to do."""
+    c = Cache(400, 500, 8)
+    q = queries(400, 8, c.dim, 2)
+    out, part = torch.empty_like(q), 512
+    ws = pk.new_workspace(q, c.tables, c.block, part)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    new, free, count = torch.ones(400, **i32), torch.zeros(1, **i32), torch.zeros(1, **i32)
+    start, seq, pos = torch.empty(401, **i32), torch.empty(400, **i32), torch.empty(400, **i32)
+
+    def reset():
+        out.fill_(-1)
+        c.lens.fill_(500)
+
+    def tables():
+        pk.paged_kv_build_tables(new, c.lens, c.tables, free, count, c.block, c.blocks, start, seq, pos)
+
+    same_as_apart([lambda: c.decode(4, q, out, part, ws), tables, lambda: c.decode(4, q, out, part, ws), tables], reset,
+                  [out, c.lens], graph)
+
+
+def test_zero_rows_behind_a_decode_of_the_same_rows():
+    """A balanced 16-bit decode of empty sequences alone, right behind a long decode
+    into the same rows, and an append of them."""
+    c = Cache(64, 4000, 8)
+    q = queries(64, 8, c.dim, 2)
+    out, part = torch.empty_like(q), pk.PARTITION_BALANCED
+    ws = [pk.new_workspace(q, c.tables, c.block, part) for _ in range(2)]
+    none = torch.zeros_like(c.lens)
+    kc, vc = (torch.empty(4, 16, 8, c.dim, dtype=F16, device="cuda") for _ in range(2))
+    slots = torch.arange(64, device="cuda")
+
+    def reset():
+        for x in (out, kc, vc):
+            x.fill_(-1)
+
+    same_as_apart([lambda: c.decode(16, q, out, part, ws[0]), lambda: c.decode(16, q, out, part, ws[1], none),
+                   lambda: pk.paged_kv_append(out, out, slots, kc, vc)], reset, [out, kc, vc], False)
+    assert bool((out == 0).all()) and bool((kc == 0).all())
