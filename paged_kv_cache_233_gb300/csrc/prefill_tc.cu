@@ -675,6 +675,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // waits for this grid before it reads the states or exits; should this
         // warp's signal not count for the CTA, it launches at the grid's end)
         if (kSplit) grid_launch_dependents();
+        // (the queries may be the outputs of a kernel that let this one start early)
+        grid_dependency_wait();
         const int tq = kTcRows / g;
         int kt = 0;
         int i = 0;

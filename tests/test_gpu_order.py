@@ -148,3 +148,29 @@ def test_zero_rows_behind_a_decode_of_the_same_rows():
     same_as_apart([lambda: c.decode(16, q, out, part, ws[0]), lambda: c.decode(16, q, out, part, ws[1], none),
                    lambda: pk.paged_kv_append(out, out, slots, kc, vc)], reset, [out, kc, vc], False)
     assert bool((out == 0).all()) and bool((kc == 0).all())
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("part", [0, 512, pk.PARTITION_BALANCED])
+@pytest.mark.parametrize("first,second", [(16, 16), (4, 16), (16, 4), (16, "prefill"), (4, "prefill")])
+def test_outputs_as_the_next_queries(first, second, part, graph):
+    """A call's outputs are the queries of the one right behind it, three in a row."""
+    S, heads = 48, 8
+    c = Cache(S, 1500, heads)
+    q = queries(S, heads, c.dim, 2)
+    xs = [torch.empty_like(q) for _ in range(3)]
+    ws = [pk.new_workspace(q, c.tables, c.block, part) for _ in range(3)]
+    starts = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+
+    def call(kind, q, out, w):
+        if kind == "prefill":
+            pk.paged_attention_prefill(q, c.kc, c.vc, c.tables, starts, c.lens, c.dim ** -0.5, out, 1)
+        else:
+            c.decode(kind, q, out, part, w)
+
+    def reset():
+        for x in xs:
+            x.fill_(-1)
+
+    same_as_apart([lambda: call(first, q, xs[0], ws[0]), lambda: call(second, xs[0], xs[1], ws[1]),
+                   lambda: call(second, xs[1], xs[2], ws[2])], reset, xs, graph)
