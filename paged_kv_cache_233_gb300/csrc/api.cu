@@ -8,6 +8,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../include/pagedkv.h"
@@ -28,7 +29,7 @@ cudaError_t launch_append_tokens(const void *k, const void *v, const int32_t *bl
                                  const int32_t *token_seq, const int32_t *token_pos,
                                  int64_t *slot_mapping, void *k_cache, void *v_cache,
                                  int num_tokens, int num_seqs, int max_blocks, int block_size,
-                                 int num_blocks, long long row_bytes, int num_sms,
+                                 int num_blocks, long long row_bytes, bool late_inputs, int num_sms,
                                  unsigned int *err, cudaStream_t st);
 cudaError_t launch_bounded_wait_check(unsigned int *err, cudaStream_t stream);
 cudaError_t launch_copy_blocks(void *k_cache, void *v_cache, const int32_t *pairs, int num_pairs,
@@ -63,6 +64,7 @@ int g_opt_mma_min_group = 1;
 int g_opt_stages = 0;
 int g_opt_prefill_path = 0;
 int g_opt_l2_hints = 0;
+std::atomic<bool> g_device_inputs{false};   // paged_kv_build_tables or paged_kv_gather_q4 was called
 int g_last_path = 0;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -234,6 +236,9 @@ namespace pkv {
 
 int api_device_state(unsigned int **err, int *sms) { return device_state(err, sms); }
 
+bool api_late_inputs() { return g_device_inputs.load(std::memory_order_relaxed); }
+void api_note_device_inputs() { g_device_inputs.store(true, std::memory_order_relaxed); }
+
 int api_encode_q_map(CUtensorMap *map, const void *q, int dtype, int head_dim, int n_q_heads, int num_tokens,
                      int group) {
     return encode_q_map(map, q, dtype, head_dim, n_q_heads, num_tokens, group);
@@ -397,7 +402,7 @@ int paged_kv_append_tokens(const void *k, const void *v, const int32_t *block_ta
     if (st != PAGEDKV_OK) return st;
     const cudaError_t e = pkv::launch_append_tokens(
         k, v, block_tables, token_seq, token_pos, slot_mapping, k_cache, v_cache, num_tokens,
-        num_seqs, max_blocks_per_seq, block_size, num_blocks, row_bytes, sms, err,
+        num_seqs, max_blocks_per_seq, block_size, num_blocks, row_bytes, pkv::api_late_inputs(), sms, err,
         static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PAGEDKV_OK : PAGEDKV_ERR_CUDA;
 }
@@ -615,6 +620,7 @@ int prefill_impl(const void *q, const void *k_cache, const void *v_cache,
         if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
     }
     p.num_blocks = num_blocks;
+    p.late_inputs = pkv::api_late_inputs() ? 1 : 0;
     int log2_block = 0;
     while ((1 << log2_block) < block_size) ++log2_block;
     p.log2_block = log2_block;
@@ -787,6 +793,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     p.block_size = block_size;
     p.log2_block = log2_block;
     p.max_blocks = max_blocks_per_seq;
+    p.late_inputs = pkv::api_late_inputs() ? 1 : 0;
     p.part_tokens = P;
     p.max_parts = int(max_parts);
     p.split = split ? 1 : 0;

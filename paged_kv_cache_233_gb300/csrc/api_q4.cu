@@ -102,6 +102,7 @@ int paged_kv_build_tables(const int32_t *new_lens, const int32_t *context_lens, 
         !api_aligned(token_seq, 4) || !api_aligned(token_pos, 4) || !api_aligned(slot_mapping, 8) ||
         !api_aligned(context_lens_out, 4) || !api_aligned(free_count_out, 4))
         return PAGEDKV_ERR_INVALID_ARG;
+    pkv::api_note_device_inputs();   // before the launch: calls that read these tables come later
     pkv::TablesParams p{};
     int sms = 0;
     const int st = api_device_state(&p.err, &sms);
@@ -143,6 +144,7 @@ int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *
                        int head_dim, int dtype, void *stream) {
     return move_rows(k, v, slot_mapping, k_cache, v_cache, num_tokens, num_blocks, block_size, n_kv_heads,
                      head_dim, dtype, [&](long long num_slots, unsigned int *err) {
+                         pkv::api_note_device_inputs();   // as above: calls that append these rows
                          return pkv::launch_gather_q4(static_cast<const uint8_t *>(k_cache),
                                                       static_cast<const uint8_t *>(v_cache), slot_mapping, k, v,
                                                       num_tokens, n_kv_heads, head_dim, block_size, num_slots,

@@ -236,9 +236,8 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const __grid_constant__ RowParams p) {
-    // (no early start for the kernel after this one, which may then not come
-    // before this grid's end: paged_kv_append_tokens, which may take these rows
-    // into another pool, reads its rows before it waits)
+    // (no early start for the kernel after this one: its work, rows of these to
+    // append or attend over, comes after this grid's end)
     grid_dependency_wait();
     constexpr unsigned int kStep = kThreads / kGatherLanes;
     const unsigned int x0 = blockIdx.x * (kStep * kGatherItems) + threadIdx.x / kGatherLanes;

@@ -717,9 +717,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if (p.late_inputs) grid_dependency_wait();
     // Every thread: the per-sequence inputs into shared memory, four sequences
     // per thread in flight (the caller's arrays; like the rest of the set-up,
-    // read before the grid dependency wait). Shared prefixes: the group id goes
+    // read before the grid dependency wait unless a kernel ahead may write them). Shared prefixes: the group id goes
     // to seq_pu until the scan below replaces it with the prefix units.
     const int cap = p.max_blocks * B;
     {
@@ -872,8 +873,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         };
         Unit cur;
         walk.next(cur);
-        // the block tables are the caller's (no kernel of this library writes
-        // them): the first window is in flight during the wait below
+        // the block tables are the caller's (what kernel of this library writes
+        // them has been waited for above): the first window is in flight during
+        // the wait below
         int nxt_base = cur.t0 >> p.log2_block;
         unsigned nxt_sh;
         int nxt_val = load_window(cur, nxt_base, nxt_sh);

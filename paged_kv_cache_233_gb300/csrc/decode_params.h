@@ -40,6 +40,7 @@ struct DecodeParams {
     int block_size;
     int log2_block;
     int max_blocks;       // block table row length
+    int late_inputs;      // 1: tables and lengths may be the kernel's just ahead: read after the wait
     int part_tokens;      // tokens per partition (multiple of kTile)
     int max_parts;        // partitions per (seq, q head) in the workspace
     int split;            // 1: multi-partition sequences write partition states

@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kQ4Threads, kQ4CtasPerSm) decode_q4_kernel(con
     }
     // lengths, tables and pools as the kernels before this one left them
     grid_dependency_wait();
-    // the merge may start its launch; without one the next kernel may not (it
-    // could be one that reads its queries, these outputs, before it waits)
+    // the merge may start its launch; without one the next kernel may not (these
+    // outputs may be what it reads first)
     if (p.merged) grid_launch_dependents();
     // ---- per sequence: length, and units (or positions) before it
     {

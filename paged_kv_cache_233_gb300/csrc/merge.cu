@@ -72,9 +72,9 @@ lse_merge_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_m,
     // the next kernel of the stream may start its set-up now: it waits for
     // this grid before it reads or writes what this grid touches
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // the lengths are the caller's (no kernel of this library writes them), so
-    // they are read while the decode may still run; its partition states only
-    // after griddepcontrol.wait
+    // the lengths are the decode's, which has waited for any kernel that writes
+    // them before it let this one start: they are read while it may still run,
+    // its partition states only after griddepcontrol.wait
     const int row = blockIdx.x;   // s * n_q_heads + qh
     const int s = row / n_q_heads;
     const int L = min(max(__ldg(lens + s), 0), cap);
@@ -155,7 +155,7 @@ lse_merge_rows_kernel(const float *__restrict__ ws_o, const float *__restrict__ 
     const int row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
-    // the length first (the caller's, read while the decode may still run),
+    // the length first (as above, read while the decode may still run),
     // the partition states only after griddepcontrol.wait
     const int s = row / n_q_heads;
     const int L = min(max(__ldg(lens + s), 0), cap);
@@ -288,9 +288,9 @@ lse_merge_pieces_kernel(const float *__restrict__ ws_o, const float *__restrict_
     const int warps = blockDim.x >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Tiles before this sequence, and in total (exact integer sums). The
-    // lengths are the caller's (no kernel of this library writes them), so
-    // this runs while the decode may still be running; the pieces are read
-    // only after griddepcontrol.wait.
+    // lengths are the decode's, which has waited for any kernel that writes
+    // them before it let this one start, so this runs while the decode may
+    // still be running; the pieces are read only after griddepcontrol.wait.
     __shared__ unsigned long long sums[2];
     if (threadIdx.x == 0) sums[0] = sums[1] = 0ull;
     const int L = min(max(__ldg(lens + s), 0), cap);

@@ -32,6 +32,7 @@ struct PrefillParams {
     int block_size;
     int log2_block;
     int max_blocks;
+    int late_inputs;             // 1: tables, lengths and offsets may be the kernel's just ahead
     // tcgen05 kernel, key split (key_parts >= 2): one CTA per SM, each taking
     // an equal contiguous range of the call's key tiles (all items' end to
     // end; no item in more than key_parts ranges). An item cut by a range

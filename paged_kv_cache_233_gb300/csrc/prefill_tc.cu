@@ -451,8 +451,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const int B = p.block_size;
     const int g = p.group;
     const int all_items = p.num_seqs * tiles * p.n_kv_heads;
-    // (with 4-bit pools the lengths and offsets may be the kernel's before this one)
-    if (kQ4) grid_dependency_wait();
+    // (the tables, lengths and offsets may be the kernel's before this one)
+    if (kQ4 || p.late_inputs) grid_dependency_wait();
 
     if (threadIdx.x == 0) {
         for (int k = 0; k < kTcStages; ++k) {
@@ -484,8 +484,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         tmem_relinquish();
     }
     // sequences ranked by decreasing context length (ties by index), when some
-    // CTA gets more than one item; the lengths are the caller's, read before
-    // any grid dependency
+    // CTA gets more than one item
     // (whole items), or the key split's plan: the item order's shared address
     uint32_t order = 0;    // 0: the sequences' own order
     if (!kSplit && p.num_seqs > 1 && p.num_seqs <= kMaxRankedSeqs && all_items > int(gridDim.x)) {

@@ -174,3 +174,42 @@ def test_outputs_as_the_next_queries(first, second, part, graph):
 
     same_as_apart([lambda: call(first, q, xs[0], ws[0]), lambda: call(second, xs[0], xs[1], ws[1]),
                    lambda: call(second, xs[1], xs[2], ws[2])], reset, xs, graph)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("part", [0, 64, pk.PARTITION_BALANCED])
+def test_16_bit_calls_right_behind_the_tables(part, graph):
+    """Tables, lengths and token lists in place, then the 16-bit append, decode and
+    prefill that read them, two steps in a row."""
+    S, heads, n = 300, 8, 95
+    c = Cache(S, n, heads)
+    more = S * 3
+    tables = torch.full((S, 12), -1, dtype=torch.int32, device="cuda")
+    tables[:, :c.tables.shape[1]] = c.tables
+    kc, vc = (torch.cat([x, torch.zeros(more, *x.shape[1:], dtype=F16, device="cuda")]) for x in (c.kc, c.vc))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    stack = torch.arange(c.blocks, c.blocks + more, **i32)
+    new, T = (torch.arange(S, **i32) % 4 + 1), int((torch.arange(S) % 4 + 1).sum())
+    t, lens, count = tables.clone(), c.lens.clone(), torch.tensor([more], **i32)
+    start, seq, pos = torch.empty(S + 1, **i32), torch.empty(T, **i32), torch.empty(T, **i32)
+    k, v = queries(T, heads, c.dim, 5), queries(T, heads, c.dim, 6)
+    q, qp = queries(S, heads, c.dim, 7), queries(T, heads, c.dim, 8)
+    outs = [torch.empty_like(q) for _ in range(2)]
+    rows = [torch.empty_like(qp) for _ in range(2)]
+    pools = [torch.empty_like(x) for x in (kc, vc)]
+    ws = pk.new_workspace(q, t, c.block, part)
+
+    def reset():
+        t.copy_(tables), lens.copy_(c.lens), count.fill_(more)
+        pools[0].copy_(kc), pools[1].copy_(vc)
+        for x in (start, seq, pos, *outs, *rows):
+            x.fill_(-1)
+
+    def step(i):
+        return [lambda: pk.paged_kv_build_tables(new, lens, t, stack, count, c.block, c.blocks + more, start, seq, pos),
+                lambda: pk.paged_kv_append_tokens(k, v, t, seq, pos, *pools),
+                lambda: pk.paged_attention_decode(q, *pools, t, lens, 0.09, outs[i], part, ws),
+                lambda: pk.paged_attention_prefill(qp, *pools, t, start, lens, 0.09, rows[i], 4)]
+
+    same_as_apart(step(0) + step(1), reset, [t, lens, count, start, seq, pos, *pools, *outs, *rows], graph)
+    assert lens.tolist() == (c.lens + 2 * new).tolist()
