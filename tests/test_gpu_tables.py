@@ -214,3 +214,51 @@ def test_the_16_bit_path_right_behind():
         got = out[i].cpu().double()
         assert bool(((got - want).abs() <= want * 2.0 ** -9).all()), f"step {i}"
     assert ctx.tolist() == (lens + steps).tolist()
+
+
+@pytest.mark.parametrize("S,chunk", [(130, 60), (2000, 60), (4096, 9)])
+@pytest.mark.parametrize("short", ["blocks", "tokens", "both", "none left"])
+def test_requests_wait_when_it_runs_short_in_place(S, chunk, short):
+    """The lengths and the count updated in place by several blocks of threads."""
+    new, ctx, tables, free, blocks = make(S, 16, S + 1, 200, chunk)
+    count = {"blocks": len(free) // 2, "tokens": len(free), "both": len(free) // 3, "none left": 0}[short]
+    cap = int(new.sum()) // 2 if short in ("tokens", "both") else int(new.sum())
+    want = walk(new, ctx, tables, free, count, 16, cap)
+    same(call(new, ctx, tables, free, count, 16, blocks, cap, in_place=True), want)
+    assert pk.device_errors() == 0
+    assert 0 <= want[3][-1] < new.sum()
+
+
+@pytest.mark.parametrize("S", [6, 1500])
+def test_bad_lengths_and_counts_in_place(S):
+    new, ctx, tables, free, blocks = make(S, 16, 2, 50, 40)
+    new[1], ctx[2], new[4] = -1, -5, 2 ** 31 - 1
+    cap = 80 if S == 6 else 20000
+    same(call(new, ctx, tables, free, len(free), 16, blocks, cap, in_place=True),
+         walk(new, ctx, tables, free, len(free), 16, cap))
+    assert pk.device_errors() == 4 | 8            # CONTEXT_LEN, POSITION
+    new[:], ctx = np.maximum(new, 0) % 41, np.maximum(ctx, 0)
+    # a count that is no count is taken as its nearest
+    for count, taken in ((len(free) + 9, len(free)), (-7, 0)):
+        same(call(new, ctx, tables, free, count, 16, blocks, cap, in_place=True),
+             walk(new, ctx, tables, free, taken, 16, cap))
+        assert pk.device_errors() == 8
+
+
+@pytest.mark.parametrize("lengths", [False, True])
+@pytest.mark.parametrize("short", [False, True])
+@pytest.mark.parametrize("S", [40, 1800])
+def test_one_of_the_two_in_place(S, short, lengths):
+    """The lengths alone, or the count alone, updated in place."""
+    new, ctx, tables, free, blocks = make(S, 16, 5, 90, 40)
+    count, cap = len(free) // (2 if short else 1), int(new.sum())
+    t = lambda x: torch.tensor(np.asarray(x, np.int32)).cuda()  # noqa: E731
+    a, c, tab, n = t(new), t(ctx), t(tables), t([count])
+    starts, seq, pos = t([-9] * (S + 1)), t([-9] * cap), t([-9] * cap)
+    slots = torch.full((cap,), -9, dtype=torch.int64).cuda()
+    c_out, n_out = (c, t([-9])) if lengths else (t([-9] * S), n)
+    pk.paged_kv_build_tables(a, c, tab, t(free), n, 16, blocks, starts, seq, pos, slots, c_out, n_out)
+    got = (tab.cpu().numpy(), c_out.tolist(), int(n_out), starts.tolist(), seq.tolist(), pos.tolist(), slots.tolist())
+    same(got, walk(new, ctx, tables, free, count, 16, cap))
+    assert c.tolist() == (got[1] if lengths else ctx.tolist()) and int(n) == (count if lengths else got[2])
+    assert pk.device_errors() == 0
