@@ -849,7 +849,8 @@ __global__ void __launch_bounds__(q4_merge_threads<kWarps>()) merge_q4_kernel(co
     if (cut.x < 0) return;
     // no cut at all, where a CTA of the decode stopped before it wrote one (a test
     // of its own: in one with the other it costs the merge 1 us)
-    const bool bad = cut.x >= groups * p.num_seqs || cut.y < 0 || cut.z >= p.decode_ctas || (cut.w & ~1) != 0;
+    const bool bad = cut.x >= groups * p.num_seqs || cut.y < 0 || cut.z < cut.y || cut.z >= p.decode_ctas ||
+                     (cut.w & ~1) != 0;
     if (bad) return;
     const int s = cut.x / groups, hg = cut.x - s * groups;
     const int c0 = cut.y, np = cut.z - c0 + 1, slot0 = cut.w;
