@@ -170,6 +170,13 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _on(stream):
+    """A context in which torch works on the call's stream."""
+    if stream is not None and not isinstance(stream, torch.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _dev(t, name, dtype=None):
     """The device address of a contiguous CUDA tensor (an int), checked."""
     if not isinstance(t, torch.Tensor):
@@ -314,6 +321,14 @@ def paged_kv_swap_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
     _check(st, "paged_kv_swap_blocks")
 
 
+def _longest_chunk(query_start, stream):
+    """The longest chunk that query_start delimits, read on the call's stream."""
+    if query_start.numel() < 2:
+        return 0
+    with _on(stream):
+        return int((query_start[1:] - query_start[:-1]).max().item())
+
+
 def paged_attention_prefill(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
                             out, max_query_len=None, stream=None, workspace=None, key_parts=1):
     """Chunked-prefill attention: q/out [num_tokens][Hq][D] hold every sequence's
@@ -325,7 +340,7 @@ def paged_attention_prefill(q, k_cache, v_cache, block_tables, query_start, cont
     equal ranges over the SMs, no item in more than key_parts of them (0: when
     the items leave SMs idle and the workspace holds the split), and a merge
     kernel combines the pieces' states; the workspace (see prefill_workspace)
-    is taken from torch's allocator when none is given."""
+    is taken from torch's allocator, on the call's stream, when none is given."""
     if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
         raise PagedKVError("q and out must be [num_tokens][n_q_heads][head_dim] of one type")
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != q.dtype:
@@ -334,7 +349,7 @@ def paged_attention_prefill(q, k_cache, v_cache, block_tables, query_start, cont
     if query_start.shape[0] != S + 1 or block_tables.shape[0] != S:
         raise PagedKVError("query_start must hold num_seqs + 1 offsets, block_tables num_seqs rows")
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
+        max_query_len = _longest_chunk(query_start, stream)
     NB, B, Hkv, D = k_cache.shape
     args = (_dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _dev(block_tables, "block_tables", torch.int32), _dev(query_start, "query_start", torch.int32),
@@ -345,7 +360,8 @@ def paged_attention_prefill(q, k_cache, v_cache, block_tables, query_start, cont
         _check(st, "paged_attention_prefill")
         return
     if workspace is None:
-        workspace = prefill_workspace(q)
+        with _on(stream):
+            workspace = prefill_workspace(q)
     ws = _dev(workspace, "workspace")
     nbytes = workspace.numel() * workspace.element_size()
     st = load().paged_attention_prefill_split(*args, int(key_parts), ws, nbytes, _stream(stream))
@@ -509,11 +525,12 @@ def paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, c
     """paged_attention_prefill over 4-bit pools, with its arguments; key_parts 0
     lets the call decide from the items and the tables' width. With key_parts
     other than 1 the workspace (see prefill_workspace) is taken from torch's
-    allocator when none is given."""
+    allocator, on the call's stream, when none is given."""
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if context_lens.numel() else 0
+        max_query_len = _longest_chunk(query_start, stream)
     if workspace is None and key_parts != 1:
-        workspace = prefill_workspace(q)
+        with _on(stream):
+            workspace = prefill_workspace(q)
     (_fast or _binding()).prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
                                      out, max_query_len, workspace, key_parts, stream)
 

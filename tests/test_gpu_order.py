@@ -213,3 +213,61 @@ def test_16_bit_calls_right_behind_the_tables(part, graph):
 
     same_as_apart(step(0) + step(1), reset, [t, lens, count, start, seq, pos, *pools, *outs, *rows], graph)
     assert lens.tolist() == (c.lens + 2 * new).tolist()
+
+
+def chunks(c, S, rows, heads):
+    """S chunks of `rows` queries at the ends of their sequences, and their outputs."""
+    q = queries(S * rows, heads, c.dim, 3)
+    starts = (torch.arange(S + 1) * rows).to(torch.int32).cuda()
+    return q, torch.zeros_like(q), starts
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_prefill_takes_its_workspace_on_the_calls_stream(bits, monkeypatch):
+    """The workspace a split call allocates for itself goes back to the stream that
+    the call runs on: memory given out next on another stream is not it."""
+    c = Cache(2, 3000, 4)
+    q, out, starts = chunks(c, 2, 40, 8)
+    f = pk.paged_attention_prefill_q4 if bits == 4 else pk.paged_attention_prefill
+    pools = (c.k4, c.v4) if bits == 4 else (c.kc, c.vc)
+    want = torch.zeros_like(q)
+    f(q, *pools, c.tables, starts, c.lens, 0.09, want, 40, workspace=pk.prefill_workspace(q), key_parts=8)
+    torch.cuda.synchronize()
+    taken = []
+    make = pk.prefill_workspace
+
+    def recording(q):
+        w = make(q)
+        taken.append((w.data_ptr(), w.numel()))
+        return w
+
+    monkeypatch.setattr(pk, "prefill_workspace", recording)
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        f(q, *pools, c.tables, starts, c.lens, 0.09, out, 40, stream=side, key_parts=8)
+        at, size = taken[-1]
+        mine = torch.empty(size, dtype=torch.uint8, device="cuda")
+        assert mine.data_ptr() + size <= at or at + size <= mine.data_ptr()
+        del mine
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_prefill_reads_the_longest_chunk_on_the_calls_stream(bits):
+    """query_start written on the call's own stream, which is behind."""
+    c = Cache(3, 200, 4)
+    q, out, starts = chunks(c, 3, 50, 8)
+    f = pk.paged_attention_prefill_q4 if bits == 4 else pk.paged_attention_prefill
+    pools = (c.k4, c.v4) if bits == 4 else (c.kc, c.vc)
+    want = torch.zeros_like(q)
+    f(q, *pools, c.tables, starts, c.lens, 0.09, want, 50)
+    late = torch.zeros_like(starts)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(starts)
+    f(q, *pools, c.tables, late, c.lens, 0.09, out, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and bool((want != 0).any())
