@@ -265,6 +265,8 @@ def _block_shape(pool):
     """(num_blocks, block_size, heads, head_dim, dtype code) that give a pool's
     bytes per block; a 4-bit pool's bytes count as pairs."""
     if pool.dtype is torch.uint8:
+        if pool.shape[2] not in (8, 16, 32) or pool.shape[3] not in (40, 80):
+            raise PagedKVError("a uint8 pool must be a 4-bit one: [NB][Hkv][8, 16 or 32][40 or 80]")
         return pool.shape[0], pool.shape[2], pool.shape[1], pool.shape[3] // 2, DTYPE_CODES[torch.float16]
     return (*pool.shape, _code(pool))
 

@@ -156,3 +156,12 @@ def test_definition_of_flat_and_broken_groups():
     y = q4.stands_for(c, s, m)
     assert float(s[0, 0, 0]) == 0 and bool((c[0, 0, 0] == 8).all()) and bool((y[0, 0, :32] == 3.25).all())
     assert bool(y[0, 0, 32:].isnan().all())
+
+
+@pytest.mark.parametrize("shape", [(4, 16, 2, 64), (4, 2, 16, 41), (4, 2, 16, 20), (4, 2, 1, 40), (4, 2, 16, 160)])
+def test_uint8_pools_that_are_no_4_bit_pools_are_refused(lib, shape):
+    pool, pairs = torch.zeros(shape, dtype=torch.uint8), torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(pk.PagedKVError, match="4-bit"):
+        pk.paged_kv_copy_blocks(pool, pool, pairs)
+    with pytest.raises(pk.PagedKVError, match="4-bit"):
+        pk.paged_kv_swap_blocks(pool, pool, pool, pool, pairs)
