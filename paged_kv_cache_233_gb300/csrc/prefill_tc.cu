@@ -1013,8 +1013,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (!__all_sync(kAll, got)) return false;
             tc_fence_after_sync();
             // the row normalised into `out`, or (key split) its part's O as it is
-            const float inv = prev_l > 0.f ? 1.f / prev_l : 0.f;
-            const bool keep = prev_row && (!split || prev_l > 0.f);
+            // (a row without keys has a sum of 0; a NaN sum goes through)
+            const float inv = prev_l != 0.f ? 1.f / prev_l : 0.f;
+            const bool keep = prev_row && (!split || prev_l != 0.f);
             uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.out) + prev_qrow * D);
             float4 *wo = reinterpret_cast<float4 *>(p.ws_o + wrow * D);
 #pragma unroll
@@ -1174,9 +1175,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 // takes it for calls of at most SMs / 9 items, where every item may (a call
 // of more items with one long one among them takes 8 at a time, in more round
 // trips).
-// A piece that held none of the row's keys left m_q = -inf and is skipped
-// (its O was not written). An item not split, or of a flagged sequence, is
-// left as the kernel left it.
+// A piece that held none of the row's keys left l_q = 0 and is skipped
+// (its O was not written); one whose scores were NaN makes the row NaN. An item
+// not split, or of a flagged sequence, is left as the kernel left it.
 constexpr int kMergeRowsPerCta = 4;
 static_assert(kMaxSplitParts <= 32, "a lane per piece");
 
@@ -1224,7 +1225,7 @@ paged_prefill_merge_kernel(const PrefillParams p, int tiles) {
     float M = mp;
 #pragma unroll
     for (int mask = 16; mask >= 1; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, mask));
-    const float w = mp > -INFINITY ? exp2f(mp - M) : 0.f;
+    const float w = lp != 0.f ? exp2f(mp - M) : 0.f;   // (NaN scores: m = -inf, l = NaN)
     float den = w * lp;
 #pragma unroll
     for (int mask = 16; mask >= 1; mask >>= 1) den += __shfl_xor_sync(kAll, den, mask);
@@ -1241,7 +1242,7 @@ paged_prefill_merge_kernel(const PrefillParams p, int tiles) {
             for (int e = 0; e < E; ++e) acc[e] = use ? fmaf(wq, x[q][e], acc[e]) : acc[e];
         }
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den != 0.f ? 1.f / den : 0.f;
     T *dst = reinterpret_cast<T *>(p.out) + qrow * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)

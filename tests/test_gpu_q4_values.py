@@ -118,3 +118,46 @@ def test_nan_reaches_the_outputs(what, heads, dtype):
         assert bool(got[sure].isnan().all()), f"part {part}"
         assert bool(torch.isfinite(got[~bad]).all()), f"part {part}"
     assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("what", ["query", "key", "keys"])
+@pytest.mark.parametrize("parts", [1, 8])
+def test_nan_reaches_the_outputs_of_a_prefill(what, parts, bits):
+    """The rows that attend to a NaN are NaN, split over the keys or not, and the
+    other rows are what they are without it, whatever the workspace held."""
+    n, rows_n, heads, group, dim, block = 6000, 40, 2, 2, 64, 16
+    k, v = rows((n, heads, dim), 2).to(F16), rows((n, heads, dim), 3).to(F16)
+    q = rows((rows_n, heads * group, dim), 1).to(F16)
+    clean = torch.ones(rows_n, heads * group, dtype=torch.bool)
+    starts, lens = torch.tensor([0, rows_n], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda()
+
+    def run(fill):
+        if bits == 4:
+            kc, vc, tables = pools(k, v, block)
+            f = pk.paged_attention_prefill_q4
+        else:
+            tables, nb = q4.tables_for([n], block, 1)
+            at = q4.sequence_slots(tables, 0, n, block)
+            kc, vc = (torch.zeros(nb * block, heads, dim, dtype=F16).index_copy_(0, at, x).view(nb, block, heads, dim)
+                      for x in (k, v))
+            f = pk.paged_attention_prefill
+        out = torch.full_like(q, 7.0).cuda()
+        ws = pk.prefill_workspace(q.cuda())
+        ws.fill_(fill)
+        f(q.cuda(), kc.cuda(), vc.cuda(), tables.cuda(), starts, lens, 0.125, out, rows_n, workspace=ws, key_parts=parts)
+        return out.cpu()
+
+    want = run(0)
+    if what == "query":
+        q[7, 3, 5] = float("nan")
+        clean[7, 3] = False
+    else:
+        at = slice(n - 20, n - 19) if what == "key" else slice(1500, 3500)     # (3500: several whole pieces)
+        k[at, 1, 40] = float("nan")
+        clean[20 if what == "key" else 0:, group:] = False
+    for fill in (0, 255):
+        got = run(fill)
+        assert bool(got[~clean].isnan().all())
+        assert torch.equal(got[clean], want[clean])
+    assert pk.device_errors() == 0
