@@ -355,10 +355,10 @@ struct Q4Consumer {
     // bits of this lane's token's largest scale.
     __device__ __forceinline__ void move(const float (&sc)[4][2], uint32_t most, int nvalid) {
         // (bits of values >= 0 order as the values; scales count as at least the
-        // smallest that a bound of type T can hold: 2^-16 in fp16, whose bound
-        // 2^(e + 2) is then a normal number, and 2^-80 in bf16, so that sums of p
-        // stay finite)
-        constexpr float kLeast = Elem<T>::kBf16 ? 0x1p-80f : 0x1p-16f;
+        // smallest that a bound can hold: 2^-16 in fp16, whose bound 2^(e + 2) is
+        // then a normal number, and 2^-32 in bf16: sums of p times middles of up to
+        // 2^64 then stay finite, and products of p and scales of 2^-49 normal)
+        constexpr float kLeast = Elem<T>::kBf16 ? 0x1p-32f : 0x1p-16f;
         const float top = fmaxf(scale_of<T>(__reduce_max_sync(kQ4All, most)), kLeast);
         const int e = int(__float_as_uint(top) >> 23) - 126;
 #pragma unroll

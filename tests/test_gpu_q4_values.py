@@ -161,3 +161,18 @@ def test_nan_reaches_the_outputs_of_a_prefill(what, parts, bits):
         assert bool(got[~clean].isnan().all())
         assert torch.equal(got[clean], want[clean])
     assert pk.device_errors() == 0
+
+
+# ------------------------------------------------- values far larger than others
+@pytest.mark.parametrize("heads,dim,block", [(4, 128, 16), (2, 64, 8)])
+@pytest.mark.parametrize("dtype,size", [(F16, 6e4), (F16, -1.0), (BF16, 1e10), (BF16, -1e15), (BF16, 1e19), (BF16, 1e-10)])
+def test_flat_values_of_any_size(dtype, size, heads, dim, block):
+    """Groups without spread, whose middles are all there is, alone and before and
+    after tiles of other sizes."""
+    q, k = rows((1, heads * 2, dim), 1).to(dtype), rows((150, heads, dim), 2).to(dtype)
+    v = torch.full((150, heads, dim), size)
+    check(q, k, v.to(dtype), block, dim ** -0.5, "flat")
+    v[40:80] = rows((40, heads, dim), 3) * abs(size) * 0.25
+    check(q, k, v.to(dtype), block, dim ** -0.5, "some flat")
+    v[:40], v[120:] = 0, size / 1000
+    check(q, k, v.to(dtype), block, dim ** -0.5, "some zero")
