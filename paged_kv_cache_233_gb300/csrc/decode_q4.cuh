@@ -33,9 +33,13 @@
 // Softmax reference. p = 2^(z - ref), and ref moves only when it must: when a
 // p or a scale passes the bounds set with ref, whose product is 2^14 (fp16
 // ends at 2^16). Then, with 2^e above the tile's largest scale, the bounds
-// become 2^(12 - e) for p and 2^(e + 2) for scales, ref becomes the tile's
-// largest score plus e - 4, if that is more, so that p * s sits in the upper
-// part of fp16's range whatever V's size, and the sums are rescaled.
+// become 2^(12 - e) for p and 2^(e + 2) for scales, ref becomes the largest
+// z_t + e_t - 4 of the tile's tokens, 2^e_t above token t's largest scale, if that
+// is more, so that the largest p * s sits in the upper part of fp16's range
+// whatever V's size, and the sums are rescaled. (With the largest z and the
+// largest e of the tile, which can be two tokens', one token of little weight
+// whose values were 10^6 times the others' took the others' products below
+// fp16's range: 2% off, 10^8 times 24%.)
 // Everything is relative to ref, so no result depends on when it moved beyond
 // rounding.
 //
@@ -354,21 +358,28 @@ struct Q4Consumer {
     // Move the reference and the bounds: sc the tile's sums of products, most the
     // bits of this lane's token's largest scale.
     __device__ __forceinline__ void move(const float (&sc)[4][2], uint32_t most, int nvalid) {
-        // (bits of values >= 0 order as the values; scales count as at least the
-        // smallest that a bound can hold: 2^-16 in fp16, whose bound 2^(e + 2) is
-        // then a normal number, and 2^-32 in bf16: sums of p times middles of up to
-        // 2^64 then stay finite, and products of p and scales of 2^-49 normal)
+        // 2^e above the scale. It counts as at least the smallest that a bound can
+        // hold, 2^-16 in fp16, whose bound 2^(e + 2) is then a normal number, and
+        // 2^-32 in bf16: sums of p times middles of up to 2^64 then stay finite, and
+        // products of p and scales of 2^-49 normal numbers. (NaN or infinite scales,
+        // whose outputs are NaN, leave it at that.)
         constexpr float kLeast = Elem<T>::kBf16 ? 0x1p-32f : 0x1p-16f;
-        const float top = fmaxf(scale_of<T>(__reduce_max_sync(kQ4All, most)), kLeast);
-        const int e = int(__float_as_uint(top) >> 23) - 126;
+        const float s = scale_of<T>(most);
+        const int mine = int(__float_as_uint(s < INFINITY ? fmaxf(s, kLeast) : kLeast) >> 23) - 126;
+        const int e = __reduce_max_sync(kQ4All, mine);
+        float top[2] = {-INFINITY, -INFINITY};   // the largest z_t + e_t - 4
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float up = float(__shfl_sync(kQ4All, mine, 8 * u + grp) - 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (8 * u + grp < nvalid) top[h] = fmaxf(top[h], fmaf(sc[u][h], kh[h], up));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float zm = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) zm = fmaxf(zm, 8 * u + grp < nvalid ? sc[u][h] * kh[h] : -INFINITY);
-#pragma unroll
-            for (int mask = 4; mask <= 16; mask <<= 1) zm = fmaxf(zm, __shfl_xor_sync(kQ4All, zm, mask));
-            const float nref = fmaxf(ref[h], zm + float(e - 4));
+            for (int mask = 4; mask <= 16; mask <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(kQ4All, top[h], mask));
+            const float nref = fmaxf(ref[h], top[h]);
             const float alpha = ref[h] == -INFINITY ? 0.f : fast_exp2(ref[h] - nref);
             ref[h] = nref;
             l[h] *= alpha;

@@ -176,3 +176,19 @@ def test_flat_values_of_any_size(dtype, size, heads, dim, block):
     check(q, k, v.to(dtype), block, dim ** -0.5, "some flat")
     v[:40], v[120:] = 0, size / 1000
     check(q, k, v.to(dtype), block, dim ** -0.5, "some zero")
+
+
+@pytest.mark.parametrize("heads,dim,block", [(4, 128, 16), (2, 64, 8)])
+@pytest.mark.parametrize("dtype,factor,base", [(F16, 1e4, 1.0), (F16, 1e6, 1e-2), (BF16, 1e4, 1.0), (BF16, 1e7, 1.0),
+                                               (BF16, 1e10, 1.0)])
+@pytest.mark.parametrize("at", [5, 70, 299])
+def test_a_token_of_large_values_and_no_weight(dtype, factor, base, at, heads, dim, block):
+    """One token whose values are `factor` times the others', with a weight of about e^-60."""
+    n, scale = 300, 0.5
+    q = rows((1, heads * 2, dim), 1)
+    q[:, 1::2] = q[:, ::2]
+    k = rows((n, heads, dim), 2) * 0.3
+    k[at] = -q[0, ::2] * 60 / scale / (q[0, ::2] ** 2).sum(-1, keepdim=True)
+    v = rows((n, heads, dim), 3) * base
+    v[at] *= factor
+    check(q.to(dtype), k.to(dtype), v.to(dtype), block, scale, "outlier")
