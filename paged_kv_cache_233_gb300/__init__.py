@@ -123,7 +123,8 @@ def load():
     lib.paged_kv_gather_q4.argtypes = [vp] * 5 + [i32] * 6 + [vp]
     lib.paged_attention_decode_q4.argtypes = lib.paged_attention_decode.argtypes
     lib.paged_attention_prefill_q4.argtypes = lib.paged_attention_prefill_split.argtypes
-    for name in EXPORTS[-5:]:
+    for name in ("paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
+                 "paged_attention_decode_q4", "paged_attention_prefill_q4"):
         getattr(lib, name).restype = i32
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz

@@ -192,3 +192,65 @@ def test_a_token_of_large_values_and_no_weight(dtype, factor, base, at, heads, d
     v = rows((n, heads, dim), 3) * base
     v[at] *= factor
     check(q.to(dtype), k.to(dtype), v.to(dtype), block, scale, "outlier")
+
+
+# ------------------------------------------------------------ far middles, repeats
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads,dim,block", [(4, 128, 16), (2, 64, 8)])
+@pytest.mark.parametrize("middle,mean", [(20.0, 1.0), (-100.0, 1.0), (20.0, -6.0)])
+def test_keys_far_off_zero_under_queries_of_one_sign(middle, mean, heads, dim, block, dtype):
+    """A score's part in the groups' middles is far larger than the scores' spread. A
+    group's sum of q is held in two parts of the type: off by half a step of the
+    second, h^2 of the sum, times 72 s + |m|; its products and sums are fp32 ones."""
+    n, group = 400, 3
+    q = (rows((1, heads * group, dim), 1) + mean).to(dtype)
+    k = (rows((n, heads, dim), 2) + middle * torch.sign(rows((heads, dim // 32), 4)).repeat_interleave(32, 1)).to(dtype)
+    v = rows((n, heads, dim), 3).to(dtype)
+    kc, vc, tables = pools(k, v, block)
+    scale = dim ** -0.5
+    ref = q4.attention(q, (kc, vc), tables, [0, 1], [n], scale, dim, dtype)
+    _, s, m, _ = q4.quantise(k)
+    far = (72 * s.double() + m.double().abs()).amax(0)[..., 0]                       # [heads][groups]
+    sums = q[0].double().unflatten(1, (-1, 32)).sum(-1).abs().unflatten(0, (heads, group))
+    wide = q[0].double().unflatten(1, (-1, 32)).abs().sum(-1).unflatten(0, (heads, group))
+    off = (q4.HALF_STEP[dtype] ** 2 * sums + 8 * 2.0 ** -24 * wide) * far[:, None]
+    worst = scale * float(off.sum(-1).max())
+    for part in SPLITS:
+        got = decode(q, kc, vc, tables, [n], scale, part).double()
+        # scores off by `worst` change a weight by a factor of up to e^(2 worst); beside the roundings
+        rel = float((got - ref).norm() / ref.norm())
+        assert rel <= 2 * q4.HALF_STEP[dtype] + 2.2 * worst, f"part {part}: {rel:.2e}, scores {worst:.2e}"
+    assert worst < 0.25 and pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_every_call_repeats_bit_for_bit(dtype):
+    heads, group, dim, block = 8, 4, 128, 16
+    lens = [3000, 17, 900, 64, 2500, 1]
+    kc, vc, tables = (x.cuda() for x in q4.filled(lens, heads, block, dim, dtype, 6))
+    L = torch.tensor(lens, dtype=torch.int32).cuda()
+    q = rows((len(lens), heads * group, dim), 1).to(dtype).cuda()
+    chunk = [min(n, 70) for n in lens]
+    starts = torch.tensor([0] + chunk).cumsum(0).to(torch.int32).cuda()
+    qp = rows((sum(chunk), heads * group, dim), 2).to(dtype).cuda()
+    x = rows((500, heads, dim), 3).to(dtype).cuda()
+    slots = torch.randperm(kc.shape[0] * block, generator=torch.Generator().manual_seed(1))[:500].cuda()
+
+    def run():
+        out = []
+        for part in SPLITS:
+            y = torch.empty_like(q)
+            pk.paged_attention_decode_q4(q, kc, vc, tables, L, 0.09, y, part, pk.new_workspace(q, tables, block, part))
+            out.append(y)
+        for parts in (1, 0, 7):
+            y = torch.empty_like(qp)
+            pk.paged_attention_prefill_q4(qp, kc, vc, tables, starts, L, 0.09, y, 70, key_parts=parts)
+            out.append(y)
+        a, b = kc.clone(), vc.clone()
+        pk.paged_kv_append_q4(x, x, slots, a, b)
+        return [*out, a, b]
+
+    first = run()
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(first, run()))
+    assert pk.device_errors() == 0
