@@ -537,14 +537,28 @@ int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *
 /*
  * paged_attention_decode_q4 -- paged_attention_decode over 4-bit pools.
  *
- * The same attention with K_s[i] and V_s[i] the rows that the codes stand for;
- * scores, softmax and the output sums are fp32, out is rounded once. Arguments,
- * limits, splits and workspace (paged_attention_workspace_bytes) as
+ * The same attention with K_s[i] and V_s[i] the rows that the codes stand for.
+ * Arguments, limits, splits and workspace (paged_attention_workspace_bytes) as
  * paged_attention_decode's, except that partition_tokens > 0 must be a
  * multiple of 32 and a balanced split's shares are of 32-token tiles and a fixed
- * cost per sequence and head. No q, K or V is expected to hold an infinity or a NaN: a
- * sequence whose rows do gets NaN outputs; what lies in a block past a
- * sequence's context never matters.
+ * cost per sequence and head.
+ *
+ * Scores, softmax statistics and output sums are fp32 and out is rounded once.
+ * Held in fewer bits on the way, each of them rounded once:
+ *   - q in fp16, scaled by a power of two per row: exact but for elements below
+ *     2^-17 (bf16: 2^-20) of the row's largest;
+ *   - the sum of a group's 32 channels of q in two parts of dtype (off by
+ *     2^-22 of it, bf16: 2^-16);
+ *   - a probability times a scale of V in fp16, relative to the largest such
+ *     product so far: what is below 2^-18 of that loses bits, for instance
+ *     channels whose values are 10^6 times smaller than others of their tokens;
+ *   - dtype PAGEDKV_BF16, head_dim 128: a probability in bf16 where it
+ *     multiplies a middle of V.
+ * fp16 caches may hold any values; bf16 caches values of V of 2^64 at most, and
+ * scales of V below 2^-49 lose bits. A NaN or an infinity in q or K makes all
+ * outputs NaN of the query heads that attend to it, one in V those of its group
+ * of channels (the other channels of these heads may be NaN or infinite too).
+ * What lies in a block past a sequence's context never matters.
  */
 int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_cache,
                               const int32_t *block_tables, const int32_t *context_lens, float scale,
@@ -558,13 +572,17 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
  *
  * The same causal attention of each sequence's chunk of query rows, with K and
  * V the rows that the codes stand for, each channel rounded once to dtype, as
- * paged_kv_gather_q4 reads them. Arguments, limits and workspace as
+ * paged_kv_gather_q4 reads them, and the probabilities rounded to dtype; scores,
+ * softmax statistics and output sums are fp32. Arguments, limits and workspace as
  * paged_attention_prefill_split's, and 1 <= key_parts means the same; a split's
  * ranges hold at least 6 key tiles here, not 16. key_parts 0 splits when the
  * workspace holds it and the items (counted from max_query_len) and the tables'
  * width say that the SMs' even share of the key tiles saves more than the extra
  * pieces and the merge cost: with few items, or with one sequence whose items
- * leave SMs without any in their last round.
+ * leave SMs without any in their last round. The width stands for the contexts,
+ * which the host does not see: with tables several times wider than the contexts
+ * of a call, name key_parts (1, or 32) where speed counts; results are right
+ * either way.
  */
 int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v_cache,
                                const int32_t *block_tables, const int32_t *query_start,

@@ -44,13 +44,20 @@ bool finite(float x) { return x == x && x != INFINITY && x != -INFINITY; }
 // pieces and a merge, which come to about 10 tiles and 0.2 per item. Items of
 // several sequences count as one round: their lengths differ, which the host
 // does not see, and whole items taken longest first then fill the SMs.
-// Measured (us, whole / shared; 8 kv heads of 128, 32 query heads, 152 SMs):
-//   one sequence      rows 33, cached 1000: 25 / 19; 33, 6001: 114 / 24;
-//                     1216, 8192 (152 items): 167 / 192; 1280, 8192 (160):
-//                     294 / 200; 2048, 2048 (256): 112 / 142; 2048, 16384: 599 / 542
-//   4 of 64 rows      up to 500 cached: 17 / 19; 4000: 78 / 43
-//   20 of 64 rows     up to 1000 cached (160 items): 25 / 59; 4000: 76 / 128
-// and the same choices with heads of 64.
+// `tiles` is the tables' width, not the contexts': exact where they are as wide.
+// Measured (us, whole / shared; 8 kv heads, 32 query heads, bf16, 152 SMs; tables
+// as wide as the longest context; the rule takes the smaller one each time):
+//                                            heads of 128     heads of 64
+//   one sequence  rows 33, cached 1000          25 / 19          21 / 15
+//                 33, 6001                     111 / 25          96 / 18
+//                 1216, 8192 (152 items)       163 / 188        138 / 151
+//                 1280, 8192 (160)             288 / 196        245 / 159
+//                 2048, 2048 (256)             110 / 140         92 / 112
+//                 2048, 16384                  585 / 524        503 / 432
+//   4 of 64 rows  up to 500 cached              17 / 21          14 / 17
+//                 up to 4000                    47 / 29          39 / 22
+//   20 of 64 rows up to 1000 (160 items)        26 / 56          21 / 43
+//                 up to 4000                    76 / 103         63 / 74
 bool split_pays(long long items, long long tiles, int seqs, int sms) {
     const long long rounds = seqs > 1 ? 1 : (items + sms - 1) / sms;
     const double gain = double(rounds * tiles) - double(items * tiles) / sms;

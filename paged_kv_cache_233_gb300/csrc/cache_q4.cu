@@ -96,8 +96,8 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[16], uint32_t (&cod
     constexpr int kBase = 0x4b400000;   // 2^23 + 2^22 as bits
     const float2 magic = make_float2(12582920.f, 12582920.f);
     if (s >= 0x1p-60f && s <= 0x1p60f) {
-        // The quotient d / s: with r the remainder of a first estimate
-        // q = d * (1 / s), exact in one fused multiply-add, q + r * (1 / s) is
+        // The quotient d / s, by Markstein's correction: with r the remainder of a
+        // first estimate q = d * (1 / s), exact in one fused multiply-add, q + r * (1 / s) is
         // exact wherever d / s is (a tie among them) and within an ulp
         // elsewhere. Adding 2^23 + 2^22 + 8 rounds it to a whole number, ties
         // to even, whose value plus 8 stands in the sum's low bits.

@@ -48,7 +48,7 @@
 // tiles, and two tiles' worth (kQ4UnitCost) for each (sequence, head group),
 // whose queries, sums and stores cost about that. (Counting tiles alone, the
 // CTAs that got many short sequences ended last: 64 sequences of 1 to 2048
-// tokens, 32 heads of 64, 45.7 us against 42.5, 256 of 1 to 512 59.1 against
+// tokens, 32 heads of 64, 45.7 us against 42.4, 256 of 1 to 512 59.1 against
 // 48.3; with one tile's worth 42.3 and 51.6, with three 43.4 and 50.1.)
 // Per CTA one producer warp copies each tile's blocks with untiled bulk copies
 // (a block's bytes of neighbouring kv heads are one run), through a ring of
@@ -58,15 +58,17 @@
 // smaller caches and shared prefixes at the time they had: their lines stay as
 // long as nothing needs the room.
 //
-// Measured (GB300, tables and lengths of a serving step; of a copy's 6.71 TB/s):
-// 8 requests of 65536 tokens, 8 kv heads of 128, 64 query heads: 671 MB in
-// 117 us, 5.74 TB/s (86%); the same bytes with head size 64 and 32 kv heads of
-// one query head each 129 us (78%); 64 requests of 1 to 2048 tokens, 32 heads
-// of 64: 168 MB in 42.5 us (59%: about 10 us are launch, ramp, pieces and
-// merge); 256 requests of 200 to 4000 tokens, 8 kv heads of 128, 32 query
-// heads, bf16: 692 MB in 121.5 us (85%).
-// The copies alone, without arithmetic, reach 94%: the consumers' instructions
-// are the bound, then that fixed part.
+// Measured (GB300, tables and lengths of a serving step; of a copy's 6.71 TB/s),
+// and the copies alone, without arithmetic:
+//   8 requests of 32768 to 131072 tokens, 8 kv heads of 128, 64 query heads,
+//   fp16: 839 MB in 147.4 us, 5.69 TB/s (85%); copies 128.3 us
+//   256 requests of 200 to 4000, 8 kv heads of 128, 32 query heads, bf16:
+//   692 MB in 122.0 us, 5.68 TB/s (85%); copies 107.7
+//   64 requests of 1 to 2048, 32 heads of 64, fp16, blocks of 8: 168 MB in
+//   42.9 us, 3.93 TB/s (59%); copies 31.1
+//   one request of 1999, 8 kv heads of 128: 8.5 us; copies 7.5
+// The copies with their ramp, pieces and merge are most of a call; the consumers'
+// instructions are what it takes beside them.
 #pragma once
 
 #include "decode_params.h"

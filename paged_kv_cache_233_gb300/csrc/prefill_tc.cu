@@ -65,9 +65,9 @@
 // zeros, so the tail's detour is not needed. A stage is then complete when all
 // four warps have arrived. The bound stays the tensor cores' and the softmax's
 // alternation, with fewer issue slots and, of 512 threads, 128 registers each:
-// 2048 rows after 16384 tokens, 8 kv heads of 128, 32 query heads, bf16: 527 us,
-// 1108 TFLOP/s, 57% of a large bf16 product's rate (16-bit pools, unsplit: 546
-// us); 1216 rows after 8192, 152 items that are not split: 162 us (149), with
+// 2048 rows after 16384 tokens, 8 kv heads of 128, 32 query heads, bf16: 525 us,
+// 1112 TFLOP/s, 57% of a large bf16 product's rate (16-bit pools, unsplit: 546
+// us); 1216 rows after 8192, 152 items that are not split: 163 us (149), with
 // heads of 64 138 us (114).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -74,7 +74,9 @@ __device__ __forceinline__ void q4_values(uint32_t w, uint32_t s2, uint32_t m2, 
 // holds nibble i of the low half in its low half and nibble i of the high
 // half in its high half. Two exponents cover four nibbles with one shift: a
 // nibble at mantissa bits 0-3 under 2^10 reads 1024 + c, one at bits 4-7
-// reads 1024 + 16 c, which one fused multiply-add takes to c - 8.
+// reads 1024 + 16 c, which one fused multiply-add takes to c - 8. (Integers
+// under a float's exponent are a published method of products with 4-bit
+// weights; the constants follow from the format.)
 __device__ __forceinline__ void q4_codes(uint32_t w, uint32_t (&out)[4]) {
     const uint32_t up = w >> 8;
     const uint32_t a = and_or(w, 0x000f000fu, 0x64006400u);
