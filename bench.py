@@ -1276,6 +1276,11 @@ def main(argv=None):
     finally:
         ctx.close()
     if result is not None:
+        # the line itself stays short enough for any reader: what `targets` sums up
+        # goes to stderr in full
+        details = {k: result.pop(k) for k in ("trace", "gates") if k in result}
+        if details:
+            print(json.dumps(details), file=sys.stderr, flush=True)
         print(json.dumps(result), flush=True)
 
 
