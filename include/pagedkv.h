@@ -24,15 +24,18 @@
  *     stream). Calls only enqueue work on it and return without
  *     synchronising; results are ready when the stream reaches them.
  *   - `dtype` is a pagedkv_dtype. q, k, v, the pools and out share it.
- *   - A call sees what the calls ahead of it on the stream wrote. One
+ *   - A call sees what the work ahead of it on the stream wrote. The
  *     exception: paged_kv_append_tokens' k and v must not be the outputs of a
  *     paged_attention_* call right ahead of it, with no other work between (its
  *     kernel starts while that call's still run and reads the rows at once;
- *     paged_kv_append has no such limit). Once paged_kv_build_tables or
- *     paged_kv_gather_q4 has been called in the process, whose results are
- *     tables, lengths and rows, paged_kv_append_tokens, paged_attention_decode
- *     and paged_attention_prefill read all their inputs after the work ahead of
- *     them, which takes them 1 to 3 us longer in a chain of small calls.
+ *     paged_kv_append has no such limit). Nor may a kernel of the caller's own
+ *     that lets its programmatic dependents start early write those rows, or
+ *     block tables, lengths and token lists, right ahead of a 16-bit call. Once
+ *     paged_kv_build_tables or paged_kv_gather_q4 has been called in the
+ *     process, whose results are tables, lengths and rows, neither limit is
+ *     left: paged_kv_append_tokens, paged_attention_decode and
+ *     paged_attention_prefill then read all their inputs after the work ahead
+ *     of them, which takes them 1 to 3 us longer in a chain of small calls.
  *   - Argument and shape checks run on the host before anything is enqueued;
  *     a failed check returns a negative pagedkv_status and enqueues nothing.
  *   - Out-of-range values found on the device (a block id outside the pool,

@@ -511,7 +511,9 @@ def paged_kv_append_q4(k, v, slot_mapping, k_cache, v_cache, stream=None):
 
 def paged_kv_gather_q4(k_cache, v_cache, slot_mapping, k, v, stream=None):
     """Rows slot_mapping[T] of 4-bit pools as k/v [T][Hkv][D] (fp16 or bf16, the
-    type they were appended in); rows of a negative slot are left as they were."""
+    type they were appended in); rows of a negative slot are left as they were.
+    From the first call on, 16-bit calls wait for the work ahead of them before they
+    read any input, as after paged_kv_build_tables."""
     (_fast or _binding()).gather_q4(k, v, slot_mapping, k_cache, v_cache, stream)
 
 
@@ -550,7 +552,10 @@ def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, fre
     The lengths and the count after the step go to context_lens_out and
     free_count_out, by default the inputs themselves. query_start[s + 1] -
     query_start[s] tells whether s was granted its new_lens[s] tokens; entries
-    past the last token are padding (pos and slot -1)."""
+    past the last token are padding (pos and slot -1). From the first call on,
+    paged_kv_append_tokens, paged_attention_decode and paged_attention_prefill wait
+    for the work ahead of them before they read any input (1 to 3 us a call in
+    chains of small ones)."""
     (_fast or _binding()).build_tables(new_lens, context_lens, block_tables, free_blocks, free_count,
                                        block_size, num_blocks, query_start, token_seq, token_pos,
                                        slot_mapping, context_lens_out, free_count_out, stream)
