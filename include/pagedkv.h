@@ -596,6 +596,106 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
                                void *stream);
 
 /*
+ * The 8-bit cache. Pools whose K and V are held as e4m3 codes, with a scale for
+ * each (block, kv head): a little more than half of the bytes of a 16-bit pool.
+ * The scale is a power of two 2^e, and a channel's code c stands for c * 2^e.
+ *
+ * A pool is uint8 [num_blocks][n_kv_heads][block_size * head_dim + tail], tail 16
+ * bytes (32 in blocks of 32); the bytes of one (block, kv head) are
+ *
+ *     codes  [head_dim / 16 panels][block_size tokens][16 channels]
+ *     scale  fp32, at block_size * head_dim; the rest is not used
+ *
+ * and tokens, slots and block tables mean what they mean for 16-bit pools. The
+ * codes do not depend on the 16-bit type of the rows. Supported: `dtype`
+ * PAGEDKV_F16 or PAGEDKV_BF16 (the type of q, k, v and out), head_dim 64 or 128,
+ * block_size 8, 16 or 32; else PAGEDKV_ERR_UNSUPPORTED. Whole blocks are copied
+ * and swapped as any other pool's: paged_kv_copy_blocks and paged_kv_swap_blocks
+ * with a block_size, n_kv_heads and head_dim of 16-bit elements that give the same
+ * bytes (block_size / 2, n_kv_heads, head_dim + tail / block_size).
+ *
+ * These entry points read all their device inputs after the kernels before them
+ * on the stream have completed, as the 4-bit cache's do.
+ */
+
+/*
+ * paged_kv_append_q8 -- quantise new tokens' K and V rows behind their
+ * sequences' older tokens.
+ *
+ * Sequence s owns rows query_start[s] .. query_start[s+1]-1 (n_s rows), which are
+ * the tokens at positions L_s - n_s .. L_s - 1, with L_s = context_lens[s] counting
+ * them (as paged_attention_prefill's chunks). For each block that they fall into
+ * and each kv head, K and V on their own,
+ *
+ *     2^e  is the smallest power of two, at least 2^-64, with |x| <= 448 * 2^e for
+ *          every finite new x of the block, and at least the block's scale where the
+ *          block holds tokens of s before position L_s - n_s;
+ *     c    = x / 2^e rounded to the nearest e4m3 value, ties to even; a NaN or an
+ *          infinity becomes NaN and leaves the others alone.
+ *
+ * Where the scale grew, the codes of the block's older tokens are divided by the
+ * growth and rounded again (exact for results of 2^-6 and more). A block without
+ * older tokens starts over: what another sequence left in it does not matter.
+ *
+ *   k, v           [num_tokens][n_kv_heads][head_dim] of dtype, device
+ *   block_tables   int32 [num_seqs][max_blocks_per_seq], device
+ *   query_start    int32 [num_seqs + 1], device, non-decreasing from 0; rows from
+ *                  query_start[num_seqs] on are padding
+ *   context_lens   int32 [num_seqs], device
+ *   k_cache,
+ *   v_cache        8-bit pools, device, updated in place
+ *
+ * No two sequences may write into one block in a call. A sequence whose rows lie
+ * outside [0, num_tokens) sets PAGEDKV_DEVERR_POSITION, one with n_s > L_s or L_s
+ * past its table PAGEDKV_DEVERR_CONTEXT_LEN, and none of its rows is written; the
+ * rows of a block id outside the pool are skipped (PAGEDKV_DEVERR_BLOCK_ID).
+ * num_seqs <= 4096.
+ */
+int paged_kv_append_q8(const void *k, const void *v, const int32_t *block_tables,
+                       const int32_t *query_start, const int32_t *context_lens, void *k_cache,
+                       void *v_cache, int num_seqs, int num_tokens, int max_blocks_per_seq,
+                       int num_blocks, int block_size, int n_kv_heads, int head_dim, int dtype,
+                       void *stream);
+
+/*
+ * paged_kv_gather_q8 -- read rows back out of 8-bit pools.
+ *
+ * k[t] and v[t] (of dtype, [num_tokens][n_kv_heads][head_dim], written) are what
+ * slot slot_mapping[t]'s codes stand for, rounded to dtype, at most its largest
+ * finite value in size. Rows with slot < 0 are left as they were, and so are rows
+ * whose slot lies past the pool (PAGEDKV_DEVERR_SLOT_RANGE). A slot may appear any
+ * number of times.
+ */
+int paged_kv_gather_q8(const void *k_cache, const void *v_cache, const int64_t *slot_mapping, void *k,
+                       void *v, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
+                       int head_dim, int dtype, void *stream);
+
+/*
+ * paged_attention_decode_q8 -- paged_attention_decode over 8-bit pools.
+ *
+ * The same attention with K_s[i] and V_s[i] the values c * 2^e that the codes stand
+ * for. Arguments, limits, splits and workspace (paged_attention_workspace_bytes) as
+ * paged_attention_decode_q4's.
+ *
+ * Scores, softmax statistics and output sums are fp32 and out is rounded once.
+ * Held in fewer bits on the way, each of them rounded once:
+ *   - q in fp16, scaled by a power of two per row: exact but for elements below
+ *     2^-24 (bf16: 2^-27) of the row's largest;
+ *   - a probability times the scale of its token's V, in fp16, relative to the
+ *     largest such product so far: what is below 2^-24 of that loses bits.
+ * In bf16 caches values of V may be 2^70 at most. A NaN or an infinity in q, or a
+ * NaN code in K, makes all outputs NaN of the query heads that attend to it, one in
+ * V those of its channel. What lies in a block past a sequence's context never
+ * matters, but for the block's scale.
+ */
+int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, float scale,
+                              void *out, int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                              int num_blocks, int block_size, int max_blocks_per_seq,
+                              int partition_tokens, void *workspace, size_t workspace_bytes,
+                              int dtype, void *stream);
+
+/*
  * paged_kv_build_tables -- a step's block tables, token lists and slots, on
  * the GPU.
  *

@@ -26,6 +26,10 @@ The entry points keep the C names:
                               partition_tokens=0, workspace=None)
     paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
                                out, max_query_len=None, workspace=None, key_parts=1)
+    paged_kv_append_q8(k, v, block_tables, query_start, context_lens, k_cache, v_cache)
+    paged_kv_gather_q8(k_cache, v_cache, slot_mapping, k, v)
+    paged_attention_decode_q8(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                              partition_tokens=0, workspace=None)
 
 All tensors live on the current CUDA device; work is enqueued on the current
 torch stream (or the stream passed) and the calls return without waiting.
@@ -48,6 +52,7 @@ __all__ = [
     "prefill_workspace_bytes", "prefill_workspace",
     "paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
     "paged_attention_decode_q4", "paged_attention_prefill_q4", "new_q4_pool",
+    "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8", "new_q8_pool",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -66,7 +71,8 @@ EXPORTS = ("paged_kv_slot_mapping", "paged_kv_append", "paged_attention_decode",
            "paged_attention_decode_shared_prefix", "paged_kv_append_tokens",
            "pagedkv_check_bounded_wait", "paged_attention_prefill_split",
            "paged_attention_prefill_workspace_bytes", "paged_kv_build_tables", "paged_kv_append_q4",
-           "paged_kv_gather_q4", "paged_attention_decode_q4", "paged_attention_prefill_q4")
+           "paged_kv_gather_q4", "paged_attention_decode_q4", "paged_attention_prefill_q4",
+           "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8")
 
 
 class PagedKVError(RuntimeError):
@@ -123,8 +129,12 @@ def load():
     lib.paged_kv_gather_q4.argtypes = [vp] * 5 + [i32] * 6 + [vp]
     lib.paged_attention_decode_q4.argtypes = lib.paged_attention_decode.argtypes
     lib.paged_attention_prefill_q4.argtypes = lib.paged_attention_prefill_split.argtypes
+    lib.paged_kv_append_q8.argtypes = [vp] * 7 + [i32] * 8 + [vp]
+    lib.paged_kv_gather_q8.argtypes = lib.paged_kv_gather_q4.argtypes
+    lib.paged_attention_decode_q8.argtypes = lib.paged_attention_decode.argtypes
     for name in ("paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
-                 "paged_attention_decode_q4", "paged_attention_prefill_q4"):
+                 "paged_attention_decode_q4", "paged_attention_prefill_q4", "paged_kv_append_q8",
+                 "paged_kv_gather_q8", "paged_attention_decode_q8"):
         getattr(lib, name).restype = i32
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
@@ -264,17 +274,22 @@ def paged_kv_append_tokens(k, v, block_tables, token_seq, token_pos, k_cache, v_
 
 def _block_shape(pool):
     """(num_blocks, block_size, heads, head_dim, dtype code) that give a pool's
-    bytes per block; a 4-bit pool's bytes count as pairs."""
+    bytes per block; a 4- or 8-bit pool's bytes count as pairs."""
     if pool.dtype is torch.uint8:
-        if pool.shape[2] not in (8, 16, 32) or pool.shape[3] not in (40, 80):
-            raise PagedKVError("a uint8 pool must be a 4-bit one: [NB][Hkv][8, 16 or 32][40 or 80]")
-        return pool.shape[0], pool.shape[2], pool.shape[1], pool.shape[3] // 2, DTYPE_CODES[torch.float16]
+        NB, H, B, row = pool.shape
+        code = DTYPE_CODES[torch.float16]
+        if B in (8, 16, 32) and row in (40, 80):
+            return NB, B, H, row // 2, code
+        if B in (8, 16, 32) and row - max(16, B) // B in (64, 128):
+            return NB, B // 2, H, row, code
+        raise PagedKVError("a uint8 pool must be a 4-bit one, [NB][Hkv][8, 16 or 32][40 or 80], or an 8-bit "
+                           "one as new_q8_pool makes it")
     return (*pool.shape, _code(pool))
 
 
 def paged_kv_copy_blocks(k_cache, v_cache, block_pairs, stream=None):
     """Copy-on-write: copy whole blocks block_pairs[i][0] -> block_pairs[i][1] in both pools
-    (of 16- or 32-bit elements, or 4-bit pools as new_q4_pool makes them)."""
+    (of 16- or 32-bit elements, or 4- and 8-bit pools as new_q4_pool and new_q8_pool make them)."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
         raise PagedKVError("expected pools [NB][B][Hkv][D] of one element type")
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
@@ -304,7 +319,7 @@ def paged_kv_swap_blocks(src_k, src_v, dst_k, dst_v, block_pairs, stream=None):
     """Copy whole blocks block_pairs[i][0] of the source pools to block_pairs[i][1]
     of the destination pools (swap-out to pinned host pools, or swap-in back).
 
-    Pools are [NB][B][Hkv][D] of one element type (or 4-bit pools); source and destination may
+    Pools are [NB][B][Hkv][D] of one element type (or 4- or 8-bit pools); source and destination may
     hold different numbers of blocks. Any argument may live in CUDA memory or in
     pinned host memory; the copy runs on the GPU, asynchronously on `stream`.
     """
@@ -538,6 +553,39 @@ def paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, c
             workspace = prefill_workspace(q)
     (_fast or _binding()).prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
                                      out, max_query_len, workspace, key_parts, stream)
+
+
+def new_q8_pool(num_blocks, n_kv_heads, block_size, head_dim, device="cuda"):
+    """An empty 8-bit pool: uint8 [num_blocks][n_kv_heads][block_size][head_dim + tail / block_size]
+    (the last two dimensions are one run of bytes, laid out as pagedkv.h says)."""
+    if block_size not in (8, 16, 32):
+        raise PagedKVError("an 8-bit pool's block_size must be 8, 16 or 32")
+    tail = max(16, block_size) // block_size
+    return torch.empty(num_blocks, n_kv_heads, block_size, head_dim + tail, dtype=torch.uint8, device=device)
+
+
+def paged_kv_append_q8(k, v, block_tables, query_start, context_lens, k_cache, v_cache, stream=None):
+    """Quantise k/v [T][Hkv][D] (fp16 or bf16) into 8-bit pools: sequence s's rows
+    query_start[s] .. query_start[s + 1] are the last tokens of its context_lens[s]
+    (they included). A block's scale is set with its first token and grows with
+    later rows; rows from query_start[-1] on are padding."""
+    (_fast or _binding()).append_q8(k, v, block_tables, query_start, context_lens, k_cache, v_cache, stream)
+
+
+def paged_kv_gather_q8(k_cache, v_cache, slot_mapping, k, v, stream=None):
+    """Rows slot_mapping[T] of 8-bit pools as k/v [T][Hkv][D] (fp16 or bf16); rows
+    of a negative slot are left as they were. From the first call on, 16-bit calls
+    wait for the work ahead of them before they read any input, as after
+    paged_kv_build_tables."""
+    (_fast or _binding()).gather_q8(k, v, slot_mapping, k_cache, v_cache, stream)
+
+
+def paged_attention_decode_q8(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                              partition_tokens=0, workspace=None, stream=None):
+    """paged_attention_decode over 8-bit pools (fixed partitions: multiples of 32
+    tokens; workspace from new_workspace)."""
+    (_fast or _binding()).decode_q8(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                                    partition_tokens, workspace, stream)
 
 
 def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, free_count, block_size,

@@ -1,6 +1,6 @@
-// api_q4.cu -- the C ABI of the 4-bit paged cache and of the tables a step
-// builds on the GPU (declared in include/pagedkv.h): host-side checks and
-// launches.
+// api_packed.cu -- the C ABI of the paged caches in 4 and in 8 bits and of the
+// tables a step builds on the GPU (declared in include/pagedkv.h): host-side
+// checks and launches.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -11,6 +11,7 @@
 #include "decode_launch.h"
 #include "prefill.h"
 #include "q4.h"
+#include "q8.h"
 
 namespace {
 
@@ -24,7 +25,7 @@ int done(cudaError_t e) { return e == cudaSuccess ? PAGEDKV_OK : PAGEDKV_ERR_CUD
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// The checks that every call on 4-bit pools shares.
+// The checks that every call on 4- or 8-bit pools shares.
 int check_pool(int num_blocks, int block_size, int n_kv_heads, int head_dim, int dtype) {
     if (num_blocks < 1 || block_size < 1 || n_kv_heads < 1 || head_dim < 1 ||
         (dtype != PAGEDKV_F32 && dtype != PAGEDKV_F16 && dtype != PAGEDKV_BF16))
@@ -81,6 +82,83 @@ int move_rows(const void *k, const void *v, const int64_t *slot_mapping, const v
     st = api_device_state(&err, &sms);
     if (st != PAGEDKV_OK) return st;
     return done(launch((long long)num_blocks * block_size, err));
+}
+
+// paged_attention_decode_q4 and paged_attention_decode_q8.
+int decode_packed(int bits, const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, float scale,
+                              void *out, int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                              int num_blocks, int block_size, int max_blocks_per_seq, int partition_tokens,
+                              void *workspace, size_t workspace_bytes, int dtype, void *stream) {
+    if (num_seqs < 0 || n_q_heads < 1 || max_blocks_per_seq < 1 ||
+        (partition_tokens < 0 && partition_tokens != PAGEDKV_PARTITION_BALANCED))
+        return PAGEDKV_ERR_INVALID_ARG;
+    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
+    if (st == PAGEDKV_ERR_INVALID_ARG) return st;
+    if (n_q_heads % n_kv_heads != 0 || !finite(scale)) return PAGEDKV_ERR_INVALID_ARG;
+    if (partition_tokens > 0 && partition_tokens % 32 != 0) return PAGEDKV_ERR_INVALID_ARG;
+    if (st != PAGEDKV_OK) return st;
+    const int group = n_q_heads / n_kv_heads;
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    if (group > 8 || num_seqs > kMaxSeqs || cap > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PAGEDKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(q, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
+        !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(context_lens, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (partition_tokens != 0) {
+        const size_t need = paged_attention_workspace_bytes(num_seqs, n_q_heads, head_dim, max_blocks_per_seq,
+                                                            block_size, partition_tokens);
+        if (need == 0 || !workspace || workspace_bytes < need || !api_aligned(workspace, 256))
+            return PAGEDKV_ERR_WORKSPACE;
+    }
+    pkv::PackedAttnParams p{};
+    int sms = 0;
+    st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.out = out;
+    p.scale_log2 = scale * pkv::kLog2e;
+    p.num_seqs = num_seqs;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = group;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    while ((1 << p.log2_block) < block_size) ++p.log2_block;
+    p.max_blocks = max_blocks_per_seq;
+    p.balanced = partition_tokens == PAGEDKV_PARTITION_BALANCED ? 1 : 0;
+    p.log2_hpu = n_kv_heads % 4 == 0 ? 2 : (n_kv_heads % 2 == 0 ? 1 : 0);
+    // (unsplit: one partition of the tables' whole width)
+    p.part_tokens = partition_tokens > 0 ? partition_tokens : int((cap + 31) / 32 * 32);
+    p.max_parts = int((cap + p.part_tokens - 1) / p.part_tokens);
+    p.merged = p.balanced || p.max_parts > 1 ? 1 : 0;
+    // the kernel counts units and tiles in ints
+    const long long units = (long long)num_seqs * (n_kv_heads >> p.log2_hpu) *
+                            (p.balanced ? (cap + 31) / 32 + (bits == 8 ? pkv::kQ8UnitCost : pkv::kQ4UnitCost) : p.max_parts);
+    if (units > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
+    if (partition_tokens != 0) {
+        // rows of partition states, or of pieces: two per CTA, as paged_attention_workspace_bytes sizes them
+        const size_t rows = p.balanced ? size_t(16) * sms * size_t(n_q_heads < 32 ? n_q_heads : 32)
+                                       : size_t(num_seqs) * n_q_heads * size_t(p.max_parts);
+        uint8_t *w = static_cast<uint8_t *>(workspace);
+        p.ws_o = reinterpret_cast<float *>(w);
+        p.ws_m = reinterpret_cast<float *>(w + round256(rows * head_dim * 4));
+        p.ws_l = reinterpret_cast<float *>(w + round256(rows * head_dim * 4) + round256(rows * 4));
+    }
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaError_t e = bits == 8 ? (dtype == PAGEDKV_BF16 ? pkv::launch_decode_q8_bf16(head_dim, p, sms, cs)
+                                                       : pkv::launch_decode_q8_f16(head_dim, p, sms, cs))
+                              : (dtype == PAGEDKV_BF16 ? pkv::launch_decode_q4_bf16(head_dim, p, sms, cs)
+                                                       : pkv::launch_decode_q4_f16(head_dim, p, sms, cs));
+    if (e == cudaSuccess && p.merged && !p.balanced)
+        e = pkv::launch_lse_merge(dtype, head_dim, p.ws_o, p.ws_m, p.ws_l, context_lens, out, num_seqs, n_q_heads,
+                                  p.part_tokens, p.max_parts, int(cap), p.err, cs);
+    return done(e);
 }
 
 }  // namespace
@@ -159,78 +237,69 @@ int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *
                      });
 }
 
+int paged_kv_append_q8(const void *k, const void *v, const int32_t *block_tables, const int32_t *query_start,
+                       const int32_t *context_lens, void *k_cache, void *v_cache, int num_seqs, int num_tokens,
+                       int max_blocks_per_seq, int num_blocks, int block_size, int n_kv_heads, int head_dim,
+                       int dtype, void *stream) {
+    if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 1) return PAGEDKV_ERR_INVALID_ARG;
+    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
+    if (st != PAGEDKV_OK) return st;
+    if (num_seqs > kMaxSeqs || num_tokens > kMaxCount || (long long)max_blocks_per_seq * block_size > INT_MAX / 2)
+        return PAGEDKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_tokens == 0) return PAGEDKV_OK;
+    if (!k || !v || !block_tables || !query_start || !context_lens || !k_cache || !v_cache)
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(k, 16) || !api_aligned(v, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
+        !api_aligned(block_tables, 4) || !api_aligned(query_start, 4) || !api_aligned(context_lens, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    pkv::Q8AppendParams p{};
+    int sms = 0;
+    st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.k = k;
+    p.v = v;
+    p.block_tables = block_tables;
+    p.query_start = query_start;
+    p.context_lens = context_lens;
+    p.k_cache = static_cast<uint8_t *>(k_cache);
+    p.v_cache = static_cast<uint8_t *>(v_cache);
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.n_kv_heads = n_kv_heads;
+    return done(pkv::launch_append_q8(p, head_dim, block_size, dtype, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_kv_gather_q8(const void *k_cache, const void *v_cache, const int64_t *slot_mapping, void *k,
+                       void *v, int num_tokens, int num_blocks, int block_size, int n_kv_heads,
+                       int head_dim, int dtype, void *stream) {
+    return move_rows(k, v, slot_mapping, k_cache, v_cache, num_tokens, num_blocks, block_size, n_kv_heads,
+                     head_dim, dtype, [&](long long num_slots, unsigned int *err) {
+                         pkv::api_note_device_inputs();   // as above: calls that append these rows
+                         return pkv::launch_gather_q8(static_cast<const uint8_t *>(k_cache),
+                                                      static_cast<const uint8_t *>(v_cache), slot_mapping, k, v,
+                                                      num_tokens, n_kv_heads, head_dim, block_size, num_slots,
+                                                      dtype, err, static_cast<cudaStream_t>(stream));
+                     });
+}
+
 int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_cache,
                               const int32_t *block_tables, const int32_t *context_lens, float scale,
                               void *out, int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
                               int num_blocks, int block_size, int max_blocks_per_seq, int partition_tokens,
                               void *workspace, size_t workspace_bytes, int dtype, void *stream) {
-    if (num_seqs < 0 || n_q_heads < 1 || max_blocks_per_seq < 1 ||
-        (partition_tokens < 0 && partition_tokens != PAGEDKV_PARTITION_BALANCED))
-        return PAGEDKV_ERR_INVALID_ARG;
-    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
-    if (st == PAGEDKV_ERR_INVALID_ARG) return st;
-    if (n_q_heads % n_kv_heads != 0 || !finite(scale)) return PAGEDKV_ERR_INVALID_ARG;
-    if (partition_tokens > 0 && partition_tokens % 32 != 0) return PAGEDKV_ERR_INVALID_ARG;
-    if (st != PAGEDKV_OK) return st;
-    const int group = n_q_heads / n_kv_heads;
-    const long long cap = (long long)max_blocks_per_seq * block_size;
-    if (group > 8 || num_seqs > kMaxSeqs || cap > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
-    if (num_seqs == 0) return PAGEDKV_OK;
-    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PAGEDKV_ERR_INVALID_ARG;
-    if (!api_aligned(q, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
-        !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(context_lens, 4))
-        return PAGEDKV_ERR_INVALID_ARG;
-    if (partition_tokens != 0) {
-        const size_t need = paged_attention_workspace_bytes(num_seqs, n_q_heads, head_dim, max_blocks_per_seq,
-                                                            block_size, partition_tokens);
-        if (need == 0 || !workspace || workspace_bytes < need || !api_aligned(workspace, 256))
-            return PAGEDKV_ERR_WORKSPACE;
-    }
-    pkv::Q4AttnParams p{};
-    int sms = 0;
-    st = api_device_state(&p.err, &sms);
-    if (st != PAGEDKV_OK) return st;
-    p.q = q;
-    p.k_cache = static_cast<const uint8_t *>(k_cache);
-    p.v_cache = static_cast<const uint8_t *>(v_cache);
-    p.block_tables = block_tables;
-    p.context_lens = context_lens;
-    p.out = out;
-    p.scale_log2 = scale * pkv::kLog2e;
-    p.num_seqs = num_seqs;
-    p.n_q_heads = n_q_heads;
-    p.n_kv_heads = n_kv_heads;
-    p.group = group;
-    p.num_blocks = num_blocks;
-    p.block_size = block_size;
-    while ((1 << p.log2_block) < block_size) ++p.log2_block;
-    p.max_blocks = max_blocks_per_seq;
-    p.balanced = partition_tokens == PAGEDKV_PARTITION_BALANCED ? 1 : 0;
-    p.log2_hpu = n_kv_heads % 4 == 0 ? 2 : (n_kv_heads % 2 == 0 ? 1 : 0);
-    // (unsplit: one partition of the tables' whole width)
-    p.part_tokens = partition_tokens > 0 ? partition_tokens : int((cap + 31) / 32 * 32);
-    p.max_parts = int((cap + p.part_tokens - 1) / p.part_tokens);
-    p.merged = p.balanced || p.max_parts > 1 ? 1 : 0;
-    // the kernel counts units and tiles in ints
-    const long long units = (long long)num_seqs * (n_kv_heads >> p.log2_hpu) *
-                            (p.balanced ? (cap + 31) / 32 + pkv::kQ4UnitCost : p.max_parts);
-    if (units > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
-    if (partition_tokens != 0) {
-        // rows of partition states, or of pieces: two per CTA, as paged_attention_workspace_bytes sizes them
-        const size_t rows = p.balanced ? size_t(16) * sms * size_t(n_q_heads < 32 ? n_q_heads : 32)
-                                       : size_t(num_seqs) * n_q_heads * size_t(p.max_parts);
-        uint8_t *w = static_cast<uint8_t *>(workspace);
-        p.ws_o = reinterpret_cast<float *>(w);
-        p.ws_m = reinterpret_cast<float *>(w + round256(rows * head_dim * 4));
-        p.ws_l = reinterpret_cast<float *>(w + round256(rows * head_dim * 4) + round256(rows * 4));
-    }
-    cudaError_t e = dtype == PAGEDKV_BF16
-                        ? pkv::launch_decode_q4_bf16(head_dim, p, sms, static_cast<cudaStream_t>(stream))
-                        : pkv::launch_decode_q4_f16(head_dim, p, sms, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess && p.merged && !p.balanced)
-        e = pkv::launch_lse_merge(dtype, head_dim, p.ws_o, p.ws_m, p.ws_l, context_lens, out, num_seqs, n_q_heads,
-                                  p.part_tokens, p.max_parts, int(cap), p.err, static_cast<cudaStream_t>(stream));
-    return done(e);
+    return decode_packed(4, q, k_cache, v_cache, block_tables, context_lens, scale, out, num_seqs, n_q_heads, n_kv_heads, head_dim,
+                         num_blocks, block_size, max_blocks_per_seq, partition_tokens, workspace, workspace_bytes, dtype, stream);
+}
+
+int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, float scale,
+                              void *out, int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                              int num_blocks, int block_size, int max_blocks_per_seq, int partition_tokens,
+                              void *workspace, size_t workspace_bytes, int dtype, void *stream) {
+    return decode_packed(8, q, k_cache, v_cache, block_tables, context_lens, scale, out, num_seqs, n_q_heads, n_kv_heads, head_dim,
+                         num_blocks, block_size, max_blocks_per_seq, partition_tokens, workspace, workspace_bytes, dtype, stream);
 }
 
 int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v_cache,

@@ -1,4 +1,4 @@
-// binding.cpp -- Python entry points of the 4-bit cache and of
+// binding.cpp -- Python entry points of the 4- and 8-bit caches and of
 // paged_kv_build_tables: tensors checked and unpacked in C++, then the C ABI.
 //
 // These are the calls of a decode step, which the GPU finishes in a few
@@ -99,10 +99,13 @@ PyObject *done(int status, const char *what) {
 struct Pools {
     int blocks, heads, block;
 };
-Pools pools(const at::Tensor &k, const at::Tensor &v, int64_t dim) {
-    if (k.dim() != 4 || v.sizes() != k.sizes() || k.size(3) * 8 != 5 * dim)
-        fail("expected 4-bit pools [NB][Hkv][B][5 D / 8] for head_dim D");
-    return {narrow(k.size(0)), narrow(k.size(1)), narrow(k.size(2))};
+Pools pools(int bits, const at::Tensor &k, const at::Tensor &v, int64_t dim) {
+    if (k.dim() != 4 || v.sizes() != k.sizes()) fail("expected pools [NB][Hkv][B][bytes]");
+    const int64_t block = k.size(2), row = k.size(3);
+    if (bits == 4 && row * 8 != 5 * dim) fail("expected 4-bit pools [NB][Hkv][B][5 D / 8] for head_dim D");
+    if (bits == 8 && (block < 1 || (row - dim) * block != (block > 16 ? block : 16)))
+        fail("expected 8-bit pools [NB][Hkv][B][D + tail / B] for head_dim D (see new_q8_pool)");
+    return {narrow(k.size(0)), narrow(k.size(1)), narrow(block)};
 }
 
 // A workspace tensor of any type, or None.
@@ -130,35 +133,68 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, Body body) {
     }
 }
 
+enum Move { kAppendQ4, kGatherQ4, kGatherQ8 };
+
 // rows (k, v, slot_mapping, k_cache, v_cache, stream), append or gather
-PyObject *rows(PyObject *const *a, bool append) {
+PyObject *rows(PyObject *const *a, Move move) {
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &slots = tensor(a[2], "slot_mapping");
     const at::Tensor &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache");
     if (k.dim() != 3 || v.sizes() != k.sizes() || slots.numel() != k.size(0))
         fail("expected k, v [T][Hkv][D] and one slot per token");
-    const Pools p = pools(kc, vc, k.size(2));
+    const Pools p = pools(move == kGatherQ8 ? 8 : 4, kc, vc, k.size(2));
     if (k.size(1) != p.heads) fail("token rows do not match the pools' kv heads");
     const int d = device_of(k), code = dtype_code(k), T = narrow(k.size(0)), D = narrow(k.size(2));
     void *kp = on(d, k, "k", k.scalar_type()), *vp = on(d, v, "v", k.scalar_type());
     const int64_t *sp = static_cast<const int64_t *>(on(d, slots, "slot_mapping", at::kLong));
     void *kcp = on(d, kc, "k_cache", at::kByte), *vcp = on(d, vc, "v_cache", at::kByte), *st = stream_of(a[5]);
-    if (append)
+    if (move == kAppendQ4)
         return done(paged_kv_append_q4(kp, vp, sp, kcp, vcp, T, p.blocks, p.block, p.heads, D, code, st),
                     "paged_kv_append_q4");
-    return done(paged_kv_gather_q4(kcp, vcp, sp, kp, vp, T, p.blocks, p.block, p.heads, D, code, st),
-                "paged_kv_gather_q4");
+    if (move == kGatherQ4)
+        return done(paged_kv_gather_q4(kcp, vcp, sp, kp, vp, T, p.blocks, p.block, p.heads, D, code, st),
+                    "paged_kv_gather_q4");
+    return done(paged_kv_gather_q8(kcp, vcp, sp, kp, vp, T, p.blocks, p.block, p.heads, D, code, st),
+                "paged_kv_gather_q8");
 }
 
 PyObject *append_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 6, [&] { return rows(a, true); });
+    return guarded(n, 6, [&] { return rows(a, kAppendQ4); });
 }
 
 PyObject *gather_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 6, [&] { return rows(a, false); });
+    return guarded(n, 6, [&] { return rows(a, kGatherQ4); });
+}
+
+PyObject *gather_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 6, [&] { return rows(a, kGatherQ8); });
+}
+
+// k, v, block_tables, query_start, context_lens, k_cache, v_cache, stream
+PyObject *append_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 8, [&] {
+        const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &bt = tensor(a[2], "block_tables");
+        const at::Tensor &start = tensor(a[3], "query_start"), &lens = tensor(a[4], "context_lens");
+        const at::Tensor &kc = tensor(a[5], "k_cache"), &vc = tensor(a[6], "v_cache");
+        if (k.dim() != 3 || v.sizes() != k.sizes()) fail("expected k, v [T][Hkv][D]");
+        const int64_t S = lens.numel();
+        if (start.numel() != S + 1 || bt.dim() != 2 || bt.size(0) != S)
+            fail("query_start must hold num_seqs + 1 offsets, block_tables num_seqs rows");
+        const Pools p = pools(8, kc, vc, k.size(2));
+        if (k.size(1) != p.heads) fail("token rows do not match the pools' kv heads");
+        const int d = device_of(k), code = dtype_code(k);
+        return done(paged_kv_append_q8(
+                        on(d, k, "k", k.scalar_type()), on(d, v, "v", k.scalar_type()),
+                        static_cast<const int32_t *>(on(d, bt, "block_tables", at::kInt)),
+                        static_cast<const int32_t *>(on(d, start, "query_start", at::kInt)),
+                        static_cast<const int32_t *>(on(d, lens, "context_lens", at::kInt)),
+                        on(d, kc, "k_cache", at::kByte), on(d, vc, "v_cache", at::kByte), narrow(S), narrow(k.size(0)),
+                        narrow(bt.size(1)), p.blocks, p.block, p.heads, narrow(k.size(2)), code, stream_of(a[7])),
+                    "paged_kv_append_q8");
+    });
 }
 
 // q, k_cache, v_cache, block_tables, context_lens, scale, out, partition_tokens, workspace, stream
-PyObject *decode_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *decode(int bits, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 10, [&] {
         const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
         const at::Tensor &bt = tensor(a[3], "block_tables"), &lens = tensor(a[4], "context_lens");
@@ -166,25 +202,29 @@ PyObject *decode_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (q.dim() != 3 || out.sizes() != q.sizes() || bt.dim() != 2 || bt.size(0) != q.size(0) ||
             lens.numel() != q.size(0))
             fail("expected q/out [S][Hq][D], block_tables [S][max_blocks] and context_lens [S]");
-        const Pools p = pools(kc, vc, q.size(2));
+        const Pools p = pools(bits, kc, vc, q.size(2));
         const double scale = PyFloat_AsDouble(a[5]);
         if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
         const int part = integer(a[7], "partition_tokens"), d = device_of(q), code = dtype_code(q);
         size_t bytes;
         void *ws = workspace_of(d, a[8], &bytes);
-        return done(paged_attention_decode_q4(
+        const auto call = bits == 8 ? paged_attention_decode_q8 : paged_attention_decode_q4;
+        return done(call(
                         on(d, q, "q", q.scalar_type()), on(d, kc, "k_cache", at::kByte), on(d, vc, "v_cache", at::kByte),
                         static_cast<const int32_t *>(on(d, bt, "block_tables", at::kInt)),
                         static_cast<const int32_t *>(on(d, lens, "context_lens", at::kInt)), float(scale),
                         on(d, out, "out", q.scalar_type()), narrow(q.size(0)), narrow(q.size(1)), p.heads,
                         narrow(q.size(2)), p.blocks, p.block, narrow(bt.size(1)), part, ws, bytes, code,
                         stream_of(a[9])),
-                    "paged_attention_decode_q4");
+                    bits == 8 ? "paged_attention_decode_q8" : "paged_attention_decode_q4");
     });
 }
 
+PyObject *decode_q4(PyObject *, PyObject *const *a, Py_ssize_t n) { return decode(4, a, n); }
+PyObject *decode_q8(PyObject *, PyObject *const *a, Py_ssize_t n) { return decode(8, a, n); }
+
 // q, k_cache, v_cache, block_tables, query_start, context_lens, scale, out, max_query_len, workspace, key_parts, stream
-PyObject *prefill_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *prefill(int bits, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 12, [&] {
         const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
         const at::Tensor &bt = tensor(a[3], "block_tables"), &start = tensor(a[4], "query_start");
@@ -193,7 +233,7 @@ PyObject *prefill_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t S = lens.numel();
         if (start.numel() != S + 1 || bt.dim() != 2 || bt.size(0) != S)
             fail("query_start must hold num_seqs + 1 offsets, block_tables num_seqs rows");
-        const Pools p = pools(kc, vc, q.size(2));
+        const Pools p = pools(bits, kc, vc, q.size(2));
         const double scale = PyFloat_AsDouble(a[6]);
         if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
         const int most = integer(a[8], "max_query_len"), parts = integer(a[10], "key_parts");
@@ -211,6 +251,8 @@ PyObject *prefill_q4(PyObject *, PyObject *const *a, Py_ssize_t n) {
                     "paged_attention_prefill_q4");
     });
 }
+
+PyObject *prefill_q4(PyObject *, PyObject *const *a, Py_ssize_t n) { return prefill(4, a, n); }
 
 // new_lens, context_lens, block_tables, free_blocks, free_count, block_size, num_blocks, query_start, token_seq,
 // token_pos, slot_mapping, context_lens_out, free_count_out, stream
@@ -252,6 +294,9 @@ PyMethodDef g_methods[] = {
     {"set_error", set_error, METH_O, "the class of the errors the others raise"},
     {"append_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_q4)), METH_FASTCALL, nullptr},
     {"gather_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gather_q4)), METH_FASTCALL, nullptr},
+    {"append_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_q8)), METH_FASTCALL, nullptr},
+    {"gather_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gather_q8)), METH_FASTCALL, nullptr},
+    {"decode_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q8)), METH_FASTCALL, nullptr},
     {"decode_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q4)), METH_FASTCALL, nullptr},
     {"prefill_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill_q4)), METH_FASTCALL, nullptr},
     {"build_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(build_tables)), METH_FASTCALL, nullptr},

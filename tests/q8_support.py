@@ -1,0 +1,150 @@
+"""The 8-bit cache's definition in 64 bits, and pools built from it, for the tests.
+
+Written from the definition alone: the tokens of a block and kv head share a scale
+2^e, a channel is an e4m3 code c that stands for c * 2^e; a pool holds
+[num_blocks][n_kv_heads] runs of codes [D / 16][B][16] followed by the scale in
+fp32 and padding up to 16 bytes (32 in blocks of 32).
+"""
+import math
+
+import torch
+
+from q4_support import HALF_STEP, TINY, assert_near, sequence_slots, tables_for  # noqa: F401  (for the tests)
+
+NAN = 0x7F
+
+
+def _table():
+    """What the codes 0 .. 127 stand for: 3 bits of mantissa under 4 of exponent, bias 7."""
+    v = [m * 2.0 ** -9 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7) for e in range(16) for m in range(8)]
+    v[NAN] = math.nan
+    return torch.tensor(v, dtype=torch.float64)
+
+
+VALUES = _table()
+
+
+def value(codes):
+    c = codes.long()
+    return torch.where(c >= 128, -VALUES[c % 128], VALUES[c % 128])
+
+
+def code(x):
+    """fp64 values to the nearest code, ties to the even one; NaN and infinities to NaN."""
+    a = x.abs()
+    v = VALUES[:NAN]
+    hi = torch.searchsorted(v, a.nan_to_num(0.0, 0.0, 0.0)).clamp(max=NAN - 1)
+    lo = (hi - 1).clamp(min=0)
+    down, up = a - v[lo], v[hi] - a
+    c = torch.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    c = c + torch.where(torch.signbit(x), 128, 0)
+    return torch.where(torch.isfinite(x), c, torch.full_like(c, NAN)).to(torch.uint8)   # (a NaN has no sign)
+
+
+def exponent(x):
+    """The smallest e >= -64 with |x| <= 448 * 2^e for every finite element (a Python int)."""
+    a = x[torch.isfinite(x)].abs()
+    top = float(a.max()) if a.numel() else 0.0
+    e = -64
+    while top > 448 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def tail(block):
+    return max(16, block) // block
+
+
+def new_pool(num_blocks, heads, block, dim, seed=0):
+    """A pool of random bytes: stale contents, NaN codes and odd scales among them."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(0, 256, (num_blocks, heads, block, dim + tail(block)), generator=g, dtype=torch.int32).to(torch.uint8)
+
+
+def views(pool, dim):
+    """Codes [NB][Hkv][D / 16][B][16] and scales [NB][Hkv][1]."""
+    nb, heads, block, _ = pool.shape
+    flat = pool.view(nb, heads, -1)
+    return (flat[..., :block * dim].unflatten(-1, (dim // 16, block, 16)),
+            flat[..., block * dim:block * dim + 4].view(torch.float32))
+
+
+def append(pool, x, tables, starts, lens):
+    """Rows [T][Hkv][D] (a CPU tensor of a 16-bit type) into a CPU pool behind each sequence's older tokens."""
+    block, dim = pool.shape[2], x.shape[-1]
+    codes, scale = views(pool, dim)
+    x = x.double()
+    for s, L in enumerate(int(n) for n in lens):
+        a, b = int(starts[s]), int(starts[s + 1])
+        old = L - (b - a)
+        if a == b:
+            continue
+        for j in range(old // block, -(-L // block)):
+            bid = int(tables[s, j])
+            first, end = max(old, j * block), min(L, (j + 1) * block)
+            held = first - j * block                       # older tokens in front of them, if any
+            new = x[a + first - old:a + end - old]         # [n][Hkv][D]
+            for h in range(x.shape[1]):
+                e = exponent(new[:, h])
+                if held:
+                    before = int(math.log2(float(scale[bid, h, 0])))
+                    if before > e:
+                        e = before
+                    elif before < e:
+                        was = codes[bid, h, :, :held]
+                        codes[bid, h, :, :held] = code(value(was) * 2.0 ** (before - e))
+                c = code(new[:, h] * 2.0 ** -e)            # [n][D]
+                codes[bid, h, :, held:held + len(new)] = c.unflatten(-1, (-1, 16)).transpose(0, 1)
+                scale[bid, h, 0] = 2.0 ** e
+
+
+def read(pool, slots, dim):
+    """fp64 rows [T][Hkv][D] of a CPU pool."""
+    block = pool.shape[2]
+    codes, scale = views(pool, dim)
+    b, o = slots // block, slots % block
+    return value(codes[b, :, :, o]).flatten(-2) * scale[b].double()
+
+
+def filled(lens, heads, block, dim, dtype, seed, spread=1.0, pad=0):
+    """Pools whose sequences hold N(0, spread) rows (each block's scale its own: every
+    third one is larger than it has to be), stale bytes elsewhere."""
+    tables, nb = tables_for(lens, block, seed, pad=pad)
+    g = torch.Generator().manual_seed(seed + 1)
+    pools = [new_pool(nb, heads, block, dim, seed + 2 + i) for i in range(2)]
+    for s, n in enumerate(int(n) for n in lens):
+        for pool in pools:
+            fill(pool, tables[s], (torch.randn(n, heads, dim, generator=g) * spread).to(dtype))
+    return pools[0], pools[1], tables
+
+
+def fill(pool, table, x):
+    """A sequence's rows x [n][Hkv][D] into its blocks, block by block at once."""
+    block, dim, n = pool.shape[2], x.shape[-1], len(x)
+    codes, scale = views(pool, dim)
+    for j in range(-(-n // block)):
+        rows, bid = x[j * block:(j + 1) * block].double(), int(table[j])
+        top = rows.abs().amax((0, 2)).clamp(min=448 * 2.0 ** -64)
+        e = torch.ceil(torch.log2(top / 448)) + (j % 3 == 2)
+        c = code(rows * torch.exp2(-e)[None, :, None])     # [n][Hkv][D]
+        codes[bid, :, :, :len(rows)] = c.unflatten(-1, (-1, 16)).permute(1, 2, 0, 3)
+        scale[bid, :, 0] = torch.exp2(e).float()
+
+
+def attention(q, pools, tables, starts, lens, scale, dim):
+    """fp64 causal attention of rows starts[s] .. starts[s + 1] over sequence s's
+    first lens[s] tokens (the chunk its last ones); zero rows without keys."""
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    heads = pools[0].shape[1]
+    group, block = q.shape[1] // heads, pools[0].shape[2]
+    for s, n in enumerate(int(n) for n in lens):
+        a, b = int(starts[s]), int(starts[s + 1])
+        if n == 0 or a == b:
+            continue
+        k, v = (read(p, sequence_slots(tables, s, n, block), dim) for p in pools)
+        x = q[a:b].double().unflatten(1, (heads, group))
+        z = torch.einsum("rhgd,khd->rhgk", x, k) * scale
+        seen = torch.arange(n)[None] <= torch.arange(n - (b - a), n)[:, None]
+        w = torch.softmax(z.masked_fill(~seen[:, None, None], float("-inf")), -1)
+        out[a:b] = torch.einsum("rhgk,khd->rhgd", w, v).flatten(1, 2)
+    return out
