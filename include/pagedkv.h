@@ -696,6 +696,25 @@ int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_
                               int dtype, void *stream);
 
 /*
+ * paged_attention_prefill_q8 -- paged_attention_prefill_split over 8-bit pools.
+ *
+ * The same causal attention of each sequence's chunk of query rows, with K and V
+ * the values that the codes stand for; a probability times its token's V scale is
+ * rounded to fp16, relative to a running maximum as in the decode; scores, softmax
+ * statistics and output sums are fp32. Arguments, limits, workspace and key_parts as
+ * paged_attention_prefill_q4's. In bf16 caches values of V may be 2^70 at most. A
+ * NaN or an infinity in a row of q makes that row's outputs of the head NaN, a NaN
+ * code in K or V those of the rows that attend to its token.
+ */
+int paged_attention_prefill_q8(const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *query_start,
+                               const int32_t *context_lens, float scale, void *out, int num_seqs,
+                               int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads,
+                               int head_dim, int num_blocks, int block_size, int max_blocks_per_seq,
+                               int dtype, int key_parts, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
  * paged_kv_build_tables -- a step's block tables, token lists and slots, on
  * the GPU.
  *

@@ -30,6 +30,8 @@ The entry points keep the C names:
     paged_kv_gather_q8(k_cache, v_cache, slot_mapping, k, v)
     paged_attention_decode_q8(q, k_cache, v_cache, block_tables, context_lens, scale, out,
                               partition_tokens=0, workspace=None)
+    paged_attention_prefill_q8(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
+                               out, max_query_len=None, workspace=None, key_parts=1)
 
 All tensors live on the current CUDA device; work is enqueued on the current
 torch stream (or the stream passed) and the calls return without waiting.
@@ -52,7 +54,8 @@ __all__ = [
     "prefill_workspace_bytes", "prefill_workspace",
     "paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
     "paged_attention_decode_q4", "paged_attention_prefill_q4", "new_q4_pool",
-    "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8", "new_q8_pool",
+    "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8", "paged_attention_prefill_q8",
+    "new_q8_pool",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,7 +75,8 @@ EXPORTS = ("paged_kv_slot_mapping", "paged_kv_append", "paged_attention_decode",
            "pagedkv_check_bounded_wait", "paged_attention_prefill_split",
            "paged_attention_prefill_workspace_bytes", "paged_kv_build_tables", "paged_kv_append_q4",
            "paged_kv_gather_q4", "paged_attention_decode_q4", "paged_attention_prefill_q4",
-           "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8")
+           "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8",
+           "paged_attention_prefill_q8")
 
 
 class PagedKVError(RuntimeError):
@@ -132,9 +136,10 @@ def load():
     lib.paged_kv_append_q8.argtypes = [vp] * 7 + [i32] * 8 + [vp]
     lib.paged_kv_gather_q8.argtypes = lib.paged_kv_gather_q4.argtypes
     lib.paged_attention_decode_q8.argtypes = lib.paged_attention_decode.argtypes
+    lib.paged_attention_prefill_q8.argtypes = lib.paged_attention_prefill_split.argtypes
     for name in ("paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
                  "paged_attention_decode_q4", "paged_attention_prefill_q4", "paged_kv_append_q8",
-                 "paged_kv_gather_q8", "paged_attention_decode_q8"):
+                 "paged_kv_gather_q8", "paged_attention_decode_q8", "paged_attention_prefill_q8"):
         getattr(lib, name).restype = i32
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
@@ -586,6 +591,19 @@ def paged_attention_decode_q8(q, k_cache, v_cache, block_tables, context_lens, s
     tokens; workspace from new_workspace)."""
     (_fast or _binding()).decode_q8(q, k_cache, v_cache, block_tables, context_lens, scale, out,
                                     partition_tokens, workspace, stream)
+
+
+def paged_attention_prefill_q8(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
+                               out, max_query_len=None, stream=None, workspace=None, key_parts=1):
+    """paged_attention_prefill over 8-bit pools, with the arguments of
+    paged_attention_prefill_q4."""
+    if max_query_len is None:
+        max_query_len = _longest_chunk(query_start, stream)
+    if workspace is None and key_parts != 1:
+        with _on(stream):
+            workspace = prefill_workspace(q)
+    (_fast or _binding()).prefill_q8(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
+                                     out, max_query_len, workspace, key_parts, stream)
 
 
 def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, free_count, block_size,

@@ -161,6 +161,72 @@ int decode_packed(int bits, const void *q, const void *k_cache, const void *v_ca
     return done(e);
 }
 
+// paged_attention_prefill_q4 and paged_attention_prefill_q8.
+int prefill_packed(int bits, const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *query_start,
+                               const int32_t *context_lens, float scale, void *out, int num_seqs,
+                               int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads, int head_dim,
+                               int num_blocks, int block_size, int max_blocks_per_seq, int dtype,
+                               int key_parts, void *workspace, size_t workspace_bytes, void *stream) {
+    if (key_parts < 0 || key_parts > 32 || num_seqs < 0 || num_tokens < 0 || max_query_len < 0 ||
+        n_q_heads < 1 || max_blocks_per_seq < 1)
+        return PAGEDKV_ERR_INVALID_ARG;
+    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
+    if (st == PAGEDKV_ERR_INVALID_ARG) return st;
+    if (n_q_heads % n_kv_heads != 0 || !finite(scale)) return PAGEDKV_ERR_INVALID_ARG;
+    if (st != PAGEDKV_OK) return st;
+    const int group = n_q_heads / n_kv_heads;
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    if (group > 64 || num_seqs > 65535 || cap > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PAGEDKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !query_start || !context_lens || !out)
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(q, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
+        !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(query_start, 4) ||
+        !api_aligned(context_lens, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    pkv::PrefillParams p{};
+    int sms = 0;
+    st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.q = q;
+    p.k_packed = static_cast<const uint8_t *>(k_cache);
+    p.v_packed = static_cast<const uint8_t *>(v_cache);
+    p.block_tables = block_tables;
+    p.query_start = query_start;
+    p.context_lens = context_lens;
+    p.out = out;
+    p.scale_log2 = scale * pkv::kLog2e;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = group;
+    p.tile_tokens = 2 * (128 / group);
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    while ((1 << p.log2_block) < block_size) ++p.log2_block;
+    p.max_blocks = max_blocks_per_seq;
+    // the persistent kernel counts its work items in ints
+    const long long per_seq = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens * n_kv_heads;
+    if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
+    if (key_parts == 0)
+        key_parts = workspace && workspace_bytes >= paged_attention_prefill_workspace_bytes(head_dim) &&
+                            split_pays(per_seq * num_seqs, (cap + 63) / 64, num_seqs, sms)
+                        ? 32
+                        : 1;
+    st = pkv::api_plan_key_split(p, key_parts, workspace, workspace_bytes, head_dim, max_query_len, sms);
+    if (st != PAGEDKV_OK) return st;
+    CUtensorMap qmap;
+    st = pkv::api_encode_q_map(&qmap, q, dtype, head_dim, n_q_heads, num_tokens, group);
+    if (st != PAGEDKV_OK) return st;
+    cudaError_t e = pkv::launch_prefill_packed_tc(bits, dtype, head_dim, qmap, p, max_query_len, sms,
+                                              static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && p.key_parts > 1)
+        e = pkv::launch_prefill_merge(dtype, head_dim, p, max_query_len, sms, static_cast<cudaStream_t>(stream));
+    return done(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -308,63 +374,20 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
                                int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads, int head_dim,
                                int num_blocks, int block_size, int max_blocks_per_seq, int dtype,
                                int key_parts, void *workspace, size_t workspace_bytes, void *stream) {
-    if (key_parts < 0 || key_parts > 32 || num_seqs < 0 || num_tokens < 0 || max_query_len < 0 ||
-        n_q_heads < 1 || max_blocks_per_seq < 1)
-        return PAGEDKV_ERR_INVALID_ARG;
-    int st = check_pool(num_blocks, block_size, n_kv_heads, head_dim, dtype);
-    if (st == PAGEDKV_ERR_INVALID_ARG) return st;
-    if (n_q_heads % n_kv_heads != 0 || !finite(scale)) return PAGEDKV_ERR_INVALID_ARG;
-    if (st != PAGEDKV_OK) return st;
-    const int group = n_q_heads / n_kv_heads;
-    const long long cap = (long long)max_blocks_per_seq * block_size;
-    if (group > 64 || num_seqs > 65535 || cap > INT_MAX / 2) return PAGEDKV_ERR_UNSUPPORTED;
-    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PAGEDKV_OK;
-    if (!q || !k_cache || !v_cache || !block_tables || !query_start || !context_lens || !out)
-        return PAGEDKV_ERR_INVALID_ARG;
-    if (!api_aligned(q, 16) || !api_aligned(k_cache, 16) || !api_aligned(v_cache, 16) ||
-        !api_aligned(out, 16) || !api_aligned(block_tables, 4) || !api_aligned(query_start, 4) ||
-        !api_aligned(context_lens, 4))
-        return PAGEDKV_ERR_INVALID_ARG;
-    pkv::PrefillParams p{};
-    int sms = 0;
-    st = api_device_state(&p.err, &sms);
-    if (st != PAGEDKV_OK) return st;
-    p.q = q;
-    p.k_q4 = static_cast<const uint8_t *>(k_cache);
-    p.v_q4 = static_cast<const uint8_t *>(v_cache);
-    p.block_tables = block_tables;
-    p.query_start = query_start;
-    p.context_lens = context_lens;
-    p.out = out;
-    p.scale_log2 = scale * pkv::kLog2e;
-    p.num_seqs = num_seqs;
-    p.num_tokens = num_tokens;
-    p.n_q_heads = n_q_heads;
-    p.n_kv_heads = n_kv_heads;
-    p.group = group;
-    p.tile_tokens = 2 * (128 / group);
-    p.num_blocks = num_blocks;
-    p.block_size = block_size;
-    while ((1 << p.log2_block) < block_size) ++p.log2_block;
-    p.max_blocks = max_blocks_per_seq;
-    // the persistent kernel counts its work items in ints
-    const long long per_seq = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens * n_kv_heads;
-    if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;
-    if (key_parts == 0)
-        key_parts = workspace && workspace_bytes >= paged_attention_prefill_workspace_bytes(head_dim) &&
-                            split_pays(per_seq * num_seqs, (cap + 63) / 64, num_seqs, sms)
-                        ? 32
-                        : 1;
-    st = pkv::api_plan_key_split(p, key_parts, workspace, workspace_bytes, head_dim, max_query_len, sms);
-    if (st != PAGEDKV_OK) return st;
-    CUtensorMap qmap;
-    st = pkv::api_encode_q_map(&qmap, q, dtype, head_dim, n_q_heads, num_tokens, group);
-    if (st != PAGEDKV_OK) return st;
-    cudaError_t e = pkv::launch_prefill_q4_tc(dtype, head_dim, qmap, p, max_query_len, sms,
-                                              static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess && p.key_parts > 1)
-        e = pkv::launch_prefill_merge(dtype, head_dim, p, max_query_len, sms, static_cast<cudaStream_t>(stream));
-    return done(e);
+    return prefill_packed(4, q, k_cache, v_cache, block_tables, query_start, context_lens, scale, out, num_seqs, num_tokens,
+                          max_query_len, n_q_heads, n_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, dtype,
+                          key_parts, workspace, workspace_bytes, stream);
+}
+
+int paged_attention_prefill_q8(const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *query_start,
+                               const int32_t *context_lens, float scale, void *out, int num_seqs,
+                               int num_tokens, int max_query_len, int n_q_heads, int n_kv_heads, int head_dim,
+                               int num_blocks, int block_size, int max_blocks_per_seq, int dtype,
+                               int key_parts, void *workspace, size_t workspace_bytes, void *stream) {
+    return prefill_packed(8, q, k_cache, v_cache, block_tables, query_start, context_lens, scale, out, num_seqs, num_tokens,
+                          max_query_len, n_q_heads, n_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, dtype,
+                          key_parts, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

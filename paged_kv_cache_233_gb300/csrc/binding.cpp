@@ -240,7 +240,8 @@ PyObject *prefill(int bits, PyObject *const *a, Py_ssize_t n) {
         const int d = device_of(q), code = dtype_code(q);
         size_t bytes;
         void *ws = workspace_of(d, a[9], &bytes);
-        return done(paged_attention_prefill_q4(
+        const auto call = bits == 8 ? paged_attention_prefill_q8 : paged_attention_prefill_q4;
+        return done(call(
                         on(d, q, "q", q.scalar_type()), on(d, kc, "k_cache", at::kByte), on(d, vc, "v_cache", at::kByte),
                         static_cast<const int32_t *>(on(d, bt, "block_tables", at::kInt)),
                         static_cast<const int32_t *>(on(d, start, "query_start", at::kInt)),
@@ -248,11 +249,12 @@ PyObject *prefill(int bits, PyObject *const *a, Py_ssize_t n) {
                         on(d, out, "out", q.scalar_type()), narrow(S), narrow(q.size(0)), most, narrow(q.size(1)),
                         p.heads, narrow(q.size(2)), p.blocks, p.block, narrow(bt.size(1)), code, parts, ws, bytes,
                         stream_of(a[11])),
-                    "paged_attention_prefill_q4");
+                    bits == 8 ? "paged_attention_prefill_q8" : "paged_attention_prefill_q4");
     });
 }
 
 PyObject *prefill_q4(PyObject *, PyObject *const *a, Py_ssize_t n) { return prefill(4, a, n); }
+PyObject *prefill_q8(PyObject *, PyObject *const *a, Py_ssize_t n) { return prefill(8, a, n); }
 
 // new_lens, context_lens, block_tables, free_blocks, free_count, block_size, num_blocks, query_start, token_seq,
 // token_pos, slot_mapping, context_lens_out, free_count_out, stream
@@ -296,6 +298,7 @@ PyMethodDef g_methods[] = {
     {"gather_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gather_q4)), METH_FASTCALL, nullptr},
     {"append_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_q8)), METH_FASTCALL, nullptr},
     {"gather_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gather_q8)), METH_FASTCALL, nullptr},
+    {"prefill_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill_q8)), METH_FASTCALL, nullptr},
     {"decode_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q8)), METH_FASTCALL, nullptr},
     {"decode_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q4)), METH_FASTCALL, nullptr},
     {"prefill_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill_q4)), METH_FASTCALL, nullptr},

@@ -56,7 +56,7 @@
 // mbarrier wait is bounded in time; on a timeout the CTA stops, waits for its
 // copies and MMAs in flight, frees its tensor memory and exits.
 //
-// 4-bit pools (kQ4, layout in q4.h) take the same kernel with four more warps.
+// 4-bit pools (kBits 4, layout in q4.h) take the same kernel with four more warps.
 // The producer copies a key tile's blocks as they lie (a bulk copy per block
 // and operand) into a ring of raw tiles of their own; warps 12-15 turn each raw
 // tile into a stage, 32 keys of one operand each: a word of eight codes becomes eight
@@ -76,6 +76,7 @@
 #include "prefill.h"
 #include "ptx.cuh"
 #include "q4.cuh"
+#include "q8.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -93,14 +94,19 @@ constexpr int kTcStages = 4;
 constexpr int kIssuer1Warp = 2 + kTcTiles * kTcRows / 32;
 constexpr int kZeroWarp = kIssuer1Warp + 1;
 constexpr int kTcThreads = 32 * (kZeroWarp + 1);
-// 4-bit pools: four more warps (two would take longer over a tile at head size
-// 128 than its MMAs), and a ring of raw key tiles (four at head size 64: the same time)
+// 4- and 8-bit pools: four more warps (two would take longer over a 4-bit tile at
+// head size 128 than its MMAs), and a ring of raw key tiles (four at head size 64:
+// the same time)
 constexpr int kDqWarp0 = kZeroWarp + 1;
 constexpr int kDqWarps = 4;
-constexpr int kRawStages = 2;
-template <bool kQ4> constexpr int tc_threads() { return kTcThreads + (kQ4 ? 32 * kDqWarps : 0); }
+template <int kBits> constexpr int tc_threads() { return kTcThreads + (kBits < 16 ? 32 * kDqWarps : 0); }
 constexpr int kTmemTile = 256;   // tensor-memory columns per Q tile: S, S, O
-constexpr float kRescaleLog2 = 8.f;  // the reference maximum moves past 2^8
+// the reference moves when a tile's maximum passes it by more than kMovePast, to
+// the maximum less kBelowMax: past 2^8, to the maximum itself; with 8-bit pools,
+// whose P carries V's exponent, past 2^14, to 2^6 below, which leaves fp16 more of its
+// small end
+template <int kBits> constexpr float move_past() { return kBits == 8 ? 14.f : 8.f; }
+template <int kBits> constexpr float below_max() { return kBits == 8 ? 6.f : 0.f; }
 
 // mbarrier indices
 constexpr int kKvFull = 0;
@@ -133,8 +139,8 @@ constexpr int kNumBars = kTailV + kTcStages;
 constexpr int kMinPartTiles = 16;
 // (a merge costs less here than the tiles that a shorter range saves: 33 rows
 // after 6001 tokens 24 us, with ranges of 16 tiles or more 31)
-constexpr int kMinPartTilesQ4 = 6;
-template <bool kQ4> constexpr int min_part_tiles() { return kQ4 ? kMinPartTilesQ4 : kMinPartTiles; }
+constexpr int kMinPartTilesPacked = 6;
+template <int kBits> constexpr int min_part_tiles() { return kBits < 16 ? kMinPartTilesPacked : kMinPartTiles; }
 constexpr int kMaxSplitParts = kPfMaxSplitParts;   // pieces of one item (a merge lane each)
 // the split's plan in the item-order region: off[i] = key tiles of items
 // before i (i = 0 .. items), then this CTA's range
@@ -144,8 +150,12 @@ constexpr int kPlanRange = 504;        // r, start, end, first item, piece count
 // items keep the sequences' own order)
 constexpr int kMaxRankedSeqs = 256;
 
-template <int D>
+template <int D, int kBits>
 struct TcLayout {
+    // (8-bit tiles of head size 128 leave room for three stages: the least that the
+    // issuers work with, two S ahead of a P V)
+    static constexpr int kStages = kBits == 8 && D == 128 ? 3 : kTcStages;
+    static constexpr int kRawStages = kBits == 8 ? 3 : 2;
     static constexpr int kSlabs = D * 2 / 128;             // 64-element column blocks per row
     static constexpr int kQSlab = kTcRows * 128;           // bytes of one Q column block
     static constexpr int kKvSlab = kTcKeys * 128;          // bytes of one K (or V) column block
@@ -154,7 +164,7 @@ struct TcLayout {
     static constexpr int kKv = kQ + kTcTiles * kQTile;     // stage s: K at kKv + s*kStage, V after it
     static constexpr int kHalf = kSlabs * kKvSlab;
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kBars = kKv + kTcStages * kStage;
+    static constexpr int kBars = kKv + kStages * kStage;
     static constexpr int kTmemSlot = kBars + 8 * kNumBars;
     static constexpr int kFlag = kTmemSlot + 8;
     static constexpr int kOrder = kFlag + 8;               // ranked sequence ids, then their lengths
@@ -164,11 +174,17 @@ struct TcLayout {
     static constexpr int kOutRow = kOrder + 8 * kMaxRankedSeqs;
     static constexpr int kRefRow = kOutRow + 8 * kTcTiles * kTcRows;
     static constexpr int kTotal = kRefRow + 4 * kTcTiles * kTcRows;
-    // 4-bit pools: the raw ring's barriers (full, empty), then its tiles: K's blocks, V's
-    static constexpr int kRawBars = (kTotal + 15) & ~15;
+    // 8-bit pools, per stage: for each 8 keys what turns their sums into scores, V's
+    // exponent and the inverse of V's scale, then a bit for each key whose V has a NaN
+    static constexpr int kScales = (kTotal + 15) & ~15;
+    static constexpr int kScalesStage = kTcKeys / 8 * 16 + 16;
+    // 4- and 8-bit pools: the raw ring's barriers (full, empty), then its tiles: K's
+    // blocks, V's (8-bit: with the scales behind the codes, blocks of 8 have the most)
+    static constexpr int kRawBars = kScales + (kBits == 8 ? kStages * kScalesStage : 0);
     static constexpr int kRaw = kRawBars + 16 * kRawStages;
-    static constexpr int kRawHalf = kTcKeys * D * 5 / 8;
-    static constexpr int kTotalQ4 = kRaw + kRawStages * 2 * kRawHalf;
+    static constexpr int kRawHalf = kBits == 8 ? kTcKeys / 8 * q8_head_bytes(8, D) : kTcKeys * D * 5 / 8;
+    static constexpr int kTotalPacked = kRaw + kRawStages * 2 * kRawHalf;
+    static_assert((kBits < 16 ? kTotalPacked : kTotal) + 1024 <= 227 * 1024, "the shared memory of a block");
     static_assert(2 * kTcKeys + D <= kTmemTile, "S buffers and O must fit a Q tile's columns");
     static_assert(kMaxSplitItems < kPlanRange && 4 * (kPlanRange + 6) <= 8 * kMaxRankedSeqs,
                   "the key split's plan must fit the item-order region");
@@ -197,6 +213,17 @@ __device__ __forceinline__ uint4 lds128_u4(uint32_t addr) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                  ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ float2 lds64_f2(uint32_t addr) {
+    float2 r;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ unsigned long long lds64_u(uint32_t addr) {
+    unsigned long long r;
+    asm volatile("ld.shared.u64 %0, [%1];" : "=l"(r) : "r"(addr) : "memory");
+    return r;
 }
 
 // Shared-memory word at a 32-bit shared address (a generic pointer would hold
@@ -336,7 +363,7 @@ __device__ __forceinline__ int pf_item_index(int m) {
 // Every thread of the CTA calls it.
 constexpr int kPieceCost = 4;   // a piece's fixed cost (Q copy, epilogue, merge) in key tiles
 constexpr int kMaxItemParts = 16;  // CTAs per item in the parts layout at most
-template <bool kQ4>
+template <int kBits>
 __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles, int items, int *off,
                                               bool report) {
     for (int i = int(threadIdx.x); i < items; i += int(blockDim.x)) {
@@ -360,7 +387,7 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
             sum += n;
             mx = max(mx, n);
             if (pp > 0) {
-                const int eff = min(pp, max(1, (n + min_part_tiles<kQ4>() - 1) / min_part_tiles<kQ4>()));
+                const int eff = min(pp, max(1, (n + min_part_tiles<kBits>() - 1) / min_part_tiles<kBits>()));
                 part_mx = max(part_mx, (n + eff - 1) / eff);
             }
         }
@@ -383,7 +410,7 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
             off[0] = 0;
             int r = (T + G - 1) / G;
             if (mx > 1) r = max(r, (mx - 2) / (p.key_parts - 1) + 1);
-            r = max(r, max(min(min_part_tiles<kQ4>(), mx), 1));
+            r = max(r, max(min(min_part_tiles<kBits>(), mx), 1));
             const int c = int(blockIdx.x);
             long long start, end;
             int first, count;
@@ -393,7 +420,7 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
             if (parts_layout) {
                 const int i = c / pp, q = c - i * pp;
                 const int n = i < items ? off[i + 1] - off[i] : 0;
-                const int eff = min(pp, max(1, (n + min_part_tiles<kQ4>() - 1) / min_part_tiles<kQ4>()));
+                const int eff = min(pp, max(1, (n + min_part_tiles<kBits>() - 1) / min_part_tiles<kBits>()));
                 first = i;
                 count = n > 0 && q < eff ? 1 : 0;
                 start = count ? off[i] + (long long)n * q / eff : 0;
@@ -431,13 +458,14 @@ __device__ __forceinline__ void pf_split_plan(const PrefillParams &p, int tiles,
 
 }  // namespace
 
-template <typename T, int D, bool kSplit, bool kQ4>
-__global__ void __launch_bounds__(tc_threads<kQ4>(), 1)
+template <typename T, int D, bool kSplit, int kBits>
+__global__ void __launch_bounds__(tc_threads<kBits>(), 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ CUtensorMap qmap, const PrefillParams p, int tiles) {
-    using Ly = TcLayout<D>;
-    constexpr bool kBf16 = Elem<T>::kBf16;
+    using Ly = TcLayout<D, kBits>;
+    constexpr bool kBf16 = Elem<T>::kBf16, kPacked = kBits < 16;
+    constexpr int kStages = Ly::kStages, kRawStages = Ly::kRawStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -452,14 +480,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const int g = p.group;
     const int all_items = p.num_seqs * tiles * p.n_kv_heads;
     // (the tables, lengths and offsets may be the kernel's before this one)
-    if (kQ4 || p.late_inputs) grid_dependency_wait();
+    if (kPacked || p.late_inputs) grid_dependency_wait();
 
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kTcStages; ++k) {
-            mbar_init(bar(kKvFull + k), kQ4 ? kDqWarps : 1);
+        for (int k = 0; k < kStages; ++k) {
+            mbar_init(bar(kKvFull + k), kPacked ? kDqWarps : 1);
             mbar_init(bar(kKvEmpty + k), kTcTiles);   // one commit per issuer and key tile
         }
-        if (kQ4) {
+        if (kPacked) {
             for (int k = 0; k < kRawStages; ++k) {
                 mbar_init(base + Ly::kRawBars + 16 * k, 1);
                 mbar_init(base + Ly::kRawBars + 16 * k + 8, kDqWarps);
@@ -475,7 +503,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             mbar_init(bar(bar_qfree(t)), 1);
         }
         mbar_init(bar(kDone), kTcTiles);
-        for (int k = 0; k < kTcStages; ++k) mbar_init(bar(kTailV + k), 1);
+        for (int k = 0; k < kStages; ++k) mbar_init(bar(kTailV + k), 1);
         sts32(flag, 0);
         fence_barrier_init();
     }
@@ -506,7 +534,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     if (kSplit) {
         // (the launcher keeps the split to at most kMaxSplitItems items)
         order = base + Ly::kOrder;
-        pf_split_plan<kQ4>(p, tiles, all_items, reinterpret_cast<int *>(sm + Ly::kOrder), blockIdx.x == 0);
+        pf_split_plan<kBits>(p, tiles, all_items, reinterpret_cast<int *>(sm + Ly::kOrder), blockIdx.x == 0);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -523,7 +551,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // each, most of a key tile's period at D = 128). Stages run on across
         // the CTA's items, so the next item's first tiles load while the
         // current one finishes.
-        if (!kQ4 && lane == 0) {
+        if (!kPacked && lane == 0) {
             tma_prefetch_descriptor(&kmap);
             tma_prefetch_descriptor(&vmap);
         }
@@ -541,7 +569,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 int c0 = 0, pieces = 0;
                 if (n > 0 && pp > 0) {
                     c0 = i * pp;
-                    pieces = min(pp, max(1, (n + min_part_tiles<kQ4>() - 1) / min_part_tiles<kQ4>()));
+                    pieces = min(pp, max(1, (n + min_part_tiles<kBits>() - 1) / min_part_tiles<kBits>()));
                 } else if (n > 0) {
                     c0 = o / r;
                     pieces = (o + n - 1) / r - c0 + 1;
@@ -562,10 +590,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             PfItem it;
             if (!pf_item<kSplit>(p, order, tiles, k, lane == 0, it)) continue;
             const int32_t *table = p.block_tables + size_t(it.s) * p.max_blocks;
-            if constexpr (kQ4) {
+            if constexpr (kPacked) {
                 // a tile's blocks, K and V, a lane per copy
-                const int hb = q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
-                const uint8_t *pool = op ? p.v_q4 : p.k_q4;
+                const int hb = kBits == 8 ? q8_head_bytes(B, D) : q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
+                const uint8_t *pool = op ? p.v_packed : p.k_packed;
                 for (int j = 0; j < it.nkt; ++j) {
                     const int gk = kt + j;
                     const int st = gk % kRawStages;
@@ -596,7 +624,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
             } else for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
-                const int st = gk % kTcStages;
+                const int st = gk % kStages;
                 const int k0 = (it.kb + j) * kTcKeys;
                 const int present = min(kTcKeys, it.L - k0);
                 const int boxes = (present + rows_per_box - 1) / rows_per_box;
@@ -608,7 +636,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 bool got = true;
                 if (lane == 0) {
                     got = !aborted() &&
-                          mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err);
+                          mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u, p.err);
                     if (got && !last_tail) {
                         mbar_arrive_expect_tx(bar(kKvFull + st), 2 * half);
                     } else if (got) {
@@ -645,10 +673,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // (a tail stage completes only with the zeroing warp's arrival: when that
             // warp stopped too, the wait ends at its time limit, its copies long done)
             sts32(flag, 1);
-            constexpr int kRing = kQ4 ? kRawStages : kTcStages;
+            constexpr int kRing = kPacked ? kRawStages : kStages;
             const int first = armed > kRing ? armed - kRing : 0;
             for (int x = first; x < armed; ++x)
-                mbar_wait(kQ4 ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kTcStages),
+                mbar_wait(kPacked ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kStages),
                           uint32_t((x / kRing) & 1), p.err);
         }
         __syncwarp();
@@ -719,8 +747,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     break;
                 }
             }
-            if (!kQ4 && it.tail) {
-                const int st = (kt + it.nkt - 1) % kTcStages;
+            if (!kPacked && it.tail) {
+                const int st = (kt + it.nkt - 1) % kStages;
                 const int present = it.L - (it.kb + it.nkt - 1) * kTcKeys;
                 bool got = true;
                 if (lane == 0)
@@ -752,15 +780,18 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (qlast[t] >= 0) mbar_wait(bar(bar_qfull(t)), uint32_t(qlast[t] & 1), p.err);
         }
         __syncwarp();
-    } else if (kQ4 && warp >= kDqWarp0) {
-        // -------------------------------------- 4-bit pools: raw tiles to stages
-        // A lane owns a key row of K or V: its pairs, then per group 16 bytes of
-        // codes, each word of which is one 16-byte chunk of the stage's row.
+    } else if (kPacked && warp >= kDqWarp0) {
+        // ------------------------------- 4- and 8-bit pools: raw tiles to stages
+        // A lane owns a key row of K or V. 4 bits: its pairs, then per group 16 bytes
+        // of codes, each word of which is one 16-byte chunk of the stage's row. 8
+        // bits: per panel 16 bytes of codes, two chunks, and for each 8 keys the scales.
         constexpr int G = D / kQ4Group;
         const int row = 32 * (warp & 1) + lane, op = (warp - kDqWarp0) >> 1;
-        const int hb = q4_head_bytes(B, D), blk = row >> p.log2_block, off = row & (B - 1);
+        const int hb = kBits == 8 ? q8_head_bytes(B, D) : q4_head_bytes(B, D);
+        const int blk = row >> p.log2_block, off = row & (B - 1);
         const uint32_t src = base + Ly::kRaw + uint32_t(blk * hb + off * 16);
         const uint32_t pairs = base + Ly::kRaw + uint32_t(blk * hb + q4_pairs_at(B, D) + off * 4 * G);
+        const uint32_t scale = base + Ly::kRaw + uint32_t(blk * hb + q8_scale_at(B, D));
         const uint32_t dst = base + Ly::kKv + uint32_t(row * 128 + ((row & 7) << 4));
         int kt = 0;
         bool ok = true;
@@ -771,19 +802,19 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
             for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
-                const int st = gk % kTcStages, rs = gk % kRawStages;
+                const int st = gk % kStages, rs = gk % kRawStages;
                 const uint32_t rfull = base + Ly::kRawBars + 16 * rs;
                 const bool live = (it.kb + j) * kTcKeys + row < it.L;
                 // the raw tile is there, and the stage's last readers are done
                 bool got = mbar_try_wait(rfull, uint32_t((gk / kRawStages) & 1)) ||
                            (!aborted() && mbar_wait(rfull, uint32_t((gk / kRawStages) & 1), p.err));
-                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u) ||
-                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err)));
+                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u) ||
+                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u, p.err)));
                 if (!__all_sync(kAll, got)) {
                     ok = false;
                     break;
                 }
-                {
+                if constexpr (kBits == 4) {
                     const uint32_t from = uint32_t(rs * 2 * Ly::kRawHalf + op * Ly::kRawHalf);
                     const uint32_t to = dst + uint32_t(st * Ly::kStage + op * Ly::kHalf);
                     auto codes = [&](int i) { return lds128_u4(src + from + uint32_t(i * B * 16)); };
@@ -817,6 +848,54 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll 1
                         for (int i = 0; i < G; ++i) put(i, codes(i), pair(i));
                     }
+                } else if constexpr (kBits == 8) {
+                    const uint32_t from = uint32_t(rs * 2 * Ly::kRawHalf + op * Ly::kRawHalf);
+                    const uint32_t to = dst + uint32_t(st * Ly::kStage + op * Ly::kHalf);
+                    const uint32_t per8 = base + Ly::kScales + uint32_t(st * Ly::kScalesStage);
+                    if ((row & 7) == 0) {
+                        // (rows past the context: any finite numbers. A factor of 0 would
+                        // turn a masked score's -inf into a NaN.)
+                        const uint32_t v = live ? uint32_t(lds32(scale + from)) : 0x3f800000u;
+                        const uint32_t at = per8 + uint32_t(row >> 3) * 16;
+                        if (op == 0) {
+                            const float k = fabsf(p.scale_log2) * __uint_as_float(v);
+                            sts32(at, __float_as_int(k == 0.f ? 0x1p-126f : k));
+                        } else {
+                            sts32(at + 4, __float_as_int(float(int(v >> 23) - 127)));
+                            sts32(at + 8, int(0x7f000000u - v));
+                        }
+                    }
+                    uint32_t nan = 0;   // the sign bits of bytes that are NaN codes
+#pragma unroll 2
+                    for (int i = 0; i < D / kQ8Panel; ++i) {
+                        uint4 cw = lds128_u4(src + from + uint32_t(i * B * 16));
+                        if (!live) cw = make_uint4(0u, 0u, 0u, 0u);
+                        uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w}, x[8];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (op == 1) {
+                                // a NaN in V counts where its key is attended to (by the
+                                // key's bit), not under the weight 0 of rows that do not see it
+                                const uint32_t bad = ((w[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                nan |= bad;
+                                w[c] &= ~((bad >> 7) * 255u);
+                            }
+                            q8_halves(w[c], x[2 * c], x[2 * c + 1]);
+                            if (kBf16 && op == 0) {
+                                const float2 a = Elem<__half>::unpack2(x[2 * c]), b = Elem<__half>::unpack2(x[2 * c + 1]);
+                                x[2 * c] = Elem<__nv_bfloat16>::pack2(a.x, a.y);
+                                x[2 * c + 1] = Elem<__nv_bfloat16>::pack2(b.x, b.y);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            sts128((to ^ uint32_t((((2 * i) & 7) + c) << 4)) + uint32_t((i >> 2) * Ly::kKvSlab),
+                                   make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
+                    }
+                    if (op == 1) {
+                        const unsigned m = __ballot_sync(kAll, nan != 0);
+                        if (lane == 0) sts32(per8 + kTcKeys / 8 * 16 + 4 * (warp & 1), int(m));
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -841,8 +920,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         {
             const int t = warp == 1 ? 0 : 1;
             const bool leader = lane == 0;
-            constexpr uint32_t kIdS = tc_idesc_f16(kBf16, false, kTcRows, kTcKeys);
-            constexpr uint32_t kIdO = tc_idesc_f16(kBf16, true, kTcRows, D);
+            // (8-bit pools: S of -Q where the scale is negative, whose size the softmax
+            // applies; P and V's codes are fp16 in bf16 calls too)
+            const uint32_t kIdS = tc_idesc_f16(kBf16, false, kTcRows, kTcKeys) |
+                                  (kBits == 8 && p.scale_log2 < 0.f ? kTcNegateA : 0u);
+            constexpr uint32_t kIdO = tc_idesc_f16(kBf16 && kBits != 8, true, kTcRows, D);
             // every lane waits; the warp goes on only if all of them saw the phase
             // (a phase already complete passes at once; the abort flag is read only
             // when the lane has to wait)
@@ -866,7 +948,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 qdesc[kk] = tc_desc_sw128(qb + (kk >> 2) * Ly::kQSlab + (kk & 3) * 32, 16, 1024);
             // S of key tile gk of the ring (gj-th key tile of this Q tile) into S buffer gj & 1
             auto issue_s = [&](int gk, int gj) {
-                const uint64_t kdesc = tc_desc_sw128(base + Ly::kKv + (gk % kTcStages) * Ly::kStage, 16, 1024);
+                const uint64_t kdesc = tc_desc_sw128(base + Ly::kKv + (gk % kStages) * Ly::kStage, 16, 1024);
                 const uint32_t d = tmem + uint32_t(t * kTmemTile + (gj & 1) * kTcKeys);
                 if (leader) {
 #pragma unroll
@@ -882,7 +964,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // O (+)= P V; `first` starts the item's accumulator
             auto issue_pv = [&](int gk, int gj, bool first) {
                 const uint64_t vdesc =
-                    tc_desc_sw128(base + Ly::kKv + (gk % kTcStages) * Ly::kStage + Ly::kHalf, Ly::kKvSlab, 1024);
+                    tc_desc_sw128(base + Ly::kKv + (gk % kStages) * Ly::kStage + Ly::kHalf, Ly::kKvSlab, 1024);
                 // P: the first 32 columns of S buffer gj & 1 (16 keys per 8 columns)
                 const uint32_t pa = tmem + uint32_t(t * kTmemTile + (gj & 1) * kTcKeys);
                 const uint32_t d = tmem + uint32_t(t * kTmemTile + 2 * kTcKeys);
@@ -909,7 +991,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (!ok) break;
                 if (nk > 0) {
                     for (int j = 0; ok && j < 2 && j < nk; ++j) {
-                        ok = wait(kKvFull + (kt + j) % kTcStages, (kt + j) / kTcStages);
+                        ok = wait(kKvFull + (kt + j) % kStages, (kt + j) / kStages);
                         if (!ok) break;
                         tc_fence_after_sync();
                         issue_s(kt + j, jt + j);
@@ -934,18 +1016,18 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const int gk2 = gk + 2;
                         const bool kv_in = __all_sync(
                             kAll, ok && ahead &&
-                                      mbar_test_wait(bar(kKvFull + gk2 % kTcStages), uint32_t((gk2 / kTcStages) & 1)));
+                                      mbar_test_wait(bar(kKvFull + gk2 % kStages), uint32_t((gk2 / kStages) & 1)));
                         if (!ok) break;
                         tc_fence_after_sync();
                         issue_pv(gk, jt + j, j == 0);
                         // the stage of key tile j is free once this P V (the last MMA of
                         // this thread that reads it) completes
-                        commit(kKvEmpty + gk % kTcStages);
+                        commit(kKvEmpty + gk % kStages);
                         // this tile's S two key tiles ahead (its S buffer is free once the
                         // P V just issued has read P)
                         if (ahead) {
                             if (!kv_in) {
-                                ok = wait(kKvFull + gk2 % kTcStages, gk2 / kTcStages);
+                                ok = wait(kKvFull + gk2 % kStages, gk2 / kStages);
                                 if (!ok) break;
                                 tc_fence_after_sync();
                             }
@@ -955,9 +1037,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     } else {
                         // a key tile this Q tile skips: its stage may be released only
                         // after it landed (the arrival belongs to this phase of the slot)
-                        ok = wait(kKvFull + gk % kTcStages, gk / kTcStages);
+                        ok = wait(kKvFull + gk % kStages, gk / kStages);
                         if (!ok) break;
-                        commit(kKvEmpty + gk % kTcStages);
+                        commit(kKvEmpty + gk % kStages);
                     }
                 }
                 if (!ok) break;
@@ -1041,6 +1123,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             return true;
         };
         int jt = 0;   // key tiles of this Q tile before the item
+        [[maybe_unused]] int kt = 0;   // ring position of the item's first key tile (8-bit pools)
         int i = 0;
         for (int m = 0; ok; ++m) {
             const int k = pf_item_index<kSplit>(m);
@@ -1090,18 +1173,32 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                     for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
                 }
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float mx;
+                [[maybe_unused]] uint32_t per8;   // the stage's factors and exponents for each 8 keys
+                if constexpr (kBits == 8) {
+                    per8 = base + Ly::kScales + uint32_t(((kt + j) % kStages) * Ly::kScalesStage);
+                    mx = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < kTcKeys; x += 8) {
-                    m4[0] = fmax3(m4[0], sc[x], sc[x + 1]);
-                    m4[1] = fmax3(m4[1], sc[x + 2], sc[x + 3]);
-                    m4[2] = fmax3(m4[2], sc[x + 4], sc[x + 5]);
-                    m4[3] = fmax3(m4[3], sc[x + 6], sc[x + 7]);
+                    for (int u = 0; u < kTcKeys / 8; ++u) {
+                        const float2 f = lds64_f2(per8 + 16 * u);
+                        const float a = fmax3(fmax3(sc[8 * u], sc[8 * u + 1], sc[8 * u + 2]), sc[8 * u + 3], sc[8 * u + 4]);
+                        mx = fmaxf(mx, fmaf(fmax3(a, fmaxf(sc[8 * u + 5], sc[8 * u + 6]), sc[8 * u + 7]), f.x, f.y));
+                    }
+                } else {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < kTcKeys; x += 8) {
+                        m4[0] = fmax3(m4[0], sc[x], sc[x + 1]);
+                        m4[1] = fmax3(m4[1], sc[x + 2], sc[x + 3]);
+                        m4[2] = fmax3(m4[2], sc[x + 4], sc[x + 5]);
+                        m4[3] = fmax3(m4[3], sc[x + 6], sc[x + 7]);
+                    }
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
                 }
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-                const bool move = mx > ref + kRescaleLog2;
-                const float alpha = move ? fast_exp2(ref - mx) : 1.f;   // 0 while no key was seen
-                if (move) ref = mx;
+                const bool move = mx > ref + move_past<kBits>();
+                const float nref = kBits == 8 ? mx - below_max<kBits>() : mx;
+                const float alpha = move ? fast_exp2(ref - nref) : 1.f;   // 0 while no key was seen
+                if (move) ref = nref;
                 if (j > 0 && __any_sync(kAll, move)) {
                     // rescale this warp's rows of O (every earlier P V has completed first)
                     got = !aborted() &&
@@ -1120,20 +1217,46 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         tmem_st32(otile + uint32_t(32 * c), v);
                     }
                 }
-                const float nu = ref == -INFINITY ? 0.f : -ref;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < kTcKeys; x += 2) {
-                    ffma2(sc[x], sc[x + 1], p.scale_log2, nu);
-                    sc[x] = fast_exp2(sc[x]);
-                    sc[x + 1] = fast_exp2(sc[x + 1]);
-                    if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
-                    else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
-                }
-                l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
                 uint32_t pk[kTcKeys / 2];
+                if constexpr (kBits == 8) {
+                    l *= alpha;
 #pragma unroll
-                for (int c = 0; c < kTcKeys / 2; ++c) pk[c] = Elem<T>::pack2(sc[2 * c], sc[2 * c + 1]);
+                    for (int u = 0; u < kTcKeys / 8; ++u) {
+                        const uint4 f = lds128_u4(per8 + 16 * u);
+                        const float k = __uint_as_float(f.x);
+                        const float nu = ref == -INFINITY ? 0.f : __uint_as_float(f.y) - ref;
+                        float s2[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int x = 8 * u; x < 8 * u + 8; x += 2) {
+                            ffma2(sc[x], sc[x + 1], k, nu);
+                            sc[x] = fast_exp2(sc[x]);
+                            sc[x + 1] = fast_exp2(sc[x + 1]);
+                            fadd2(s2[0], s2[1], sc[x], sc[x + 1]);
+                            pk[x / 2] = Elem<__half>::pack2(sc[x], sc[x + 1]);
+                        }
+                        l = fmaf(s2[0] + s2[1], __uint_as_float(f.z), l);
+                    }
+                    // keys whose V holds a NaN, among those that this row attends to
+                    const unsigned long long bad = lds64_u(per8 + kTcKeys / 8 * 16);
+                    if (bad != 0) {
+                        const int seen = min(max(pos - k0 + 1, 0), kTcKeys);
+                        if (seen > 0 && (bad << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
+                    }
+                } else {
+                    const float nu = ref == -INFINITY ? 0.f : -ref;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < kTcKeys; x += 2) {
+                        ffma2(sc[x], sc[x + 1], p.scale_log2, nu);
+                        sc[x] = fast_exp2(sc[x]);
+                        sc[x + 1] = fast_exp2(sc[x + 1]);
+                        if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
+                        else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
+                    }
+                    l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+#pragma unroll
+                    for (int c = 0; c < kTcKeys / 2; ++c) pk[c] = Elem<T>::pack2(sc[2 * c], sc[2 * c + 1]);
+                }
                 tmem_st32u(trow + uint32_t(b * kTcKeys), pk);
                 // each lane's tensor-memory store has completed (tmem_st32u waits) and is
                 // ordered before the warp barrier; then one lane arrives for the warp
@@ -1147,6 +1270,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             prev_l = l;
             if (kSplit) sts32(ref_row, __float_as_int(ref));
             jt += nk;
+            if (kBits == 8) kt += it.nkt;
             ++i;
         }
         // the last item's output
@@ -1250,15 +1374,15 @@ paged_prefill_merge_kernel(const PrefillParams p, int tiles) {
 }
 
 int prefill_tc_smem_bytes(int head_dim) {
-    return (head_dim == 64 ? TcLayout<64>::kTotal : TcLayout<128>::kTotal) + 1024;
+    return (head_dim == 64 ? TcLayout<64, 16>::kTotal : TcLayout<128, 16>::kTotal) + 1024;
 }
 
-template <typename T, int D, bool kSplit, bool kQ4 = false>
+template <typename T, int D, bool kSplit, int kBits = 16>
 static cudaError_t launch_tc_instance(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                       const CUtensorMap &qmap, const PrefillParams &p, int max_query_len, int num_sms,
                                       cudaStream_t stream) {
-    auto kernel = paged_prefill_tc_kernel<T, D, kSplit, kQ4>;
-    const int smem = (kQ4 ? TcLayout<D>::kTotalQ4 : TcLayout<D>::kTotal) + 1024;
+    auto kernel = paged_prefill_tc_kernel<T, D, kSplit, kBits>;
+    const int smem = (kBits < 16 ? TcLayout<D, kBits>::kTotalPacked : TcLayout<D, kBits>::kTotal) + 1024;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1283,7 +1407,7 @@ static cudaError_t launch_tc_instance(const CUtensorMap &kmap, const CUtensorMap
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(tc_threads<kQ4>());
+    cfg.blockDim = dim3(tc_threads<kBits>());
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1345,22 +1469,29 @@ cudaError_t launch_prefill_tc(int dtype, int head_dim, const CUtensorMap &kmap,
                 : launch_tc_instance<__half, 128, false>(kmap, vmap, qmap, p, max_query_len, num_sms, stream);
 }
 
-template <typename T, int D>
-static cudaError_t launch_q4_instance(const CUtensorMap &qmap, const PrefillParams &p, int max_query_len,
-                                      int num_sms, cudaStream_t stream) {
+template <typename T, int D, int kBits>
+static cudaError_t launch_packed_instance(const CUtensorMap &qmap, const PrefillParams &p, int max_query_len,
+                                          int num_sms, cudaStream_t stream) {
     return p.key_parts > 1
-               ? launch_tc_instance<T, D, true, true>(qmap, qmap, qmap, p, max_query_len, num_sms, stream)
-               : launch_tc_instance<T, D, false, true>(qmap, qmap, qmap, p, max_query_len, num_sms, stream);
+               ? launch_tc_instance<T, D, true, kBits>(qmap, qmap, qmap, p, max_query_len, num_sms, stream)
+               : launch_tc_instance<T, D, false, kBits>(qmap, qmap, qmap, p, max_query_len, num_sms, stream);
 }
 
-cudaError_t launch_prefill_q4_tc(int dtype, int head_dim, const CUtensorMap &qmap, const PrefillParams &p,
+template <int kBits>
+static cudaError_t launch_packed(int dtype, int head_dim, const CUtensorMap &qmap, const PrefillParams &p,
                                  int max_query_len, int num_sms, cudaStream_t stream) {
     const bool bf16 = dtype == PAGEDKV_BF16;
     if (head_dim == 64)
-        return bf16 ? launch_q4_instance<__nv_bfloat16, 64>(qmap, p, max_query_len, num_sms, stream)
-                    : launch_q4_instance<__half, 64>(qmap, p, max_query_len, num_sms, stream);
-    return bf16 ? launch_q4_instance<__nv_bfloat16, 128>(qmap, p, max_query_len, num_sms, stream)
-                : launch_q4_instance<__half, 128>(qmap, p, max_query_len, num_sms, stream);
+        return bf16 ? launch_packed_instance<__nv_bfloat16, 64, kBits>(qmap, p, max_query_len, num_sms, stream)
+                    : launch_packed_instance<__half, 64, kBits>(qmap, p, max_query_len, num_sms, stream);
+    return bf16 ? launch_packed_instance<__nv_bfloat16, 128, kBits>(qmap, p, max_query_len, num_sms, stream)
+                : launch_packed_instance<__half, 128, kBits>(qmap, p, max_query_len, num_sms, stream);
+}
+
+cudaError_t launch_prefill_packed_tc(int bits, int dtype, int head_dim, const CUtensorMap &qmap,
+                                     const PrefillParams &p, int max_query_len, int num_sms, cudaStream_t stream) {
+    return bits == 8 ? launch_packed<8>(dtype, head_dim, qmap, p, max_query_len, num_sms, stream)
+                     : launch_packed<4>(dtype, head_dim, qmap, p, max_query_len, num_sms, stream);
 }
 
 }  // namespace pkv

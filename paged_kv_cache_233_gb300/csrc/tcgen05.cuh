@@ -11,7 +11,7 @@
 //     [61,64) layout: 2 = 128-byte swizzle
 //   instruction descriptor for kind::f16, 32 bits
 //     [4,6) accumulator type (1 = f32)    [7,10) A type, [10,13) B type (0 = f16, 1 = bf16)
-//     bit 15 A major, bit 16 B major (0 = K-major, 1 = M/N-major)
+//     bit 13 negate A, bit 15 A major, bit 16 B major (0 = K-major, 1 = M/N-major)
 //     [17,23) N >> 3                      [24,29) M >> 4
 // A 128-byte-swizzled operand is stored as 8-row atoms of 128-byte rows whose
 // 16-byte chunks are permuted by XOR with (row & 7): the layout that a TMA
@@ -109,6 +109,9 @@ __device__ __forceinline__ void tc_mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tm
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// Bit of the instruction descriptor that negates A.
+constexpr uint32_t kTcNegateA = 1u << 13;
 
 __host__ __device__ constexpr uint32_t tc_idesc_f16(bool bf16, bool b_mn_major, int M, int N) {
     return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) |

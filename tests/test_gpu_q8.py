@@ -294,6 +294,127 @@ def test_decode_nan_in_a_context_is_nan_and_past_it_is_nothing(operand):
             assert bool(torch.isfinite(out[0, 2:, 4:]).all()) and bool(torch.isfinite(out[0, 2:, :3]).all())
 
 
+# ------------------------------------------------------------------ prefill
+def prefill(q, kc, vc, tables, starts, lens, scale, out=None, most=None, **kw):
+    out = torch.full_like(q, 5.0).cuda() if out is None else out
+    pk.paged_attention_prefill_q8(q.cuda(), kc.cuda(), vc.cuda(), tables.cuda(), i32(starts), i32(lens), scale, out, most, **kw)
+    return out
+
+
+def check_prefill(dtype, cached, chunk, heads, group, dim, block, seed=0, extra=0, most=None, spread=1.0, scale=None, **kw):
+    lens = [c + n for c, n in zip(cached, chunk)]
+    kc, vc, tables = q8.filled(lens, heads, block, dim, dtype, seed + 20, spread, pad=seed % 2)
+    starts = torch.tensor([0] + chunk).cumsum(0)
+    total = int(starts[-1])
+    q = rows((total + extra, heads * group, dim), dtype, seed + 3)
+    scale = dim ** -0.5 if scale is None else scale
+    out = prefill(q, kc, vc, tables, starts, lens, scale, None, most, **kw)
+    assert pk.device_errors() == 0
+    assert bool((out[total:] == 5).all())
+    ref = q8.attention(q[:total], (kc, vc), tables, starts, lens, scale, dim)
+    # the output and the probabilities (to fp16, the finer of the types)
+    q8.assert_near(out[:total], ref, dtype, 2, f"{dtype} cached {cached} chunk {chunk}")
+
+
+@pytest.mark.parametrize("parts", [1, 0, 2, 32])
+@pytest.mark.parametrize("dtype,heads,group,dim,block", [
+    (F16, 8, 4, 128, 16), (BF16, 2, 8, 128, 32), (F16, 1, 1, 64, 8), (BF16, 4, 3, 64, 16), (F16, 2, 6, 128, 8),
+    (BF16, 1, 16, 64, 32), (F16, 1, 64, 128, 16), (BF16, 3, 7, 128, 16), (BF16, 2, 4, 128, 8), (F16, 2, 2, 64, 32)])
+def test_prefill(dtype, heads, group, dim, block, parts):
+    check_prefill(dtype, [0, 5, 300, 64, 0], [1, 40, 17, 0, 130], heads, group, dim, block, seed=heads, extra=3,
+                  key_parts=parts)
+
+
+@pytest.mark.parametrize("parts", [1, 0])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_prefill_long_context(dtype, parts):
+    check_prefill(dtype, [5000, 0], [70, 600], 2, 4, 128, 16, seed=3, key_parts=parts)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
+def test_prefill_scales(dtype, scale):
+    check_prefill(dtype, [50, 129], [33, 70], 2, 4, 64, 16, scale=scale)
+
+
+@pytest.mark.parametrize("dtype,spread", [(F16, 1e-3), (F16, 300.0), (BF16, 1e-17), (BF16, 1e5), (BF16, 1e19)])
+def test_prefill_small_and_large_values(dtype, spread):
+    """V of any size (K's size goes into the scale)."""
+    check_prefill(dtype, [40, 700], [20, 100], 4, 2, 128, 16, spread=spread, scale=128 ** -0.5 / spread, key_parts=0)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_prefill_values_that_grow_along_the_context(dtype):
+    for up in (False, True):
+        n, heads, dim, block = 600, 2, 128, 16
+        tables, nb = q8.tables_for([n], block, 4)
+        kc, vc = q8.new_pool(nb, heads, block, dim, 1), q8.new_pool(nb, heads, block, dim, 2)
+        ramp = torch.logspace(-3, 3, n) if up else torch.logspace(3, -3, n)
+        q8.fill(kc, tables[0], (rows((n, heads, dim), torch.float32, 5) * ramp.sqrt()[:, None, None] * 0.3).to(dtype))
+        q8.fill(vc, tables[0], (rows((n, heads, dim), torch.float32, 6) * ramp[:, None, None]).to(dtype))
+        q = rows((90, heads * 4, dim), dtype, 7)
+        for parts in (1, 32):
+            got = prefill(q, kc, vc, tables, [0, 90], [n], dim ** -0.5, key_parts=parts)
+            ref = q8.attention(q, (kc, vc), tables, [0, 90], [n], dim ** -0.5, dim)
+            # each row on its own: their outputs differ by orders of magnitude
+            for r in range(0, 90, 7):
+                q8.assert_near(got[r], ref[r], dtype, 2, f"up {up} parts {parts} row {r}")
+
+
+def test_prefill_single_tokens_equal_decode():
+    lens = [1, 50, 700]
+    kc, vc, tables = q8.filled(lens, 4, 16, 128, BF16, 8)
+    q = rows((3, 16, 128), BF16, 9)
+    a = decode(q, kc, vc, tables, lens, 0.09, 0)
+    b = prefill(q, kc, vc, tables, range(4), lens, 0.09)
+    ref = q8.attention(q, (kc, vc), tables, range(4), lens, 0.09, 128)
+    for got in (a, b):
+        q8.assert_near(got, ref, BF16, 2)
+
+
+def test_prefill_reports_bad_sequences_and_leaves_their_rows():
+    lens = [40, 40, 40]
+    kc, vc, tables = q8.filled(lens, 2, 16, 64, F16, 3)
+    q = rows((30, 4, 64), F16, 1)
+
+    def run(lens, most=10, tab=tables):
+        return prefill(q, kc, vc, tab, [0, 10, 20, 30], lens, 0.1, None, most), pk.device_errors()
+
+    out, err = run([40, 3, 40])                  # shorter than its chunk
+    assert err == 4 and bool((out[10:20] == 5).all()) and not bool((out[:10] == 5).any())
+    out, err = run([40, 40, 4000])               # past its table
+    assert err == 4 and bool((out[20:] == 5).all())
+    bad = tables.clone()
+    bad[0, 0] = -7
+    assert run(lens, tab=bad)[1] == 2            # BLOCK_ID
+
+
+@pytest.mark.parametrize("dtype,dim,block", [(F16, 64, 16), (BF16, 128, 8)])
+@pytest.mark.parametrize("operand", ["q", "k", "v"])
+def test_prefill_nan_reaches_the_rows_that_attend_to_it(operand, dtype, dim, block):
+    """A NaN at a chunk's token: rows before it, other heads and sequences stay finite."""
+    n, chunk, heads, at = 83, 40, 2, 60
+    tables, nb = q8.tables_for([n, n], block, 3)
+    kc, vc = (torch.full((nb, heads, block, dim + q8.tail(block)), 0xFF, dtype=torch.uint8) for _ in range(2))
+    for s in range(2):
+        for pool in (kc, vc):
+            q8.fill(pool, tables[s], rows((n, heads, dim), dtype, 5 + s))
+    q = rows((2 * chunk, 4, dim), dtype, 1)
+    first = at - (n - chunk)                     # the chunk's row at that token
+    if operand == "q":
+        q[first, 2:, 5] = float("inf")
+    else:
+        pool = kc if operand == "k" else vc
+        q8.views(pool, dim)[0][int(tables[0, at // block]), 1, 1, at % block, 3] = q8.NAN
+    for parts in (1, 32):
+        out = prefill(q, kc, vc, tables, [0, chunk, 2 * chunk], [n, n], 0.125, key_parts=parts).cpu()
+        assert bool(torch.isfinite(out[:, :2]).all()) and bool(torch.isfinite(out[chunk:]).all())
+        assert bool(torch.isfinite(out[:first]).all())
+        assert bool(out[first, 2:].isnan().all())
+        after = out[first + 1:chunk, 2:]
+        assert bool(torch.isfinite(after).all()) if operand == "q" else bool(after.isnan().all())
+
+
 # ---------------------------------------------------- blocks, streams, graphs
 @pytest.mark.parametrize("dtype,block", [(F16, 8), (BF16, 16), (F16, 32)])
 def test_blocks_copy_and_swap(dtype, block):
