@@ -31,9 +31,9 @@
  *     paged_kv_append has no such limit). Nor may a kernel of the caller's own
  *     that lets its programmatic dependents start early write those rows, or
  *     block tables, lengths and token lists, right ahead of a 16-bit call. Once
- *     paged_kv_build_tables or paged_kv_gather_q4 has been called in the
- *     process, whose results are tables, lengths and rows, neither limit is
- *     left: paged_kv_append_tokens, paged_attention_decode and
+ *     paged_kv_build_tables, paged_kv_fork, paged_kv_release,
+ *     paged_kv_gather_q4 or paged_kv_gather_q8 has been called in the process,
+ *     whose results are tables, lengths and rows, neither limit is left: paged_kv_append_tokens, paged_attention_decode and
  *     paged_attention_prefill then read all their inputs after the work ahead
  *     of them, which takes them 1 to 3 us longer in a chain of small calls.
  *   - Argument and shape checks run on the host before anything is enqueued;
@@ -767,6 +767,88 @@ int paged_kv_build_tables(const int32_t *new_lens, const int32_t *context_lens,
                           int32_t *free_count_out, int num_seqs, int max_blocks_per_seq,
                           int free_capacity, int token_capacity, int block_size, int num_blocks,
                           void *stream);
+
+/*
+ * paged_kv_fork -- rows that take over other rows' tokens, their blocks shared.
+ *
+ * Pages "How a serving engine actually works" (section "Copy-on-write, because
+ * you have used fork()") and "Paged-KV + Continuous Batching From Scratch" (section
+ * 1): samples of one prompt share its physical blocks, a count instead of a copy.
+ * shared[b] is the number of block b's holders beyond the first: 0 for a free block
+ * and for one that a single row holds, as paged_kv_build_tables hands them out.
+ *
+ * Row s with parents[s] = p >= 0 becomes a copy of row p and of its L =
+ * context_lens[p] tokens: the floor(L / block_size) whole blocks go into its row and
+ * shared of each is raised by one; where L % block_size != 0 a block comes off the
+ * free stack for a copy of the started one. Both rows may then be appended to.
+ * Children are granted in order, first come, first served: s is granted when it
+ * needs no block, or when children 0 .. s together need at most as many as are free
+ * (the j-th one is free_blocks[free_count - 1 - j]). What s held before is
+ * forgotten, not given back: release it first.
+ *
+ *   parents         int32 [num_seqs], device: a row that is no child itself, or -1
+ *   context_lens    int32 [num_seqs], device
+ *   block_tables    int32 [num_seqs][max_blocks_per_seq], device, updated: the entries
+ *                   of granted children's blocks alone are written
+ *   shared          int32 [num_blocks], device, updated
+ *   free_blocks     int32 [free_capacity], device: a stack, not written
+ *   free_count      int32 [1], device: blocks on the stack
+ *   block_pairs     int32 [num_seqs][2], device, written: {started block, its copy}, or
+ *                   {0, 0} for rows that need none; the block_pairs of a
+ *                   paged_kv_copy_blocks call for each layer's pools, which has to come
+ *                   before any append to parent or child
+ *   context_lens_out int32 [num_seqs], device, written: L for granted children, else
+ *                   unchanged; may be context_lens itself
+ *   free_count_out  int32 [1], device, written: blocks left; may be free_count
+ *
+ * A parent outside [-1, num_seqs) or one that is a child of the same call sets
+ * PAGEDKV_DEVERR_SEQ_INDEX, a parent's length outside its table
+ * PAGEDKV_DEVERR_CONTEXT_LEN; such a child is not granted. A free_count outside [0,
+ * free_capacity] is clamped (PAGEDKV_DEVERR_POSITION). A block id outside [0,
+ * num_blocks) is copied as it is, not counted, and sets PAGEDKV_DEVERR_BLOCK_ID.
+ * num_seqs <= 4096; outputs other than those named must not overlap inputs.
+ */
+int paged_kv_fork(const int32_t *parents, const int32_t *context_lens, int32_t *block_tables,
+                  int32_t *shared, const int32_t *free_blocks, const int32_t *free_count,
+                  int32_t *block_pairs, int32_t *context_lens_out, int32_t *free_count_out,
+                  int num_seqs, int max_blocks_per_seq, int free_capacity, int block_size,
+                  int num_blocks, void *stream);
+
+/*
+ * paged_kv_release -- blocks that sequences no longer need, back onto the stack.
+ *
+ * Row s keeps its first min(keep_lens[s], context_lens[s]) tokens: 0 ends the
+ * sequence, less than it holds takes tokens back (a rejected draft), a large number
+ * leaves it alone. Each of its blocks past ceil(kept / block_size) loses a holder:
+ * shared is lowered by one, and a block that has lost its last holder (shared was 0)
+ * goes onto the free stack. The call's blocks are pushed in the order of their ids.
+ * Entries of the table past the kept blocks stay as they were.
+ *
+ *   keep_lens       int32 [num_seqs], device, >= 0
+ *   context_lens    int32 [num_seqs], device
+ *   block_tables    int32 [num_seqs][max_blocks_per_seq], device
+ *   shared          int32 [num_blocks], device, updated; none negative
+ *   free_blocks     int32 [free_capacity], device: a stack, updated from free_count on
+ *   free_count      int32 [1], device: blocks on the stack
+ *   context_lens_out int32 [num_seqs], device, written: tokens kept; may be
+ *                   context_lens itself
+ *   free_count_out  int32 [1], device, written; may be free_count
+ *
+ * A row that keeps part of a block that others hold may be read, not appended to
+ * (its next token would go into their block); rows of paged_kv_fork share whole
+ * blocks only, so taking back tokens that were appended after a fork is always fine.
+ * A length outside the table or a negative keep_lens sets PAGEDKV_DEVERR_CONTEXT_LEN
+ * and the row stays as it was; a block id outside [0, num_blocks), or a block given
+ * back more often than it has holders (it goes onto the stack once), sets
+ * PAGEDKV_DEVERR_BLOCK_ID; blocks past the stack's capacity are lost, and a
+ * free_count outside [0, free_capacity] is clamped (PAGEDKV_DEVERR_POSITION).
+ * num_seqs <= 4096; outputs other than those named must not overlap inputs.
+ */
+int paged_kv_release(const int32_t *keep_lens, const int32_t *context_lens,
+                     const int32_t *block_tables, int32_t *shared, int32_t *free_blocks,
+                     const int32_t *free_count, int32_t *context_lens_out, int32_t *free_count_out,
+                     int num_seqs, int max_blocks_per_seq, int free_capacity, int block_size,
+                     int num_blocks, void *stream);
 
 /*
  * pagedkv_device_errors -- read (and optionally clear) the sticky device

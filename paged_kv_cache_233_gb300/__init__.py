@@ -1,7 +1,7 @@
 """GB300-native paged KV cache: append and fused paged-attention decode.
 
 A thin binding over ``libpagedkv.so`` (C ABI in ``include/pagedkv.h``): ctypes,
-and for the 4-bit cache and the step's tables a small C++ module, ``_binding.so``.
+and for the 4- and 8-bit caches and the step's tables a small C++ module, ``_binding.so``.
 It only marshals torch tensors into pointers and sizes: every step of the
 path runs in the library's CUDA kernels, and there is no CPU fallback. If the
 library has not been built, the first call raises ``PagedKVError`` (build it
@@ -26,6 +26,10 @@ The entry points keep the C names:
                               partition_tokens=0, workspace=None)
     paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, context_lens, scale,
                                out, max_query_len=None, workspace=None, key_parts=1)
+    paged_kv_fork(parents, context_lens, block_tables, shared, free_blocks, free_count, block_pairs,
+                  block_size, context_lens_out=None, free_count_out=None)
+    paged_kv_release(keep_lens, context_lens, block_tables, shared, free_blocks, free_count, block_size,
+                     context_lens_out=None, free_count_out=None)
     paged_kv_append_q8(k, v, block_tables, query_start, context_lens, k_cache, v_cache)
     paged_kv_gather_q8(k_cache, v_cache, slot_mapping, k, v)
     paged_attention_decode_q8(q, k_cache, v_cache, block_tables, context_lens, scale, out,
@@ -55,7 +59,7 @@ __all__ = [
     "paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
     "paged_attention_decode_q4", "paged_attention_prefill_q4", "new_q4_pool",
     "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8", "paged_attention_prefill_q8",
-    "new_q8_pool",
+    "new_q8_pool", "paged_kv_fork", "paged_kv_release",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -76,7 +80,7 @@ EXPORTS = ("paged_kv_slot_mapping", "paged_kv_append", "paged_attention_decode",
            "paged_attention_prefill_workspace_bytes", "paged_kv_build_tables", "paged_kv_append_q4",
            "paged_kv_gather_q4", "paged_attention_decode_q4", "paged_attention_prefill_q4",
            "paged_kv_append_q8", "paged_kv_gather_q8", "paged_attention_decode_q8",
-           "paged_attention_prefill_q8")
+           "paged_attention_prefill_q8", "paged_kv_fork", "paged_kv_release")
 
 
 class PagedKVError(RuntimeError):
@@ -133,13 +137,16 @@ def load():
     lib.paged_kv_gather_q4.argtypes = [vp] * 5 + [i32] * 6 + [vp]
     lib.paged_attention_decode_q4.argtypes = lib.paged_attention_decode.argtypes
     lib.paged_attention_prefill_q4.argtypes = lib.paged_attention_prefill_split.argtypes
+    lib.paged_kv_fork.argtypes = [vp] * 9 + [i32] * 5 + [vp]
+    lib.paged_kv_release.argtypes = [vp] * 8 + [i32] * 5 + [vp]
     lib.paged_kv_append_q8.argtypes = [vp] * 7 + [i32] * 8 + [vp]
     lib.paged_kv_gather_q8.argtypes = lib.paged_kv_gather_q4.argtypes
     lib.paged_attention_decode_q8.argtypes = lib.paged_attention_decode.argtypes
     lib.paged_attention_prefill_q8.argtypes = lib.paged_attention_prefill_split.argtypes
     for name in ("paged_kv_build_tables", "paged_kv_append_q4", "paged_kv_gather_q4",
                  "paged_attention_decode_q4", "paged_attention_prefill_q4", "paged_kv_append_q8",
-                 "paged_kv_gather_q8", "paged_attention_decode_q8", "paged_attention_prefill_q8"):
+                 "paged_kv_gather_q8", "paged_attention_decode_q8", "paged_attention_prefill_q8",
+                 "paged_kv_fork", "paged_kv_release"):
         getattr(lib, name).restype = i32
     lib.paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.paged_attention_workspace_bytes.restype = sz
@@ -625,6 +632,36 @@ def paged_kv_build_tables(new_lens, context_lens, block_tables, free_blocks, fre
     (_fast or _binding()).build_tables(new_lens, context_lens, block_tables, free_blocks, free_count,
                                        block_size, num_blocks, query_start, token_seq, token_pos,
                                        slot_mapping, context_lens_out, free_count_out, stream)
+
+
+def paged_kv_fork(parents, context_lens, block_tables, shared, free_blocks, free_count, block_pairs,
+                  block_size, context_lens_out=None, free_count_out=None, stream=None):
+    """Rows that take over other rows' tokens, their blocks shared.
+
+    Row s with parents[s] >= 0 (-1: none) becomes a copy of that row: it shares the
+    whole blocks (shared [num_blocks] counts a block's holders beyond the first) and,
+    where the last one is only started, takes a block off the stack free_blocks
+    (free_count[0] ids) for a copy of it. block_pairs [num_seqs][2] is then the pairs
+    of a paged_kv_copy_blocks call for each layer's pools ({0, 0}: nothing to copy).
+    Children are granted in order while blocks are left. The lengths and the count
+    after the call go to context_lens_out and free_count_out, by default the inputs
+    themselves. From the first call on, 16-bit calls wait for the work ahead of them
+    before they read any input, as after paged_kv_build_tables."""
+    (_fast or _binding()).fork(parents, context_lens, block_tables, shared, free_blocks, free_count, block_pairs,
+                               block_size, context_lens_out, free_count_out, stream)
+
+
+def paged_kv_release(keep_lens, context_lens, block_tables, shared, free_blocks, free_count, block_size,
+                     context_lens_out=None, free_count_out=None, stream=None):
+    """Blocks that sequences no longer need, back onto the stack: row s keeps its
+    first keep_lens[s] tokens (0: it is finished; at least its length: all of them).
+    A block whose last holder lets go is pushed; one call's in the order of their
+    ids. The lengths and the count after the call go to context_lens_out and
+    free_count_out, by default the inputs themselves. From the first call on, 16-bit
+    calls wait for the work ahead of them before they read any input, as after
+    paged_kv_build_tables."""
+    (_fast or _binding()).release(keep_lens, context_lens, block_tables, shared, free_blocks, free_count, block_size,
+                                  context_lens_out, free_count_out, stream)
 
 
 def check_bounded_wait(stream=None):

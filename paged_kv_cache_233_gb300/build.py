@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIBRARY = os.path.join(HERE, "libpagedkv.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["api.cu", "api_packed.cu", "append.cu", "cache_q4.cu", "cache_q8.cu", "tables.cu", "swap.cu",
+SOURCES = ["api.cu", "api_packed.cu", "append.cu", "cache_q4.cu", "cache_q8.cu", "tables.cu", "pages.cu", "swap.cu",
            "merge.cu", "prefill.cu", "prefill_tc.cu", "decode_f32.cu", "decode_f16.cu",
            "decode_bf16.cu", "decode_q4_f16.cu", "decode_q4_bf16.cu", "decode_q8_f16.cu", "decode_q8_bf16.cu",
            "decode_noalloc.cu"]

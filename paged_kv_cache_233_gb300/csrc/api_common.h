@@ -23,8 +23,9 @@ int api_plan_key_split(PrefillParams &p, int key_parts, void *workspace, size_t 
                        int max_query_len, int sms);
 
 // Whether block tables, lengths, token lists and rows to append may be what a
-// kernel of this library just ahead on the stream writes: paged_kv_build_tables
-// or paged_kv_gather_q4 has been called in this process (they note it here). The
+// kernel of this library just ahead on the stream writes: a call with such results
+// (paged_kv_build_tables, paged_kv_fork, paged_kv_release, the gathers of the packed
+// caches) has been made in this process (they note it here). The
 // 16-bit kernels then read them after their dependency wait; before it
 // otherwise (with small steps in a graph the wait comes to a quarter of the rate:
 // 16 slots of the batching trace 3.6 TB/s against 5.0).

@@ -1,6 +1,6 @@
-// api_packed.cu -- the C ABI of the paged caches in 4 and in 8 bits and of the
-// tables a step builds on the GPU (declared in include/pagedkv.h): host-side
-// checks and launches.
+// api_packed.cu -- the C ABI of the paged caches in 4 and in 8 bits, of the tables
+// a step builds on the GPU and of forks and releases (declared in
+// include/pagedkv.h): host-side checks and launches.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -9,6 +9,7 @@
 #include "../../include/pagedkv.h"
 #include "api_common.h"
 #include "decode_launch.h"
+#include "pages.h"
 #include "prefill.h"
 #include "q4.h"
 #include "q8.h"
@@ -82,6 +83,34 @@ int move_rows(const void *k, const void *v, const int64_t *slot_mapping, const v
     st = api_device_state(&err, &sms);
     if (st != PAGEDKV_OK) return st;
     return done(launch((long long)num_blocks * block_size, err));
+}
+
+// paged_kv_fork (with pairs) and paged_kv_release.
+template <typename Launch>
+int change_pages(pkv::PagesParams p, bool pairs, Launch launch) {
+    if (p.num_seqs < 0 || p.max_blocks < 1 || p.num_blocks < 1 || p.free_capacity < 0 || p.block_size < 1)
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (p.num_seqs > kMaxSeqs || p.num_blocks > kMaxCount || p.free_capacity > kMaxCount ||
+        (long long)p.max_blocks * p.block_size > INT_MAX / 2)
+        return PAGEDKV_ERR_UNSUPPORTED;
+    if (!p.free_count || !p.free_count_out || !p.shared || (p.free_capacity > 0 && !p.free_blocks))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (p.num_seqs > 0 && (!p.choice || !p.context_lens || !p.block_tables || !p.context_lens_out ||
+                           (pairs && !p.block_pairs)))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (!api_aligned(p.choice, 4) || !api_aligned(p.context_lens, 4) || !api_aligned(p.block_tables, 4) ||
+        !api_aligned(p.shared, 4) || !api_aligned(p.free_blocks, 4) || !api_aligned(p.free_count, 4) ||
+        !api_aligned(p.block_pairs, 8) || !api_aligned(p.context_lens_out, 4) || !api_aligned(p.free_count_out, 4))
+        return PAGEDKV_ERR_INVALID_ARG;
+    if (p.num_seqs == 0 && p.free_count == p.free_count_out) return PAGEDKV_OK;
+    pkv::api_note_device_inputs();   // as above: calls that read these tables come later
+    int sms = 0;
+    const int st = api_device_state(&p.err, &sms);
+    if (st != PAGEDKV_OK) return st;
+    p.shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if ((1 << i) == p.block_size) p.shift = i;
+    return done(launch(p, sms));
 }
 
 // paged_attention_decode_q4 and paged_attention_decode_q8.
@@ -348,6 +377,30 @@ int paged_kv_gather_q8(const void *k_cache, const void *v_cache, const int64_t *
                                                       num_tokens, n_kv_heads, head_dim, block_size, num_slots,
                                                       dtype, err, static_cast<cudaStream_t>(stream));
                      });
+}
+
+int paged_kv_fork(const int32_t *parents, const int32_t *context_lens, int32_t *block_tables, int32_t *shared,
+                  const int32_t *free_blocks, const int32_t *free_count, int32_t *block_pairs,
+                  int32_t *context_lens_out, int32_t *free_count_out, int num_seqs, int max_blocks_per_seq,
+                  int free_capacity, int block_size, int num_blocks, void *stream) {
+    const pkv::PagesParams p{parents, context_lens, block_tables, shared, const_cast<int32_t *>(free_blocks), free_count,
+                             block_pairs, context_lens_out, free_count_out, nullptr, num_seqs, max_blocks_per_seq,
+                             num_blocks, free_capacity, block_size, -1};
+    return change_pages(p, true, [&](const pkv::PagesParams &q, int sms) {
+        return pkv::launch_fork(q, sms, static_cast<cudaStream_t>(stream));
+    });
+}
+
+int paged_kv_release(const int32_t *keep_lens, const int32_t *context_lens, const int32_t *block_tables,
+                     int32_t *shared, int32_t *free_blocks, const int32_t *free_count, int32_t *context_lens_out,
+                     int32_t *free_count_out, int num_seqs, int max_blocks_per_seq, int free_capacity,
+                     int block_size, int num_blocks, void *stream) {
+    const pkv::PagesParams p{keep_lens, context_lens, const_cast<int32_t *>(block_tables), shared, free_blocks, free_count,
+                             nullptr, context_lens_out, free_count_out, nullptr, num_seqs, max_blocks_per_seq,
+                             num_blocks, free_capacity, block_size, -1};
+    return change_pages(p, false, [&](const pkv::PagesParams &q, int sms) {
+        return pkv::launch_release(q, sms, static_cast<cudaStream_t>(stream));
+    });
 }
 
 int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_cache,

@@ -286,6 +286,55 @@ PyObject *build_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+struct Pages {
+    int32_t *choice, *lens, *tables, *shared, *stack, *count, *lens_out, *count_out;
+    int seqs, width, capacity, block, blocks;
+    void *stream;
+};
+
+// choice, context_lens, block_tables, shared, free_blocks, free_count; block_size, context_lens_out, free_count_out, stream
+Pages pages(PyObject *const *a, PyObject *const *b, const char *choice_name) {
+    const at::Tensor &choice = tensor(a[0], choice_name), &lens = tensor(a[1], "context_lens");
+    const at::Tensor &bt = tensor(a[2], "block_tables"), &shared = tensor(a[3], "shared");
+    const at::Tensor &stack = tensor(a[4], "free_blocks"), &count = tensor(a[5], "free_count");
+    const at::Tensor &lens_out = b[1] == Py_None ? lens : tensor(b[1], "context_lens_out");
+    const at::Tensor &count_out = b[2] == Py_None ? count : tensor(b[2], "free_count_out");
+    const int64_t S = choice.numel();
+    if (lens.numel() != S || lens_out.numel() != S || bt.dim() != 2 || bt.size(0) != S)
+        fail("lengths and block_tables differ in their number of sequences");
+    if (count.numel() != 1 || count_out.numel() != 1) fail("free_count must hold one number");
+    const int block = integer(b[0], "block_size"), d = device_of(choice);
+    auto i32 = [&](const at::Tensor &t, const char *name) { return static_cast<int32_t *>(on(d, t, name, at::kInt)); };
+    return {i32(choice, choice_name), i32(lens, "context_lens"), i32(bt, "block_tables"), i32(shared, "shared"),
+            i32(stack, "free_blocks"), i32(count, "free_count"), i32(lens_out, "context_lens_out"),
+            i32(count_out, "free_count_out"), narrow(S), narrow(bt.size(1)), narrow(stack.numel()), block,
+            narrow(shared.numel()), stream_of(b[3])};
+}
+
+// parents, context_lens, block_tables, shared, free_blocks, free_count, block_pairs, block_size, context_lens_out,
+// free_count_out, stream
+PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&] {
+        const Pages p = pages(a, a + 7, "parents");
+        const at::Tensor &pairs = tensor(a[6], "block_pairs");
+        if (pairs.dim() != 2 || pairs.size(0) != p.seqs || pairs.size(1) != 2) fail("block_pairs must be [num_seqs][2]");
+        int32_t *pp = static_cast<int32_t *>(on(device_of(pairs), pairs, "block_pairs", at::kInt));
+        return done(paged_kv_fork(p.choice, p.lens, p.tables, p.shared, p.stack, p.count, pp, p.lens_out, p.count_out, p.seqs,
+                                  p.width, p.capacity, p.block, p.blocks, p.stream),
+                    "paged_kv_fork");
+    });
+}
+
+// keep_lens, context_lens, block_tables, shared, free_blocks, free_count, block_size, context_lens_out, free_count_out, stream
+PyObject *release(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const Pages p = pages(a, a + 6, "keep_lens");
+        return done(paged_kv_release(p.choice, p.lens, p.tables, p.shared, p.stack, p.count, p.lens_out, p.count_out, p.seqs,
+                                     p.width, p.capacity, p.block, p.blocks, p.stream),
+                    "paged_kv_release");
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *cls) {
     Py_INCREF(cls);
     Py_XSETREF(g_error, cls);
@@ -302,6 +351,8 @@ PyMethodDef g_methods[] = {
     {"decode_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q8)), METH_FASTCALL, nullptr},
     {"decode_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_q4)), METH_FASTCALL, nullptr},
     {"prefill_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill_q4)), METH_FASTCALL, nullptr},
+    {"fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fork_rows)), METH_FASTCALL, nullptr},
+    {"release", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(release)), METH_FASTCALL, nullptr},
     {"build_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(build_tables)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
