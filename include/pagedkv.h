@@ -604,7 +604,9 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
  * bytes (32 in blocks of 32); the bytes of one (block, kv head) are
  *
  *     codes  [head_dim / 16 panels][block_size tokens][16 channels]
- *     scale  fp32, at block_size * head_dim; the rest is not used
+ *     scale  fp32, at block_size * head_dim
+ *     marks  32 bits behind it, bit t set when token t's row holds a NaN; the rest
+ *            is not used
  *
  * and tokens, slots and block tables mean what they mean for 16-bit pools. The
  * codes do not depend on the 16-bit type of the rows. Supported: `dtype`
@@ -631,7 +633,7 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
  *          every finite new x of the block, and at least the block's scale where the
  *          block holds tokens of s before position L_s - n_s;
  *     c    = x / 2^e rounded to the nearest e4m3 value, ties to even; a NaN or an
- *          infinity becomes NaN and leaves the others alone.
+ *          infinity becomes NaN, sets its token's mark and leaves the others alone.
  *
  * Where the scale grew, the codes of the block's older tokens are divided by the
  * growth and rounded again (exact for results of 2^-6 and more). A block without
@@ -703,8 +705,8 @@ int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_
  * rounded to fp16, relative to a running maximum as in the decode; scores, softmax
  * statistics and output sums are fp32. Arguments, limits, workspace and key_parts as
  * paged_attention_prefill_q4's. In bf16 caches values of V may be 2^70 at most. A
- * NaN or an infinity in a row of q makes that row's outputs of the head NaN, a NaN
- * code in K or V those of the rows that attend to its token.
+ * NaN or an infinity in a row of q makes that row's outputs of the head NaN; a token
+ * that is marked as holding a NaN, in K or in V, those of the rows that attend to it.
  */
 int paged_attention_prefill_q8(const void *q, const void *k_cache, const void *v_cache,
                                const int32_t *block_tables, const int32_t *query_start,

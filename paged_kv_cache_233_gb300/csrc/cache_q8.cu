@@ -5,7 +5,8 @@
 //     2^e the smallest power of two (at least 2^-64) with |x| <= 448 * 2^e for
 //     every finite x of the run, and no smaller than the block's scale where the
 //     block holds tokens from before;
-//     c = x / 2^e rounded to e4m3, ties to even; a NaN or an infinity is NaN.
+//     c = x / 2^e rounded to e4m3, ties to even; a NaN or an infinity is NaN, and
+//     the token's bit is set in the block's marks.
 // Where the block's older tokens had a smaller scale their codes are divided by
 // the growth and rounded again. A block without older tokens starts over, so that
 // what it held for another sequence never matters.
@@ -107,7 +108,8 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
         float *scale_at = reinterpret_cast<float *>(base + q8_scale_at(B, D));
         uint4 w[kPasses][2];
         uint32_t top2 = 0;
-        const float was = x.held ? *scale_at : 0.f;
+        const uint2 was = x.held ? *reinterpret_cast<const uint2 *>(scale_at) : make_uint2(0u, 0u);
+        uint32_t marks = was.y & ((1ull << x.held) - 1);
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = i * kRows + r0;
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
         if (top >= kInfBits<T>) {
             // a NaN or an infinity among them: each becomes a NaN, and the others set the scale
             top = 0;
+            uint32_t mine = 0;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
 #pragma unroll
@@ -143,14 +146,16 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
                         else top = max(top, lo);
                         if (hi >= kInfBits<T>) c[e] |= 0x7fff0000u;
                         else top = max(top, hi);
+                        if (max(lo, hi) >= kInfBits<T>) mine |= 1u << ((i * kRows + r0) & 31);
                     }
                     w[i][j] = make_uint4(c[0], c[1], c[2], c[3]);
                 }
             }
             top = __reduce_max_sync(kAll, top);
+            marks |= __reduce_or_sync(kAll, mine) << x.held;
         }
         int e = q8_exponent_for(Elem<T>::unpack2(top).x);
-        const int before = x.held ? min(max(q8_exponent(was), kQ8LeastExp), kQ8MostExp) : e;
+        const int before = x.held ? min(max(q8_exponent(__uint_as_float(was.x)), kQ8LeastExp), kQ8MostExp) : e;
         if (before < e) {
             // the block's older codes under the larger scale (a result below 2^-10 is zero)
             const float shrink = q8_power(max(before - e, -100));
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
                     make_uint4(four(a.x, a.y), four(a.z, a.w), four(b.x, b.y), four(b.z, b.w));
             }
         }
-        if (lane == 0) *scale_at = q8_power(e);
+        if (lane == 0) *reinterpret_cast<uint2 *>(scale_at) = make_uint2(__float_as_uint(q8_power(e)), marks);
     }
     if (blockIdx.x == 0 && o == 0) report_bad(p, starts, B);
 }

@@ -72,6 +72,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "launch_cache.h"
 #include "prefill.h"
 #include "ptx.cuh"
@@ -152,10 +154,9 @@ constexpr int kMaxRankedSeqs = 256;
 
 template <int D, int kBits>
 struct TcLayout {
-    // (8-bit tiles of head size 128 leave room for three stages: the least that the
-    // issuers work with, two S ahead of a P V)
-    static constexpr int kStages = kBits == 8 && D == 128 ? 3 : kTcStages;
-    static constexpr int kRawStages = kBits == 8 ? 3 : 2;
+    // the raw ring: 4-bit key tiles, or 8-bit ones of K or V alone, of which head size
+    // 128 leaves room for three beside four stages
+    static constexpr int kRawStages = kBits == 8 ? (D == 128 ? 3 : 6) : 2;
     static constexpr int kSlabs = D * 2 / 128;             // 64-element column blocks per row
     static constexpr int kQSlab = kTcRows * 128;           // bytes of one Q column block
     static constexpr int kKvSlab = kTcKeys * 128;          // bytes of one K (or V) column block
@@ -164,7 +165,7 @@ struct TcLayout {
     static constexpr int kKv = kQ + kTcTiles * kQTile;     // stage s: K at kKv + s*kStage, V after it
     static constexpr int kHalf = kSlabs * kKvSlab;
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kBars = kKv + kStages * kStage;
+    static constexpr int kBars = kKv + kTcStages * kStage;
     static constexpr int kTmemSlot = kBars + 8 * kNumBars;
     static constexpr int kFlag = kTmemSlot + 8;
     static constexpr int kOrder = kFlag + 8;               // ranked sequence ids, then their lengths
@@ -174,16 +175,16 @@ struct TcLayout {
     static constexpr int kOutRow = kOrder + 8 * kMaxRankedSeqs;
     static constexpr int kRefRow = kOutRow + 8 * kTcTiles * kTcRows;
     static constexpr int kTotal = kRefRow + 4 * kTcTiles * kTcRows;
-    // 8-bit pools, per stage: for each 8 keys what turns their sums into scores, V's
-    // exponent and the inverse of V's scale, then a bit for each key whose V has a NaN
+    // 8-bit pools, per stage: for each 16 keys what turns their sums into scores, V's
+    // exponent, the inverse of V's scale, and a bit for each key whose K or V has a NaN
     static constexpr int kScales = (kTotal + 15) & ~15;
-    static constexpr int kScalesStage = kTcKeys / 8 * 16 + 16;
+    static constexpr int kScalesStage = kTcKeys / 16 * 16;
     // 4- and 8-bit pools: the raw ring's barriers (full, empty), then its tiles: K's
     // blocks, V's (8-bit: with the scales behind the codes, blocks of 8 have the most)
-    static constexpr int kRawBars = kScales + (kBits == 8 ? kStages * kScalesStage : 0);
+    static constexpr int kRawBars = kScales + (kBits == 8 ? kTcStages * kScalesStage : 0);
     static constexpr int kRaw = kRawBars + 16 * kRawStages;
     static constexpr int kRawHalf = kBits == 8 ? kTcKeys / 8 * q8_head_bytes(8, D) : kTcKeys * D * 5 / 8;
-    static constexpr int kTotalPacked = kRaw + kRawStages * 2 * kRawHalf;
+    static constexpr int kTotalPacked = kRaw + kRawStages * (kBits == 8 ? 1 : 2) * kRawHalf;
     static_assert((kBits < 16 ? kTotalPacked : kTotal) + 1024 <= 227 * 1024, "the shared memory of a block");
     static_assert(2 * kTcKeys + D <= kTmemTile, "S buffers and O must fit a Q tile's columns");
     static_assert(kMaxSplitItems < kPlanRange && 4 * (kPlanRange + 6) <= 8 * kMaxRankedSeqs,
@@ -215,14 +216,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                  ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ uint2 lds64_u2(uint32_t addr) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+    return r;
+}
 __device__ __forceinline__ float2 lds64_f2(uint32_t addr) {
     float2 r;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
-    return r;
-}
-__device__ __forceinline__ unsigned long long lds64_u(uint32_t addr) {
-    unsigned long long r;
-    asm volatile("ld.shared.u64 %0, [%1];" : "=l"(r) : "r"(addr) : "memory");
     return r;
 }
 
@@ -465,7 +466,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const PrefillParams p, int tiles) {
     using Ly = TcLayout<D, kBits>;
     constexpr bool kBf16 = Elem<T>::kBf16, kPacked = kBits < 16;
-    constexpr int kStages = Ly::kStages, kRawStages = Ly::kRawStages;
+    constexpr int kRawStages = Ly::kRawStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -483,7 +484,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     if (kPacked || p.late_inputs) grid_dependency_wait();
 
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kStages; ++k) {
+        for (int k = 0; k < kTcStages; ++k) {
             mbar_init(bar(kKvFull + k), kPacked ? kDqWarps : 1);
             mbar_init(bar(kKvEmpty + k), kTcTiles);   // one commit per issuer and key tile
         }
@@ -503,7 +504,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             mbar_init(bar(bar_qfree(t)), 1);
         }
         mbar_init(bar(kDone), kTcTiles);
-        for (int k = 0; k < kStages; ++k) mbar_init(bar(kTailV + k), 1);
+        for (int k = 0; k < kTcStages; ++k) mbar_init(bar(kTailV + k), 1);
         sts32(flag, 0);
         fence_barrier_init();
     }
@@ -590,9 +591,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             PfItem it;
             if (!pf_item<kSplit>(p, order, tiles, k, lane == 0, it)) continue;
             const int32_t *table = p.block_tables + size_t(it.s) * p.max_blocks;
-            if constexpr (kPacked) {
+            if constexpr (kBits == 4) {
                 // a tile's blocks, K and V, a lane per copy
-                const int hb = kBits == 8 ? q8_head_bytes(B, D) : q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
+                const int hb = q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
                 const uint8_t *pool = op ? p.v_packed : p.k_packed;
                 for (int j = 0; j < it.nkt; ++j) {
                     const int gk = kt + j;
@@ -622,9 +623,47 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     }
                     ++armed;
                 }
+            } else if constexpr (kBits == 8) {
+                // a tile's blocks, a lane per copy: K's, then V's. The next tile's block
+                // ids are loaded while this one's slots are waited for.
+                const int hb = q8_head_bytes(B, D), per = kTcKeys >> p.log2_block;
+                const int32_t *ids = table + ((it.kb * kTcKeys) >> p.log2_block) + lane;
+                int left = it.L - it.kb * kTcKeys, next = lane < per && lane * B < left ? __ldg(ids) : 0;
+                for (int x = 0; x < 2 * it.nkt; ++x) {
+                    const int h = 2 * kt + x, op = x & 1, st = h % kRawStages;
+                    const int blocks = (min(kTcKeys, left) + B - 1) >> p.log2_block;
+                    const bool mine = lane < blocks;
+                    int pb = next;
+                    if (op) {
+                        ids += per;
+                        left -= kTcKeys;
+                        next = lane < per && lane * B < left ? __ldg(ids) : 0;
+                    }
+                    const uint32_t full = base + Ly::kRawBars + 16 * st;
+                    bool got = true;
+                    if (lane == 0) {
+                        got = !aborted() && mbar_wait(full + 8, uint32_t((h / kRawStages) & 1) ^ 1u, p.err);
+                        if (got) mbar_arrive_expect_tx(full, uint32_t(blocks * hb));
+                    }
+                    __syncwarp();
+                    if (!__shfl_sync(kAll, got ? 1 : 0, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (mine) {
+                        if (pb < 0 || pb >= p.num_blocks) {
+                            atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+                            pb = 0;
+                        }
+                        bulk_load(base + Ly::kRaw + st * Ly::kRawHalf + lane * hb,
+                                  (op ? p.v_packed : p.k_packed) + (size_t(pb) * p.n_kv_heads + it.h) * hb, uint32_t(hb),
+                                  full);
+                    }
+                    ++armed;
+                }
             } else for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
-                const int st = gk % kStages;
+                const int st = gk % kTcStages;
                 const int k0 = (it.kb + j) * kTcKeys;
                 const int present = min(kTcKeys, it.L - k0);
                 const int boxes = (present + rows_per_box - 1) / rows_per_box;
@@ -636,7 +675,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 bool got = true;
                 if (lane == 0) {
                     got = !aborted() &&
-                          mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u, p.err);
+                          mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err);
                     if (got && !last_tail) {
                         mbar_arrive_expect_tx(bar(kKvFull + st), 2 * half);
                     } else if (got) {
@@ -673,10 +712,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // (a tail stage completes only with the zeroing warp's arrival: when that
             // warp stopped too, the wait ends at its time limit, its copies long done)
             sts32(flag, 1);
-            constexpr int kRing = kPacked ? kRawStages : kStages;
+            constexpr int kRing = kPacked ? kRawStages : kTcStages;
             const int first = armed > kRing ? armed - kRing : 0;
             for (int x = first; x < armed; ++x)
-                mbar_wait(kPacked ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kStages),
+                mbar_wait(kPacked ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kTcStages),
                           uint32_t((x / kRing) & 1), p.err);
         }
         __syncwarp();
@@ -748,7 +787,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
             }
             if (!kPacked && it.tail) {
-                const int st = (kt + it.nkt - 1) % kStages;
+                const int st = (kt + it.nkt - 1) % kTcStages;
                 const int present = it.L - (it.kb + it.nkt - 1) * kTcKeys;
                 bool got = true;
                 if (lane == 0)
@@ -780,18 +819,15 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (qlast[t] >= 0) mbar_wait(bar(bar_qfull(t)), uint32_t(qlast[t] & 1), p.err);
         }
         __syncwarp();
-    } else if (kPacked && warp >= kDqWarp0) {
-        // ------------------------------- 4- and 8-bit pools: raw tiles to stages
-        // A lane owns a key row of K or V. 4 bits: its pairs, then per group 16 bytes
-        // of codes, each word of which is one 16-byte chunk of the stage's row. 8
-        // bits: per panel 16 bytes of codes, two chunks, and for each 8 keys the scales.
+    } else if (kBits == 4 && warp >= kDqWarp0) {
+        // -------------------------------------- 4-bit pools: raw tiles to stages
+        // A lane owns a key row of K or V: its pairs, then per group 16 bytes of
+        // codes, each word of which is one 16-byte chunk of the stage's row.
         constexpr int G = D / kQ4Group;
         const int row = 32 * (warp & 1) + lane, op = (warp - kDqWarp0) >> 1;
-        const int hb = kBits == 8 ? q8_head_bytes(B, D) : q4_head_bytes(B, D);
-        const int blk = row >> p.log2_block, off = row & (B - 1);
+        const int hb = q4_head_bytes(B, D), blk = row >> p.log2_block, off = row & (B - 1);
         const uint32_t src = base + Ly::kRaw + uint32_t(blk * hb + off * 16);
         const uint32_t pairs = base + Ly::kRaw + uint32_t(blk * hb + q4_pairs_at(B, D) + off * 4 * G);
-        const uint32_t scale = base + Ly::kRaw + uint32_t(blk * hb + q8_scale_at(B, D));
         const uint32_t dst = base + Ly::kKv + uint32_t(row * 128 + ((row & 7) << 4));
         int kt = 0;
         bool ok = true;
@@ -802,19 +838,19 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
             for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
-                const int st = gk % kStages, rs = gk % kRawStages;
+                const int st = gk % kTcStages, rs = gk % kRawStages;
                 const uint32_t rfull = base + Ly::kRawBars + 16 * rs;
                 const bool live = (it.kb + j) * kTcKeys + row < it.L;
                 // the raw tile is there, and the stage's last readers are done
                 bool got = mbar_try_wait(rfull, uint32_t((gk / kRawStages) & 1)) ||
                            (!aborted() && mbar_wait(rfull, uint32_t((gk / kRawStages) & 1), p.err));
-                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u) ||
-                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u, p.err)));
+                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u) ||
+                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err)));
                 if (!__all_sync(kAll, got)) {
                     ok = false;
                     break;
                 }
-                if constexpr (kBits == 4) {
+                {
                     const uint32_t from = uint32_t(rs * 2 * Ly::kRawHalf + op * Ly::kRawHalf);
                     const uint32_t to = dst + uint32_t(st * Ly::kStage + op * Ly::kHalf);
                     auto codes = [&](int i) { return lds128_u4(src + from + uint32_t(i * B * 16)); };
@@ -848,54 +884,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll 1
                         for (int i = 0; i < G; ++i) put(i, codes(i), pair(i));
                     }
-                } else if constexpr (kBits == 8) {
-                    const uint32_t from = uint32_t(rs * 2 * Ly::kRawHalf + op * Ly::kRawHalf);
-                    const uint32_t to = dst + uint32_t(st * Ly::kStage + op * Ly::kHalf);
-                    const uint32_t per8 = base + Ly::kScales + uint32_t(st * Ly::kScalesStage);
-                    if ((row & 7) == 0) {
-                        // (rows past the context: any finite numbers. A factor of 0 would
-                        // turn a masked score's -inf into a NaN.)
-                        const uint32_t v = live ? uint32_t(lds32(scale + from)) : 0x3f800000u;
-                        const uint32_t at = per8 + uint32_t(row >> 3) * 16;
-                        if (op == 0) {
-                            const float k = fabsf(p.scale_log2) * __uint_as_float(v);
-                            sts32(at, __float_as_int(k == 0.f ? 0x1p-126f : k));
-                        } else {
-                            sts32(at + 4, __float_as_int(float(int(v >> 23) - 127)));
-                            sts32(at + 8, int(0x7f000000u - v));
-                        }
-                    }
-                    uint32_t nan = 0;   // the sign bits of bytes that are NaN codes
-#pragma unroll 2
-                    for (int i = 0; i < D / kQ8Panel; ++i) {
-                        uint4 cw = lds128_u4(src + from + uint32_t(i * B * 16));
-                        if (!live) cw = make_uint4(0u, 0u, 0u, 0u);
-                        uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w}, x[8];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (op == 1) {
-                                // a NaN in V counts where its key is attended to (by the
-                                // key's bit), not under the weight 0 of rows that do not see it
-                                const uint32_t bad = ((w[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                                nan |= bad;
-                                w[c] &= ~((bad >> 7) * 255u);
-                            }
-                            q8_halves(w[c], x[2 * c], x[2 * c + 1]);
-                            if (kBf16 && op == 0) {
-                                const float2 a = Elem<__half>::unpack2(x[2 * c]), b = Elem<__half>::unpack2(x[2 * c + 1]);
-                                x[2 * c] = Elem<__nv_bfloat16>::pack2(a.x, a.y);
-                                x[2 * c + 1] = Elem<__nv_bfloat16>::pack2(b.x, b.y);
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            sts128((to ^ uint32_t((((2 * i) & 7) + c) << 4)) + uint32_t((i >> 2) * Ly::kKvSlab),
-                                   make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
-                    }
-                    if (op == 1) {
-                        const unsigned m = __ballot_sync(kAll, nan != 0);
-                        if (lane == 0) sts32(per8 + kTcKeys / 8 * 16 + 4 * (warp & 1), int(m));
-                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -905,6 +893,146 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
             }
             kt += it.nkt;
+        }
+        if (lane == 0 && !ok) sts32(flag, 1);
+        __syncwarp();
+    } else if (kBits == 8 && warp >= kDqWarp0) {
+        // -------------------------------------- 8-bit pools: raw tiles to stages
+        // K's raw tile, then V's. A warp takes 16 key rows: half a warp their even
+        // panels, the other the odd ones, 16 bytes of codes to two 16-byte chunks of the
+        // stage's row. (Every warp meets every raw tile: one that took K's alone would
+        // pass a slot's barrier on the phase before last, V's tile in between.)
+        const int w = warp - kDqWarp0, row = 16 * w + (lane & 15), odd = lane >> 4;
+        const int hb = q8_head_bytes(B, D), off = row & (B - 1);
+        const uint32_t block = uint32_t((row >> p.log2_block) * hb);
+        const uint32_t src = block + uint32_t((off + odd * B) * 16), scale = block + uint32_t(q8_scale_at(B, D));
+        const uint32_t step = uint32_t(2 * B * 16);               // between this lane's panels
+        const uint32_t dst = base + Ly::kKv + uint32_t(row * 128 + ((row & 7) << 4));
+        int rs = 0, st = 0;                                       // raw slot and stage, and their phases
+        uint32_t rphase = 0, sphase = 1;
+        bool ok = true;
+        for (int m = 0; ok; ++m) {
+            const int k = pf_item_index<kSplit>(m);
+            if (k >= num_items) break;
+            PfItem it;
+            if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
+            float factor = 0.f;      // of the 16 keys' sums
+            unsigned nans = 0;       // keys of them with a NaN
+            const int past = it.L - (it.kb + it.nkt - 1) * kTcKeys;   // the last tile's keys within the context
+#pragma unroll 1
+            for (int x = 2 * it.nkt; x > 0; --x) {
+                const bool of_v = x & 1;
+                const uint32_t rfull = base + Ly::kRawBars + 16 * rs, raw = base + Ly::kRaw + uint32_t(rs * Ly::kRawHalf);
+                // the raw tile is there, and (K) the stage's last readers are done
+                bool got = mbar_try_wait(rfull, rphase);
+                if (!of_v) got = mbar_try_wait(bar(kKvEmpty + st), sphase) && got;
+                if (!__all_sync(kAll, got)) {
+                    got = !aborted() && mbar_wait(rfull, rphase, p.err) &&
+                          (of_v || mbar_wait(bar(kKvEmpty + st), sphase, p.err));
+                    if (!__all_sync(kAll, got)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                const uint2 info = lds64_u2(raw + scale);
+                // 16 keys under one scale, that of their block. Two blocks of 8 may have two:
+                // the smaller one's codes then go down by a power of two, exactly to 2^-15.
+                int most = min(max(int((info.x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp);
+                unsigned marked = 0;
+                bool rare = x <= 2 || info.y != 0, live = true;
+                uint32_t by = 0x3c003c00u;      // 1
+                if (B == 8 || rare) {
+                    live = x > 2 || row < past;
+                    // (a block past the context has no scale; one that begins before its end has)
+                    const int e = x > 2 || (row & ~7) < past ? most : kQ8LeastExp;
+                    most = __reduce_max_sync(kAll, e);
+                    marked = __ballot_sync(kAll, live && ((info.y >> off) & 1u)) & 0xffffu;
+                    rare = __any_sync(kAll, rare || e != most) != 0;
+                    by = pack_half2(q8_power(max(e - most, -24)));
+                }
+                const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
+                auto load = [&](int i) { return lds128_u4(raw + src + uint32_t(i) * step); };
+                auto put = [&](int i, const uint32_t (&v)[8]) {
+                    // panel 2 i + odd: chunks 2 (2 i + odd) and the next of the row, swizzled by its low bits
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        sts128((to ^ uint32_t((((4 * i + 2 * odd) & 7) + c) << 4)) + uint32_t((i >> 1) * Ly::kKvSlab),
+                               make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+                };
+                auto to_bf16 = [](uint32_t (&v)[8]) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float2 a = Elem<__half>::unpack2(v[c]);
+                        v[c] = Elem<__nv_bfloat16>::pack2(a.x, a.y);
+                    }
+                };
+                // One run of instructions, all loads in flight. (With the rare cases below as
+                // conditions in it, jumped over panel by panel, the warps took longer than a
+                // key tile's MMAs.)
+                auto plain = [&](auto bf16) {
+                    uint4 cw[D / 32];
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) cw[i] = load(i);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t v[8];
+                        q8_halves(cw[i].x, v[0], v[1]);
+                        q8_halves(cw[i].y, v[2], v[3]);
+                        q8_halves(cw[i].z, v[4], v[5]);
+                        q8_halves(cw[i].w, v[6], v[7]);
+                        if constexpr (decltype(bf16)::value) to_bf16(v);
+                        put(i, v);
+                    }
+                };
+                if (rare) {
+#pragma unroll 1
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint4 cw = load(i);
+                        const uint32_t c4[4] = {cw.x, cw.y, cw.z, cw.w};
+                        uint32_t v[8];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // A NaN counts where its key is attended to, by the key's bit: in
+                            // the stage it is a zero, since it must not meet the weight 0 of
+                            // rows that do not see it. A row past the context is zeros.
+                            const uint32_t bad = ((c4[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            q8_halves(live ? c4[c] & ~((bad >> 7) * 255u) : 0u, v[2 * c], v[2 * c + 1]);
+                            v[2 * c] = hmul2_u(v[2 * c], by);
+                            v[2 * c + 1] = hmul2_u(v[2 * c + 1], by);
+                        }
+                        if (kBf16 && !of_v) to_bf16(v);
+                        put(i, v);
+                    }
+                } else if (kBf16 && !of_v) {
+                    plain(std::true_type{});
+                } else {
+                    plain(std::false_type{});
+                }
+                if (!of_v) {
+                    // (a factor of 0 would turn a masked score's -inf into a NaN)
+                    factor = fmaxf(fabsf(p.scale_log2) * q8_power(most), 0x1p-126f);
+                    nans = marked;
+                } else {
+                    if (lane == 0)
+                        sts128(base + Ly::kScales + uint32_t(st * Ly::kScalesStage + 16 * w),
+                               make_uint4(__float_as_uint(factor), __float_as_uint(float(most)),
+                                          __float_as_uint(q8_power(-most)), nans | marked));
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(rfull + 8);
+                    if (of_v) mbar_arrive(bar(kKvFull + st));
+                }
+                if (++rs == kRawStages) {
+                    rs = 0;
+                    rphase ^= 1u;
+                }
+                if (of_v && ++st == kTcStages) {
+                    st = 0;
+                    sphase ^= 1u;
+                }
+            }
         }
         if (lane == 0 && !ok) sts32(flag, 1);
         __syncwarp();
@@ -948,7 +1076,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 qdesc[kk] = tc_desc_sw128(qb + (kk >> 2) * Ly::kQSlab + (kk & 3) * 32, 16, 1024);
             // S of key tile gk of the ring (gj-th key tile of this Q tile) into S buffer gj & 1
             auto issue_s = [&](int gk, int gj) {
-                const uint64_t kdesc = tc_desc_sw128(base + Ly::kKv + (gk % kStages) * Ly::kStage, 16, 1024);
+                const uint64_t kdesc = tc_desc_sw128(base + Ly::kKv + (gk % kTcStages) * Ly::kStage, 16, 1024);
                 const uint32_t d = tmem + uint32_t(t * kTmemTile + (gj & 1) * kTcKeys);
                 if (leader) {
 #pragma unroll
@@ -964,7 +1092,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // O (+)= P V; `first` starts the item's accumulator
             auto issue_pv = [&](int gk, int gj, bool first) {
                 const uint64_t vdesc =
-                    tc_desc_sw128(base + Ly::kKv + (gk % kStages) * Ly::kStage + Ly::kHalf, Ly::kKvSlab, 1024);
+                    tc_desc_sw128(base + Ly::kKv + (gk % kTcStages) * Ly::kStage + Ly::kHalf, Ly::kKvSlab, 1024);
                 // P: the first 32 columns of S buffer gj & 1 (16 keys per 8 columns)
                 const uint32_t pa = tmem + uint32_t(t * kTmemTile + (gj & 1) * kTcKeys);
                 const uint32_t d = tmem + uint32_t(t * kTmemTile + 2 * kTcKeys);
@@ -991,7 +1119,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (!ok) break;
                 if (nk > 0) {
                     for (int j = 0; ok && j < 2 && j < nk; ++j) {
-                        ok = wait(kKvFull + (kt + j) % kStages, (kt + j) / kStages);
+                        ok = wait(kKvFull + (kt + j) % kTcStages, (kt + j) / kTcStages);
                         if (!ok) break;
                         tc_fence_after_sync();
                         issue_s(kt + j, jt + j);
@@ -1016,18 +1144,18 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const int gk2 = gk + 2;
                         const bool kv_in = __all_sync(
                             kAll, ok && ahead &&
-                                      mbar_test_wait(bar(kKvFull + gk2 % kStages), uint32_t((gk2 / kStages) & 1)));
+                                      mbar_test_wait(bar(kKvFull + gk2 % kTcStages), uint32_t((gk2 / kTcStages) & 1)));
                         if (!ok) break;
                         tc_fence_after_sync();
                         issue_pv(gk, jt + j, j == 0);
                         // the stage of key tile j is free once this P V (the last MMA of
                         // this thread that reads it) completes
-                        commit(kKvEmpty + gk % kStages);
+                        commit(kKvEmpty + gk % kTcStages);
                         // this tile's S two key tiles ahead (its S buffer is free once the
                         // P V just issued has read P)
                         if (ahead) {
                             if (!kv_in) {
-                                ok = wait(kKvFull + gk2 % kStages, gk2 / kStages);
+                                ok = wait(kKvFull + gk2 % kTcStages, gk2 / kTcStages);
                                 if (!ok) break;
                                 tc_fence_after_sync();
                             }
@@ -1037,9 +1165,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     } else {
                         // a key tile this Q tile skips: its stage may be released only
                         // after it landed (the arrival belongs to this phase of the slot)
-                        ok = wait(kKvFull + gk % kStages, gk / kStages);
+                        ok = wait(kKvFull + gk % kTcStages, gk / kTcStages);
                         if (!ok) break;
-                        commit(kKvEmpty + gk % kStages);
+                        commit(kKvEmpty + gk % kTcStages);
                     }
                 }
                 if (!ok) break;
@@ -1174,15 +1302,20 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
                 }
                 float mx;
-                [[maybe_unused]] uint32_t per8;   // the stage's factors and exponents for each 8 keys
+                [[maybe_unused]] uint32_t per16;   // the stage's factors and exponents for each 16 keys
                 if constexpr (kBits == 8) {
-                    per8 = base + Ly::kScales + uint32_t(((kt + j) % kStages) * Ly::kScalesStage);
+                    per16 = base + Ly::kScales + uint32_t(((kt + j) % kTcStages) * Ly::kScalesStage);
                     mx = -INFINITY;
 #pragma unroll
-                    for (int u = 0; u < kTcKeys / 8; ++u) {
-                        const float2 f = lds64_f2(per8 + 16 * u);
-                        const float a = fmax3(fmax3(sc[8 * u], sc[8 * u + 1], sc[8 * u + 2]), sc[8 * u + 3], sc[8 * u + 4]);
-                        mx = fmaxf(mx, fmaf(fmax3(a, fmaxf(sc[8 * u + 5], sc[8 * u + 6]), sc[8 * u + 7]), f.x, f.y));
+                    for (int u = 0; u < kTcKeys / 16; ++u) {
+                        float m2[2] = {fmaxf(sc[16 * u], sc[16 * u + 1]), fmaxf(sc[16 * u + 2], sc[16 * u + 3])};
+#pragma unroll
+                        for (int x = 16 * u + 4; x < 16 * u + 16; x += 4) {
+                            m2[0] = fmax3(m2[0], sc[x], sc[x + 1]);
+                            m2[1] = fmax3(m2[1], sc[x + 2], sc[x + 3]);
+                        }
+                        const float2 f = lds64_f2(per16 + 16 * u);
+                        mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), f.x, f.y));
                     }
                 } else {
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1220,27 +1353,32 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 uint32_t pk[kTcKeys / 2];
                 if constexpr (kBits == 8) {
                     l *= alpha;
+                    const float back = ref == -INFINITY ? 0.f : -ref;
+                    uint32_t bad[kTcKeys / 16];
 #pragma unroll
-                    for (int u = 0; u < kTcKeys / 8; ++u) {
-                        const uint4 f = lds128_u4(per8 + 16 * u);
-                        const float k = __uint_as_float(f.x);
-                        const float nu = ref == -INFINITY ? 0.f : __uint_as_float(f.y) - ref;
-                        float s2[2] = {0.f, 0.f};
+                    for (int u = 0; u < kTcKeys / 16; ++u) {
+                        const uint4 f = lds128_u4(per16 + 16 * u);
+                        const float k = __uint_as_float(f.x), nu = __uint_as_float(f.y) + back;
+                        bad[u] = f.w;
+                        float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int x = 8 * u; x < 8 * u + 8; x += 2) {
+                        for (int x = 16 * u; x < 16 * u + 16; x += 2) {
                             ffma2(sc[x], sc[x + 1], k, nu);
                             sc[x] = fast_exp2(sc[x]);
                             sc[x + 1] = fast_exp2(sc[x + 1]);
-                            fadd2(s2[0], s2[1], sc[x], sc[x + 1]);
-                            pk[x / 2] = Elem<__half>::pack2(sc[x], sc[x + 1]);
+                            if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
+                            else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
                         }
-                        l = fmaf(s2[0] + s2[1], __uint_as_float(f.z), l);
+                        l = fmaf((s4[0] + s4[1]) + (s4[2] + s4[3]), __uint_as_float(f.z), l);
                     }
-                    // keys whose V holds a NaN, among those that this row attends to
-                    const unsigned long long bad = lds64_u(per8 + kTcKeys / 8 * 16);
-                    if (bad != 0) {
+#pragma unroll
+                    for (int c = 0; c < kTcKeys / 2; ++c) pk[c] = Elem<__half>::pack2(sc[2 * c], sc[2 * c + 1]);
+                    // keys whose K or V holds a NaN, among those that this row attends to
+                    if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0) {
+                        const unsigned long long keys =
+                            (bad[0] | bad[1] << 16) | (unsigned long long)(bad[2] | bad[3] << 16) << 32;
                         const int seen = min(max(pos - k0 + 1, 0), kTcKeys);
-                        if (seen > 0 && (bad << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
+                        if (seen > 0 && (keys << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
                     }
                 } else {
                     const float nu = ref == -INFINITY ? 0.f : -ref;

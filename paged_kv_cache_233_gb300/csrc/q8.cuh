@@ -22,6 +22,14 @@ __device__ __forceinline__ uint32_t q8_codes(float x0, float x1, float x2, float
     return w;
 }
 
+// A float of fp16's range twice, and packed products.
+__device__ __forceinline__ uint32_t pack_half2(float x) { return Elem<__half>::pack2(x, x); }
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // 2^e for e of [-126, 127], and the exponent of a scale.
 __device__ __forceinline__ float q8_power(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 __device__ __forceinline__ int q8_exponent(float scale) { return int((__float_as_uint(scale) >> 23) & 255u) - 127; }

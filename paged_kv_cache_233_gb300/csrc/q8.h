@@ -7,7 +7,9 @@
 // that fall below 2^-6, when a new row takes the scale up.) The bytes of one
 // (block, kv head) are
 //     codes  [head_dim / 16 panels][block_size tokens][16 channels]
-//     scale  fp32, then nothing up to 16 bytes (32 in blocks of 32)
+//     scale  fp32
+//     marks  32 bits, bit t set when token t's row holds a NaN; then nothing up to 16
+//            bytes in all (32 in blocks of 32)
 // a multiple of 16; a pool is [num_blocks][n_kv_heads] of them, so the blocks of
 // neighbouring kv heads are one contiguous run that an untiled bulk copy brings in,
 // scale and all. Eight tokens' codes of one panel are 128 contiguous bytes: the

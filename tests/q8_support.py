@@ -3,7 +3,8 @@
 Written from the definition alone: the tokens of a block and kv head share a scale
 2^e, a channel is an e4m3 code c that stands for c * 2^e; a pool holds
 [num_blocks][n_kv_heads] runs of codes [D / 16][B][16] followed by the scale in
-fp32 and padding up to 16 bytes (32 in blocks of 32).
+fp32, 32 marks of tokens whose rows hold a NaN, and padding up to 16 bytes (32 in
+blocks of 32).
 """
 import math
 
@@ -62,17 +63,26 @@ def new_pool(num_blocks, heads, block, dim, seed=0):
 
 
 def views(pool, dim):
-    """Codes [NB][Hkv][D / 16][B][16] and scales [NB][Hkv][1]."""
+    """Codes [NB][Hkv][D / 16][B][16], scales [NB][Hkv][1] and marks [NB][Hkv][1] (int32)."""
     nb, heads, block, _ = pool.shape
-    flat = pool.view(nb, heads, -1)
-    return (flat[..., :block * dim].unflatten(-1, (dim // 16, block, 16)),
-            flat[..., block * dim:block * dim + 4].view(torch.float32))
+    flat, at = pool.view(nb, heads, -1), block * dim
+    return (flat[..., :at].unflatten(-1, (dim // 16, block, 16)), flat[..., at:at + 4].view(torch.float32),
+            flat[..., at + 4:at + 8].view(torch.int32))
+
+
+def marks(rows):
+    """The marks of rows [n][D] as the first tokens of a block (a Python int)."""
+    return sum(1 << t for t in range(len(rows)) if not bool(torch.isfinite(rows[t]).all()))
+
+
+def signed(x):
+    return x - (1 << 32) if x >= 1 << 31 else x
 
 
 def append(pool, x, tables, starts, lens):
     """Rows [T][Hkv][D] (a CPU tensor of a 16-bit type) into a CPU pool behind each sequence's older tokens."""
     block, dim = pool.shape[2], x.shape[-1]
-    codes, scale = views(pool, dim)
+    codes, scale, mark = views(pool, dim)
     x = x.double()
     for s, L in enumerate(int(n) for n in lens):
         a, b = int(starts[s]), int(starts[s + 1])
@@ -96,12 +106,14 @@ def append(pool, x, tables, starts, lens):
                 c = code(new[:, h] * 2.0 ** -e)            # [n][D]
                 codes[bid, h, :, held:held + len(new)] = c.unflatten(-1, (-1, 16)).transpose(0, 1)
                 scale[bid, h, 0] = 2.0 ** e
+                old_marks = int(mark[bid, h, 0]) & ((1 << held) - 1)
+                mark[bid, h, 0] = signed(old_marks | marks(new[:, h]) << held)
 
 
 def read(pool, slots, dim):
     """fp64 rows [T][Hkv][D] of a CPU pool."""
     block = pool.shape[2]
-    codes, scale = views(pool, dim)
+    codes, scale, _ = views(pool, dim)
     b, o = slots // block, slots % block
     return value(codes[b, :, :, o]).flatten(-2) * scale[b].double()
 
@@ -121,7 +133,7 @@ def filled(lens, heads, block, dim, dtype, seed, spread=1.0, pad=0):
 def fill(pool, table, x):
     """A sequence's rows x [n][Hkv][D] into its blocks, block by block at once."""
     block, dim, n = pool.shape[2], x.shape[-1], len(x)
-    codes, scale = views(pool, dim)
+    codes, scale, mark = views(pool, dim)
     for j in range(-(-n // block)):
         rows, bid = x[j * block:(j + 1) * block].double(), int(table[j])
         top = rows.abs().amax((0, 2)).clamp(min=448 * 2.0 ** -64)
@@ -129,6 +141,7 @@ def fill(pool, table, x):
         c = code(rows * torch.exp2(-e)[None, :, None])     # [n][Hkv][D]
         codes[bid, :, :, :len(rows)] = c.unflatten(-1, (-1, 16)).permute(1, 2, 0, 3)
         scale[bid, :, 0] = torch.exp2(e).float()
+        mark[bid] = 0
 
 
 def attention(q, pools, tables, starts, lens, scale, dim):

@@ -36,7 +36,7 @@ def append(k, v, tables, starts, lens, kc, vc):
 
 
 def same_pool(got, want, dim):
-    """Codes and scales of every block; the bytes behind a scale are nobody's."""
+    """Codes, scales and marks of every block; the bytes behind them are nobody's."""
     return all(torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
                for a, b in zip(q8.views(got.cpu(), dim), q8.views(want, dim)))
 
@@ -405,7 +405,9 @@ def test_prefill_nan_reaches_the_rows_that_attend_to_it(operand, dtype, dim, blo
         q[first, 2:, 5] = float("inf")
     else:
         pool = kc if operand == "k" else vc
-        q8.views(pool, dim)[0][int(tables[0, at // block]), 1, 1, at % block, 3] = q8.NAN
+        codes, _, mark = q8.views(pool, dim)
+        codes[int(tables[0, at // block]), 1, 1, at % block, 3] = q8.NAN
+        mark[int(tables[0, at // block]), 1] = 1 << at % block
     for parts in (1, 32):
         out = prefill(q, kc, vc, tables, [0, chunk, 2 * chunk], [n, n], 0.125, key_parts=parts).cpu()
         assert bool(torch.isfinite(out[:, :2]).all()) and bool(torch.isfinite(out[chunk:]).all())
