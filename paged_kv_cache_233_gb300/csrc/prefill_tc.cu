@@ -175,10 +175,11 @@ struct TcLayout {
     static constexpr int kOutRow = kOrder + 8 * kMaxRankedSeqs;
     static constexpr int kRefRow = kOutRow + 8 * kTcTiles * kTcRows;
     static constexpr int kTotal = kRefRow + 4 * kTcTiles * kTcRows;
-    // 8-bit pools, per stage: for each 16 keys what turns their sums into scores, V's
-    // exponent, the inverse of V's scale, and a bit for each key whose K or V has a NaN
+    // 8-bit pools, per stage: what turns the tile's sums into scores, V's exponent, the
+    // inverse of V's scale, whether a key is marked as holding a NaN; then a bit for each
+    // key whose K, and whose V, is
     static constexpr int kScales = (kTotal + 15) & ~15;
-    static constexpr int kScalesStage = kTcKeys / 16 * 16;
+    static constexpr int kScalesStage = 16 + 2 * kTcKeys / 8;
     // 4- and 8-bit pools: the raw ring's barriers (full, empty), then its tiles: K's
     // blocks, V's (8-bit: with the scales behind the codes, blocks of 8 have the most)
     static constexpr int kRawBars = kScales + (kBits == 8 ? kTcStages * kScalesStage : 0);
@@ -221,10 +222,8 @@ __device__ __forceinline__ uint2 lds64_u2(uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
     return r;
 }
-__device__ __forceinline__ float2 lds64_f2(uint32_t addr) {
-    float2 r;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
-    return r;
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(uint16_t(v)) : "memory");
 }
 
 // Shared-memory word at a 32-bit shared address (a generic pointer would hold
@@ -898,14 +897,18 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         __syncwarp();
     } else if (kBits == 8 && warp >= kDqWarp0) {
         // -------------------------------------- 8-bit pools: raw tiles to stages
-        // K's raw tile, then V's. A warp takes 16 key rows: half a warp their even
-        // panels, the other the odd ones, 16 bytes of codes to two 16-byte chunks of the
-        // stage's row. (Every warp meets every raw tile: one that took K's alone would
-        // pass a slot's barrier on the phase before last, V's tile in between.)
+        // K's raw tile and V's: at head size 64 both at once, whose waits and loads then
+        // overlap; at 128, where three of the ring's slots fit, one after the other. A
+        // warp takes 16 key rows: half a warp their even panels, the other the odd ones, 16
+        // bytes of codes to two 16-byte chunks of the stage's row. (Every warp meets every
+        // slot's every phase: one that took K's tiles alone would pass a slot's barrier on
+        // the phase before last, V's tile in between.)
+        constexpr int kAtOnce = D == 64 ? 2 : 1;
+        static_assert(kRawStages % kAtOnce == 0, "K's slot and V's of one phase");
         const int w = warp - kDqWarp0, row = 16 * w + (lane & 15), odd = lane >> 4;
         const int hb = q8_head_bytes(B, D), off = row & (B - 1);
-        const uint32_t block = uint32_t((row >> p.log2_block) * hb);
-        const uint32_t src = block + uint32_t((off + odd * B) * 16), scale = block + uint32_t(q8_scale_at(B, D));
+        const int blk = row >> p.log2_block, some = lane & ((kTcKeys >> p.log2_block) - 1);   // a block for each lane
+        const uint32_t src = uint32_t(blk * hb + (off + odd * B) * 16), scale = uint32_t(some * hb + q8_scale_at(B, D));
         const uint32_t step = uint32_t(2 * B * 16);               // between this lane's panels
         const uint32_t dst = base + Ly::kKv + uint32_t(row * 128 + ((row & 7) << 4));
         int rs = 0, st = 0;                                       // raw slot and stage, and their phases
@@ -916,119 +919,133 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (k >= num_items) break;
             PfItem it;
             if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
-            float factor = 0.f;      // of the 16 keys' sums
-            unsigned nans = 0;       // keys of them with a NaN
+            float factor = 0.f;      // of the tile's sums
+            bool any_k = false;      // a key of it is marked
             const int past = it.L - (it.kb + it.nkt - 1) * kTcKeys;   // the last tile's keys within the context
 #pragma unroll 1
-            for (int x = 2 * it.nkt; x > 0; --x) {
-                const bool of_v = x & 1;
+            for (int x = 2 * it.nkt; x > 0; x -= kAtOnce) {
+                const bool first = kAtOnce == 2 || !(x & 1);          // K is among them
                 const uint32_t rfull = base + Ly::kRawBars + 16 * rs, raw = base + Ly::kRaw + uint32_t(rs * Ly::kRawHalf);
-                // the raw tile is there, and (K) the stage's last readers are done
+                // the raw tiles are there, and (K) the stage's last readers are done
                 bool got = mbar_try_wait(rfull, rphase);
-                if (!of_v) got = mbar_try_wait(bar(kKvEmpty + st), sphase) && got;
+                if (kAtOnce == 2) got = mbar_try_wait(rfull + 16, rphase) && got;
+                if (first) got = mbar_try_wait(bar(kKvEmpty + st), sphase) && got;
                 if (!__all_sync(kAll, got)) {
                     got = !aborted() && mbar_wait(rfull, rphase, p.err) &&
-                          (of_v || mbar_wait(bar(kKvEmpty + st), sphase, p.err));
+                          (kAtOnce == 1 || mbar_wait(rfull + 16, rphase, p.err)) &&
+                          (!first || mbar_wait(bar(kKvEmpty + st), sphase, p.err));
                     if (!__all_sync(kAll, got)) {
                         ok = false;
                         break;
                     }
                 }
-                const uint2 info = lds64_u2(raw + scale);
-                // 16 keys under one scale, that of their block. Two blocks of 8 may have two:
-                // the smaller one's codes then go down by a power of two, exactly to 2^-15.
-                int most = min(max(int((info.x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp);
-                unsigned marked = 0;
-                bool rare = x <= 2 || info.y != 0, live = true;
-                uint32_t by = 0x3c003c00u;      // 1
-                if (B == 8 || rare) {
-                    live = x > 2 || row < past;
-                    // (a block past the context has no scale; one that begins before its end has)
-                    const int e = x > 2 || (row & ~7) < past ? most : kQ8LeastExp;
-                    most = __reduce_max_sync(kAll, e);
-                    marked = __ballot_sync(kAll, live && ((info.y >> off) & 1u)) & 0xffffu;
-                    rare = __any_sync(kAll, rare || e != most) != 0;
-                    by = pack_half2(q8_power(max(e - most, -24)));
+                uint2 info[kAtOnce];
+                uint4 cw[kAtOnce][D / 32];
+#pragma unroll
+                for (int o = 0; o < kAtOnce; ++o) {
+                    const uint32_t from = raw + uint32_t(o * Ly::kRawHalf);
+                    info[o] = lds64_u2(from + scale);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) cw[o][i] = lds128_u4(from + src + uint32_t(i) * step);
                 }
-                const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
-                auto load = [&](int i) { return lds128_u4(raw + src + uint32_t(i) * step); };
-                auto put = [&](int i, const uint32_t (&v)[8]) {
-                    // panel 2 i + odd: chunks 2 (2 i + odd) and the next of the row, swizzled by its low bits
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        sts128((to ^ uint32_t((((4 * i + 2 * odd) & 7) + c) << 4)) + uint32_t((i >> 1) * Ly::kKvSlab),
-                               make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
-                };
-                auto to_bf16 = [](uint32_t (&v)[8]) {
+                for (int o = 0; o < kAtOnce; ++o) {
+                    const bool of_v = kAtOnce == 2 ? o == 1 : !first;
+                    // The tile's keys under one scale, 2^6 below their blocks' largest (448 *
+                    // 2^6 is in fp16's range): a power of two takes each code there, exactly
+                    // unless its block's scale is more than 2^21 below the largest.
+                    const bool there = x > 2 || some * B < past;    // (a block past the context has no scale)
+                    const int e = there ? min(max(int((info[o].x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp) : kQ8LeastExp;
+                    const int most = __reduce_max_sync(kAll, e);
+                    const bool any = __any_sync(kAll, there && info[o].y != 0) != 0;
+                    const uint32_t by = pack_half2(q8_power(max(__shfl_sync(kAll, e, blk) - most, -30) + 6));
+                    const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
+                    auto put = [&](int i, const uint32_t (&v)[8]) {
+                        // panel 2 i + odd: chunks 2 (2 i + odd) and the next of the row, swizzled by its low bits
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float2 a = Elem<__half>::unpack2(v[c]);
-                        v[c] = Elem<__nv_bfloat16>::pack2(a.x, a.y);
-                    }
-                };
-                // One run of instructions, all loads in flight. (With the rare cases below as
-                // conditions in it, jumped over panel by panel, the warps took longer than a
-                // key tile's MMAs.)
-                auto plain = [&](auto bf16) {
-                    uint4 cw[D / 32];
+                        for (int c = 0; c < 2; ++c)
+                            sts128((to ^ uint32_t((((4 * i + 2 * odd) & 7) + c) << 4)) + uint32_t((i >> 1) * Ly::kKvSlab),
+                                   make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+                    };
+                    auto to_bf16 = [](uint32_t (&v)[8]) {
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) cw[i] = load(i);
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t v[8];
-                        q8_halves(cw[i].x, v[0], v[1]);
-                        q8_halves(cw[i].y, v[2], v[3]);
-                        q8_halves(cw[i].z, v[4], v[5]);
-                        q8_halves(cw[i].w, v[6], v[7]);
-                        if constexpr (decltype(bf16)::value) to_bf16(v);
-                        put(i, v);
-                    }
-                };
-                if (rare) {
-#pragma unroll 1
-                    for (int i = 0; i < D / 32; ++i) {
-                        const uint4 cw = load(i);
-                        const uint32_t c4[4] = {cw.x, cw.y, cw.z, cw.w};
-                        uint32_t v[8];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            // A NaN counts where its key is attended to, by the key's bit: in
-                            // the stage it is a zero, since it must not meet the weight 0 of
-                            // rows that do not see it. A row past the context is zeros.
-                            const uint32_t bad = ((c4[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                            q8_halves(live ? c4[c] & ~((bad >> 7) * 255u) : 0u, v[2 * c], v[2 * c + 1]);
-                            v[2 * c] = hmul2_u(v[2 * c], by);
-                            v[2 * c + 1] = hmul2_u(v[2 * c + 1], by);
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 a = Elem<__half>::unpack2(v[c]);
+                            v[c] = Elem<__nv_bfloat16>::pack2(a.x, a.y);
                         }
-                        if (kBf16 && !of_v) to_bf16(v);
-                        put(i, v);
+                    };
+                    // One run of instructions. (With the rare cases below as conditions in it,
+                    // jumped over panel by panel, the warps took longer than a key tile's MMAs.)
+                    auto plain = [&](auto bf16) {
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            uint32_t v[8];
+                            q8_halves(cw[o][i].x, v[0], v[1]);
+                            q8_halves(cw[o][i].y, v[2], v[3]);
+                            q8_halves(cw[o][i].z, v[4], v[5]);
+                            q8_halves(cw[o][i].w, v[6], v[7]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) v[c] = hmul2_u(v[c], by);
+                            if constexpr (decltype(bf16)::value) to_bf16(v);
+                            put(i, v);
+                        }
+                    };
+                    if (x <= 2 || any || (of_v && any_k)) {
+                        const bool live = x > 2 || row < past;
+                        const uint32_t mine = __shfl_sync(kAll, info[o].y, blk) >> off;
+                        const unsigned marked = __ballot_sync(kAll, live && (mine & 1u)) & 0xffffu;
+                        if (lane == 0) {
+                            const uint32_t at = base + Ly::kScales + uint32_t(st * Ly::kScalesStage + 16 + 2 * w);
+                            sts16(at + (of_v ? 8u : 0u), marked);
+                            if (of_v && x > 2 && !any_k) sts16(at, 0u);    // (K's run wrote none)
+                        }
+#pragma unroll 1
+                        for (int i = 0; i < D / 32; ++i) {
+                            const uint4 c = lds128_u4(raw + uint32_t(o * Ly::kRawHalf) + src + uint32_t(i) * step);
+                            const uint32_t c4[4] = {c.x, c.y, c.z, c.w};
+                            uint32_t v[8];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                // A NaN counts where its key is attended to, by the key's bit: in
+                                // the stage it is a zero, since it must not meet the weight 0 of
+                                // rows that do not see it. A row past the context is zeros.
+                                const uint32_t bad = ((c4[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                q8_halves(live ? c4[j] & ~((bad >> 7) * 255u) : 0u, v[2 * j], v[2 * j + 1]);
+                                v[2 * j] = hmul2_u(v[2 * j], by);
+                                v[2 * j + 1] = hmul2_u(v[2 * j + 1], by);
+                            }
+                            if (kBf16 && !of_v) to_bf16(v);
+                            put(i, v);
+                        }
+                    } else if (kBf16 && !of_v) {
+                        plain(std::true_type{});
+                    } else {
+                        plain(std::false_type{});
                     }
-                } else if (kBf16 && !of_v) {
-                    plain(std::true_type{});
-                } else {
-                    plain(std::false_type{});
+                    if (!of_v) {
+                        // (a factor of 0 would turn a masked score's -inf into a NaN)
+                        factor = fmaxf(fabsf(p.scale_log2) * q8_power(most - 6), 0x1p-126f);
+                        any_k = any;
+                    } else if (w == 0 && lane == 0) {
+                        sts128(base + Ly::kScales + uint32_t(st * Ly::kScalesStage),
+                               make_uint4(__float_as_uint(factor), __float_as_uint(float(most - 6)),
+                                          __float_as_uint(q8_power(6 - most)), any || any_k ? 1u : 0u));
+                    }
                 }
-                if (!of_v) {
-                    // (a factor of 0 would turn a masked score's -inf into a NaN)
-                    factor = fmaxf(fabsf(p.scale_log2) * q8_power(most), 0x1p-126f);
-                    nans = marked;
-                } else {
-                    if (lane == 0)
-                        sts128(base + Ly::kScales + uint32_t(st * Ly::kScalesStage + 16 * w),
-                               make_uint4(__float_as_uint(factor), __float_as_uint(float(most)),
-                                          __float_as_uint(q8_power(-most)), nans | marked));
-                    fence_proxy_async_smem();
-                }
+                const bool whole = kAtOnce == 2 || !first;            // the stage is complete
+                if (whole) fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(rfull + 8);
-                    if (of_v) mbar_arrive(bar(kKvFull + st));
+                    if (kAtOnce == 2) mbar_arrive(rfull + 24);
+                    if (whole) mbar_arrive(bar(kKvFull + st));
                 }
-                if (++rs == kRawStages) {
+                rs += kAtOnce;
+                if (rs == kRawStages) {
                     rs = 0;
                     rphase ^= 1u;
                 }
-                if (of_v && ++st == kTcStages) {
+                if (whole && ++st == kTcStages) {
                     st = 0;
                     sphase ^= 1u;
                 }
@@ -1301,33 +1318,20 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                     for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
                 }
-                float mx;
-                [[maybe_unused]] uint32_t per16;   // the stage's factors and exponents for each 16 keys
-                if constexpr (kBits == 8) {
-                    per16 = base + Ly::kScales + uint32_t(((kt + j) % kTcStages) * Ly::kScalesStage);
-                    mx = -INFINITY;
+                // 8-bit pools: the tile's factor, V's exponent, the inverse of its scale, marks
+                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % kTcStages) * Ly::kScalesStage);
+                const uint4 of8 = kBits == 8 ? lds128_u4(tile) : make_uint4(0u, 0u, 0u, 0u);
+                const float factor = kBits == 8 ? __uint_as_float(of8.x) : p.scale_log2;
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int u = 0; u < kTcKeys / 16; ++u) {
-                        float m2[2] = {fmaxf(sc[16 * u], sc[16 * u + 1]), fmaxf(sc[16 * u + 2], sc[16 * u + 3])};
-#pragma unroll
-                        for (int x = 16 * u + 4; x < 16 * u + 16; x += 4) {
-                            m2[0] = fmax3(m2[0], sc[x], sc[x + 1]);
-                            m2[1] = fmax3(m2[1], sc[x + 2], sc[x + 3]);
-                        }
-                        const float2 f = lds64_f2(per16 + 16 * u);
-                        mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), f.x, f.y));
-                    }
-                } else {
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int x = 0; x < kTcKeys; x += 8) {
-                        m4[0] = fmax3(m4[0], sc[x], sc[x + 1]);
-                        m4[1] = fmax3(m4[1], sc[x + 2], sc[x + 3]);
-                        m4[2] = fmax3(m4[2], sc[x + 4], sc[x + 5]);
-                        m4[3] = fmax3(m4[3], sc[x + 6], sc[x + 7]);
-                    }
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+                for (int x = 0; x < kTcKeys; x += 8) {
+                    m4[0] = fmax3(m4[0], sc[x], sc[x + 1]);
+                    m4[1] = fmax3(m4[1], sc[x + 2], sc[x + 3]);
+                    m4[2] = fmax3(m4[2], sc[x + 4], sc[x + 5]);
+                    m4[3] = fmax3(m4[3], sc[x + 6], sc[x + 7]);
                 }
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float mx = kBits == 8 ? fmaf(top, factor, __uint_as_float(of8.y)) : top * factor;
                 const bool move = mx > ref + move_past<kBits>();
                 const float nref = kBits == 8 ? mx - below_max<kBits>() : mx;
                 const float alpha = move ? fast_exp2(ref - nref) : 1.f;   // 0 while no key was seen
@@ -1350,50 +1354,28 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         tmem_st32(otile + uint32_t(32 * c), v);
                     }
                 }
+                const float nu = ref == -INFINITY ? 0.f : kBits == 8 ? __uint_as_float(of8.y) - ref : -ref;
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < kTcKeys; x += 2) {
+                    ffma2(sc[x], sc[x + 1], factor, nu);
+                    sc[x] = fast_exp2(sc[x]);
+                    sc[x + 1] = fast_exp2(sc[x + 1]);
+                    if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
+                    else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
+                }
+                const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                l = kBits == 8 ? fmaf(sum, __uint_as_float(of8.z), l * alpha) : l * alpha + sum;
                 uint32_t pk[kTcKeys / 2];
-                if constexpr (kBits == 8) {
-                    l *= alpha;
-                    const float back = ref == -INFINITY ? 0.f : -ref;
-                    uint32_t bad[kTcKeys / 16];
 #pragma unroll
-                    for (int u = 0; u < kTcKeys / 16; ++u) {
-                        const uint4 f = lds128_u4(per16 + 16 * u);
-                        const float k = __uint_as_float(f.x), nu = __uint_as_float(f.y) + back;
-                        bad[u] = f.w;
-                        float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int x = 16 * u; x < 16 * u + 16; x += 2) {
-                            ffma2(sc[x], sc[x + 1], k, nu);
-                            sc[x] = fast_exp2(sc[x]);
-                            sc[x + 1] = fast_exp2(sc[x + 1]);
-                            if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
-                            else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
-                        }
-                        l = fmaf((s4[0] + s4[1]) + (s4[2] + s4[3]), __uint_as_float(f.z), l);
-                    }
-#pragma unroll
-                    for (int c = 0; c < kTcKeys / 2; ++c) pk[c] = Elem<__half>::pack2(sc[2 * c], sc[2 * c + 1]);
+                for (int c = 0; c < kTcKeys / 2; ++c)
+                    pk[c] = kBits == 8 ? Elem<__half>::pack2(sc[2 * c], sc[2 * c + 1]) : Elem<T>::pack2(sc[2 * c], sc[2 * c + 1]);
+                if (kBits == 8 && of8.w != 0) {
                     // keys whose K or V holds a NaN, among those that this row attends to
-                    if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0) {
-                        const unsigned long long keys =
-                            (bad[0] | bad[1] << 16) | (unsigned long long)(bad[2] | bad[3] << 16) << 32;
-                        const int seen = min(max(pos - k0 + 1, 0), kTcKeys);
-                        if (seen > 0 && (keys << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
-                    }
-                } else {
-                    const float nu = ref == -INFINITY ? 0.f : -ref;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int x = 0; x < kTcKeys; x += 2) {
-                        ffma2(sc[x], sc[x + 1], p.scale_log2, nu);
-                        sc[x] = fast_exp2(sc[x]);
-                        sc[x + 1] = fast_exp2(sc[x + 1]);
-                        if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
-                        else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
-                    }
-                    l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-#pragma unroll
-                    for (int c = 0; c < kTcKeys / 2; ++c) pk[c] = Elem<T>::pack2(sc[2 * c], sc[2 * c + 1]);
+                    const uint4 marks = lds128_u4(tile + 16);
+                    const unsigned long long keys = (marks.x | marks.z) | (unsigned long long)(marks.y | marks.w) << 32;
+                    const int seen = min(max(pos - k0 + 1, 0), kTcKeys);
+                    if (seen > 0 && (keys << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
                 }
                 tmem_st32u(trow + uint32_t(b * kTcKeys), pk);
                 // each lane's tensor-memory store has completed (tmem_st32u waits) and is
