@@ -808,7 +808,8 @@ int paged_kv_build_tables(const int32_t *new_lens, const int32_t *context_lens,
  * PAGEDKV_DEVERR_CONTEXT_LEN; such a child is not granted. A free_count outside [0,
  * free_capacity] is clamped (PAGEDKV_DEVERR_POSITION). A block id outside [0,
  * num_blocks) is copied as it is, not counted, and sets PAGEDKV_DEVERR_BLOCK_ID.
- * num_seqs <= 4096; outputs other than those named must not overlap inputs.
+ * num_seqs <= 4096, num_blocks <= 2^24; outputs other than those named must not
+ * overlap inputs.
  */
 int paged_kv_fork(const int32_t *parents, const int32_t *context_lens, int32_t *block_tables,
                   int32_t *shared, const int32_t *free_blocks, const int32_t *free_count,
@@ -844,7 +845,8 @@ int paged_kv_fork(const int32_t *parents, const int32_t *context_lens, int32_t *
  * back more often than it has holders (it goes onto the stack once), sets
  * PAGEDKV_DEVERR_BLOCK_ID; blocks past the stack's capacity are lost, and a
  * free_count outside [0, free_capacity] is clamped (PAGEDKV_DEVERR_POSITION).
- * num_seqs <= 4096; outputs other than those named must not overlap inputs.
+ * num_seqs <= 4096, num_blocks <= 2^24; outputs other than those named must not
+ * overlap inputs.
  */
 int paged_kv_release(const int32_t *keep_lens, const int32_t *context_lens,
                      const int32_t *block_tables, int32_t *shared, int32_t *free_blocks,

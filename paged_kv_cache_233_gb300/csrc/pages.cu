@@ -16,7 +16,10 @@
 // go onto the stack in the order of their ids, whatever the order of the atomics.
 //
 // The sums over the sequences run in one block of threads, and every block runs
-// them for itself; the entries are taken 32 at a time, a warp each.
+// them for itself, keeping what each sequence's entries need in shared memory; the
+// entries are taken 128 at a time, a warp each with four loads in flight. The push
+// is a cluster's work: a bit per block in shared memory, counts over the cluster by
+// distributed shared memory, then the marked ids from the bits.
 #include "launch_cache.h"
 #include "pages.h"
 #include "ptx.cuh"
@@ -28,6 +31,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kPerThread = 4;          // sequences per thread: 4096 at most
+constexpr int kRun = 128;              // entries of a warp's run
 
 struct Divisor {                       // x / B and x % B, x >= 0
     int B, shift;
@@ -43,46 +47,68 @@ __device__ __forceinline__ int free_blocks_of(const PagesParams &p, bool report)
     return min(max(n, 0), p.free_capacity);
 }
 
-// What a fork asks for s: its parent, or -1 (bad ones are reported).
-__device__ __forceinline__ int parent_of(const PagesParams &p, int s, bool report) {
-    const int of = __ldcg(p.choice + s);
-    if (of == -1) return -1;
-    if (of < 0 || of >= p.num_seqs || __ldcg(p.choice + of) != -1) {   // (a parent is no child of this call)
-        if (report) atomicOr(p.err, PAGEDKV_DEVERR_SEQ_INDEX);
-        return -1;
-    }
-    return of;
-}
-
 __device__ __forceinline__ bool bad_length(const PagesParams &p, int L) {
     return L < 0 || (long long)L > (long long)p.max_blocks * p.block_size;
 }
 
+// What a fork asks for s: its parent (or -1) and the parent's tokens. Bad ones are reported.
+__device__ __forceinline__ int parent_of(const PagesParams &p, int of, bool report, int &L) {
+    L = 0;
+    if (of == -1) return -1;
+    const bool in = of >= 0 && of < p.num_seqs;
+    const int above = in ? __ldcg(p.choice + of) : 0, tokens = in ? __ldcg(p.context_lens + of) : 0;
+    if (above != -1) {              // (a parent is no child of this call)
+        if (report) atomicOr(p.err, PAGEDKV_DEVERR_SEQ_INDEX);
+        return -1;
+    }
+    if (bad_length(p, tokens)) {
+        if (report) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
+        return -1;
+    }
+    L = tokens;
+    return of;
+}
+
+// What the entries' part of a kernel needs of each sequence, in shared memory.
+struct Runs {
+    int *run0;            // [num_seqs + 1]: runs before each sequence's
+    int *count;           // [num_seqs]: entries
+    uint16_t *of;         // [num_seqs]: fork's parent
+    __device__ Runs(int *memory, int S) : run0(memory), count(memory + S + 1), of(reinterpret_cast<uint16_t *>(memory + 2 * S + 1)) {}
+};
+int runs_bytes(int S) { return 4 * (2 * S + 1) + 2 * S; }
+
+// Every run of entries there is, a warp each: body(sequence, its first entry's number, entries left).
+template <typename Body>
+__device__ __forceinline__ void for_runs(const Runs &r, int S, int total, Body body) {
+    const int warps = int(blockDim.x >> 5);
+    for (int c = int(blockIdx.x) * warps + int(threadIdx.x >> 5); c < total; c += int(gridDim.x) * warps) {
+        const int s = last_at_or_before(r.run0, S, c), first = (c - r.run0[s]) * kRun;
+        body(s, first, r.count[s] - first);
+    }
+}
+
 // `totals`: write the count after the call too.
 __global__ void __launch_bounds__(kMaxThreads) fork_kernel(const __grid_constant__ PagesParams p, bool totals) {
-    extern __shared__ int chunk0[];    // [num_seqs + 1]: runs of 32 entries before each sequence's
+    extern __shared__ int memory[];
     __shared__ uint2 warp_sums[32];
     const Divisor by(p);
     const int S = p.num_seqs;
+    const Runs r(memory, S);
     const unsigned rank = blockIdx.x;
     grid_dependency_wait();
     const int count = free_blocks_of(p, rank == 0 && threadIdx.x == 0);
     const int per = (S + int(blockDim.x) - 1) / int(blockDim.x), s0 = int(threadIdx.x) * per;
     int of[kPerThread], L[kPerThread];
-    unsigned need = 0, chunks = 0, t0, t1;
+    unsigned need = 0, runs = 0, t0, t1;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) of[i] = i < per && s0 + i < S ? parent_of(p, s0 + i, rank == 0) : -1;
+    for (int i = 0; i < kPerThread; ++i) of[i] = i < per && s0 + i < S ? __ldcg(p.choice + s0 + i) : -1;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-        L[i] = of[i] >= 0 ? __ldcg(p.context_lens + of[i]) : 0;
-        if (bad_length(p, L[i])) {
-            if (rank == 0) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
-            of[i] = -1;
-            L[i] = 0;
-        }
+        of[i] = parent_of(p, of[i], rank == 0, L[i]);
         need += unsigned(by.blocks(L[i]) - by.quotient(L[i]));
     }
-    block_scan(need, chunks, t0, t1, warp_sums);       // (no chunks yet)
+    block_scan(need, runs, t0, t1, warp_sums);         // (no runs yet)
     const unsigned needed = min(t0, unsigned(count));
     unsigned nth = need;
 #pragma unroll
@@ -91,7 +117,8 @@ __global__ void __launch_bounds__(kMaxThreads) fork_kernel(const __grid_constant
         const bool started = by.blocks(L[i]) > full;
         const int s = s0 + i;
         const bool go = of[i] >= 0 && (!started || nth < unsigned(count));
-        if (rank == 0 && i < per && s < S) {
+        // (the blocks take turns with the sequences)
+        if (i < per && s < S && unsigned(s) % gridDim.x == rank) {
             int2 pair = make_int2(0, 0);
             if (go && started) {
                 const int id = __ldcg(p.free_blocks + (count - 1 - int(nth)));
@@ -106,32 +133,38 @@ __global__ void __launch_bounds__(kMaxThreads) fork_kernel(const __grid_constant
             else if (p.context_lens_out != p.context_lens) p.context_lens_out[s] = __ldcg(p.context_lens + s);
         }
         if (started) ++nth;
-        if (!go) L[i] = 0;
-        chunks += unsigned(by.quotient(L[i]) + 31) / 32;
+        L[i] = go ? full : 0;                          // entries to copy, from here on
+        runs += unsigned(L[i] + kRun - 1) / kRun;
     }
     unsigned zero = 0;
-    block_scan(chunks, zero, t0, t1, warp_sums);
+    block_scan(runs, zero, t0, t1, warp_sums);
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         if (i < per && s0 + i < S) {
-            chunk0[s0 + i] = int(chunks);
-            chunks += unsigned(by.quotient(L[i]) + 31) / 32;
+            r.run0[s0 + i] = int(runs);
+            r.count[s0 + i] = L[i];
+            r.of[s0 + i] = uint16_t(of[i]);
+            runs += unsigned(L[i] + kRun - 1) / kRun;
         }
     }
-    if (threadIdx.x == 0) chunk0[S] = int(t0);
+    if (threadIdx.x == 0) r.run0[S] = int(t0);
     __syncthreads();
     if (totals && rank == 0 && threadIdx.x == 0) *p.free_count_out = count - int(needed);
-    const int lane = threadIdx.x & 31, warps = int(blockDim.x >> 5);
-    for (int c = int(rank) * warps + int(threadIdx.x >> 5); c < int(t0); c += int(gridDim.x) * warps) {
-        const int s = last_at_or_before(chunk0, S, c);
-        const int parent = __ldcg(p.choice + s);
-        const int j = (c - chunk0[s]) * 32 + lane;
-        if (j >= by.quotient(__ldcg(p.context_lens + parent))) continue;
-        const int id = __ldcg(p.block_tables + size_t(parent) * p.max_blocks + j);
-        p.block_tables[size_t(s) * p.max_blocks + j] = id;
-        if (id < 0 || id >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-        else atomicAdd(p.shared + id, 1);
-    }
+    const int lane = threadIdx.x & 31;
+    for_runs(r, S, int(t0), [&](int s, int first, int left) {
+        const int32_t *src = p.block_tables + size_t(r.of[s]) * p.max_blocks + first + lane;
+        int32_t *dst = p.block_tables + size_t(s) * p.max_blocks + first + lane;
+        int id[kRun / 32];
+#pragma unroll
+        for (int i = 0; i < kRun / 32; ++i) id[i] = 32 * i + lane < left ? __ldcg(src + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < kRun / 32; ++i) {
+            if (32 * i + lane >= left) continue;
+            dst[32 * i] = id[i];
+            if (id[i] < 0 || id[i] >= p.num_blocks) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+            else atomicAdd(p.shared + id[i], 1);
+        }
+    });
 }
 
 // The count after a fork, in place: how many started blocks were copied.
@@ -141,10 +174,9 @@ __global__ void __launch_bounds__(kMaxThreads) fork_total_kernel(const __grid_co
     const Divisor by(p);
     int taken = 0;
     for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
-        const int of = parent_of(p, s, false);
-        if (of < 0) continue;
-        const int L = __ldcg(p.context_lens + of);
-        if (!bad_length(p, L)) taken += by.blocks(L) - by.quotient(L);
+        int L;
+        parent_of(p, __ldcg(p.choice + s), false, L);
+        taken += by.blocks(L) - by.quotient(L);
     }
     taken = __reduce_add_sync(kAllLanes, taken);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = taken;
@@ -161,53 +193,62 @@ __device__ __forceinline__ int kept(const PagesParams &p, int L, int keep) {
     return bad_length(p, L) || keep < 0 ? -1 : min(L, keep);
 }
 
-__global__ void __launch_bounds__(kMaxThreads) release_kernel(const __grid_constant__ PagesParams p) {
-    extern __shared__ int chunk0[];    // [num_seqs + 1]: runs of 32 entries before each sequence's
-    __shared__ uint2 warp_sums[32];
+// The blocks that are given back lose a holder.
+__device__ __forceinline__ void drop_holders(const PagesParams &p, int *memory, uint2 *warp_sums) {
     const Divisor by(p);
     const int S = p.num_seqs;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    const Runs r(memory, S);
     const int per = (S + int(blockDim.x) - 1) / int(blockDim.x), s0 = int(threadIdx.x) * per;
-    int given[kPerThread];
-    unsigned chunks = 0, zero = 0, t0, t1;
+    int L[kPerThread], keep[kPerThread];
+    unsigned runs = 0, zero = 0, t0, t1;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-        given[i] = 0;
-        if (i >= per || s0 + i >= S) continue;
-        const int L = __ldcg(p.context_lens + s0 + i), keep = kept(p, L, __ldcg(p.choice + s0 + i));
-        if (keep < 0) {
-            if (blockIdx.x == 0) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
-            continue;
-        }
-        given[i] = by.blocks(L) - by.blocks(keep);
-        chunks += unsigned(given[i] + 31) / 32;
+        const bool in = i < per && s0 + i < S;
+        L[i] = in ? __ldcg(p.context_lens + s0 + i) : 0;
+        keep[i] = in ? __ldcg(p.choice + s0 + i) : 0;
     }
-    block_scan(chunks, zero, t0, t1, warp_sums);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        keep[i] = kept(p, L[i], keep[i]);
+        if (keep[i] < 0) {
+            if (blockIdx.x == 0) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
+            keep[i] = L[i] = 0;
+        }
+        runs += unsigned(by.blocks(L[i]) - by.blocks(keep[i]) + kRun - 1) / kRun;
+    }
+    block_scan(runs, zero, t0, t1, warp_sums);
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         if (i < per && s0 + i < S) {
-            chunk0[s0 + i] = int(chunks);
-            chunks += unsigned(given[i] + 31) / 32;
+            const int given = by.blocks(L[i]) - by.blocks(keep[i]);
+            r.run0[s0 + i] = int(runs);
+            r.count[s0 + i] = given;
+            runs += unsigned(given + kRun - 1) / kRun;
         }
     }
-    if (threadIdx.x == 0) chunk0[S] = int(t0);
+    if (threadIdx.x == 0) r.run0[S] = int(t0);
     __syncthreads();
-    const int lane = threadIdx.x & 31, warps = int(blockDim.x >> 5);
-    for (int c = int(blockIdx.x) * warps + int(threadIdx.x >> 5); c < int(t0); c += int(gridDim.x) * warps) {
-        const int s = last_at_or_before(chunk0, S, c);
-        const int L = __ldcg(p.context_lens + s), first = by.blocks(min(L, __ldcg(p.choice + s)));
-        const int j = first + (c - chunk0[s]) * 32 + lane;
-        if (j >= by.blocks(L)) continue;
-        const int id = __ldcg(p.block_tables + size_t(s) * p.max_blocks + j);
-        // (given back more often than it has holders: once is what it counts)
-        if (id < 0 || id >= p.num_blocks || atomicSub(p.shared + id, 1) < 0) atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-    }
+    const int lane = threadIdx.x & 31;
+    for_runs(r, S, int(t0), [&](int s, int first, int left) {
+        // (its last r.count[s] entries)
+        const int end = by.blocks(__ldcg(p.context_lens + s));
+        const int32_t *src = p.block_tables + size_t(s) * p.max_blocks + (end - left) + lane;
+        int id[kRun / 32];
+#pragma unroll
+        for (int i = 0; i < kRun / 32; ++i) id[i] = 32 * i + lane < left ? __ldcg(src + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < kRun / 32; ++i) {
+            // (given back more often than it has holders: once is what it counts)
+            if (32 * i + lane < left && (id[i] < 0 || id[i] >= p.num_blocks || atomicSub(p.shared + id[i], 1) < 0))
+                atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+        }
+    });
 }
 
 // Blocks whose count went below zero, onto the stack in the order of their ids; the
-// lengths and the count after the call. A cluster, a run of the blocks per warp.
-constexpr int kPushCtas = 8;
+// lengths and the count after the call. A run of 32-block words per warp.
+constexpr int kPushCtas = 16;
+constexpr int kSmallBlocks = 1 << 15;  // up to as many, one block of threads pushes
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -225,33 +266,43 @@ __device__ __forceinline__ int cluster_load(const int *p, uint32_t rank) {
     return v;
 }
 
+__host__ __device__ constexpr int push_words(int num_blocks, int ctas) {   // a warp's words, of 1024 threads
+    return ((num_blocks + 31) / 32 + 32 * ctas - 1) / (32 * ctas);
+}
+
 template <bool kCluster>
-__global__ void __launch_bounds__(kMaxThreads) push_kernel(const __grid_constant__ PagesParams p) {
+__device__ __forceinline__ void push(const PagesParams &p, uint32_t *words) {
     __shared__ int warp_sums[32], total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = kCluster ? kPushCtas : 1, rank = kCluster ? int(cluster_rank()) : 0;
-    grid_dependency_wait();
     const int count = free_blocks_of(p, rank == 0 && threadIdx.x == 0);
     for (int s = rank * kMaxThreads + int(threadIdx.x); s < p.num_seqs; s += ctas * kMaxThreads) {
         const int L = __ldcg(p.context_lens + s), keep = kept(p, L, __ldcg(p.choice + s));
         p.context_lens_out[s] = keep < 0 ? L : keep;
     }
-    // this warp's run of blocks
-    const int warps = ctas * 32, per = ((p.num_blocks + warps - 1) / warps + 31) / 32 * 32;
-    const int b0 = min((long long)(rank * 32 + warp) * per, (long long)p.num_blocks), b1 = min(b0 + per, p.num_blocks);
-    int mine = 0;
-    for (int b = b0; b < b1; b += 128) {
-        int v[4];
+    // this warp's words: a bit for each block that is gone
+    const int per = push_words(p.num_blocks, ctas), w0 = (rank * 32 + warp) * per;
+    uint32_t *mine = words + warp * per;
+    int gone = 0;
+    constexpr int kBatch = 8;
+    for (int w = 0; w < per; w += kBatch) {
+        int v[kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = b + 32 * i + lane < b1 ? __ldcg(p.shared + b + 32 * i + lane) : 0;
+        for (int i = 0; i < kBatch; ++i) {
+            const long long b = (long long)(w0 + w + i) * 32 + lane;
+            v[i] = w + i < per && b < p.num_blocks ? __ldcg(p.shared + b) : 0;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mine += __popc(__ballot_sync(kAllLanes, v[i] < 0));
+        for (int i = 0; i < kBatch; ++i) {
+            const unsigned m = __ballot_sync(kAllLanes, v[i] < 0);
+            gone += __popc(m);
+            if (lane == 0 && w + i < per) mine[w + i] = m;
+        }
     }
-    if (lane == 0) warp_sums[warp] = mine;
+    if (lane == 0) warp_sums[warp] = gone;
     __syncthreads();
-    int w = warp_sums[lane];
-    const int all = __reduce_add_sync(kAllLanes, w);
-    int at = __reduce_add_sync(kAllLanes, lane < warp ? w : 0);   // pushed by the warps before this one
+    const int sum = warp_sums[lane], all = __reduce_add_sync(kAllLanes, sum);
+    int at = __reduce_add_sync(kAllLanes, lane < warp ? sum : 0);   // pushed by the warps before this one
     int pushed = all;
     if (kCluster) {
         if (threadIdx.x == 0) total = all;
@@ -260,26 +311,39 @@ __global__ void __launch_bounds__(kMaxThreads) push_kernel(const __grid_constant
         at += __reduce_add_sync(kAllLanes, lane < rank ? other : 0);
         pushed = __reduce_add_sync(kAllLanes, other);
         cluster_sync();          // (no block leaves while another reads its total; every block has read the count)
-    } else {
-        __syncthreads();
     }
     if (rank == 0 && threadIdx.x == 0) {
         const int room = p.free_capacity - count;
         if (pushed > room) atomicOr(p.err, PAGEDKV_DEVERR_POSITION);
         *p.free_count_out = count + min(pushed, room);
     }
-    if (mine == 0) return;
+    if (gone == 0) return;
     at += count;
-    for (int b = b0; b < b1; b += 32) {
-        const bool gone = b + lane < b1 && __ldcg(p.shared + b + lane) < 0;
-        const unsigned m = __ballot_sync(kAllLanes, gone);
-        if (gone) {
+    for (int w = 0; w < per; ++w) {
+        const unsigned m = mine[w];
+        const int b = (w0 + w) * 32 + lane;
+        if ((m >> lane) & 1u) {
             const int to = at + __popc(m & ((1u << lane) - 1));
-            if (to < p.free_capacity) p.free_blocks[to] = b + lane;
-            p.shared[b + lane] = 0;
+            if (to < p.free_capacity) p.free_blocks[to] = b;
+            p.shared[b] = 0;
         }
         at += __popc(m);
     }
+}
+
+__global__ void __launch_bounds__(kMaxThreads) release_kernel(const __grid_constant__ PagesParams p) {
+    extern __shared__ int memory[];
+    __shared__ uint2 warp_sums[32];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    drop_holders(p, memory, warp_sums);
+}
+
+template <bool kCluster>
+__global__ void __launch_bounds__(kMaxThreads) push_kernel(const __grid_constant__ PagesParams p) {
+    extern __shared__ int memory[];
+    grid_dependency_wait();
+    push<kCluster>(p, reinterpret_cast<uint32_t *>(memory));
 }
 
 cudaLaunchConfig_t config(cudaLaunchAttribute *attr, int grid, int threads, int smem, cudaStream_t st) {
@@ -295,12 +359,10 @@ cudaLaunchConfig_t config(cudaLaunchAttribute *attr, int grid, int threads, int 
     return cfg;
 }
 
-// Threads and blocks for the sums over the sequences and a warp for each 32 entries that there may be.
+// Threads and blocks for the sums over the sequences and a warp for each run of entries that there may be.
 void shape(const PagesParams &p, int num_sms, int &threads, int &blocks) {
-    threads = 128;
-    while (threads < kMaxThreads && threads * kPerThread < p.num_seqs) threads <<= 1;
-    if (threads < 512 && p.num_seqs > 32) threads = 512;
-    const long long warps = (long long)p.num_seqs * ((p.max_blocks + 31) / 32), want = (warps * 32 + threads - 1) / threads;
+    threads = p.num_seqs > 512 ? kMaxThreads : p.num_seqs > 32 ? 512 : 128;
+    const long long warps = (long long)p.num_seqs * ((p.max_blocks + kRun - 1) / kRun), want = (warps * 32 + threads - 1) / threads;
     blocks = int(want < 1 ? 1 : want < num_sms ? want : num_sms);
 }
 
@@ -311,7 +373,7 @@ cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
     shape(p, num_sms, threads, blocks);
     const bool totals = blocks == 1 || p.free_count_out != p.free_count;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config(attr, blocks, threads, int(sizeof(int)) * (p.num_seqs + 1), st);
+    cudaLaunchConfig_t cfg = config(attr, blocks, threads, runs_bytes(p.num_seqs), st);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fork_kernel, p, totals);
     if (e != cudaSuccess || totals) return e;
     cfg = config(attr, 1, p.num_seqs > 256 ? kMaxThreads : 256, 0, st);
@@ -319,17 +381,34 @@ cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
 }
 
 cudaError_t launch_release(const PagesParams &p, int num_sms, cudaStream_t st) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg;
     int threads, blocks;
     shape(p, num_sms, threads, blocks);
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config(attr, blocks, threads, int(sizeof(int)) * (p.num_seqs + 1), st);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, release_kernel, p);
+    cfg = config(attr, blocks, threads, runs_bytes(p.num_seqs), st);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, release_kernel, p);
     if (e != cudaSuccess) return e;
-    if (p.num_blocks <= 32 * kMaxThreads) {
-        cfg = config(attr, 1, kMaxThreads, 0, st);
+    if (p.num_blocks <= kSmallBlocks) {
+        cfg = config(attr, 1, kMaxThreads, 4 * 32 * push_words(p.num_blocks, 1), st);
         return cudaLaunchKernelEx(&cfg, push_kernel<false>, p);
     }
-    cfg = config(attr, kPushCtas, kMaxThreads, 0, st);
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int smem = 4 * 32 * push_words(p.num_blocks, kPushCtas);
+    static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
+    e = open_dynamic_smem(opened, dev, push_kernel<true>, smem);
+    if (e != cudaSuccess) return e;
+    // (clusters of more than 8 blocks have to be asked for, once in each context)
+    static std::atomic<unsigned long long> allowed[kLaunchCacheDevices];
+    const unsigned long long ctx = current_context_id();
+    const bool cached = ctx != 0 && dev >= 0 && dev < kLaunchCacheDevices;
+    if (!cached || allowed[dev].load(std::memory_order_acquire) != ctx) {
+        e = cudaFuncSetAttribute(push_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (cached) allowed[dev].store(ctx, std::memory_order_release);
+    }
+    cfg = config(attr, kPushCtas, kMaxThreads, smem, st);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = kPushCtas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
