@@ -28,7 +28,8 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;          // append
+constexpr int kGatherThreads = 128, kGatherItems = 2;
 constexpr int kMaxTile = 32;        // rows of a CTA's tile at most: a lane each
 
 template <typename T> constexpr uint32_t kInfBits = Elem<T>::kBf16 ? 0x7f80u : 0x7c00u;
@@ -97,10 +98,11 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_consta
         if (lane == 0) num_runs = __popc(m);
     }
     __syncthreads();
-    const int o = blockIdx.y, H = p.n_kv_heads;
+    const int H = p.n_kv_heads;
+    const int panel = lane % kPanels, r0 = lane / kPanels;
+    const int o = blockIdx.y;
     const uint4 *src = static_cast<const uint4 *>(o ? p.v : p.k);
     uint8_t *pool = o ? p.v_cache : p.k_cache;
-    const int panel = lane % kPanels, r0 = lane / kPanels;
     for (int u = warp; u < num_runs * H; u += kThreads / 32) {
         const Run x = runs[u / H];
         const int h = u % H;
@@ -196,60 +198,72 @@ struct GatherParams {
     const uint8_t *cache[2];      // K, V
     uint4 *rows[2];               // k, v [num_tokens][n_kv_heads][head_dim]
     unsigned int *err;
-    unsigned int count;           // panels of all tokens of one operand
-    unsigned int per_token;       // n_kv_heads * head_dim / 16
+    unsigned int count;           // tokens
     int n_kv_heads, log2_block;
     long long num_slots;
 };
 
+// An item is half a panel of a token and head: 8 bytes in, 16 out. Four
+// neighbouring tokens' panels are neighbouring items, whole sectors where their slots
+// are neighbours, as a prompt's are.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) gather_q8_kernel(const __grid_constant__ GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) gather_q8_kernel(const __grid_constant__ GatherParams p) {
     // (no early start for the kernel after this one: its work, rows of these to
     // append or attend over, comes after this grid's end)
     grid_dependency_wait();
-    constexpr int kPanels = D / kQ8Panel;
-    const unsigned int x = blockIdx.x * kThreads + threadIdx.x;
-    if (x >= p.count) return;
+    constexpr unsigned kPanels = D / kQ8Panel;
     const int o = blockIdx.y, B = 1 << p.log2_block;
-    const unsigned int t = x / p.per_token, hp = x - t * p.per_token;
-    const long long slot = __ldg(reinterpret_cast<const long long *>(p.slots) + t);
-    if (slot < 0) return;
-    if (slot >= p.num_slots) {
-        if (hp == 0) atomicOr(p.err, PAGEDKV_DEVERR_SLOT_RANGE);
-        return;
-    }
-    const int h = int(hp / kPanels), panel = int(hp % kPanels), off = int(slot & (B - 1));
-    const uint8_t *base = p.cache[o] + ((slot >> p.log2_block) * p.n_kv_heads + h) * q8_head_bytes(B, D);
-    const uint4 c = *reinterpret_cast<const uint4 *>(base + (panel * B + off) * 16);
-    const float scale = *reinterpret_cast<const float *>(base + q8_scale_at(B, D));
-    constexpr float kMost = Elem<T>::kBf16 ? 0x1.fep127f : 65504.f;
-    auto value = [&](float v) {
-        v *= scale;
-        return fabsf(v) > kMost ? copysignf(kMost, v) : v;     // (a NaN stays one)
-    };
-    auto two = [&](uint32_t half) {
-        const float2 f = Elem<__half>::unpack2(half);
-        return Elem<T>::pack2(value(f.x), value(f.y));
-    };
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t r[8];
+    const unsigned H = unsigned(p.n_kv_heads), x0 = blockIdx.x * (kGatherThreads * kGatherItems) + threadIdx.x;
+    long long slot[kGatherItems];
+    unsigned token[kGatherItems], head[kGatherItems], panel[kGatherItems];
+    const unsigned half = threadIdx.x & 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t lo, hi;
-        q8_halves(w[i], lo, hi);
-        r[2 * i] = two(lo);
-        r[2 * i + 1] = two(hi);
+    for (int i = 0; i < kGatherItems; ++i) {
+        const unsigned x = x0 + i * kGatherThreads, run = x >> 3, hp = run / kPanels, quad = hp / H;
+        panel[i] = run % kPanels;
+        head[i] = hp - quad * H;
+        token[i] = quad * 4 + ((x >> 1) & 3);
+        slot[i] = token[i] < p.count ? __ldg(reinterpret_cast<const long long *>(p.slots) + token[i]) : -1;
+        if (slot[i] >= p.num_slots) {
+            if (head[i] + panel[i] + half == 0) atomicOr(p.err, PAGEDKV_DEVERR_SLOT_RANGE);
+            slot[i] = -1;
+        }
     }
-    __stcs(p.rows[o] + size_t(x) * 2, make_uint4(r[0], r[1], r[2], r[3]));
-    __stcs(p.rows[o] + size_t(x) * 2 + 1, make_uint4(r[4], r[5], r[6], r[7]));
+    uint2 c[kGatherItems];
+    float scale[kGatherItems];
+#pragma unroll
+    for (int i = 0; i < kGatherItems; ++i) {
+        if (slot[i] < 0) continue;
+        const uint8_t *base = p.cache[o] + ((slot[i] >> p.log2_block) * p.n_kv_heads + head[i]) * q8_head_bytes(B, D);
+        c[i] = *reinterpret_cast<const uint2 *>(base + (panel[i] * B + unsigned(slot[i] & (B - 1))) * 16 + half * 8);
+        scale[i] = *reinterpret_cast<const float *>(base + q8_scale_at(B, D));
+    }
+    constexpr float kMost = Elem<T>::kBf16 ? 0x1.fep127f : 65504.f;
+#pragma unroll
+    for (int i = 0; i < kGatherItems; ++i) {
+        if (slot[i] < 0) continue;
+        auto value = [&](float v) {
+            v *= scale[i];
+            return fabsf(v) > kMost ? copysignf(kMost, v) : v;     // (a NaN stays one)
+        };
+        auto two = [&](uint32_t pair) {
+            const float2 f = Elem<__half>::unpack2(pair);
+            return Elem<T>::pack2(value(f.x), value(f.y));
+        };
+        uint32_t r[4];
+        q8_halves(c[i].x, r[0], r[1]);
+        q8_halves(c[i].y, r[2], r[3]);
+        __stcs(p.rows[o] + ((size_t(token[i]) * H + head[i]) * kPanels + panel[i]) * 2 + half,
+               make_uint4(two(r[0]), two(r[1]), two(r[2]), two(r[3])));
+    }
 }
 
-cudaLaunchConfig_t config(cudaLaunchAttribute *attr, dim3 grid, int smem, cudaStream_t st) {
+cudaLaunchConfig_t config(cudaLaunchAttribute *attr, dim3 grid, int threads, int smem, cudaStream_t st) {
     attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr->val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
     cfg.attrs = attr;
@@ -264,7 +278,7 @@ cudaError_t append_sized(Q8AppendParams p, int sms, cudaStream_t st) {
     while (p.rows > 1 && (long long)p.num_tokens < (long long)p.rows * sms) p.rows >>= 1;
     const dim3 grid(unsigned((p.num_tokens + p.rows - 1) / p.rows), 2);
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(&attr, grid, int(sizeof(int)) * (p.num_seqs + 1), st);
+    const cudaLaunchConfig_t cfg = config(&attr, grid, kThreads, int(sizeof(int)) * (p.num_seqs + 1), st);
     return cudaLaunchKernelEx(&cfg, append_q8_kernel<T, D, B>, p);
 }
 
@@ -281,17 +295,20 @@ cudaError_t append_typed(const Q8AppendParams &p, int head_dim, int block_size, 
 
 template <typename T, int D>
 cudaError_t gather_typed(GatherParams p, int num_tokens, cudaStream_t st) {
-    // launches of at most 2^31 panels per operand
-    const int most = int((1ll << 31) / p.per_token);
+    // launches of at most 2^31 items per operand
+    const long long per_quad = 8ll * p.n_kv_heads * (D / kQ8Panel);
+    const int most = int((1ll << 31) / per_quad) * 4;
     for (int t0 = 0; t0 < num_tokens;) {
         const int n = num_tokens - t0 < most ? num_tokens - t0 : most;
-        p.count = unsigned(n) * p.per_token;
+        p.count = unsigned(n);
+        const long long items = (n + 3) / 4 * per_quad;
+        constexpr long long kPerCta = kGatherThreads * kGatherItems;
         cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t cfg = config(&attr, dim3((p.count + unsigned(kThreads) - 1) / unsigned(kThreads), 2), 0, st);
+        const cudaLaunchConfig_t cfg = config(&attr, dim3(unsigned((items + kPerCta - 1) / kPerCta), 2), kGatherThreads, 0, st);
         const cudaError_t e = cudaLaunchKernelEx(&cfg, gather_q8_kernel<T, D>, p);
         if (e != cudaSuccess) return e;
         p.slots += n;
-        for (auto &r : p.rows) r += size_t(p.count) * 2;
+        for (auto &r : p.rows) r += size_t(n) * p.n_kv_heads * (D / 8);
         t0 += n;
     }
     return cudaSuccess;
@@ -315,7 +332,6 @@ cudaError_t launch_gather_q8(const uint8_t *k_cache, const uint8_t *v_cache, con
     p.rows[0] = static_cast<uint4 *>(k);
     p.rows[1] = static_cast<uint4 *>(v);
     p.err = err;
-    p.per_token = unsigned(n_kv_heads) * unsigned(head_dim / kQ8Panel);
     p.n_kv_heads = n_kv_heads;
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.num_slots = num_slots;

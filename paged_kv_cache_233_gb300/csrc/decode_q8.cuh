@@ -37,7 +37,7 @@ namespace pkv {
 template <typename T, int D, int B>
 struct Q8Consumer {
     using Type = T;
-    static constexpr int kDim = D, kBlock = B, kCtasPerSm = D == 128 ? 2 : 3, kUnitCost = kQ8UnitCost;
+    static constexpr int kDim = D, kBlock = B, kCtasPerSm = 2, kUnitCost = kQ8UnitCost;
     static constexpr int kHead = q8_head_bytes(B, D);    // bytes of a (block, kv head)
     static constexpr int P = D / kQ8Panel;
     static constexpr int kPanel = B * kQ8Panel;          // bytes between panels
