@@ -432,3 +432,251 @@ def test_blocks_copy_and_swap(dtype, block):
     pk.paged_kv_swap_blocks(hk, hv, a, b, i32([[1, 2]]))
     assert torch.equal(a[2].cpu(), kc[5])
     assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("dtype,dim,block", [(F16, 128, 16), (BF16, 64, 8)])
+def test_serving_loop(dtype, dim, block, graph):
+    """Forks with their blocks' copies, tables, append, prefill, decode and release
+    together, step after step, on a side stream and captured: each step's attention is
+    that of caches kept by the definition, and no block is lost or held twice."""
+    from test_gpu_pages import ALL, Cache
+    heads, group, steps, most = 2, 3, 6, 5
+    start = [0, block - 1, 2 * block, 100, 3, 0, 0, 0]
+    c = Cache(start, block, 20, 60, 7)
+    S, nb = len(start), c.blocks
+    T = S * most
+    kc, vc = q8.new_pool(nb, heads, block, dim, 1), q8.new_pool(nb, heads, block, dim, 2)
+    for s, n in enumerate(start):
+        for i, pool in enumerate((kc, vc)):
+            q8.fill(pool, c.tables[s], rows((n, heads, dim), dtype, 10 * s + i))
+    d = c.device()
+    gk, gv, lens, count = kc.cuda(), vc.cuda(), d["lens"], d["count"]
+    dev = dict(device="cuda", dtype=torch.int32)
+    parents, keep, new = torch.full((S,), -1, **dev), torch.full((S,), ALL, **dev), torch.zeros(S, **dev)
+    pairs, starts = torch.zeros(S, 2, **dev), torch.zeros(S + 1, **dev)
+    seq, pos = torch.zeros(T, **dev), torch.zeros(T, **dev)
+    k, v = (torch.zeros(T, heads, dim, dtype=dtype, device="cuda") for _ in range(2))
+    q, qd = (torch.zeros(n, heads * group, dim, dtype=dtype, device="cuda") for n in (T, S))
+    out, outd = torch.zeros_like(q), torch.zeros_like(qd)
+    ws, wp = pk.new_workspace(qd, d["tables"], block, pk.PARTITION_BALANCED), pk.prefill_workspace(q)
+
+    def step():
+        pk.paged_kv_fork(parents, lens, d["tables"], d["shared"], d["free"], count, pairs, block)
+        pk.paged_kv_copy_blocks(gk, gv, pairs)
+        pk.paged_kv_build_tables(new, lens, d["tables"], d["free"], count, block, nb, starts, seq, pos)
+        pk.paged_kv_append_q8(k, v, d["tables"], starts, lens, gk, gv)
+        pk.paged_attention_prefill_q8(q, gk, gv, d["tables"], starts, lens, dim ** -0.5, out, most, workspace=wp, key_parts=0)
+        pk.paged_attention_decode_q8(qd, gk, gv, d["tables"], lens, dim ** -0.5, outd, pk.PARTITION_BALANCED, ws)
+        pk.paged_kv_release(keep, lens, d["tables"], d["shared"], d["free"], count, block)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    if graph:
+        with torch.cuda.stream(side):
+            step()                      # with nothing to do: it leaves the state as it is
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+    for i in range(steps):
+        fork_of = [-1] * S
+        if i % 2 == 0:
+            empty, full = ([s for s in range(S) if (c.lens[s] == 0) == e and s > 0] for e in (True, False))
+            for e, s in zip(empty[:2], full):
+                fork_of[e] = s
+        want_pairs = c.fork(fork_of)
+        for a, b in want_pairs:
+            for pool in (kc, vc):
+                pool[b] = pool[a].clone()
+        add = [(s + i) % (most + 1) if c.lens[s] else 0 for s in range(S)]
+        x, y, z = [rows(k.shape, dtype, 100 + 3 * i + j) for j in range(2)], rows(q.shape, dtype, 300 + i), rows(qd.shape, dtype, 400 + i)
+        before = list(c.lens)
+        st = [0]
+        for s in range(S):
+            for j in range(-(-before[s] // block), -(-(before[s] + add[s]) // block)):
+                c.tables[s, j] = c.stack.pop()
+            c.lens[s] += add[s]
+            st.append(st[-1] + add[s])
+        now = list(c.lens)
+        drop = [0 if (s + i) % 5 == 4 else max(0, now[s] - 2) if (s + i) % 4 == 1 and now[s] - 2 >= before[s] else ALL
+                for s in range(S)]
+        torch.cuda.synchronize()
+        for t, value in ((parents, fork_of), (new, add), (keep, drop)):
+            t.copy_(torch.tensor(value, dtype=torch.int32))
+        k.copy_(x[0]), v.copy_(x[1]), q.copy_(y), qd.copy_(z)
+        torch.cuda.synchronize()
+        if graph:
+            g.replay()
+        else:
+            with torch.cuda.stream(side):
+                step()
+        torch.cuda.synchronize()
+        assert pk.device_errors() == 0
+        assert pairs.tolist() == want_pairs and starts.tolist() == st
+        t = torch.from_numpy(c.tables)
+        for pool, r in ((kc, x[0]), (vc, x[1])):
+            q8.append(pool, r, t, st, now)
+        ref = q8.attention(y[:st[-1]], (kc, vc), t, st, now, dim ** -0.5, dim)
+        q8.assert_near(out[:st[-1]], ref, dtype, 2, f"prefill step {i}")
+        ref = q8.attention(z, (kc, vc), t, range(S + 1), now, dim ** -0.5, dim)
+        q8.assert_near(outd, ref, dtype, 2, f"decode step {i}")
+        c.release(drop)
+        c.check(d, lens, count)
+
+
+def test_calls_repeat_bit_for_bit():
+    lens, heads, dim, block = [3000, 17, 1, 640], 4, 128, 16
+    kc, vc, tables = q8.filled(lens, heads, block, dim, BF16, 4)
+    q, qp = rows((4, heads * 4, dim), BF16, 5), rows((80, heads * 4, dim), BF16, 6)
+    first = [decode(q, kc, vc, tables, lens, 0.09, part) for part in (0, 256, pk.PARTITION_BALANCED)]
+    chunk = [0, 60, 70, 71, 80]
+    first += [prefill(qp, kc, vc, tables, chunk, lens, 0.09, key_parts=parts) for parts in (1, 0, 32)]
+    for _ in range(10):
+        again = [decode(q, kc, vc, tables, lens, 0.09, part) for part in (0, 256, pk.PARTITION_BALANCED)]
+        again += [prefill(qp, kc, vc, tables, chunk, lens, 0.09, key_parts=parts) for parts in (1, 0, 32)]
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    assert pk.device_errors() == 0
+
+
+def test_prefill_many_items_per_block():
+    """More items than SMs, of one to many key tiles, whole and split: the rings and
+    their phases run on across items."""
+    lens = [(1, 40, 64, 65, 300, 900)[(5 * i + i // 6) % 6] for i in range(90)]
+    chunk = [min(n, (1, 7, 40, 130)[i % 4]) for i, n in enumerate(lens)]
+    for dtype, dim, block in ((BF16, 128, 8), (F16, 64, 16)):
+        kc, vc, tables = q8.filled(lens, 4, block, dim, dtype, 4)
+        starts = torch.tensor([0] + chunk).cumsum(0)
+        q = rows((int(starts[-1]), 8, dim), dtype, 6)
+        ref = q8.attention(q, (kc, vc), tables, starts, lens, dim ** -0.5, dim)
+        for parts in (1, 32):
+            out = prefill(q, kc, vc, tables, starts, lens, dim ** -0.5, key_parts=parts)
+            q8.assert_near(out, ref, dtype, 2, f"parts {parts}")
+    assert pk.device_errors() == 0
+
+
+def test_pools_past_4_gib():
+    """Blocks whose bytes lie past 2^32 in their pool."""
+    heads, dim, block, dtype = 8, 128, 32, BF16
+    nb = (1 << 32) // (heads * block * (dim + 1)) + 40
+    pools = [pk.new_q8_pool(nb, heads, block, dim) for _ in range(2)]
+    lens = [300, 70]
+    tables = torch.tensor([[nb - 1 - 2 * j for j in range(10)], [nb - 2 - 2 * j if j < 3 else -1 for j in range(10)]],
+                          dtype=torch.int32)
+    small = [q8.new_pool(40, heads, block, dim, i) for i in range(2)]      # the pools' last 40 blocks
+    near = torch.where(tables >= 0, tables - (nb - 40), tables)
+    slots = torch.cat([q8.sequence_slots(tables, s, n, block) for s, n in enumerate(lens)])
+    near_slots = torch.cat([q8.sequence_slots(near, s, n, block) for s, n in enumerate(lens)])
+    k, v = rows((370, heads, dim), dtype, 1), rows((370, heads, dim), dtype, 2)
+    starts = [0, 300, 370]
+    for pool, x in zip(small, (k, v)):
+        q8.append(pool, x, near, starts, lens)
+    for pool in pools:
+        pool[nb - 40:] = 255
+    pk.paged_kv_append_q8(k.cuda(), v.cuda(), tables.cuda(), i32(starts), i32(lens), *pools)
+    back = [torch.zeros(370, heads, dim, dtype=dtype, device="cuda") for _ in range(2)]
+    pk.paged_kv_gather_q8(*pools, slots.cuda(), *back)
+    for got, pool in zip(back, small):
+        assert torch.equal(got.cpu().double(), q8.read(pool, near_slots, dim))
+    q = rows((2, heads * 4, dim), dtype, 3)
+    ref = q8.attention(q, small, near, range(3), lens, 0.09, dim)
+    for part in (0, pk.PARTITION_BALANCED):
+        q8.assert_near(decode(q, pools[0], pools[1], tables, lens, 0.09, part), ref, dtype, 2)
+    qp = rows((370, heads * 4, dim), dtype, 4)
+    out = prefill(qp, *pools, tables, starts, lens, 0.09, torch.zeros_like(qp).cuda(), 300)
+    q8.assert_near(out, q8.attention(qp, small, near, starts, lens, 0.09, dim), dtype, 2)
+    assert pk.device_errors() == 0
+
+
+def test_decode_4096_sequences():
+    rng = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 40, (4096,), generator=rng).tolist()
+    for heads, group, dim in ((4, 2, 128), (1, 1, 64)):
+        kc, vc, tables = q8.filled(lens, heads, 8, dim, BF16, 6)
+        q = rows((4096, heads * group, dim), BF16, 7)
+        ref = q8.attention(q, (kc, vc), tables, range(4097), lens, dim ** -0.5, dim)
+        for part in (0, 32, pk.PARTITION_BALANCED):
+            q8.assert_near(decode(q, kc, vc, tables, lens, dim ** -0.5, part), ref, BF16, 2)
+        assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("heads, dim, block", [(32, 64, 8), (2, 128, 32), (3, 64, 16)])
+def test_decode_short_sequences_beside_long_ones(heads, dim, block):
+    """A balanced split over sequences of one or two tiles, empty ones and a few long
+    ones, in an order that ends shares inside, before and behind each of them."""
+    lens = [(5000, 0, 1, 32, 33, 64, 700, 31)[(3 * i + i // 8) % 8] for i in range(150)]
+    kc, vc, tables = q8.filled(lens, heads, block, dim, F16, 4)
+    q = rows((len(lens), heads, dim), F16, 6)
+    ref = q8.attention(q, (kc, vc), tables, range(len(lens) + 1), lens, dim ** -0.5, dim)
+    q8.assert_near(decode(q, kc, vc, tables, lens, dim ** -0.5, pk.PARTITION_BALANCED), ref, F16, 2, "short and long")
+    assert pk.device_errors() == 0
+
+
+def test_two_streams_with_a_workspace_each():
+    lens, heads, dim, block = [2000, 700, 31], 4, 128, 16
+    kc, vc, tables = q8.filled(lens, heads, block, dim, BF16, 4)
+    gk, gv, gt, L = kc.cuda(), vc.cuda(), tables.cuda(), i32(lens)
+    qs = [rows((3, heads * 2, dim), BF16, 20 + i).cuda() for i in range(2)]
+    outs = [torch.zeros_like(q) for q in qs]
+    ws = [pk.new_workspace(q, gt, block, pk.PARTITION_BALANCED) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(40):
+        s = i % 2
+        pk.paged_attention_decode_q8(qs[s], gk, gv, gt, L, 0.09, outs[s], pk.PARTITION_BALANCED, ws[s], stream=streams[s])
+    torch.cuda.synchronize()
+    for q, out in zip(qs, outs):
+        q8.assert_near(out, q8.attention(q.cpu(), (kc, vc), tables, range(4), lens, 0.09, dim), BF16, 2)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gather_into_a_16_bit_pool(dtype):
+    """An 8-bit sequence moved into 16-bit pools: paged_kv_append_tokens right behind
+    the gather that makes its rows, many times over."""
+    n, heads, dim, block = 3000, 8, 128, 16
+    kc, vc, tables = q8.filled([n], heads, block, dim, dtype, 5)
+    slots = q8.sequence_slots(tables, 0, n, block).cuda()
+    gk, gv, gt = kc.cuda(), vc.cuda(), tables.cuda()
+    seq, pos = torch.zeros(n, dtype=torch.int32).cuda(), torch.arange(n, dtype=torch.int32).cuda()
+    want = [q8.read(p, slots.cpu(), dim) for p in (kc, vc)]
+    for i in range(5):
+        k, v = (torch.full((n, heads, dim), float(i), dtype=dtype, device="cuda") for _ in range(2))
+        k16, v16 = (torch.zeros(kc.shape[0], block, heads, dim, dtype=dtype, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        pk.paged_kv_gather_q8(gk, gv, slots, k, v)
+        pk.paged_kv_append_tokens(k, v, gt, seq, pos, k16, v16)
+        torch.cuda.synchronize()
+        for pool, ref in ((k16, want[0]), (v16, want[1])):
+            assert torch.equal(pool.flatten(0, 1)[slots].cpu().double(), ref)
+
+
+def test_refusals_on_the_gpu():
+    kc, vc, tables = (t.cuda() for t in q8.filled([20], 2, 16, 64, F16, 1))
+    q, L, out = torch.zeros(1, 4, 64, dtype=F16, device="cuda"), i32([20]), torch.zeros(1, 4, 64, dtype=F16, device="cuda")
+    with pytest.raises(pk.PagedKVError, match="contiguous"):
+        pk.paged_attention_decode_q8(q.transpose(1, 2).contiguous().transpose(1, 2), kc, vc, tables, L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="out must be"):
+        pk.paged_attention_decode_q8(q, kc, vc, tables, L, 0.1, out.bfloat16())
+    with pytest.raises(pk.PagedKVError, match="current device"):
+        pk.paged_attention_decode_q8(q, kc, vc, tables.cpu(), L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="unsupported"):
+        pk.paged_attention_decode_q8(q.float(), kc, vc, tables, L, 0.1, out.float())
+    with pytest.raises(pk.PagedKVError, match="8-bit pools"):
+        pk.paged_attention_decode_q8(q, *(pk.new_q4_pool(4, 2, 16, 64) for _ in range(2)), tables, L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="4-bit pools"):
+        pk.paged_attention_decode_q4(q, kc, vc, tables, L, 0.1, out)
+    with pytest.raises(pk.PagedKVError, match="workspace"):
+        pk.paged_attention_decode_q8(q, kc, vc, tables, L, 0.1, out, 32)
+    with pytest.raises(pk.PagedKVError, match="workspace"):
+        pk.paged_attention_prefill_q8(q, kc, vc, tables, i32([0, 1]), L, 0.1, out, 1,
+                                      workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"), key_parts=4)
+    k = torch.zeros(3, 2, 64, dtype=F16, device="cuda")
+    with pytest.raises(pk.PagedKVError, match="kv heads"):
+        pk.paged_kv_append_q8(k[:, :1].contiguous(), k[:, :1].contiguous(), tables, i32([0, 3]), L, kc, vc)
+    with pytest.raises(pk.PagedKVError, match="query_start must"):
+        pk.paged_kv_append_q8(k, k, tables, i32([0, 3, 3]), L, kc, vc)
+    with pytest.raises(pk.PagedKVError, match="v must be"):
+        pk.paged_kv_append_q8(k, k.bfloat16(), tables, i32([0, 3]), L, kc, vc)
+    pk.paged_attention_decode_q8(q[:0], kc, vc, tables[:0], L[:0], 0.1, out[:0])
+    pk.paged_kv_append_q8(k[:0], k[:0], tables, i32([0, 0]), L, kc, vc)
+    assert pk.device_errors() == 0
