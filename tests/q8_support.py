@@ -32,12 +32,10 @@ def value(codes):
 
 def code(x):
     """fp64 values to the nearest code, ties to the even one; NaN and infinities to NaN."""
-    a = x.abs()
-    v = VALUES[:NAN]
-    hi = torch.searchsorted(v, a.nan_to_num(0.0, 0.0, 0.0)).clamp(max=NAN - 1)
-    lo = (hi - 1).clamp(min=0)
-    down, up = a - v[lo], v[hi] - a
-    c = torch.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    a = x.abs().nan_to_num(0.0, 0.0, 0.0)
+    e = (torch.frexp(a.clamp(min=2.0 ** -7))[1] - 1).clamp(min=-6)   # the binade, smaller ones in that of 2^-6
+    r = torch.round(torch.ldexp(a, 3 - e))                     # eighths of it: 8 .. 16, less below 2^-6
+    c = ((e + 6) * 8 + r.int()).clamp(max=NAN - 1)             # (16 eighths are the next binade's 8)
     c = c + torch.where(torch.signbit(x), 128, 0)
     return torch.where(torch.isfinite(x), c, torch.full_like(c, NAN)).to(torch.uint8)   # (a NaN has no sign)
 
@@ -131,17 +129,25 @@ def filled(lens, heads, block, dim, dtype, seed, spread=1.0, pad=0):
 
 
 def fill(pool, table, x):
-    """A sequence's rows x [n][Hkv][D] into its blocks, block by block at once."""
+    """A sequence's rows x [n][Hkv][D] into its blocks, all at once (whole blocks: what
+    lies behind the last row becomes zeros and NaN)."""
     block, dim, n = pool.shape[2], x.shape[-1], len(x)
+    blocks = -(-n // block)
+    if n == 0:
+        return
     codes, scale, mark = views(pool, dim)
-    for j in range(-(-n // block)):
-        rows, bid = x[j * block:(j + 1) * block].double(), int(table[j])
-        top = rows.abs().amax((0, 2)).clamp(min=448 * 2.0 ** -64)
-        e = torch.ceil(torch.log2(top / 448)) + (j % 3 == 2)
-        c = code(rows * torch.exp2(-e)[None, :, None])     # [n][Hkv][D]
-        codes[bid, :, :, :len(rows)] = c.unflatten(-1, (-1, 16)).permute(1, 2, 0, 3)
-        scale[bid, :, 0] = torch.exp2(e).float()
-        mark[bid] = 0
+    rows = torch.zeros(blocks * block, *x.shape[1:], dtype=torch.float64)
+    rows[:n] = x.double()
+    rows = rows.unflatten(0, (blocks, block))                  # [blocks][B][Hkv][D]
+    top = rows.abs().amax((1, 3)).clamp(min=448 * 2.0 ** -64)
+    e = torch.ceil(torch.log2(top / 448)) + (torch.arange(blocks) % 3 == 2)[:, None]
+    c = code(rows * torch.exp2(-e)[:, None, :, None])
+    if n % block:
+        c[-1, n % block:, :, ::3] = NAN
+    ids = torch.as_tensor(table)[:blocks].long()
+    codes[ids] = c.unflatten(-1, (-1, 16)).permute(0, 2, 3, 1, 4)
+    scale[ids, :, 0] = torch.exp2(e).float()
+    mark[ids] = 0
 
 
 def attention(q, pools, tables, starts, lens, scale, dim):
