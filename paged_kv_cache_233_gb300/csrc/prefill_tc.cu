@@ -154,9 +154,9 @@ constexpr int kMaxRankedSeqs = 256;
 
 template <int D, int kBits>
 struct TcLayout {
-    // the raw ring: 4-bit key tiles, or 8-bit ones of K or V alone, of which head size
-    // 128 leaves room for three beside four stages
-    static constexpr int kRawStages = kBits == 8 ? (D == 128 ? 3 : 6) : 2;
+    // (8-bit tiles of head size 128 leave room for three stages beside their raw ring)
+    static constexpr int kStages = kBits == 8 && D == 128 ? 3 : kTcStages;
+    static constexpr int kRawStages = kBits == 8 ? 3 : 2;      // the raw ring
     static constexpr int kSlabs = D * 2 / 128;             // 64-element column blocks per row
     static constexpr int kQSlab = kTcRows * 128;           // bytes of one Q column block
     static constexpr int kKvSlab = kTcKeys * 128;          // bytes of one K (or V) column block
@@ -165,7 +165,7 @@ struct TcLayout {
     static constexpr int kKv = kQ + kTcTiles * kQTile;     // stage s: K at kKv + s*kStage, V after it
     static constexpr int kHalf = kSlabs * kKvSlab;
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kBars = kKv + kTcStages * kStage;
+    static constexpr int kBars = kKv + kStages * kStage;
     static constexpr int kTmemSlot = kBars + 8 * kNumBars;
     static constexpr int kFlag = kTmemSlot + 8;
     static constexpr int kOrder = kFlag + 8;               // ranked sequence ids, then their lengths
@@ -182,10 +182,10 @@ struct TcLayout {
     static constexpr int kScalesStage = 16 + 2 * kTcKeys / 8;
     // 4- and 8-bit pools: the raw ring's barriers (full, empty), then its tiles: K's
     // blocks, V's (8-bit: with the scales behind the codes, blocks of 8 have the most)
-    static constexpr int kRawBars = kScales + (kBits == 8 ? kTcStages * kScalesStage : 0);
+    static constexpr int kRawBars = kScales + (kBits == 8 ? kStages * kScalesStage : 0);
     static constexpr int kRaw = kRawBars + 16 * kRawStages;
     static constexpr int kRawHalf = kBits == 8 ? kTcKeys / 8 * q8_head_bytes(8, D) : kTcKeys * D * 5 / 8;
-    static constexpr int kTotalPacked = kRaw + kRawStages * (kBits == 8 ? 1 : 2) * kRawHalf;
+    static constexpr int kTotalPacked = kRaw + kRawStages * 2 * kRawHalf;
     static_assert((kBits < 16 ? kTotalPacked : kTotal) + 1024 <= 227 * 1024, "the shared memory of a block");
     static_assert(2 * kTcKeys + D <= kTmemTile, "S buffers and O must fit a Q tile's columns");
     static_assert(kMaxSplitItems < kPlanRange && 4 * (kPlanRange + 6) <= 8 * kMaxRankedSeqs,
@@ -235,6 +235,13 @@ __device__ __forceinline__ int lds32(uint32_t addr) {
 }
 __device__ __forceinline__ void sts32(uint32_t addr, int v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// One lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // One work item: (sequence, kv head, query tile of tile_tokens chunk tokens =
@@ -465,7 +472,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const PrefillParams p, int tiles) {
     using Ly = TcLayout<D, kBits>;
     constexpr bool kBf16 = Elem<T>::kBf16, kPacked = kBits < 16;
-    constexpr int kRawStages = Ly::kRawStages;
+    constexpr int kStages = Ly::kStages, kRawStages = Ly::kRawStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -483,7 +490,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     if (kPacked || p.late_inputs) grid_dependency_wait();
 
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kTcStages; ++k) {
+        for (int k = 0; k < kStages; ++k) {
             mbar_init(bar(kKvFull + k), kPacked ? kDqWarps : 1);
             mbar_init(bar(kKvEmpty + k), kTcTiles);   // one commit per issuer and key tile
         }
@@ -503,7 +510,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             mbar_init(bar(bar_qfree(t)), 1);
         }
         mbar_init(bar(kDone), kTcTiles);
-        for (int k = 0; k < kTcStages; ++k) mbar_init(bar(kTailV + k), 1);
+        for (int k = 0; k < kStages; ++k) mbar_init(bar(kTailV + k), 1);
         sts32(flag, 0);
         fence_barrier_init();
     }
@@ -590,9 +597,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             PfItem it;
             if (!pf_item<kSplit>(p, order, tiles, k, lane == 0, it)) continue;
             const int32_t *table = p.block_tables + size_t(it.s) * p.max_blocks;
-            if constexpr (kBits == 4) {
+            if constexpr (kPacked) {
                 // a tile's blocks, K and V, a lane per copy
-                const int hb = q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
+                const int hb = kBits == 8 ? q8_head_bytes(B, D) : q4_head_bytes(B, D), blk = lane >> 1, op = lane & 1;
                 const uint8_t *pool = op ? p.v_packed : p.k_packed;
                 for (int j = 0; j < it.nkt; ++j) {
                     const int gk = kt + j;
@@ -622,47 +629,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     }
                     ++armed;
                 }
-            } else if constexpr (kBits == 8) {
-                // a tile's blocks, a lane per copy: K's, then V's. The next tile's block
-                // ids are loaded while this one's slots are waited for.
-                const int hb = q8_head_bytes(B, D), per = kTcKeys >> p.log2_block;
-                const int32_t *ids = table + ((it.kb * kTcKeys) >> p.log2_block) + lane;
-                int left = it.L - it.kb * kTcKeys, next = lane < per && lane * B < left ? __ldg(ids) : 0;
-                for (int x = 0; x < 2 * it.nkt; ++x) {
-                    const int h = 2 * kt + x, op = x & 1, st = h % kRawStages;
-                    const int blocks = (min(kTcKeys, left) + B - 1) >> p.log2_block;
-                    const bool mine = lane < blocks;
-                    int pb = next;
-                    if (op) {
-                        ids += per;
-                        left -= kTcKeys;
-                        next = lane < per && lane * B < left ? __ldg(ids) : 0;
-                    }
-                    const uint32_t full = base + Ly::kRawBars + 16 * st;
-                    bool got = true;
-                    if (lane == 0) {
-                        got = !aborted() && mbar_wait(full + 8, uint32_t((h / kRawStages) & 1) ^ 1u, p.err);
-                        if (got) mbar_arrive_expect_tx(full, uint32_t(blocks * hb));
-                    }
-                    __syncwarp();
-                    if (!__shfl_sync(kAll, got ? 1 : 0, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    if (mine) {
-                        if (pb < 0 || pb >= p.num_blocks) {
-                            atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-                            pb = 0;
-                        }
-                        bulk_load(base + Ly::kRaw + st * Ly::kRawHalf + lane * hb,
-                                  (op ? p.v_packed : p.k_packed) + (size_t(pb) * p.n_kv_heads + it.h) * hb, uint32_t(hb),
-                                  full);
-                    }
-                    ++armed;
-                }
             } else for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
-                const int st = gk % kTcStages;
+                const int st = gk % kStages;
                 const int k0 = (it.kb + j) * kTcKeys;
                 const int present = min(kTcKeys, it.L - k0);
                 const int boxes = (present + rows_per_box - 1) / rows_per_box;
@@ -674,7 +643,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 bool got = true;
                 if (lane == 0) {
                     got = !aborted() &&
-                          mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err);
+                          mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u, p.err);
                     if (got && !last_tail) {
                         mbar_arrive_expect_tx(bar(kKvFull + st), 2 * half);
                     } else if (got) {
@@ -711,10 +680,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // (a tail stage completes only with the zeroing warp's arrival: when that
             // warp stopped too, the wait ends at its time limit, its copies long done)
             sts32(flag, 1);
-            constexpr int kRing = kPacked ? kRawStages : kTcStages;
+            constexpr int kRing = kPacked ? kRawStages : kStages;
             const int first = armed > kRing ? armed - kRing : 0;
             for (int x = first; x < armed; ++x)
-                mbar_wait(kPacked ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kTcStages),
+                mbar_wait(kPacked ? base + Ly::kRawBars + 16 * (x % kRing) : bar(kKvFull + x % kStages),
                           uint32_t((x / kRing) & 1), p.err);
         }
         __syncwarp();
@@ -786,7 +755,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
             }
             if (!kPacked && it.tail) {
-                const int st = (kt + it.nkt - 1) % kTcStages;
+                const int st = (kt + it.nkt - 1) % kStages;
                 const int present = it.L - (it.kb + it.nkt - 1) * kTcKeys;
                 bool got = true;
                 if (lane == 0)
@@ -837,14 +806,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
             for (int j = 0; j < it.nkt; ++j) {
                 const int gk = kt + j;
-                const int st = gk % kTcStages, rs = gk % kRawStages;
+                const int st = gk % kStages, rs = gk % kRawStages;
                 const uint32_t rfull = base + Ly::kRawBars + 16 * rs;
                 const bool live = (it.kb + j) * kTcKeys + row < it.L;
                 // the raw tile is there, and the stage's last readers are done
                 bool got = mbar_try_wait(rfull, uint32_t((gk / kRawStages) & 1)) ||
                            (!aborted() && mbar_wait(rfull, uint32_t((gk / kRawStages) & 1), p.err));
-                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u) ||
-                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kTcStages) & 1) ^ 1u, p.err)));
+                got = got && (mbar_try_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u) ||
+                              (!aborted() && mbar_wait(bar(kKvEmpty + st), uint32_t((gk / kStages) & 1) ^ 1u, p.err)));
                 if (!__all_sync(kAll, got)) {
                     ok = false;
                     break;
@@ -897,14 +866,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         __syncwarp();
     } else if (kBits == 8 && warp >= kDqWarp0) {
         // -------------------------------------- 8-bit pools: raw tiles to stages
-        // K's raw tile and V's: at head size 64 both at once, whose waits and loads then
-        // overlap; at 128, where three of the ring's slots fit, one after the other. A
-        // warp takes 16 key rows: half a warp their even panels, the other the odd ones, 16
-        // bytes of codes to two 16-byte chunks of the stage's row. (Every warp meets every
-        // slot's every phase: one that took K's tiles alone would pass a slot's barrier on
-        // the phase before last, V's tile in between.)
-        constexpr int kAtOnce = D == 64 ? 2 : 1;
-        static_assert(kRawStages % kAtOnce == 0, "K's slot and V's of one phase");
+        // A warp takes 16 key rows of K and of V: half a warp their even panels, the
+        // other the odd ones, 16 bytes of codes to two 16-byte chunks of the stage's row.
+        // (Two warps for K and two for V would leave K's with twice the work in bf16.)
         const int w = warp - kDqWarp0, row = 16 * w + (lane & 15), odd = lane >> 4;
         const int hb = q8_head_bytes(B, D), off = row & (B - 1);
         const int blk = row >> p.log2_block, some = lane & ((kTcKeys >> p.log2_block) - 1);   // a block for each lane
@@ -919,42 +883,38 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (k >= num_items) break;
             PfItem it;
             if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
-            float factor = 0.f;      // of the tile's sums
-            bool any_k = false;      // a key of it is marked
             const int past = it.L - (it.kb + it.nkt - 1) * kTcKeys;   // the last tile's keys within the context
 #pragma unroll 1
-            for (int x = 2 * it.nkt; x > 0; x -= kAtOnce) {
-                const bool first = kAtOnce == 2 || !(x & 1);          // K is among them
-                const uint32_t rfull = base + Ly::kRawBars + 16 * rs, raw = base + Ly::kRaw + uint32_t(rs * Ly::kRawHalf);
-                // the raw tiles are there, and (K) the stage's last readers are done
+            for (int x = it.nkt; x > 0; --x) {
+                const uint32_t rfull = base + Ly::kRawBars + 16 * rs, raw = base + Ly::kRaw + uint32_t(rs * 2 * Ly::kRawHalf);
+                // the raw tile is there, and the stage's last readers are done
                 bool got = mbar_try_wait(rfull, rphase);
-                if (kAtOnce == 2) got = mbar_try_wait(rfull + 16, rphase) && got;
-                if (first) got = mbar_try_wait(bar(kKvEmpty + st), sphase) && got;
+                got = mbar_try_wait(bar(kKvEmpty + st), sphase) && got;
                 if (!__all_sync(kAll, got)) {
-                    got = !aborted() && mbar_wait(rfull, rphase, p.err) &&
-                          (kAtOnce == 1 || mbar_wait(rfull + 16, rphase, p.err)) &&
-                          (!first || mbar_wait(bar(kKvEmpty + st), sphase, p.err));
+                    got = !aborted() && mbar_wait(rfull, rphase, p.err) && mbar_wait(bar(kKvEmpty + st), sphase, p.err);
                     if (!__all_sync(kAll, got)) {
                         ok = false;
                         break;
                     }
                 }
-                uint2 info[kAtOnce];
-                uint4 cw[kAtOnce][D / 32];
+                float factor = 0.f;      // of the tile's sums
+                bool any_k = false;      // a key of it is marked in K
+                uint2 info[2];
+                uint4 cw[2][D / 32];
 #pragma unroll
-                for (int o = 0; o < kAtOnce; ++o) {
+                for (int o = 0; o < 2; ++o) {
                     const uint32_t from = raw + uint32_t(o * Ly::kRawHalf);
                     info[o] = lds64_u2(from + scale);
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) cw[o][i] = lds128_u4(from + src + uint32_t(i) * step);
                 }
 #pragma unroll
-                for (int o = 0; o < kAtOnce; ++o) {
-                    const bool of_v = kAtOnce == 2 ? o == 1 : !first;
+                for (int o = 0; o < 2; ++o) {
+                    const bool of_v = o == 1;
                     // The tile's keys under one scale, 2^6 below their blocks' largest (448 *
                     // 2^6 is in fp16's range): a power of two takes each code there, exactly
                     // unless its block's scale is more than 2^21 below the largest.
-                    const bool there = x > 2 || some * B < past;    // (a block past the context has no scale)
+                    const bool there = x > 1 || some * B < past;    // (a block past the context has no scale)
                     const int e = there ? min(max(int((info[o].x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp) : kQ8LeastExp;
                     const int most = __reduce_max_sync(kAll, e);
                     const bool any = __any_sync(kAll, there && info[o].y != 0) != 0;
@@ -990,14 +950,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                             put(i, v);
                         }
                     };
-                    if (x <= 2 || any || (of_v && any_k)) {
-                        const bool live = x > 2 || row < past;
+                    if (x == 1 || any || (of_v && any_k)) {
+                        const bool live = x > 1 || row < past;
                         const uint32_t mine = __shfl_sync(kAll, info[o].y, blk) >> off;
                         const unsigned marked = __ballot_sync(kAll, live && (mine & 1u)) & 0xffffu;
                         if (lane == 0) {
                             const uint32_t at = base + Ly::kScales + uint32_t(st * Ly::kScalesStage + 16 + 2 * w);
                             sts16(at + (of_v ? 8u : 0u), marked);
-                            if (of_v && x > 2 && !any_k) sts16(at, 0u);    // (K's run wrote none)
+                            if (of_v && x > 1 && !any_k) sts16(at, 0u);    // (K's run wrote none)
                         }
 #pragma unroll 1
                         for (int i = 0; i < D / 32; ++i) {
@@ -1032,20 +992,17 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                                           __float_as_uint(q8_power(6 - most)), any || any_k ? 1u : 0u));
                     }
                 }
-                const bool whole = kAtOnce == 2 || !first;            // the stage is complete
-                if (whole) fence_proxy_async_smem();
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(rfull + 8);
-                    if (kAtOnce == 2) mbar_arrive(rfull + 24);
-                    if (whole) mbar_arrive(bar(kKvFull + st));
+                    mbar_arrive(bar(kKvFull + st));
                 }
-                rs += kAtOnce;
-                if (rs == kRawStages) {
+                if (++rs == kRawStages) {
                     rs = 0;
                     rphase ^= 1u;
                 }
-                if (whole && ++st == kTcStages) {
+                if (++st == kStages) {
                     st = 0;
                     sphase ^= 1u;
                 }
@@ -1063,8 +1020,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // addresses are warp-uniform values), and lane 0 alone issues each
         // tcgen05.mma and tcgen05.commit (a commit tracks its own thread's MMAs).
         {
-            const int t = warp == 1 ? 0 : 1;
-            const bool leader = lane == 0;
+            // (values by a shuffle are the compiler's to keep in uniform registers)
+            const int t = __shfl_sync(kAll, warp == 1 ? 0 : 1, 0);
+            const uint32_t tm = __shfl_sync(kAll, tmem, 0) + uint32_t(t * kTmemTile);
+            const bool leader = elect_one();
             // (8-bit pools: S of -Q where the scale is negative, whose size the softmax
             // applies; P and V's codes are fp16 in bf16 calls too)
             const uint32_t kIdS = tc_idesc_f16(kBf16, false, kTcRows, kTcKeys) |
@@ -1093,9 +1052,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 qdesc[kk] = tc_desc_sw128(qb + (kk >> 2) * Ly::kQSlab + (kk & 3) * 32, 16, 1024);
             // S of key tile gk of the ring (gj-th key tile of this Q tile) into S buffer gj & 1
             auto issue_s = [&](int gk, int gj) {
-                const uint64_t kdesc = tc_desc_sw128(base + Ly::kKv + (gk % kTcStages) * Ly::kStage, 16, 1024);
-                const uint32_t d = tmem + uint32_t(t * kTmemTile + (gj & 1) * kTcKeys);
-                if (leader) {
+                const uint64_t kdesc = tc_desc_sw128(base + Ly::kKv + (gk % kStages) * Ly::kStage, 16, 1024);
+                const uint32_t d = tm + uint32_t((gj & 1) * kTcKeys);
+                {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         // (start addresses stay below 2^18 bytes: the offset never carries
@@ -1109,11 +1068,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             // O (+)= P V; `first` starts the item's accumulator
             auto issue_pv = [&](int gk, int gj, bool first) {
                 const uint64_t vdesc =
-                    tc_desc_sw128(base + Ly::kKv + (gk % kTcStages) * Ly::kStage + Ly::kHalf, Ly::kKvSlab, 1024);
+                    tc_desc_sw128(base + Ly::kKv + (gk % kStages) * Ly::kStage + Ly::kHalf, Ly::kKvSlab, 1024);
                 // P: the first 32 columns of S buffer gj & 1 (16 keys per 8 columns)
-                const uint32_t pa = tmem + uint32_t(t * kTmemTile + (gj & 1) * kTcKeys);
-                const uint32_t d = tmem + uint32_t(t * kTmemTile + 2 * kTcKeys);
-                if (leader) {
+                const uint32_t pa = tm + uint32_t((gj & 1) * kTcKeys);
+                const uint32_t d = tm + uint32_t(2 * kTcKeys);
+                {
 #pragma unroll
                     for (int kk = 0; kk < kTcKeys / 16; ++kk)
                         tc_mma_f16_tmem_a(d, pa + uint32_t(8 * kk), vdesc + uint64_t((kk * 2048) >> 4), kIdO,
@@ -1130,22 +1089,22 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (k >= num_items) break;
                 PfItem it;
                 if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
-                const int nk = it.nk[t];
+                const int nk = __shfl_sync(kAll, it.nk[t], 0), nkt = __shfl_sync(kAll, it.nkt, 0);
                 // the item's Q rows of this tile are in shared memory
                 ok = wait(bar_qfull(t), i);
                 if (!ok) break;
                 if (nk > 0) {
                     for (int j = 0; ok && j < 2 && j < nk; ++j) {
-                        ok = wait(kKvFull + (kt + j) % kTcStages, (kt + j) / kTcStages);
+                        ok = wait(kKvFull + (kt + j) % kStages, (kt + j) / kStages);
                         if (!ok) break;
                         tc_fence_after_sync();
-                        issue_s(kt + j, jt + j);
+                        if (leader) issue_s(kt + j, jt + j);
                     }
                     if (!ok) break;
                     // Q may be overwritten once the item's last S has completed
                     if (nk <= 2) commit(bar_qfree(t));
                 }
-                for (int j = 0; ok && j < it.nkt; ++j) {
+                for (int j = 0; ok && j < nkt; ++j) {
                     const int gk = kt + j;
                     if (j < nk) {
                         // P of key tile j (the first P of an item comes after the softmax
@@ -1156,41 +1115,48 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         // time, left the tensor core idle for hundreds of cycles per key
                         // tile). Only when the K/V is not there yet (an item's first key
                         // tiles) does the warp wait for it, after the P V
-                        ok = wait(bar_p(t, (jt + j) & 1), (jt + j) >> 1);
                         const bool ahead = j + 2 < nk;
                         const int gk2 = gk + 2;
-                        const bool kv_in = __all_sync(
-                            kAll, ok && ahead &&
-                                      mbar_test_wait(bar(kKvFull + gk2 % kTcStages), uint32_t((gk2 / kTcStages) & 1)));
-                        if (!ok) break;
+                        const int pb = bar_p(t, (jt + j) & 1), kb = kKvFull + gk2 % kStages;
+                        bool got = mbar_try_wait(bar(pb), uint32_t(((jt + j) >> 1) & 1));
+                        const bool landed = ahead && mbar_test_wait(bar(kb), uint32_t((gk2 / kStages) & 1));
+                        if (!__all_sync(kAll, got)) {
+                            got = !aborted() && mbar_wait(bar(pb), uint32_t(((jt + j) >> 1) & 1), p.err);
+                            ok = __all_sync(kAll, got);
+                            if (!ok) break;
+                        }
+                        const bool kv_in = __all_sync(kAll, landed);
                         tc_fence_after_sync();
-                        issue_pv(gk, jt + j, j == 0);
-                        // the stage of key tile j is free once this P V (the last MMA of
-                        // this thread that reads it) completes
-                        commit(kKvEmpty + gk % kTcStages);
-                        // this tile's S two key tiles ahead (its S buffer is free once the
-                        // P V just issued has read P)
+                        if (leader) {
+                            issue_pv(gk, jt + j, j == 0);
+                            // the stage of key tile j is free once this P V (the last MMA of
+                            // this thread that reads it) completes
+                            tc_commit(bar(kKvEmpty + gk % kStages));
+                            // this tile's S two key tiles ahead (its S buffer is free once the
+                            // P V just issued has read P)
+                            if (kv_in) issue_s(gk2, jt + j + 2);
+                        }
                         if (ahead) {
                             if (!kv_in) {
-                                ok = wait(kKvFull + gk2 % kTcStages, gk2 / kTcStages);
+                                ok = wait(kb, gk2 / kStages);
                                 if (!ok) break;
                                 tc_fence_after_sync();
+                                if (leader) issue_s(gk2, jt + j + 2);
                             }
-                            issue_s(gk2, jt + j + 2);
                             if (j + 2 == nk - 1) commit(bar_qfree(t));
                         }
                     } else {
                         // a key tile this Q tile skips: its stage may be released only
                         // after it landed (the arrival belongs to this phase of the slot)
-                        ok = wait(kKvFull + gk % kTcStages, gk / kTcStages);
+                        ok = wait(kKvFull + gk % kStages, gk / kStages);
                         if (!ok) break;
-                        commit(kKvEmpty + gk % kTcStages);
+                        commit(kKvEmpty + gk % kStages);
                     }
                 }
                 if (!ok) break;
                 // no MMA of this tile reads Q in this item: Q is free at once
                 if (nk == 0 && leader) mbar_arrive(bar(bar_qfree(t)));
-                kt += it.nkt;
+                kt += nkt;
                 jt += nk;
                 ++i;
             }
@@ -1319,7 +1285,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
                 }
                 // 8-bit pools: the tile's factor, V's exponent, the inverse of its scale, marks
-                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % kTcStages) * Ly::kScalesStage);
+                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % kStages) * Ly::kScalesStage);
                 const uint4 of8 = kBits == 8 ? lds128_u4(tile) : make_uint4(0u, 0u, 0u, 0u);
                 const float factor = kBits == 8 ? __uint_as_float(of8.x) : p.scale_log2;
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
