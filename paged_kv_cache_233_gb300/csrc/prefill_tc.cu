@@ -92,14 +92,22 @@ constexpr int kTcKeys = 64;      // keys per pipeline stage
 constexpr int kTcStages = 4;
 // warp 0 producer, warp 1 MMA issuer of Q tile 0, warps 2-9 softmax, warp 10
 // MMA issuer of Q tile 1, warp 11 copies Q tiles and zeroes the V rows past a
-// context
-constexpr int kIssuer1Warp = 2 + kTcTiles * kTcRows / 32;
-constexpr int kZeroWarp = kIssuer1Warp + 1;
-constexpr int kTcThreads = 32 * (kZeroWarp + 1);
+// context; 8-bit pools: issuer 1 and the Q copies in warps 2 and 3, softmax in 4-11,
+// so that a warpgroup's warps share a number of registers (below)
+template <int kBits> constexpr int softmax_warp0() { return kBits == 8 ? 4 : 2; }
+template <int kBits> constexpr int issuer1_warp() { return kBits == 8 ? 2 : 2 + kTcTiles * kTcRows / 32; }
+template <int kBits> constexpr int zero_warp() { return issuer1_warp<kBits>() + 1; }
+constexpr int kTcThreads = 32 * (2 + kTcTiles * kTcRows / 32 + 2);
+// 8-bit pools: of the 512 threads' 128 registers each, the softmax's 256 take 40 more,
+// which the other 256 give up: the softmax then holds its row without spilling.
+// (setmaxnreg has to be the same instruction in a warpgroup's four warps, and the
+// shares have to come out of what the block was launched with: 256 * 168 + 256 * 88 =
+// 512 * 128.)
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 // 4- and 8-bit pools: four more warps (two would take longer over a 4-bit tile at
 // head size 128 than its MMAs), and a ring of raw key tiles (four at head size 64:
 // the same time)
-constexpr int kDqWarp0 = kZeroWarp + 1;
+constexpr int kDqWarp0 = kTcThreads / 32;
 constexpr int kDqWarps = 4;
 template <int kBits> constexpr int tc_threads() { return kTcThreads + (kBits < 16 ? 32 * kDqWarps : 0); }
 constexpr int kTmemTile = 256;   // tensor-memory columns per Q tile: S, S, O
@@ -550,6 +558,207 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     // items (key split: this CTA's pieces) to work through
     const int num_items = kSplit ? lds32(order + 4u * (kPlanRange + 4)) : all_items;
 
+    auto softmax = [&]() {
+        // ------------------------------------------------------------ softmax
+        const int t = (warp - softmax_warp0<kBits>()) >> 2;                 // Q tile of this warp
+        const int quarter = warp & 3;                  // tensor-memory lanes this warp may read
+        const int r = 32 * quarter + lane;             // row within the Q tile
+        const int R = t * kTcRows + r;                 // row slot within the item
+        const int tq = kTcRows / g;                    // whole tokens per Q tile
+        const uint32_t trow = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(t * kTmemTile);
+        const uint32_t otile = trow + uint32_t(2 * kTcKeys);
+        bool ok = true;
+        // the previous item's results, stored once its O is complete (while this
+        // tile's MMAs of the next item already run); its output row waits in
+        // shared memory (all ones: a row past the item)
+        const uint32_t out_row = base + Ly::kOutRow + 8u * uint32_t(R);
+        const uint32_t ref_row = base + Ly::kRefRow + 4u * uint32_t(R);
+        int prev_nk = 0, prev_jend = 0;
+        float prev_l = 0.f;
+        auto epilogue = [&]() -> bool {
+            const unsigned long long v_row = (unsigned long long)(unsigned)lds32(out_row) |
+                                             ((unsigned long long)(unsigned)lds32(out_row + 4) << 32);
+            const bool prev_row = v_row != ~0ull;
+            const unsigned long long prev_qrow = prev_row ? v_row & ((1ull << 48) - 1) : 0ull;
+            const bool split = kSplit && prev_row && ((v_row >> 62) & 1ull);
+            // key split: every row of the item leaves its piece's state in the
+            // piece's slot, m = -inf when the piece held none of its keys (its O
+            // is then not written)
+            const size_t wrow = size_t((v_row >> 48) & 0x3fffull) * size_t(kTcTiles * kTcRows) + size_t(R);
+            if (split && prev_row) {
+                p.ws_m[wrow] = prev_nk > 0 ? __int_as_float(lds32(ref_row)) : -INFINITY;
+                p.ws_l[wrow] = prev_nk > 0 ? prev_l : 0.f;
+            }
+            if (prev_nk == 0) return true;
+            // the last P V's completion covers every earlier MMA of the issuing thread
+            const int e = prev_jend - 1;
+            const bool got = !aborted() && mbar_wait(bar(bar_o(t, e & 1)), uint32_t((e >> 1) & 1), p.err);
+            if (!__all_sync(kAll, got)) return false;
+            tc_fence_after_sync();
+            // the row normalised into `out`, or (key split) its part's O as it is
+            // (a row without keys has a sum of 0; a NaN sum goes through)
+            const float inv = prev_l != 0.f ? 1.f / prev_l : 0.f;
+            const bool keep = prev_row && (!split || prev_l != 0.f);
+            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.out) + prev_qrow * D);
+            float4 *wo = reinterpret_cast<float4 *>(p.ws_o + wrow * D);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32];
+                tmem_ld32(otile + uint32_t(32 * c), v);
+                if (keep && split) {
+#pragma unroll
+                    for (int e4 = 0; e4 < 8; ++e4)
+                        wo[8 * c + e4] = make_float4(v[4 * e4], v[4 * e4 + 1], v[4 * e4 + 2], v[4 * e4 + 3]);
+                } else if (keep) {
+#pragma unroll
+                    for (int e4 = 0; e4 < 4; ++e4) {
+                        uint4 w;
+                        w.x = Elem<T>::pack2(v[8 * e4 + 0] * inv, v[8 * e4 + 1] * inv);
+                        w.y = Elem<T>::pack2(v[8 * e4 + 2] * inv, v[8 * e4 + 3] * inv);
+                        w.z = Elem<T>::pack2(v[8 * e4 + 4] * inv, v[8 * e4 + 5] * inv);
+                        w.w = Elem<T>::pack2(v[8 * e4 + 6] * inv, v[8 * e4 + 7] * inv);
+                        dst[4 * c + e4] = w;
+                    }
+                }
+            }
+            return true;
+        };
+        int jt = 0;   // key tiles of this Q tile before the item
+        [[maybe_unused]] int kt = 0;   // ring position of the item's first key tile (8-bit pools)
+        int i = 0;
+        for (int m = 0; ok; ++m) {
+            const int k = pf_item_index<kSplit>(m);
+            if (k >= num_items) break;
+            PfItem it;
+            if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
+            const int nk = it.nk[t];
+            // this thread's row: token tok of the item (t*tq + r/g), head r%g of the
+            // group; none past the tile's tq*g rows or the item's tokens
+            const int tok = t * tq + r / g;
+            const bool row = r < tq * g && tok < it.ntok;
+            const int pos = row ? it.pos0 + tok : -1;
+            const unsigned long long qrow =
+                (unsigned long long)(it.q0 + it.j0 + (row ? tok : 0)) * p.n_q_heads + it.h * g + (row ? r % g : 0);
+            // the previous item's output (its tensor-memory loads complete before
+            // this warp's next arrival on a P barrier, which lets O be overwritten)
+            if (i > 0 && !epilogue()) {
+                ok = false;
+                break;
+            }
+            {
+                // (a piece of a split item: its slot in bits 48-61, bit 62 set)
+                const unsigned long long v =
+                    row ? (kSplit ? qrow | ((unsigned long long)it.slot << 48) | (it.split ? 1ull << 62 : 0ull) : qrow)
+                        : ~0ull;
+                sts32(out_row, int(unsigned(v)));
+                sts32(out_row + 4, int(unsigned(v >> 32)));
+            }
+            float ref = -INFINITY;   // reference maximum (base 2) that P and O are relative to
+            float l = 0.f;
+            for (int j = 0; j < nk; ++j) {
+                const int gj = jt + j;
+                const int b = gj & 1;
+                // (a phase already complete passes at once; the abort flag is read
+                // only when the warp has to wait)
+                bool got = mbar_try_wait(bar(bar_s(t, b)), uint32_t((gj >> 1) & 1));
+                if (!got) got = !aborted() && mbar_wait(bar(bar_s(t, b)), uint32_t((gj >> 1) & 1), p.err);
+                if (!__all_sync(kAll, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                float sc[kTcKeys];
+                tmem_ld64(trow + uint32_t(b * kTcKeys), sc);
+                const int k0 = (it.kb + j) * kTcKeys;   // absolute key index of the tile's first key
+                if (k0 + kTcKeys - 1 > pos) {
+#pragma unroll
+                    for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
+                }
+                // 8-bit pools: the tile's factor, V's exponent, the inverse of its scale, marks
+                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % kStages) * Ly::kScalesStage);
+                const uint4 of8 = kBits == 8 ? lds128_u4(tile) : make_uint4(0u, 0u, 0u, 0u);
+                const float factor = kBits == 8 ? __uint_as_float(of8.x) : p.scale_log2;
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < kTcKeys; x += 8) {
+                    m4[0] = fmax3(m4[0], sc[x], sc[x + 1]);
+                    m4[1] = fmax3(m4[1], sc[x + 2], sc[x + 3]);
+                    m4[2] = fmax3(m4[2], sc[x + 4], sc[x + 5]);
+                    m4[3] = fmax3(m4[3], sc[x + 6], sc[x + 7]);
+                }
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float mx = kBits == 8 ? fmaf(top, factor, __uint_as_float(of8.y)) : top * factor;
+                const bool move = mx > ref + move_past<kBits>();
+                const float nref = kBits == 8 ? mx - below_max<kBits>() : mx;
+                const float alpha = move ? fast_exp2(ref - nref) : 1.f;   // 0 while no key was seen
+                if (move) ref = nref;
+                if (j > 0 && __any_sync(kAll, move)) {
+                    // rescale this warp's rows of O (every earlier P V has completed first)
+                    got = !aborted() &&
+                          mbar_wait(bar(bar_o(t, (gj - 1) & 1)), uint32_t(((gj - 1) >> 1) & 1), p.err);
+                    if (!__all_sync(kAll, got)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(otile + uint32_t(32 * c), v);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) v[x] *= alpha;
+                        tmem_st32(otile + uint32_t(32 * c), v);
+                    }
+                }
+                const float nu = ref == -INFINITY ? 0.f : kBits == 8 ? __uint_as_float(of8.y) - ref : -ref;
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < kTcKeys; x += 2) {
+                    ffma2(sc[x], sc[x + 1], factor, nu);
+                    sc[x] = fast_exp2(sc[x]);
+                    sc[x + 1] = fast_exp2(sc[x + 1]);
+                    if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
+                    else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
+                }
+                const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                l = kBits == 8 ? fmaf(sum, __uint_as_float(of8.z), l * alpha) : l * alpha + sum;
+                uint32_t pk[kTcKeys / 2];
+#pragma unroll
+                for (int c = 0; c < kTcKeys / 2; ++c)
+                    pk[c] = kBits == 8 ? Elem<__half>::pack2(sc[2 * c], sc[2 * c + 1]) : Elem<T>::pack2(sc[2 * c], sc[2 * c + 1]);
+                if (kBits == 8 && of8.w != 0) {
+                    // keys whose K or V holds a NaN, among those that this row attends to
+                    const uint4 marks = lds128_u4(tile + 16);
+                    const unsigned long long keys = (marks.x | marks.z) | (unsigned long long)(marks.y | marks.w) << 32;
+                    const int seen = min(max(pos - k0 + 1, 0), kTcKeys);
+                    if (seen > 0 && (keys << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
+                }
+                tmem_st32u(trow + uint32_t(b * kTcKeys), pk);
+                // each lane's tensor-memory store has completed (tmem_st32u waits) and is
+                // ordered before the warp barrier; then one lane arrives for the warp
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bar_p(t, b)));
+            }
+            if (!ok) break;
+            prev_nk = nk;
+            prev_jend = jt + nk;
+            prev_l = l;
+            if (kSplit) sts32(ref_row, __float_as_int(ref));
+            jt += nk;
+            if (kBits == 8) kt += it.nkt;
+            ++i;
+        }
+        // the last item's output
+        if (ok && i > 0 && !epilogue()) ok = false;
+        if (!ok) sts32(flag, 1);
+    };
+
+    if (kBits == 8 && warp >= softmax_warp0<kBits>() && warp < kDqWarp0) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        softmax();
+    } else {
+    if constexpr (kBits == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         // Per key tile, lane 0 waits for a free stage and arms its barrier;
@@ -687,7 +896,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                           uint32_t((x / kRing) & 1), p.err);
         }
         __syncwarp();
-    } else if (warp == kZeroWarp) {
+    } else if (warp == zero_warp<kBits>()) {
         // ------------------------------------------------ Q copies and V tails
         // Q: lane 0 copies each Q tile of an item with one TMA box per
         // 64-column block ([tq = 128/g whole tokens][g heads][64 columns],
@@ -1010,7 +1219,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         }
         if (lane == 0 && !ok) sts32(flag, 1);
         __syncwarp();
-    } else if (warp == 1 || warp == kIssuer1Warp) {
+    } else if (warp == 1 || warp == issuer1_warp<kBits>()) {
         // ------------------------------------------------------- MMA issuers
         // One warp per Q tile issues that tile's MMAs. A thread that issues
         // tcgen05.mma runs only about two MMAs ahead of the tensor core, so
@@ -1168,200 +1377,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             }
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ softmax
-        const int t = (warp - 2) >> 2;                 // Q tile of this warp
-        const int quarter = warp & 3;                  // tensor-memory lanes this warp may read
-        const int r = 32 * quarter + lane;             // row within the Q tile
-        const int R = t * kTcRows + r;                 // row slot within the item
-        const int tq = kTcRows / g;                    // whole tokens per Q tile
-        const uint32_t trow = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(t * kTmemTile);
-        const uint32_t otile = trow + uint32_t(2 * kTcKeys);
-        bool ok = true;
-        // the previous item's results, stored once its O is complete (while this
-        // tile's MMAs of the next item already run); its output row waits in
-        // shared memory (all ones: a row past the item)
-        const uint32_t out_row = base + Ly::kOutRow + 8u * uint32_t(R);
-        const uint32_t ref_row = base + Ly::kRefRow + 4u * uint32_t(R);
-        int prev_nk = 0, prev_jend = 0;
-        float prev_l = 0.f;
-        auto epilogue = [&]() -> bool {
-            const unsigned long long v_row = (unsigned long long)(unsigned)lds32(out_row) |
-                                             ((unsigned long long)(unsigned)lds32(out_row + 4) << 32);
-            const bool prev_row = v_row != ~0ull;
-            const unsigned long long prev_qrow = prev_row ? v_row & ((1ull << 48) - 1) : 0ull;
-            const bool split = kSplit && prev_row && ((v_row >> 62) & 1ull);
-            // key split: every row of the item leaves its piece's state in the
-            // piece's slot, m = -inf when the piece held none of its keys (its O
-            // is then not written)
-            const size_t wrow = size_t((v_row >> 48) & 0x3fffull) * size_t(kTcTiles * kTcRows) + size_t(R);
-            if (split && prev_row) {
-                p.ws_m[wrow] = prev_nk > 0 ? __int_as_float(lds32(ref_row)) : -INFINITY;
-                p.ws_l[wrow] = prev_nk > 0 ? prev_l : 0.f;
-            }
-            if (prev_nk == 0) return true;
-            // the last P V's completion covers every earlier MMA of the issuing thread
-            const int e = prev_jend - 1;
-            const bool got = !aborted() && mbar_wait(bar(bar_o(t, e & 1)), uint32_t((e >> 1) & 1), p.err);
-            if (!__all_sync(kAll, got)) return false;
-            tc_fence_after_sync();
-            // the row normalised into `out`, or (key split) its part's O as it is
-            // (a row without keys has a sum of 0; a NaN sum goes through)
-            const float inv = prev_l != 0.f ? 1.f / prev_l : 0.f;
-            const bool keep = prev_row && (!split || prev_l != 0.f);
-            uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.out) + prev_qrow * D);
-            float4 *wo = reinterpret_cast<float4 *>(p.ws_o + wrow * D);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float v[32];
-                tmem_ld32(otile + uint32_t(32 * c), v);
-                if (keep && split) {
-#pragma unroll
-                    for (int e4 = 0; e4 < 8; ++e4)
-                        wo[8 * c + e4] = make_float4(v[4 * e4], v[4 * e4 + 1], v[4 * e4 + 2], v[4 * e4 + 3]);
-                } else if (keep) {
-#pragma unroll
-                    for (int e4 = 0; e4 < 4; ++e4) {
-                        uint4 w;
-                        w.x = Elem<T>::pack2(v[8 * e4 + 0] * inv, v[8 * e4 + 1] * inv);
-                        w.y = Elem<T>::pack2(v[8 * e4 + 2] * inv, v[8 * e4 + 3] * inv);
-                        w.z = Elem<T>::pack2(v[8 * e4 + 4] * inv, v[8 * e4 + 5] * inv);
-                        w.w = Elem<T>::pack2(v[8 * e4 + 6] * inv, v[8 * e4 + 7] * inv);
-                        dst[4 * c + e4] = w;
-                    }
-                }
-            }
-            return true;
-        };
-        int jt = 0;   // key tiles of this Q tile before the item
-        [[maybe_unused]] int kt = 0;   // ring position of the item's first key tile (8-bit pools)
-        int i = 0;
-        for (int m = 0; ok; ++m) {
-            const int k = pf_item_index<kSplit>(m);
-            if (k >= num_items) break;
-            PfItem it;
-            if (!pf_item<kSplit>(p, order, tiles, k, false, it)) continue;
-            const int nk = it.nk[t];
-            // this thread's row: token tok of the item (t*tq + r/g), head r%g of the
-            // group; none past the tile's tq*g rows or the item's tokens
-            const int tok = t * tq + r / g;
-            const bool row = r < tq * g && tok < it.ntok;
-            const int pos = row ? it.pos0 + tok : -1;
-            const unsigned long long qrow =
-                (unsigned long long)(it.q0 + it.j0 + (row ? tok : 0)) * p.n_q_heads + it.h * g + (row ? r % g : 0);
-            // the previous item's output (its tensor-memory loads complete before
-            // this warp's next arrival on a P barrier, which lets O be overwritten)
-            if (i > 0 && !epilogue()) {
-                ok = false;
-                break;
-            }
-            {
-                // (a piece of a split item: its slot in bits 48-61, bit 62 set)
-                const unsigned long long v =
-                    row ? (kSplit ? qrow | ((unsigned long long)it.slot << 48) | (it.split ? 1ull << 62 : 0ull) : qrow)
-                        : ~0ull;
-                sts32(out_row, int(unsigned(v)));
-                sts32(out_row + 4, int(unsigned(v >> 32)));
-            }
-            float ref = -INFINITY;   // reference maximum (base 2) that P and O are relative to
-            float l = 0.f;
-            for (int j = 0; j < nk; ++j) {
-                const int gj = jt + j;
-                const int b = gj & 1;
-                // (a phase already complete passes at once; the abort flag is read
-                // only when the warp has to wait)
-                bool got = mbar_try_wait(bar(bar_s(t, b)), uint32_t((gj >> 1) & 1));
-                if (!got) got = !aborted() && mbar_wait(bar(bar_s(t, b)), uint32_t((gj >> 1) & 1), p.err);
-                if (!__all_sync(kAll, got)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                float sc[kTcKeys];
-                tmem_ld64(trow + uint32_t(b * kTcKeys), sc);
-                const int k0 = (it.kb + j) * kTcKeys;   // absolute key index of the tile's first key
-                if (k0 + kTcKeys - 1 > pos) {
-#pragma unroll
-                    for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
-                }
-                // 8-bit pools: the tile's factor, V's exponent, the inverse of its scale, marks
-                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % kStages) * Ly::kScalesStage);
-                const uint4 of8 = kBits == 8 ? lds128_u4(tile) : make_uint4(0u, 0u, 0u, 0u);
-                const float factor = kBits == 8 ? __uint_as_float(of8.x) : p.scale_log2;
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int x = 0; x < kTcKeys; x += 8) {
-                    m4[0] = fmax3(m4[0], sc[x], sc[x + 1]);
-                    m4[1] = fmax3(m4[1], sc[x + 2], sc[x + 3]);
-                    m4[2] = fmax3(m4[2], sc[x + 4], sc[x + 5]);
-                    m4[3] = fmax3(m4[3], sc[x + 6], sc[x + 7]);
-                }
-                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                const float mx = kBits == 8 ? fmaf(top, factor, __uint_as_float(of8.y)) : top * factor;
-                const bool move = mx > ref + move_past<kBits>();
-                const float nref = kBits == 8 ? mx - below_max<kBits>() : mx;
-                const float alpha = move ? fast_exp2(ref - nref) : 1.f;   // 0 while no key was seen
-                if (move) ref = nref;
-                if (j > 0 && __any_sync(kAll, move)) {
-                    // rescale this warp's rows of O (every earlier P V has completed first)
-                    got = !aborted() &&
-                          mbar_wait(bar(bar_o(t, (gj - 1) & 1)), uint32_t(((gj - 1) >> 1) & 1), p.err);
-                    if (!__all_sync(kAll, got)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float v[32];
-                        tmem_ld32(otile + uint32_t(32 * c), v);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) v[x] *= alpha;
-                        tmem_st32(otile + uint32_t(32 * c), v);
-                    }
-                }
-                const float nu = ref == -INFINITY ? 0.f : kBits == 8 ? __uint_as_float(of8.y) - ref : -ref;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < kTcKeys; x += 2) {
-                    ffma2(sc[x], sc[x + 1], factor, nu);
-                    sc[x] = fast_exp2(sc[x]);
-                    sc[x + 1] = fast_exp2(sc[x + 1]);
-                    if (x & 2) fadd2(s4[2], s4[3], sc[x], sc[x + 1]);
-                    else fadd2(s4[0], s4[1], sc[x], sc[x + 1]);
-                }
-                const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                l = kBits == 8 ? fmaf(sum, __uint_as_float(of8.z), l * alpha) : l * alpha + sum;
-                uint32_t pk[kTcKeys / 2];
-#pragma unroll
-                for (int c = 0; c < kTcKeys / 2; ++c)
-                    pk[c] = kBits == 8 ? Elem<__half>::pack2(sc[2 * c], sc[2 * c + 1]) : Elem<T>::pack2(sc[2 * c], sc[2 * c + 1]);
-                if (kBits == 8 && of8.w != 0) {
-                    // keys whose K or V holds a NaN, among those that this row attends to
-                    const uint4 marks = lds128_u4(tile + 16);
-                    const unsigned long long keys = (marks.x | marks.z) | (unsigned long long)(marks.y | marks.w) << 32;
-                    const int seen = min(max(pos - k0 + 1, 0), kTcKeys);
-                    if (seen > 0 && (keys << (kTcKeys - seen)) != 0) l = __int_as_float(0x7fffffff);
-                }
-                tmem_st32u(trow + uint32_t(b * kTcKeys), pk);
-                // each lane's tensor-memory store has completed (tmem_st32u waits) and is
-                // ordered before the warp barrier; then one lane arrives for the warp
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bar_p(t, b)));
-            }
-            if (!ok) break;
-            prev_nk = nk;
-            prev_jend = jt + nk;
-            prev_l = l;
-            if (kSplit) sts32(ref_row, __float_as_int(ref));
-            jt += nk;
-            if (kBits == 8) kt += it.nkt;
-            ++i;
-        }
-        // the last item's output
-        if (ok && i > 0 && !epilogue()) ok = false;
-        if (!ok) sts32(flag, 1);
+    } else if constexpr (kBits != 8) {
+        softmax();
+    }
     }
 
     // ---- every role is done: release the tensor memory
