@@ -176,7 +176,8 @@ struct TcLayout {
     static constexpr int kBars = kKv + kStages * kStage;
     static constexpr int kTmemSlot = kBars + 8 * kNumBars;
     static constexpr int kFlag = kTmemSlot + 8;
-    static constexpr int kOrder = kFlag + 8;               // ranked sequence ids, then their lengths
+    static constexpr int kOrder = kFlag + 8;               // ranked sequence ids, then the items before each (all
+                                                           // of them behind the flag)
     // per softmax thread, the output row of its item (kept here through the key
     // loop; under a key split the item's part in bits 48-63), then the row's
     // reference maximum at the item's end (key split)
@@ -268,29 +269,49 @@ struct PfItem {
 // length (ranked, when there are few enough), within a sequence its query
 // tiles from the last (the most keys), then kv heads, so that the items that
 // read a sequence's K/V run close together in time and share it through L2.
-// Item k of that order: fills `it` but for its key range and returns its key
-// tiles N (through its last row's position), or 0 for an item with no rows or
-// a sequence whose chunk or length is invalid (reported once per sequence
+// Ranked sequences' items are those that have rows; else every sequence counts
+// with the longest chunk's query tiles, and items without rows are dealt too (six
+// chunks of 350 to 700 rows, 112 of 432 items: the slowest SM got 50 key tiles'
+// worth where the mean was 33, now 41).
+// A sequence's rows and context are valid (reported when `report`).
+__device__ __forceinline__ bool pf_valid(const PrefillParams &p, int tiles, int q0, int q1, int L, bool report) {
+    const int n = q1 - q0;
+    const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens && n <= tiles * p.tile_tokens;
+    const bool len_ok = L >= n && L <= p.max_blocks * p.block_size;
+    if (rows_ok && len_ok) return true;
+    if (report) atomicOr(p.err, rows_ok ? PAGEDKV_DEVERR_CONTEXT_LEN : PAGEDKV_DEVERR_POSITION);
+    return false;
+}
+
+// Item k of that order (`ranked`: the ranked sequences' ids, then the items before
+// each of them; every lane of the warp calls it): fills `it` but for its key range
+// and returns its key tiles N (through its last row's position), or 0 for an item
+// with no rows or of an invalid sequence (unranked: reported once per sequence
 // when `report`).
 __device__ __forceinline__ int pf_decode(const PrefillParams &p, uint32_t ranked, int tiles, int k,
                                          bool report, PfItem &it, int (&nk_all)[kTcTiles]) {
-    const int per_seq = tiles * p.n_kv_heads;
-    const int r = k / per_seq;
-    const int rem = k - r * per_seq;
-    const int s = ranked ? lds32(ranked + 4u * uint32_t(r)) : r;
-    const int qt = tiles - 1 - rem / p.n_kv_heads;
-    const int h = rem - (rem / p.n_kv_heads) * p.n_kv_heads;
+    const int H = p.n_kv_heads;
+    int s, rem;
+    if (ranked) {
+        const int lane = int(threadIdx.x & 31);
+        int r = -1;     // the last sequence whose items begin at or before k
+        for (int i = 0; i < p.num_seqs; i += 32)
+            r += __popc(__ballot_sync(kAll, i + lane < p.num_seqs &&
+                                                lds32(ranked + 4u * uint32_t(kMaxRankedSeqs + i + lane)) <= k));
+        s = lds32(ranked + 4u * uint32_t(r));
+        rem = k - lds32(ranked + 4u * uint32_t(kMaxRankedSeqs + r));
+    } else {
+        s = k / (tiles * H);
+        rem = k - s * tiles * H;
+    }
     const int q0 = __ldg(p.query_start + s);
     const int q1 = __ldg(p.query_start + s + 1);
     const int n = q1 - q0;
     const int L = __ldg(p.context_lens + s);
-    const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens && n <= tiles * p.tile_tokens;
-    const bool len_ok = L >= n && L <= p.max_blocks * p.block_size;
-    if (!rows_ok || !len_ok) {
-        if (report && qt == tiles - 1 && h == 0)
-            atomicOr(p.err, rows_ok ? PAGEDKV_DEVERR_CONTEXT_LEN : PAGEDKV_DEVERR_POSITION);
-        return 0;
-    }
+    const int last = ranked ? (n + p.tile_tokens - 1) / p.tile_tokens - 1 : tiles - 1;
+    const int qt = last - rem / H;
+    const int h = rem - (rem / H) * H;
+    if (!ranked && !pf_valid(p, tiles, q0, q1, L, report && rem == 0)) return 0;
     const int j0 = qt * p.tile_tokens;
     if (j0 >= n) return 0;
     it.s = s;
@@ -545,6 +566,28 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             }
             ids[rank] = s;
         }
+        __syncthreads();
+        // then, in the lengths' place, the items before each ranked sequence
+        if (threadIdx.x < 32) {
+            int before = 0;
+            for (int i = 0; i < p.num_seqs; i += 32) {
+                const int r = i + lane;
+                int items = 0;
+                if (r < p.num_seqs) {
+                    const int s = ids[r], q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
+                    if (pf_valid(p, tiles, q0, q1, __ldg(p.context_lens + s), blockIdx.x == 0))
+                        items = (q1 - q0 + p.tile_tokens - 1) / p.tile_tokens * p.n_kv_heads;
+                }
+                int incl = items;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(kAll, incl, d);
+                    if (lane >= d) incl += y;
+                }
+                if (r < p.num_seqs) lens[r] = before + incl - items;
+                before += __shfl_sync(kAll, incl, 31);
+            }
+            if (lane == 0) sts32(flag + 4, before);
+        }
     }
     if (kSplit) {
         // (the launcher keeps the split to at most kMaxSplitItems items)
@@ -556,7 +599,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     tc_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + Ly::kTmemSlot);
     // items (key split: this CTA's pieces) to work through
-    const int num_items = kSplit ? lds32(order + 4u * (kPlanRange + 4)) : all_items;
+    const int num_items = kSplit ? lds32(order + 4u * (kPlanRange + 4)) : order ? lds32(flag + 4) : all_items;
 
     auto softmax = [&]() {
         // ------------------------------------------------------------ softmax
