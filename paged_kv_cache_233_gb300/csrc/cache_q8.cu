@@ -30,6 +30,7 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;          // append
 constexpr int kGatherThreads = 128, kGatherItems = 2;
+template <int D> constexpr int gather_tokens() { return kGatherThreads * kGatherItems / (D / 8); }   // of a CTA
 constexpr int kMaxTile = 32;        // rows of a CTA's tile at most: a lane each
 
 template <typename T> constexpr uint32_t kInfBits = Elem<T>::kBf16 ? 0x7f80u : 0x7c00u;
@@ -198,34 +199,35 @@ struct GatherParams {
     const uint8_t *cache[2];      // K, V
     uint4 *rows[2];               // k, v [num_tokens][n_kv_heads][head_dim]
     unsigned int *err;
-    unsigned int count;           // tokens
-    int n_kv_heads, log2_block;
+    int num_tokens, n_kv_heads, log2_block;
     long long num_slots;
 };
 
-// An item is half a panel of a token and head: 8 bytes in, 16 out. Four
-// neighbouring tokens' panels are neighbouring items, whole sectors where their slots
-// are neighbours, as a prompt's are.
+// An item is half a panel of a token: 8 bytes in, 16 out. A CTA takes some tokens of
+// one kv head of K or V, four neighbouring tokens' half panels as neighbouring items:
+// whole sectors where their slots are neighbours, as a prompt's are.
 template <typename T, int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_q8_kernel(const __grid_constant__ GatherParams p) {
     // (no early start for the kernel after this one: its work, rows of these to
     // append or attend over, comes after this grid's end)
     grid_dependency_wait();
-    constexpr unsigned kPanels = D / kQ8Panel;
+    constexpr int kHalves = D / 8, kTokens = gather_tokens<D>();
+    constexpr float kMost = Elem<T>::kBf16 ? 0x1.fep127f : 65504.f;
     const int o = blockIdx.y, B = 1 << p.log2_block;
-    const unsigned H = unsigned(p.n_kv_heads), x0 = blockIdx.x * (kGatherThreads * kGatherItems) + threadIdx.x;
+    const int tile = blockIdx.x / unsigned(p.n_kv_heads), h = blockIdx.x - tile * p.n_kv_heads;
+    const uint8_t *pool = p.cache[o] + size_t(h) * q8_head_bytes(B, D);
+    const size_t block_bytes = size_t(p.n_kv_heads) * q8_head_bytes(B, D);
+    const int half = threadIdx.x & 1;
     long long slot[kGatherItems];
-    unsigned token[kGatherItems], head[kGatherItems], panel[kGatherItems];
-    const unsigned half = threadIdx.x & 1;
+    int token[kGatherItems], panel[kGatherItems];
 #pragma unroll
     for (int i = 0; i < kGatherItems; ++i) {
-        const unsigned x = x0 + i * kGatherThreads, run = x >> 3, hp = run / kPanels, quad = hp / H;
-        panel[i] = run % kPanels;
-        head[i] = hp - quad * H;
-        token[i] = quad * 4 + ((x >> 1) & 3);
-        slot[i] = token[i] < p.count ? __ldg(reinterpret_cast<const long long *>(p.slots) + token[i]) : -1;
+        const int x = (int(threadIdx.x) + i * kGatherThreads) >> 1;       // [quad][panel][4 tokens]
+        panel[i] = (x >> 2) % (kHalves / 2);
+        token[i] = tile * kTokens + (x >> 2) / (kHalves / 2) * 4 + (x & 3);
+        slot[i] = token[i] < p.num_tokens ? __ldg(reinterpret_cast<const long long *>(p.slots) + token[i]) : -1;
         if (slot[i] >= p.num_slots) {
-            if (head[i] + panel[i] + half == 0) atomicOr(p.err, PAGEDKV_DEVERR_SLOT_RANGE);
+            if (h + panel[i] + half == 0) atomicOr(p.err, PAGEDKV_DEVERR_SLOT_RANGE);
             slot[i] = -1;
         }
     }
@@ -234,27 +236,37 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q8_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < kGatherItems; ++i) {
         if (slot[i] < 0) continue;
-        const uint8_t *base = p.cache[o] + ((slot[i] >> p.log2_block) * p.n_kv_heads + head[i]) * q8_head_bytes(B, D);
-        c[i] = *reinterpret_cast<const uint2 *>(base + (panel[i] * B + unsigned(slot[i] & (B - 1))) * 16 + half * 8);
+        const uint8_t *base = pool + size_t(slot[i] >> p.log2_block) * block_bytes;
+        c[i] = *reinterpret_cast<const uint2 *>(base + (panel[i] * B + int(slot[i] & (B - 1))) * 16 + half * 8);
         scale[i] = *reinterpret_cast<const float *>(base + q8_scale_at(B, D));
     }
-    constexpr float kMost = Elem<T>::kBf16 ? 0x1.fep127f : 65504.f;
 #pragma unroll
     for (int i = 0; i < kGatherItems; ++i) {
         if (slot[i] < 0) continue;
-        auto value = [&](float v) {
-            v *= scale[i];
-            return fabsf(v) > kMost ? copysignf(kMost, v) : v;     // (a NaN stays one)
-        };
-        auto two = [&](uint32_t pair) {
-            const float2 f = Elem<__half>::unpack2(pair);
-            return Elem<T>::pack2(value(f.x), value(f.y));
-        };
         uint32_t r[4];
         q8_halves(c[i].x, r[0], r[1]);
         q8_halves(c[i].y, r[2], r[3]);
-        __stcs(p.rows[o] + ((size_t(token[i]) * H + head[i]) * kPanels + panel[i]) * 2 + half,
-               make_uint4(two(r[0]), two(r[1]), two(r[2]), two(r[3])));
+        // a scale of 2^-14 .. 2^7 takes a code to fp16 in one rounding and to no
+        // infinity; the others, and bf16, go through fp32
+        if (!Elem<T>::kBf16 && scale[i] >= 0x1p-14f && scale[i] <= 0x1p7f) {
+            const uint32_t by = pack_half2(scale[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = hmul2_u(r[j], by);
+        } else {
+            const bool near = fabsf(scale[i]) < (Elem<T>::kBf16 ? 0x1p119f : 0x1p7f);     // nothing past the type's range
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 f = Elem<__half>::unpack2(r[j]);
+                f.x *= scale[i];
+                f.y *= scale[i];
+                if (!near) {      // (a NaN stays one)
+                    if (fabsf(f.x) > kMost) f.x = copysignf(kMost, f.x);
+                    if (fabsf(f.y) > kMost) f.y = copysignf(kMost, f.y);
+                }
+                r[j] = Elem<T>::pack2(f.x, f.y);
+            }
+        }
+        __stcs(p.rows[o] + (size_t(token[i]) * p.n_kv_heads + h) * kHalves + panel[i] * 2 + half, make_uint4(r[0], r[1], r[2], r[3]));
     }
 }
 
@@ -294,24 +306,12 @@ cudaError_t append_typed(const Q8AppendParams &p, int head_dim, int block_size, 
 }
 
 template <typename T, int D>
-cudaError_t gather_typed(GatherParams p, int num_tokens, cudaStream_t st) {
-    // launches of at most 2^31 items per operand
-    const long long per_quad = 8ll * p.n_kv_heads * (D / kQ8Panel);
-    const int most = int((1ll << 31) / per_quad) * 4;
-    for (int t0 = 0; t0 < num_tokens;) {
-        const int n = num_tokens - t0 < most ? num_tokens - t0 : most;
-        p.count = unsigned(n);
-        const long long items = (n + 3) / 4 * per_quad;
-        constexpr long long kPerCta = kGatherThreads * kGatherItems;
-        cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t cfg = config(&attr, dim3(unsigned((items + kPerCta - 1) / kPerCta), 2), kGatherThreads, 0, st);
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, gather_q8_kernel<T, D>, p);
-        if (e != cudaSuccess) return e;
-        p.slots += n;
-        for (auto &r : p.rows) r += size_t(n) * p.n_kv_heads * (D / 8);
-        t0 += n;
-    }
-    return cudaSuccess;
+cudaError_t gather_typed(const GatherParams &p, cudaStream_t st) {
+    const long long ctas = ((long long)p.num_tokens + gather_tokens<D>() - 1) / gather_tokens<D>() * p.n_kv_heads;
+    if (ctas > INT_MAX) return cudaErrorInvalidConfiguration;      // (rows of 16 TB)
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(&attr, dim3(unsigned(ctas), 2), kGatherThreads, 0, st);
+    return cudaLaunchKernelEx(&cfg, gather_q8_kernel<T, D>, p);
 }
 
 }  // namespace
@@ -332,14 +332,15 @@ cudaError_t launch_gather_q8(const uint8_t *k_cache, const uint8_t *v_cache, con
     p.rows[0] = static_cast<uint4 *>(k);
     p.rows[1] = static_cast<uint4 *>(v);
     p.err = err;
+    p.num_tokens = num_tokens;
     p.n_kv_heads = n_kv_heads;
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.num_slots = num_slots;
     if (dtype == PAGEDKV_BF16)
-        return head_dim == 64 ? gather_typed<__nv_bfloat16, 64>(p, num_tokens, st)
-                              : gather_typed<__nv_bfloat16, 128>(p, num_tokens, st);
-    return head_dim == 64 ? gather_typed<__half, 64>(p, num_tokens, st)
-                          : gather_typed<__half, 128>(p, num_tokens, st);
+        return head_dim == 64 ? gather_typed<__nv_bfloat16, 64>(p, st)
+                              : gather_typed<__nv_bfloat16, 128>(p, st);
+    return head_dim == 64 ? gather_typed<__half, 64>(p, st)
+                          : gather_typed<__half, 128>(p, st);
 }
 
 }  // namespace pkv
