@@ -16,7 +16,18 @@
 // block follow from the offsets, so no two owners meet in a block, and nothing is
 // sorted, counted or locked), and a warp takes the run of one kv head of K or V: its
 // rows stay in registers between the largest value and the codes, so each is read
-// once. A lane holds a panel of a row, 32 bytes in, 16 out.
+// once. A lane holds a panel of a row, 32 bytes in, 16 out (half a panel a lane, whole
+// lines a load: 3% slower). Bound by memory latency: what counts is how many warps have
+// their rows in flight, hence four CTAs to an SM where a run's rows fit 64 registers.
+//
+// Measured (one GB300, us; GB/s of rows in and codes out, or the other way):
+//                                                       append        gather
+//     64 rows of 8 heads of 128, blocks of 16            3.2           2.0
+//     12 x 1024 rows, the same                          12.7 (4480)   12.4 (4650)
+//     16,383 rows of 32 heads of 64, blocks of 32       36.6 (5500)   40.4 (4980)
+//     16,383 rows of 8 heads of 128, blocks of 16       20.7 (4870)   20.3 (4980)
+// append with three CTAs to an SM, as its registers come out by themselves: 14.8, 38.9
+// and 21.5; with tiles of 16 rows, or CTAs of 128 or 512 threads: up to 20% slower.
 #include <limits.h>
 #include <math.h>
 
@@ -77,7 +88,7 @@ __device__ __forceinline__ void report_bad(const Q8AppendParams &p, const int *s
 }
 
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const __grid_constant__ Q8AppendParams p) {
+__global__ void __launch_bounds__(kThreads, D * B <= 2048 ? 4 : 2) append_q8_kernel(const __grid_constant__ Q8AppendParams p) {
     constexpr int kPanels = D / kQ8Panel;
     constexpr int kRows = 32 / kPanels;                 // rows of a pass
     constexpr int kPasses = B > kRows ? B / kRows : 1;
@@ -205,7 +216,9 @@ struct GatherParams {
 
 // An item is half a panel of a token: 8 bytes in, 16 out. A CTA takes some tokens of
 // one kv head of K or V, four neighbouring tokens' half panels as neighbouring items:
-// whole sectors where their slots are neighbours, as a prompt's are.
+// whole sectors where their slots are neighbours, as a prompt's are. Its issue slots are
+// two thirds used: heads by blockIdx and the products packed where they can be (fp16)
+// took 12 x 1024 rows from 13.0 to 12.4 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_q8_kernel(const __grid_constant__ GatherParams p) {
     // (no early start for the kernel after this one: its work, rows of these to
