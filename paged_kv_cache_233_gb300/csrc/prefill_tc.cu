@@ -1170,7 +1170,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const int e = there ? min(max(int((info[o].x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp) : kQ8LeastExp;
                     const int most = __reduce_max_sync(kAll, e);
                     const bool any = __any_sync(kAll, there && info[o].y != 0) != 0;
-                    const uint32_t by = pack_half2(q8_power(max(__shfl_sync(kAll, e, blk) - most, -30) + 6));
+                    // (bf16's K leaves its conversion at 2^-120 of the code, and loses nothing)
+                    const int down = __shfl_sync(kAll, e, blk) - most;
+                    const float power = q8_power(kBf16 && !of_v ? down + 126 : max(down, -30) + 6);
+                    const uint32_t by = kBf16 && !of_v ? Elem<__nv_bfloat16>::pack2(power, power) : pack_half2(power);
                     const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
                     auto put = [&](int i, const uint32_t (&v)[8]) {
                         // panel 2 i + odd: chunks 2 (2 i + odd) and the next of the row, swizzled by its low bits
@@ -1179,11 +1182,15 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                             sts128((to ^ uint32_t((((4 * i + 2 * odd) & 7) + c) << 4)) + uint32_t((i >> 1) * Ly::kKvSlab),
                                    make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
                     };
-                    auto to_bf16 = [](uint32_t (&v)[8]) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float2 a = Elem<__half>::unpack2(v[c]);
-                            v[c] = Elem<__nv_bfloat16>::pack2(a.x, a.y);
+                    auto word = [&](auto bf16, uint32_t c, uint32_t &lo, uint32_t &hi) {
+                        if constexpr (decltype(bf16)::value) {
+                            q8_bf16(c, lo, hi);
+                            lo = bmul2_u(lo, by);
+                            hi = bmul2_u(hi, by);
+                        } else {
+                            q8_halves(c, lo, hi);
+                            lo = hmul2_u(lo, by);
+                            hi = hmul2_u(hi, by);
                         }
                     };
                     // One run of instructions. (With the rare cases below as conditions in it,
@@ -1192,13 +1199,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                         for (int i = 0; i < D / 32; ++i) {
                             uint32_t v[8];
-                            q8_halves(cw[o][i].x, v[0], v[1]);
-                            q8_halves(cw[o][i].y, v[2], v[3]);
-                            q8_halves(cw[o][i].z, v[4], v[5]);
-                            q8_halves(cw[o][i].w, v[6], v[7]);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) v[c] = hmul2_u(v[c], by);
-                            if constexpr (decltype(bf16)::value) to_bf16(v);
+                            word(bf16, cw[o][i].x, v[0], v[1]);
+                            word(bf16, cw[o][i].y, v[2], v[3]);
+                            word(bf16, cw[o][i].z, v[4], v[5]);
+                            word(bf16, cw[o][i].w, v[6], v[7]);
                             put(i, v);
                         }
                     };
@@ -1222,15 +1226,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                                 // the stage it is a zero, since it must not meet the weight 0 of
                                 // rows that do not see it. A row past the context is zeros.
                                 const uint32_t bad = ((c4[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                                q8_halves(live ? c4[j] & ~((bad >> 7) * 255u) : 0u, v[2 * j], v[2 * j + 1]);
-                                v[2 * j] = hmul2_u(v[2 * j], by);
-                                v[2 * j + 1] = hmul2_u(v[2 * j + 1], by);
+                                const uint32_t good = live ? c4[j] & ~((bad >> 7) * 255u) : 0u;
+                                if (kBf16 && !of_v) word(std::bool_constant<kBf16>{}, good, v[2 * j], v[2 * j + 1]);
+                                else word(std::false_type{}, good, v[2 * j], v[2 * j + 1]);
                             }
-                            if (kBf16 && !of_v) to_bf16(v);
                             put(i, v);
                         }
                     } else if (kBf16 && !of_v) {
-                        plain(std::true_type{});
+                        plain(std::bool_constant<kBf16>{});
                     } else {
                         plain(std::false_type{});
                     }

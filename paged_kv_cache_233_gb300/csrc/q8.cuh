@@ -13,6 +13,22 @@ __device__ __forceinline__ void q8_halves(uint32_t w, uint32_t &lo, uint32_t &hi
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+// The same codes times 2^-120 as bf16, exact: a code's exponent and mantissa are where
+// bf16 has its lowest exponent bits and its highest mantissa bits once it is moved up
+// by 4 in its half, and a code below 2^-6 is below 2^-126 then, bf16's own small end.
+// (Not for NaN codes, which come out as 480 * 2^-120.)
+__device__ __forceinline__ void q8_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    // a byte to the low half of 16 bits, its top bit to all of the high half
+    asm("prmt.b32 %0, %2, 0, 0x9180;\n\tprmt.b32 %1, %2, 0, 0xb3a2;" : "=r"(lo), "=r"(hi) : "r"(w));
+    lo = (lo << 4) & 0x87f087f0u;
+    hi = (hi << 4) & 0x87f087f0u;
+}
+__device__ __forceinline__ uint32_t bmul2_u(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Four floats, at most 448 in size or NaN, to codes, x0 in byte 0: ties to even.
 __device__ __forceinline__ uint32_t q8_codes(float x0, float x1, float x2, float x3) {
     uint32_t w;

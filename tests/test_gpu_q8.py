@@ -417,6 +417,30 @@ def test_prefill_nan_reaches_the_rows_that_attend_to_it(operand, dtype, dim, blo
         assert bool(torch.isfinite(after).all()) if operand == "q" else bool(after.isnan().all())
 
 
+@pytest.mark.parametrize("far", [0, 4, 20])
+@pytest.mark.parametrize("dtype,dim,block", [(F16, 64, 8), (BF16, 128, 16), (BF16, 64, 32), (BF16, 128, 8)])
+def test_every_code(dtype, dim, block, far):
+    """Codes drawn from all that are numbers, those below 2^-6 among them, and K's scales
+    up to 2^far apart within 64 tokens."""
+    heads, lens, chunk = 2, [230, 64, 77], [70, 64, 1]
+    kc, vc, tables = q8.filled(lens, heads, block, dim, dtype, 8)
+    g = torch.Generator().manual_seed(9)
+    for pool, most in ((kc, far), (vc, 3)):
+        codes, scale, mark = q8.views(pool, dim)
+        codes[:] = torch.randint(0, 256, codes.shape, generator=g, dtype=torch.int32).to(torch.uint8)
+        codes[(codes & 0x7f) == 0x7f] = 3
+        scale[:] = torch.exp2(-torch.randint(0, most + 1, scale.shape, generator=g).float())
+        mark[:] = 0
+    starts = torch.tensor([0] + chunk).cumsum(0)
+    q = (torch.randn(int(starts[-1]), 2 * heads, dim, generator=g) * 0.1).to(dtype)
+    out = prefill(q, kc, vc, tables, starts, lens, 0.125)
+    q8.assert_near(out, q8.attention(q, (kc, vc), tables, starts, lens, 0.125, dim), dtype, 2, "prefill")
+    one = torch.arange(4)
+    out = decode(q[:3], kc, vc, tables, lens, 0.125, 0)
+    q8.assert_near(out, q8.attention(q[:3], (kc, vc), tables, one, lens, 0.125, dim), dtype, 2, "decode")
+    assert pk.device_errors() == 0
+
+
 # ---------------------------------------------------- blocks, streams, graphs
 @pytest.mark.parametrize("dtype,block", [(F16, 8), (BF16, 16), (F16, 32)])
 def test_blocks_copy_and_swap(dtype, block):
