@@ -33,7 +33,8 @@
  *     block tables, lengths and token lists, right ahead of a 16-bit call. Once
  *     paged_kv_build_tables, paged_kv_fork, paged_kv_release,
  *     paged_kv_gather_q4 or paged_kv_gather_q8 has been called in the process,
- *     whose results are tables, lengths and rows, neither limit is left: paged_kv_append_tokens, paged_attention_decode and
+ *     whose results are tables, lengths and rows, neither limit is left:
+ *     paged_kv_append_tokens, paged_attention_decode and
  *     paged_attention_prefill then read all their inputs after the work ahead
  *     of them, which takes them 1 to 3 us longer in a chain of small calls.
  *   - Argument and shape checks run on the host before anything is enqueued;
@@ -703,7 +704,9 @@ int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_
  * The same causal attention of each sequence's chunk of query rows, with K and V
  * the values that the codes stand for; a probability times its token's V scale is
  * rounded to fp16, relative to a running maximum as in the decode; scores, softmax
- * statistics and output sums are fp32. Arguments, limits, workspace and key_parts as
+ * statistics and output sums are fp32. The blocks that hold 64 neighbouring tokens are
+ * brought to one scale, exactly unless one's scale is 2^21 and more below the largest
+ * (its values then lose bits; K of bf16 calls none). Arguments, limits, workspace and key_parts as
  * paged_attention_prefill_q4's. In bf16 caches values of V may be 2^70 at most. A
  * NaN or an infinity in a row of q makes that row's outputs of the head NaN; a token
  * that is marked as holding a NaN, in K or in V, those of the rows that attend to it.

@@ -64,11 +64,32 @@
 // 16-byte chunk of the swizzled row. Rows past the context are written as
 // zeros, so the tail's detour is not needed. A stage is then complete when all
 // four warps have arrived. The bound stays the tensor cores' and the softmax's
-// alternation, with fewer issue slots and, of 512 threads, 128 registers each:
-// 2048 rows after 16384 tokens, 8 kv heads of 128, 32 query heads, bf16: 525 us,
-// 1112 TFLOP/s, 57% of a large bf16 product's rate (16-bit pools, unsplit: 546
-// us); 1216 rows after 8192, 152 items that are not split: 163 us (149), with
-// heads of 64 138 us (114).
+// alternation, with fewer issue slots and, of 512 threads, 128 registers each.
+//
+// 8-bit pools (kBits 8, layout in q8.h): the same with warps 12-15 taking 16 keys of
+// K and of V each. A tile's blocks have a scale each, powers of two: each code is
+// brought exactly to one scale of the tile (of K, and of V), whose exponents go to the
+// softmax with the stage: S is multiplied by K's, and P is 2^(z + b - ref) with V's
+// exponent b in it, the sum over 2^-b. K is held in the 16-bit type, V and P in fp16
+// in both types (e4m3 codes are exact in fp16, not every scale's product is). A
+// key whose row holds a NaN is zeroed in the stage, and the rows that attend to it get
+// a sum of NaN. In bf16 K's codes become bf16 by moving bits (a conversion by way of
+// fp32 took 2% longer). The softmax's warps take registers from the others (below),
+// and at head size 128 the raw ring leaves room for three stages, not four.
+//
+// Measured (us, TFLOP/s; 8 kv heads, 32 query heads, bf16; a large bf16 product runs
+// at 1919 TFLOP/s, which bounds the first row at 304 us):
+//                                       4 bits        8 bits        16 bits
+//     2048 rows after 16384 tokens
+//         heads of 128                  473  1235     515  1134     542  1079 (unsplit)
+//         heads of 64                   385   759     375   779     395   740 (unsplit)
+//     1216 rows after 8192, 152 items, unsplit
+//         heads of 128                  144  1222     148  1185     153  1145
+//         heads of 64                   129   679     115   761     112   783
+//     33 rows after 6001, split         25             24            31
+// (8 bits, fp16: 488 in the first row. 49% of the tensor pipe's cycles and 53% of the issue
+// slots are used, 25% of the exp2 unit: the two Q tiles' softmaxes, key tile by key tile,
+// and the issuers' hand-overs leave the tensor pipe idle in between.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -99,7 +120,8 @@ template <int kBits> constexpr int issuer1_warp() { return kBits == 8 ? 2 : 2 + 
 template <int kBits> constexpr int zero_warp() { return issuer1_warp<kBits>() + 1; }
 constexpr int kTcThreads = 32 * (2 + kTcTiles * kTcRows / 32 + 2);
 // 8-bit pools: of the 512 threads' 128 registers each, the softmax's 256 take 40 more,
-// which the other 256 give up: the softmax then holds its row without spilling.
+// which the other 256 give up: the softmax then holds its row without spilling (2048
+// rows after 16384 tokens, heads of 128, fp16: 527 -> 490 us).
 // (setmaxnreg has to be the same instruction in a warpgroup's four warps, and the
 // shares have to come out of what the block was launched with: 256 * 168 + 256 * 88 =
 // 512 * 128.)
@@ -148,7 +170,7 @@ constexpr int kNumBars = kTailV + kTcStages;
 // an item cut into several pieces leaves per-row states for the merge
 constexpr int kMinPartTiles = 16;
 // (a merge costs less here than the tiles that a shorter range saves: 33 rows
-// after 6001 tokens 24 us, with ranges of 16 tiles or more 31)
+// after 6001 tokens 24 us in 4 bits as in 8, with ranges of 16 tiles or more 31)
 constexpr int kMinPartTilesPacked = 6;
 template <int kBits> constexpr int min_part_tiles() { return kBits < 16 ? kMinPartTilesPacked : kMinPartTiles; }
 constexpr int kMaxSplitParts = kPfMaxSplitParts;   // pieces of one item (a merge lane each)

@@ -579,6 +579,58 @@ def test_prefill_many_items_per_block():
     assert pk.device_errors() == 0
 
 
+@pytest.mark.parametrize("seqs", [7, 256, 257, 300])
+def test_prefill_of_many_sequences_some_without_rows(seqs):
+    """Up to 256 sequences are taken longest first, more in their own order; those
+    without rows in this call come between the others."""
+    lens = [(0, 33, 90, 16, 200)[(3 * i + i // 7) % 5] for i in range(seqs)]
+    chunk = [min(n, (0, 9, 70, 0, 1)[i % 5]) for i, n in enumerate(lens)]
+    kc, vc, tables = q8.filled(lens, 2, 16, 64, F16, 11)
+    starts = torch.tensor([0] + chunk).cumsum(0)
+    q = rows((int(starts[-1]) + 2, 6, 64), F16, 12)
+    ref = q8.attention(q[:-2], (kc, vc), tables, starts, lens, 0.125, 64)
+    for parts in (1, 2, 0):
+        out = prefill(q, kc, vc, tables, starts, lens, 0.125, most=max(chunk), key_parts=parts)
+        assert bool((out[-2:] == 5).all())
+        q8.assert_near(out[:-2], ref, F16, 2, f"parts {parts}")
+    assert pk.device_errors() == 0
+
+
+def test_two_graphs_take_turns_with_one_workspace():
+    """Two captured steps share their workspaces; each replay gives what the eager call did."""
+    steps = []
+    for i, (lens, chunk) in enumerate((([700, 40, 64], [20, 1, 9]), ([25, 900, 33], [5, 20, 5]))):
+        kc, vc, tables = q8.filled(lens, 4, 16, 128, BF16, 13 + i)
+        tables = torch.cat([tables, torch.full((3, 60 - tables.shape[1]), -1, dtype=torch.int32)], 1)
+        one, many = rows((3, 16, 128), BF16, 14 + i), rows((30, 16, 128), BF16, 15 + i)
+        steps.append([t.cuda() for t in (one, many, kc, vc, tables)] + [i32([0] + torch.tensor(chunk).cumsum(0).tolist()), i32(lens)])
+    ws = pk.new_workspace(steps[0][0], steps[0][4], 16, pk.PARTITION_BALANCED)
+    split = pk.prefill_workspace(steps[0][1])
+
+    def step(x, out):
+        one, many, kc, vc, tables, starts, lens = x
+        pk.paged_attention_decode_q8(one, kc, vc, tables, lens, 0.1, out[0], pk.PARTITION_BALANCED, ws)
+        pk.paged_attention_prefill_q8(many, kc, vc, tables, starts, lens, 0.1, out[1], 20, workspace=split, key_parts=32)
+
+    outs = [[torch.zeros_like(t) for t in x[:2]] for x in steps]
+    want, graphs = [], []
+    for x, out in zip(steps, outs):
+        step(x, out)
+        want.append([t.clone() for t in out])
+    torch.cuda.synchronize()
+    for x, out in zip(steps, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(x, out)
+    for i in (0, 1, 1, 0, 1):
+        for t in outs[i]:
+            t.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
+    assert pk.device_errors() == 0
+
+
 def test_pools_past_4_gib():
     """Blocks whose bytes lie past 2^32 in their pool."""
     heads, dim, block, dtype = 8, 128, 32, BF16
