@@ -17,16 +17,17 @@
 //
 // The sums over the sequences run in one block of threads, and every block runs
 // them for itself, keeping what each sequence's entries need in shared memory; the
-// entries are taken 128 at a time, a warp each with four loads in flight. The push
+// entries are taken 64 at a time, a warp each with its loads in flight. The push
 // is a cluster's work: a bit per block in shared memory, counts over the cluster by
 // distributed shared memory, then the marked ids from the bits.
 //
 // Bound by launches and dependent reads (a length, an entry, a count; the entries and
-// counts of the second case below are 2 us of bandwidth). Measured (one GB300, us):
-//     24 + 8 rows of up to 1500 tokens, fork and release              12
-//     1024 + 1000 rows of up to 8192 tokens, copies of what they change included   30
-// the second: fork 11, release 9, push 11 under a profiler. Before entries were taken 128
-// at a time and the push spread over a cluster it took 40.
+// counts of the second case below are 2 us of bandwidth). Measured (one GB300, us,
+// in a graph, fork, release and a copy of what they change):
+//     24 + 8 rows of up to 1500 tokens            9.6
+//     1024 + 1000 rows of up to 8192 tokens      25.7, of which the fork 10.1
+// With runs of 128 entries 27.7, of 32 entries 27.1; before the runs, and with the push by one block of threads,
+// the whole took 40 us, 28 with them (not in a graph).
 #include "launch_cache.h"
 #include "pages.h"
 #include "ptx.cuh"
@@ -38,7 +39,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kPerThread = 4;          // sequences per thread: 4096 at most
-constexpr int kRun = 128;              // entries of a warp's run
+constexpr int kRun = 64;               // entries of a warp's run
 
 struct Divisor {                       // x / B and x % B, x >= 0
     int B, shift;
@@ -47,8 +48,9 @@ struct Divisor {                       // x / B and x % B, x >= 0
     __device__ int blocks(int x) const { return quotient(x) + (x - quotient(x) * B > 0 ? 1 : 0); }   // ceil(x / B)
 };
 
-__device__ __forceinline__ int free_blocks_of(const PagesParams &p, bool report) {
-    const int n = __ldcg(p.free_count);
+// The blocks on the stack, n as it was read. (Checks come after the loads that do not
+// depend on them: a kernel here is a few dependent reads long.)
+__device__ __forceinline__ int free_blocks_of(const PagesParams &p, int n, bool report) {
     if (n >= 0 && n <= p.free_capacity) return n;
     if (report) atomicOr(p.err, PAGEDKV_DEVERR_POSITION);
     return min(max(n, 0), p.free_capacity);
@@ -58,32 +60,39 @@ __device__ __forceinline__ bool bad_length(const PagesParams &p, int L) {
     return L < 0 || (long long)L > (long long)p.max_blocks * p.block_size;
 }
 
-// What a fork asks for s: its parent (or -1) and the parent's tokens. Bad ones are reported.
-__device__ __forceinline__ int parent_of(const PagesParams &p, int of, bool report, int &L) {
-    L = 0;
-    if (of == -1) return -1;
-    const bool in = of >= 0 && of < p.num_seqs;
-    const int above = in ? __ldcg(p.choice + of) : 0, tokens = in ? __ldcg(p.context_lens + of) : 0;
-    if (above != -1) {              // (a parent is no child of this call)
-        if (report) atomicOr(p.err, PAGEDKV_DEVERR_SEQ_INDEX);
-        return -1;
+// What a fork asks for with parent `of`: the parent again (or -1) and its tokens. Bad ones are reported.
+struct Parent {
+    int above, tokens;       // its own parent, its length
+    __device__ void read(const PagesParams &p, int of) {
+        const bool in = of >= 0 && of < p.num_seqs;
+        above = in ? __ldcg(p.choice + of) : 0;
+        tokens = in ? __ldcg(p.context_lens + of) : 0;
     }
-    if (bad_length(p, tokens)) {
-        if (report) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
-        return -1;
+    __device__ int check(const PagesParams &p, int of, bool report, int &L) const {
+        L = 0;
+        if (of == -1) return -1;
+        if (above != -1) {              // (a parent is no child of this call)
+            if (report) atomicOr(p.err, PAGEDKV_DEVERR_SEQ_INDEX);
+            return -1;
+        }
+        if (bad_length(p, tokens)) {
+            if (report) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
+            return -1;
+        }
+        L = tokens;
+        return of;
     }
-    L = tokens;
-    return of;
-}
+};
 
 // What the entries' part of a kernel needs of each sequence, in shared memory.
 struct Runs {
     int *run0;            // [num_seqs + 1]: runs before each sequence's
     int *count;           // [num_seqs]: entries
-    uint16_t *of;         // [num_seqs]: fork's parent
-    __device__ Runs(int *memory, int S) : run0(memory), count(memory + S + 1), of(reinterpret_cast<uint16_t *>(memory + 2 * S + 1)) {}
+    int *from;            // [num_seqs]: the parent's row (fork), the first of them (release)
+    __device__ Runs(int *memory, int S) : run0(memory), count(memory + S + 1), from(memory + 2 * S + 1) {}
 };
-int runs_bytes(int S) { return 4 * (2 * S + 1) + 2 * S; }
+int runs_bytes(int S) { return 4 * (3 * S + 1); }
+__device__ __forceinline__ unsigned runs_of(int entries) { return unsigned(entries + kRun - 1) / kRun; }
 
 // Every run of entries there is, a warp each: body(sequence, its first entry's number, entries left).
 template <typename Body>
@@ -104,62 +113,65 @@ __global__ void __launch_bounds__(kMaxThreads) fork_kernel(const __grid_constant
     const Runs r(memory, S);
     const unsigned rank = blockIdx.x;
     grid_dependency_wait();
-    const int count = free_blocks_of(p, rank == 0 && threadIdx.x == 0);
+    const int on_stack = __ldcg(p.free_count);
     const int per = (S + int(blockDim.x) - 1) / int(blockDim.x), s0 = int(threadIdx.x) * per;
     int of[kPerThread], L[kPerThread];
-    unsigned need = 0, runs = 0, t0, t1;
+    Parent parent[kPerThread];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) of[i] = i < per && s0 + i < S ? __ldcg(p.choice + s0 + i) : -1;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        of[i] = parent_of(p, of[i], rank == 0, L[i]);
-        need += unsigned(by.blocks(L[i]) - by.quotient(L[i]));
-    }
-    block_scan(need, runs, t0, t1, warp_sums);         // (no runs yet)
-    const unsigned needed = min(t0, unsigned(count));
-    unsigned nth = need;
+    for (int i = 0; i < kPerThread; ++i) parent[i].read(p, of[i]);
+    const int count = free_blocks_of(p, on_stack, rank == 0 && threadIdx.x == 0);
+    unsigned need = 0, runs = 0, t0, t1;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-        const int full = by.quotient(L[i]);
+        of[i] = parent[i].check(p, of[i], rank == 0, L[i]);
+        need += unsigned(by.blocks(L[i]) - by.quotient(L[i]));
+        runs += runs_of(by.quotient(L[i]));
+    }
+    block_scan(need, runs, t0, t1, warp_sums);
+    // A child's started block: which one it gets, and what it is a copy of. (The
+    // blocks take turns with the sequences.)
+    int id[kPerThread], source[kPerThread];
+    unsigned nth = need, granted = 0, granted_runs = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int full = by.quotient(L[i]), s = s0 + i;
         const bool started = by.blocks(L[i]) > full;
-        const int s = s0 + i;
         const bool go = of[i] >= 0 && (!started || nth < unsigned(count));
-        // (the blocks take turns with the sequences)
-        if (i < per && s < S && unsigned(s) % gridDim.x == rank) {
-            int2 pair = make_int2(0, 0);
-            if (go && started) {
-                const int id = __ldcg(p.free_blocks + (count - 1 - int(nth)));
-                const int from = __ldcg(p.block_tables + size_t(of[i]) * p.max_blocks + full);
-                if (id < 0 || id >= p.num_blocks || from < 0 || from >= p.num_blocks)
-                    atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
-                else pair = make_int2(from, id);
-                p.block_tables[size_t(s) * p.max_blocks + full] = id;
-            }
-            reinterpret_cast<int2 *>(p.block_pairs)[s] = pair;
-            if (go) p.context_lens_out[s] = L[i];
-            else if (p.context_lens_out != p.context_lens) p.context_lens_out[s] = __ldcg(p.context_lens + s);
+        id[i] = source[i] = 0;
+        if (go && started && unsigned(s) % gridDim.x == rank) {
+            id[i] = __ldcg(p.free_blocks + (count - 1 - int(nth)));
+            source[i] = __ldcg(p.block_tables + size_t(of[i]) * p.max_blocks + full);
         }
         if (started) ++nth;
-        L[i] = go ? full : 0;                          // entries to copy, from here on
-        runs += unsigned(L[i] + kRun - 1) / kRun;
+        if (go) {
+            granted |= 1u << i;
+            granted_runs += runs_of(full);
+        }
     }
-    unsigned zero = 0;
-    block_scan(runs, zero, t0, t1, warp_sums);
+    const unsigned needed = min(t0, unsigned(count));
+    if (t0 > unsigned(count)) {            // not all of them are granted
+        unsigned zero = 0, t;
+        runs = granted_runs;
+        block_scan(runs, zero, t1, t, warp_sums);
+    }
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         if (i < per && s0 + i < S) {
+            const int entries = (granted >> i) & 1u ? by.quotient(L[i]) : 0;
             r.run0[s0 + i] = int(runs);
-            r.count[s0 + i] = L[i];
-            r.of[s0 + i] = uint16_t(of[i]);
-            runs += unsigned(L[i] + kRun - 1) / kRun;
+            r.count[s0 + i] = entries;
+            r.from[s0 + i] = of[i];
+            runs += runs_of(entries);
         }
     }
-    if (threadIdx.x == 0) r.run0[S] = int(t0);
+    if (threadIdx.x == 0) r.run0[S] = int(t1);
     __syncthreads();
     if (totals && rank == 0 && threadIdx.x == 0) *p.free_count_out = count - int(needed);
     const int lane = threadIdx.x & 31;
-    for_runs(r, S, int(t0), [&](int s, int first, int left) {
-        const int32_t *src = p.block_tables + size_t(r.of[s]) * p.max_blocks + first + lane;
+    for_runs(r, S, int(t1), [&](int s, int first, int left) {
+        const int32_t *src = p.block_tables + size_t(r.from[s]) * p.max_blocks + first + lane;
         int32_t *dst = p.block_tables + size_t(s) * p.max_blocks + first + lane;
         int id[kRun / 32];
 #pragma unroll
@@ -172,6 +184,22 @@ __global__ void __launch_bounds__(kMaxThreads) fork_kernel(const __grid_constant
             else atomicAdd(p.shared + id[i], 1);
         }
     });
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int s = s0 + i, full = by.quotient(L[i]);
+        if (i >= per || s >= S || unsigned(s) % gridDim.x != rank) continue;
+        const bool go = (granted >> i) & 1u;
+        int2 pair = make_int2(0, 0);
+        if (go && by.blocks(L[i]) > full) {
+            if (id[i] < 0 || id[i] >= p.num_blocks || source[i] < 0 || source[i] >= p.num_blocks)
+                atomicOr(p.err, PAGEDKV_DEVERR_BLOCK_ID);
+            else pair = make_int2(source[i], id[i]);
+            p.block_tables[size_t(s) * p.max_blocks + full] = id[i];
+        }
+        reinterpret_cast<int2 *>(p.block_pairs)[s] = pair;
+        if (go) p.context_lens_out[s] = L[i];
+        else if (p.context_lens_out != p.context_lens) p.context_lens_out[s] = __ldcg(p.context_lens + s);
+    }
 }
 
 // The count after a fork, in place: how many started blocks were copied.
@@ -182,7 +210,10 @@ __global__ void __launch_bounds__(kMaxThreads) fork_total_kernel(const __grid_co
     int taken = 0;
     for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
         int L;
-        parent_of(p, __ldcg(p.choice + s), false, L);
+        const int of = __ldcg(p.choice + s);
+        Parent parent;
+        parent.read(p, of);
+        parent.check(p, of, false, L);
         taken += by.blocks(L) - by.quotient(L);
     }
     taken = __reduce_add_sync(kAllLanes, taken);
@@ -190,7 +221,7 @@ __global__ void __launch_bounds__(kMaxThreads) fork_total_kernel(const __grid_co
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < int(blockDim.x >> 5); ++w) taken += sums[w];
-        const int count = free_blocks_of(p, false);
+        const int count = free_blocks_of(p, __ldcg(p.free_count), false);
         *p.free_count_out = count - min(taken, count);
     }
 }
@@ -221,7 +252,7 @@ __device__ __forceinline__ void drop_holders(const PagesParams &p, int *memory, 
             if (blockIdx.x == 0) atomicOr(p.err, PAGEDKV_DEVERR_CONTEXT_LEN);
             keep[i] = L[i] = 0;
         }
-        runs += unsigned(by.blocks(L[i]) - by.blocks(keep[i]) + kRun - 1) / kRun;
+        runs += runs_of(by.blocks(L[i]) - by.blocks(keep[i]));
     }
     block_scan(runs, zero, t0, t1, warp_sums);
 #pragma unroll
@@ -230,16 +261,15 @@ __device__ __forceinline__ void drop_holders(const PagesParams &p, int *memory, 
             const int given = by.blocks(L[i]) - by.blocks(keep[i]);
             r.run0[s0 + i] = int(runs);
             r.count[s0 + i] = given;
-            runs += unsigned(given + kRun - 1) / kRun;
+            r.from[s0 + i] = by.blocks(keep[i]);
+            runs += runs_of(given);
         }
     }
     if (threadIdx.x == 0) r.run0[S] = int(t0);
     __syncthreads();
     const int lane = threadIdx.x & 31;
     for_runs(r, S, int(t0), [&](int s, int first, int left) {
-        // (its last r.count[s] entries)
-        const int end = by.blocks(__ldcg(p.context_lens + s));
-        const int32_t *src = p.block_tables + size_t(s) * p.max_blocks + (end - left) + lane;
+        const int32_t *src = p.block_tables + size_t(s) * p.max_blocks + r.from[s] + first + lane;
         int id[kRun / 32];
 #pragma unroll
         for (int i = 0; i < kRun / 32; ++i) id[i] = 32 * i + lane < left ? __ldcg(src + 32 * i) : 0;
@@ -282,10 +312,14 @@ __device__ __forceinline__ void push(const PagesParams &p, uint32_t *words) {
     __shared__ int warp_sums[32], total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = kCluster ? kPushCtas : 1, rank = kCluster ? int(cluster_rank()) : 0;
-    const int count = free_blocks_of(p, rank == 0 && threadIdx.x == 0);
-    for (int s = rank * kMaxThreads + int(threadIdx.x); s < p.num_seqs; s += ctas * kMaxThreads) {
-        const int L = __ldcg(p.context_lens + s), keep = kept(p, L, __ldcg(p.choice + s));
-        p.context_lens_out[s] = keep < 0 ? L : keep;
+    const int on_stack = __ldcg(p.free_count);
+    constexpr int kSeqs = kCluster ? 1 : kPerThread;         // of a thread
+    int L[kSeqs], keep[kSeqs];
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+        const int s = (rank * kSeqs + i) * kMaxThreads + int(threadIdx.x);
+        L[i] = s < p.num_seqs ? __ldcg(p.context_lens + s) : 0;
+        keep[i] = s < p.num_seqs ? __ldcg(p.choice + s) : 0;
     }
     // this warp's words: a bit for each block that is gone
     const int per = push_words(p.num_blocks, ctas), w0 = (rank * 32 + warp) * per;
@@ -307,6 +341,13 @@ __device__ __forceinline__ void push(const PagesParams &p, uint32_t *words) {
         }
     }
     if (lane == 0) warp_sums[warp] = gone;
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+        const int s = (rank * kSeqs + i) * kMaxThreads + int(threadIdx.x);
+        const int k = kept(p, L[i], keep[i]);
+        if (s < p.num_seqs) p.context_lens_out[s] = k < 0 ? L[i] : k;
+    }
+    const int count = free_blocks_of(p, on_stack, rank == 0 && threadIdx.x == 0);
     __syncthreads();
     const int sum = warp_sums[lane], all = __reduce_add_sync(kAllLanes, sum);
     int at = __reduce_add_sync(kAllLanes, lane < warp ? sum : 0);   // pushed by the warps before this one
@@ -376,12 +417,17 @@ void shape(const PagesParams &p, int num_sms, int &threads, int &blocks) {
 }  // namespace
 
 cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
-    int threads, blocks;
+    int threads, blocks, dev = 0;
     shape(p, num_sms, threads, blocks);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
+    e = open_dynamic_smem(opened, dev, fork_kernel, runs_bytes(p.num_seqs));
+    if (e != cudaSuccess) return e;
     const bool totals = blocks == 1 || p.free_count_out != p.free_count;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = config(attr, blocks, threads, runs_bytes(p.num_seqs), st);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fork_kernel, p, totals);
+    e = cudaLaunchKernelEx(&cfg, fork_kernel, p, totals);
     if (e != cudaSuccess || totals) return e;
     cfg = config(attr, 1, p.num_seqs > 256 ? kMaxThreads : 256, 0, st);
     return cudaLaunchKernelEx(&cfg, fork_total_kernel, p);
@@ -390,18 +436,20 @@ cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
 cudaError_t launch_release(const PagesParams &p, int num_sms, cudaStream_t st) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg;
-    int threads, blocks;
+    int threads, blocks, dev = 0;
     shape(p, num_sms, threads, blocks);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<unsigned long long> opened_runs[kLaunchCacheDevices];
+    e = open_dynamic_smem(opened_runs, dev, release_kernel, runs_bytes(p.num_seqs));
+    if (e != cudaSuccess) return e;
     cfg = config(attr, blocks, threads, runs_bytes(p.num_seqs), st);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, release_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, release_kernel, p);
     if (e != cudaSuccess) return e;
     if (p.num_blocks <= kSmallBlocks) {
         cfg = config(attr, 1, kMaxThreads, 4 * 32 * push_words(p.num_blocks, 1), st);
         return cudaLaunchKernelEx(&cfg, push_kernel<false>, p);
     }
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     const int smem = 4 * 32 * push_words(p.num_blocks, kPushCtas);
     static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
     e = open_dynamic_smem(opened, dev, push_kernel<true>, smem);
