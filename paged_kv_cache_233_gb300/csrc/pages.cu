@@ -414,15 +414,23 @@ void shape(const PagesParams &p, int num_sms, int &threads, int &blocks) {
     blocks = int(want < 1 ? 1 : want < num_sms ? want : num_sms);
 }
 
+// Beyond 48 KB, static part included, a block's shared memory has to be asked for (more
+// than 4000 rows or so; the question costs the host time).
+template <typename Kernel>
+cudaError_t open_runs(std::atomic<unsigned long long> *opened, Kernel kernel, int smem) {
+    if (smem <= 47 * 1024) return cudaSuccess;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : open_dynamic_smem(opened, dev, kernel, smem);
+}
+
 }  // namespace
 
 cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
-    int threads, blocks, dev = 0;
+    int threads, blocks;
     shape(p, num_sms, threads, blocks);
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
-    e = open_dynamic_smem(opened, dev, fork_kernel, runs_bytes(p.num_seqs));
+    cudaError_t e = open_runs(opened, fork_kernel, runs_bytes(p.num_seqs));
     if (e != cudaSuccess) return e;
     const bool totals = blocks == 1 || p.free_count_out != p.free_count;
     cudaLaunchAttribute attr[1];
@@ -436,12 +444,10 @@ cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
 cudaError_t launch_release(const PagesParams &p, int num_sms, cudaStream_t st) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg;
-    int threads, blocks, dev = 0;
+    int threads, blocks;
     shape(p, num_sms, threads, blocks);
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     static std::atomic<unsigned long long> opened_runs[kLaunchCacheDevices];
-    e = open_dynamic_smem(opened_runs, dev, release_kernel, runs_bytes(p.num_seqs));
+    cudaError_t e = open_runs(opened_runs, release_kernel, runs_bytes(p.num_seqs));
     if (e != cudaSuccess) return e;
     cfg = config(attr, blocks, threads, runs_bytes(p.num_seqs), st);
     e = cudaLaunchKernelEx(&cfg, release_kernel, p);
@@ -450,6 +456,9 @@ cudaError_t launch_release(const PagesParams &p, int num_sms, cudaStream_t st) {
         cfg = config(attr, 1, kMaxThreads, 4 * 32 * push_words(p.num_blocks, 1), st);
         return cudaLaunchKernelEx(&cfg, push_kernel<false>, p);
     }
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     const int smem = 4 * 32 * push_words(p.num_blocks, kPushCtas);
     static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
     e = open_dynamic_smem(opened, dev, push_kernel<true>, smem);
