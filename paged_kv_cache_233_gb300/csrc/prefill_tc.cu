@@ -162,7 +162,15 @@ constexpr int kDone = 2 * kTcStages + kPerTileBars * kTcTiles;
 // (one phase per such use of the stage: it is not reused before the stage
 // completes and both issuers have released it)
 constexpr int kTailV = kDone + 1;
-constexpr int kNumBars = kTailV + kTcStages;
+// 8-bit pools of head size 128: a stage's K and V are filled and freed apart, K on the
+// stage's own full barrier. V of key tile j is read two key tiles after K is, so with one
+// barrier for both K's place, and the four warps that fill it, wait for the P V: with
+// three stages that leaves them a single key tile's time (2048 rows after 16384 tokens 513
+// us, apart 458, fp16 487 and 451; with the four stages of head size 64, where they
+// are not behind, 374 and 388: an issuer's third wait costs more than it gives)
+constexpr int kVFull = kTailV;
+constexpr int kKFree = kTailV + kTcStages;
+constexpr int kNumBars = kKFree + kTcStages;
 // key split: the CTAs share the call's key tiles (all items' tiles end to end)
 // in equal contiguous ranges of r tiles, r at least min(kMinPartTiles, the
 // longest item) so that an item is not cut into pieces shorter than that
@@ -186,6 +194,7 @@ template <int D, int kBits>
 struct TcLayout {
     // (8-bit tiles of head size 128 leave room for three stages beside their raw ring)
     static constexpr int kStages = kBits == 8 && D == 128 ? 3 : kTcStages;
+    static constexpr bool kApart = kBits == 8 && D == 128;     // K and V of a stage are
     static constexpr int kRawStages = kBits == 8 ? 3 : 2;      // the raw ring
     static constexpr int kSlabs = D * 2 / 128;             // 64-element column blocks per row
     static constexpr int kQSlab = kTcRows * 128;           // bytes of one Q column block
@@ -206,14 +215,18 @@ struct TcLayout {
     static constexpr int kOutRow = kOrder + 8 * kMaxRankedSeqs;
     static constexpr int kRefRow = kOutRow + 8 * kTcTiles * kTcRows;
     static constexpr int kTotal = kRefRow + 4 * kTcTiles * kTcRows;
-    // 8-bit pools, per stage: what turns the tile's sums into scores, V's exponent, the
+    // 8-bit pools, per key tile: what turns the tile's sums into scores, V's exponent, the
     // inverse of V's scale, whether a key is marked as holding a NaN; then a bit for each
-    // key whose K, and whose V, is
+    // key whose K, and whose V, is. Written with K of the tile, when S of kStages tiles
+    // before is complete, whose issue came after the P of two tiles before that: the
+    // softmax may still read the scales of the tiles behind it
     static constexpr int kScales = (kTotal + 15) & ~15;
-    static constexpr int kScalesStage = 16 + 2 * kTcKeys / 8;
+    static constexpr int kScalesTile = 16 + 2 * kTcKeys / 8;
+    static constexpr int kScalesRing = 8;
+    static_assert(kScalesRing >= kStages + 2, "a tile's scales outlive its stage");
     // 4- and 8-bit pools: the raw ring's barriers (full, empty), then its tiles: K's
     // blocks, V's (8-bit: with the scales behind the codes, blocks of 8 have the most)
-    static constexpr int kRawBars = kScales + (kBits == 8 ? kStages * kScalesStage : 0);
+    static constexpr int kRawBars = kScales + (kBits == 8 ? kScalesRing * kScalesTile : 0);
     static constexpr int kRaw = kRawBars + 16 * kRawStages;
     static constexpr int kRawHalf = kBits == 8 ? kTcKeys / 8 * q8_head_bytes(8, D) : kTcKeys * D * 5 / 8;
     static constexpr int kTotalPacked = kRaw + kRawStages * 2 * kRawHalf;
@@ -561,7 +574,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             mbar_init(bar(bar_qfree(t)), 1);
         }
         mbar_init(bar(kDone), kTcTiles);
-        for (int k = 0; k < kStages; ++k) mbar_init(bar(kTailV + k), 1);
+        for (int k = 0; k < kStages; ++k) {
+            mbar_init(bar(kTailV + k), Ly::kApart ? kDqWarps : 1);
+            if (Ly::kApart) mbar_init(bar(kKFree + k), kTcTiles);   // one arrival per Q tile and key tile
+        }
         sts32(flag, 0);
         fence_barrier_init();
     }
@@ -732,6 +748,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     break;
                 }
                 tc_fence_after_sync();
+                // (S is complete: K's place is free as far as this Q tile goes)
+                if (Ly::kApart && (warp - softmax_warp0<kBits>()) % (kTcRows / 32) == 0 && lane == 0)
+                    mbar_arrive(bar(kKFree + (kt + j) % kStages));
                 float sc[kTcKeys];
                 tmem_ld64(trow + uint32_t(b * kTcKeys), sc);
                 const int k0 = (it.kb + j) * kTcKeys;   // absolute key index of the tile's first key
@@ -740,7 +759,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
                 }
                 // 8-bit pools: the tile's factor, V's exponent, the inverse of its scale, marks
-                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % kStages) * Ly::kScalesStage);
+                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % Ly::kScalesRing) * Ly::kScalesTile);
                 const uint4 of8 = kBits == 8 ? lds128_u4(tile) : make_uint4(0u, 0u, 0u, 0u);
                 const float factor = kBits == 8 ? __uint_as_float(of8.x) : p.scale_log2;
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1149,8 +1168,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         const uint32_t src = uint32_t(blk * hb + (off + odd * B) * 16), scale = uint32_t(some * hb + q8_scale_at(B, D));
         const uint32_t step = uint32_t(2 * B * 16);               // between this lane's panels
         const uint32_t dst = base + Ly::kKv + uint32_t(row * 128 + ((row & 7) << 4));
-        int rs = 0, st = 0;                                       // raw slot and stage, and their phases
-        uint32_t rphase = 0, sphase = 1;
+        int rs = 0, st = 0, ring = 0;                             // raw slot, stage, place of the scales; the
+        uint32_t rphase = 0, sphase = 1;                          // slot's and the stage's phases
         bool ok = true;
         for (int m = 0; ok; ++m) {
             const int k = pf_item_index<kSplit>(m);
@@ -1161,18 +1180,15 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll 1
             for (int x = it.nkt; x > 0; --x) {
                 const uint32_t rfull = base + Ly::kRawBars + 16 * rs, raw = base + Ly::kRaw + uint32_t(rs * 2 * Ly::kRawHalf);
-                // the raw tile is there, and the stage's last readers are done
-                bool got = mbar_try_wait(rfull, rphase);
-                got = mbar_try_wait(bar(kKvEmpty + st), sphase) && got;
-                if (!__all_sync(kAll, got)) {
-                    got = !aborted() && mbar_wait(rfull, rphase, p.err) && mbar_wait(bar(kKvEmpty + st), sphase, p.err);
-                    if (!__all_sync(kAll, got)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                float factor = 0.f;      // of the tile's sums
-                bool any_k = false;      // a key of it is marked in K
+                auto ready = [&](uint32_t place) {     // the raw tile is there, and the place's last readers are done
+                    bool got = mbar_try_wait(rfull, rphase);
+                    got = mbar_try_wait(place, sphase) && got;
+                    if (__all_sync(kAll, got)) return true;
+                    got = !aborted() && mbar_wait(rfull, rphase, p.err) && mbar_wait(place, sphase, p.err);
+                    return __all_sync(kAll, got) != 0;
+                };
+                ok = ready(bar((Ly::kApart ? kKFree : kKvEmpty) + st));
+                if (!ok) break;
                 uint2 info[2];
                 uint4 cw[2][D / 32];
 #pragma unroll
@@ -1182,18 +1198,38 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) cw[o][i] = lds128_u4(from + src + uint32_t(i) * step);
                 }
+                // The tile's keys under one scale, 2^6 below their blocks' largest (448 *
+                // 2^6 is in fp16's range): a power of two takes each code there, exactly
+                // unless its block's scale is more than 2^21 below the largest.
+                const bool there = x > 1 || some * B < past;    // (a block past the context has no scale)
+                const bool live = x > 1 || row < past;
+                int e[2], most[2];
+                bool any[2];                                    // a key of the tile is marked
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    e[o] = there ? min(max(int((info[o].x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp) : kQ8LeastExp;
+                    most[o] = __reduce_max_sync(kAll, e[o]);
+                    any[o] = __any_sync(kAll, there && info[o].y != 0) != 0;
+                }
+                const uint32_t scales = base + Ly::kScales + uint32_t(ring * Ly::kScalesTile);
+                if (any[0] || any[1]) {
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const uint32_t mine = __shfl_sync(kAll, info[o].y, blk) >> off;
+                        const unsigned marked = __ballot_sync(kAll, live && (mine & 1u)) & 0xffffu;
+                        if (lane == 0) sts16(scales + uint32_t(16 + 8 * o + 2 * w), marked);
+                    }
+                }
+                // (a factor of 0 would turn a masked score's -inf into a NaN)
+                if (w == 0 && lane == 0)
+                    sts128(scales, make_uint4(__float_as_uint(fmaxf(fabsf(p.scale_log2) * q8_power(most[0] - 6), 0x1p-126f)),
+                                              __float_as_uint(float(most[1] - 6)), __float_as_uint(q8_power(6 - most[1])),
+                                              any[0] || any[1] ? 1u : 0u));
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const bool of_v = o == 1;
-                    // The tile's keys under one scale, 2^6 below their blocks' largest (448 *
-                    // 2^6 is in fp16's range): a power of two takes each code there, exactly
-                    // unless its block's scale is more than 2^21 below the largest.
-                    const bool there = x > 1 || some * B < past;    // (a block past the context has no scale)
-                    const int e = there ? min(max(int((info[o].x >> 23) & 255u) - 127, kQ8LeastExp), kQ8MostExp) : kQ8LeastExp;
-                    const int most = __reduce_max_sync(kAll, e);
-                    const bool any = __any_sync(kAll, there && info[o].y != 0) != 0;
                     // (bf16's K leaves its conversion at 2^-120 of the code, and loses nothing)
-                    const int down = __shfl_sync(kAll, e, blk) - most;
+                    const int down = __shfl_sync(kAll, e[o], blk) - most[o];
                     const float power = q8_power(kBf16 && !of_v ? down + 126 : max(down, -30) + 6);
                     const uint32_t by = kBf16 && !of_v ? Elem<__nv_bfloat16>::pack2(power, power) : pack_half2(power);
                     const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
@@ -1228,15 +1264,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                             put(i, v);
                         }
                     };
-                    if (x == 1 || any || (of_v && any_k)) {
-                        const bool live = x > 1 || row < past;
-                        const uint32_t mine = __shfl_sync(kAll, info[o].y, blk) >> off;
-                        const unsigned marked = __ballot_sync(kAll, live && (mine & 1u)) & 0xffffu;
-                        if (lane == 0) {
-                            const uint32_t at = base + Ly::kScales + uint32_t(st * Ly::kScalesStage + 16 + 2 * w);
-                            sts16(at + (of_v ? 8u : 0u), marked);
-                            if (of_v && x > 1 && !any_k) sts16(at, 0u);    // (K's run wrote none)
-                        }
+                    if (Ly::kApart && of_v) {
+                        ok = ready(bar(kKvEmpty + st));
+                        if (!ok) break;
+                    }
+                    if (x == 1 || any[o]) {
 #pragma unroll 1
                         for (int i = 0; i < D / 32; ++i) {
                             const uint4 c = lds128_u4(raw + uint32_t(o * Ly::kRawHalf) + src + uint32_t(i) * step);
@@ -1259,22 +1291,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     } else {
                         plain(std::false_type{});
                     }
-                    if (!of_v) {
-                        // (a factor of 0 would turn a masked score's -inf into a NaN)
-                        factor = fmaxf(fabsf(p.scale_log2) * q8_power(most - 6), 0x1p-126f);
-                        any_k = any;
-                    } else if (w == 0 && lane == 0) {
-                        sts128(base + Ly::kScales + uint32_t(st * Ly::kScalesStage),
-                               make_uint4(__float_as_uint(factor), __float_as_uint(float(most - 6)),
-                                          __float_as_uint(q8_power(6 - most)), any || any_k ? 1u : 0u));
+                    if (!Ly::kApart && !of_v) continue;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (of_v) mbar_arrive(rfull + 8);
+                        mbar_arrive(bar((Ly::kApart && of_v ? kVFull : kKvFull) + st));
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(rfull + 8);
-                    mbar_arrive(bar(kKvFull + st));
-                }
+                if (!ok) break;
+                ring = (ring + 1) % Ly::kScalesRing;
                 if (++rs == kRawStages) {
                     rs = 0;
                     rphase ^= 1u;
@@ -1396,9 +1422,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const int gk2 = gk + 2;
                         const int pb = bar_p(t, (jt + j) & 1), kb = kKvFull + gk2 % kStages;
                         bool got = mbar_try_wait(bar(pb), uint32_t(((jt + j) >> 1) & 1));
+                        if (Ly::kApart) got = mbar_try_wait(bar(kVFull + gk % kStages), uint32_t((gk / kStages) & 1)) && got;
                         const bool landed = ahead && mbar_test_wait(bar(kb), uint32_t((gk2 / kStages) & 1));
                         if (!__all_sync(kAll, got)) {
                             got = !aborted() && mbar_wait(bar(pb), uint32_t(((jt + j) >> 1) & 1), p.err);
+                            if (Ly::kApart) got = got && mbar_wait(bar(kVFull + gk % kStages), uint32_t((gk / kStages) & 1), p.err);
                             ok = __all_sync(kAll, got);
                             if (!ok) break;
                         }
@@ -1427,6 +1455,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         // after it landed (the arrival belongs to this phase of the slot)
                         ok = wait(kKvFull + gk % kStages, gk / kStages);
                         if (!ok) break;
+                        if (Ly::kApart) {
+                            if (leader) mbar_arrive(bar(kKFree + gk % kStages));
+                            ok = wait(kVFull + gk % kStages, gk / kStages);
+                            if (!ok) break;
+                        }
                         commit(kKvEmpty + gk % kStages);
                     }
                 }
