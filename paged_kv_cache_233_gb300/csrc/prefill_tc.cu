@@ -750,7 +750,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 tc_fence_after_sync();
                 // (S is complete: K's place is free as far as this Q tile goes)
                 if (Ly::kApart && (warp - softmax_warp0<kBits>()) % (kTcRows / 32) == 0 && lane == 0)
-                    mbar_arrive(bar(kKFree + (kt + j) % kStages));
+                    mbar_arrive(bar(kKFree + int(uint32_t(kt + j) % uint32_t(kStages))));
                 float sc[kTcKeys];
                 tmem_ld64(trow + uint32_t(b * kTcKeys), sc);
                 const int k0 = (it.kb + j) * kTcKeys;   // absolute key index of the tile's first key
@@ -759,7 +759,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     for (int x = 0; x < kTcKeys; ++x) sc[x] = k0 + x <= pos ? sc[x] : -INFINITY;
                 }
                 // 8-bit pools: the tile's factor, V's exponent, the inverse of its scale, marks
-                const uint32_t tile = base + Ly::kScales + uint32_t(((kt + j) % Ly::kScalesRing) * Ly::kScalesTile);
+                const uint32_t tile = base + Ly::kScales + uint32_t(kt + j) % uint32_t(Ly::kScalesRing) * uint32_t(Ly::kScalesTile);
                 const uint4 of8 = kBits == 8 ? lds128_u4(tile) : make_uint4(0u, 0u, 0u, 0u);
                 const float factor = kBits == 8 ? __uint_as_float(of8.x) : p.scale_log2;
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
