@@ -53,19 +53,19 @@ bool finite(float x) { return x == x && x != INFINITY && x != -INFINITY; }
 //                                        4 bits                    8 bits
 //                                   128         64            128         64
 //   one sequence
-//     rows 33, cached 1000        24 / 19     21 / 15       24 / 19     20 / 15
-//     33, 6001                   103 / 25     96 / 18      104 / 24     89 / 18
-//     1216, 8192 (152 items)     143 / 173   129 / 138     148 / 187   115 / 134
-//     1280, 8192 (160)           248 / 179   220 / 144     264 / 196   199 / 140
-//     2048, 2048 (256)            98 / 131    86 / 103     104 / 144    78 / 100
-//     2048, 16384                506 / 473   458 / 385     541 / 515   405 / 375
+//     rows 33, cached 1000        24 / 19     21 / 15       23 / 18     20 / 15
+//     33, 6001                   103 / 25     96 / 18       98 / 24     87 / 18
+//     1216, 8192 (152 items)     143 / 173   129 / 138     134 / 166   115 / 134
+//     1280, 8192 (160)           248 / 179   220 / 144     234 / 173   197 / 140
+//     2048, 2048 (256)            98 / 131    86 / 103      94 / 130    77 / 100
+//     2048, 16384                506 / 473   458 / 385     479 / 454   404 / 375
 //   4 of 64 rows, contexts evenly
-//     up to 500                   16 / 21     13 / 16       17 / 22     13 / 16
-//     up to 4000                  65 / 37     58 / 26       67 / 37     52 / 25
+//     up to 500                   16 / 21     13 / 16       15 / 21     13 / 16
+//     up to 4000                  65 / 37     58 / 26       61 / 37     52 / 25
 //   20 of 64 rows (160 items)
-//     up to 1000                  26 / 62     22 / 46       27 / 60     21 / 44
-//     up to 4000                  69 / 97     60 / 69       70 / 94     55 / 64
-//     all of 4000                157 / 124   118 / 84      139 / 115   104 / 82
+//     up to 1000                  26 / 62     22 / 46       25 / 60     21 / 44
+//     up to 4000                  69 / 97     60 / 69       65 / 94     55 / 66
+//     all of 4000                157 / 124   118 / 84      125 / 104   104 / 81
 bool split_pays(long long items, long long tiles, int seqs, int sms) {
     const long long rounds = seqs > 1 ? 1 : (items + sms - 1) / sms;
     const double gain = double(rounds * tiles) - double(items * tiles) / sms;

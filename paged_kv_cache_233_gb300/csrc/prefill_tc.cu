@@ -74,22 +74,24 @@
 // in both types (e4m3 codes are exact in fp16, not every scale's product is). A
 // key whose row holds a NaN is zeroed in the stage, and the rows that attend to it get
 // a sum of NaN. In bf16 K's codes become bf16 by moving bits (a conversion by way of
-// fp32 took 2% longer). The softmax's warps take registers from the others (below),
-// and at head size 128 the raw ring leaves room for three stages, not four.
+// fp32 took 2% longer). The softmax's warps take registers from the others (below).
+// At head size 128 the raw ring leaves room for three stages, not four, whose K and V
+// are filled and freed apart.
 //
 // Measured (us, TFLOP/s; 8 kv heads, 32 query heads, bf16; a large bf16 product runs
 // at 1919 TFLOP/s, which bounds the first row at 304 us):
 //                                       4 bits        8 bits        16 bits
 //     2048 rows after 16384 tokens
-//         heads of 128                  473  1235     515  1134     542  1079 (unsplit)
-//         heads of 64                   385   759     375   779     395   740 (unsplit)
+//         heads of 128                  473  1235     455  1285     540  1082 (unsplit)
+//         heads of 64                   385   759     376   777     395   740 (unsplit)
 //     1216 rows after 8192, 152 items, unsplit
-//         heads of 128                  144  1222     148  1185     153  1145
+//         heads of 128                  143  1228     134  1305     151  1160
 //         heads of 64                   129   679     115   761     112   783
 //     33 rows after 6001, split         25             24            31
-// (8 bits, fp16: 488 in the first row. 49% of the tensor pipe's cycles and 53% of the issue
-// slots are used, 25% of the exp2 unit: the two Q tiles' softmaxes, key tile by key tile,
-// and the issuers' hand-overs leave the tensor pipe idle in between.)
+// (8 bits, fp16: 447 in the first row. In 8 bits 57% of the tensor pipe's cycles, 60% of
+// the issue slots and 29% of the exp2 unit's are used: the two Q tiles' softmaxes, key
+// tile by key tile, and the issuers' hand-overs leave the tensor pipe idle in between.
+// With three quarters of the dequantising left out 420 us: that is what is left of it.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
