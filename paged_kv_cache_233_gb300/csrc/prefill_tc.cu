@@ -827,6 +827,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (lane == 0) mbar_arrive(bar(bar_p(t, b)));
             }
             if (!ok) break;
+            // 8-bit pools: a row that has met a key and has no maximum met -inf alone (an
+            // infinite query, or scores past fp32): no weights, and a sum of NaN
+            if (kBits == 8 && ref == -INFINITY && it.kb * kTcKeys <= pos) l = __int_as_float(0x7fffffff);
             prev_nk = nk;
             prev_jend = jt + nk;
             prev_l = l;
