@@ -705,9 +705,10 @@ int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_
  * the values that the codes stand for; a probability times its token's V scale is
  * rounded to fp16, relative to a running maximum as in the decode; scores, softmax
  * statistics and output sums are fp32. The blocks that hold 64 neighbouring tokens are
- * brought to one scale, exactly unless one's scale is 2^21 and more below the largest
- * (its values then lose bits; K of bf16 calls none). Arguments, limits, workspace and key_parts as
- * paged_attention_prefill_q4's. In bf16 caches values of V may be 2^70 at most. A
+ * brought to one scale, exactly unless one's scale is more than 2^21 below the largest:
+ * its values are then rounded to multiples of 2^-30 of that scale, and count as zeros where
+ * it is more than 2^30 below (K of bf16 calls loses nothing within 2^100). Arguments,
+ * limits, workspace and key_parts as paged_attention_prefill_q4's. In bf16 caches values of V may be 2^70 at most. A
  * NaN or an infinity in a row of q makes that row's outputs of the head NaN; a token
  * that is marked as holding a NaN, in K or in V, those of the rows that attend to it.
  */

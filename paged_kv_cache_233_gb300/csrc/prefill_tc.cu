@@ -1205,7 +1205,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
                 // The tile's keys under one scale, 2^6 below their blocks' largest (448 *
                 // 2^6 is in fp16's range): a power of two takes each code there, exactly
-                // unless its block's scale is more than 2^21 below the largest.
+                // unless its block's scale is more than 2^21 below the largest. (Past 2^30
+                // below it that power is below fp16's smallest number: zeros.)
                 const bool there = x > 1 || some * B < past;    // (a block past the context has no scale)
                 const bool live = x > 1 || row < past;
                 int e[2], most[2];
@@ -1235,7 +1236,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const bool of_v = o == 1;
                     // (bf16's K leaves its conversion at 2^-120 of the code, and loses nothing)
                     const int down = __shfl_sync(kAll, e[o], blk) - most[o];
-                    const float power = q8_power(kBf16 && !of_v ? down + 126 : max(down, -30) + 6);
+                    const float power = q8_power(kBf16 && !of_v ? down + 126 : max(down, -100) + 6);
                     const uint32_t by = kBf16 && !of_v ? Elem<__nv_bfloat16>::pack2(power, power) : pack_half2(power);
                     const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
                     auto put = [&](int i, const uint32_t (&v)[8]) {

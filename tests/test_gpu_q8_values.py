@@ -79,3 +79,81 @@ def test_an_infinite_query_is_nan(dtype, dim, block, n, chunk, sign):
         assert bool(out[bad[-1:]].isnan().all()), f"part {part}"
         q8.assert_near(out[~bad[-1:]], one[~bad[-1:]], dtype, 2, f"part {part}")
     assert pk.device_errors() == 0
+
+
+# --------------------------------------------------- scales far apart in a key tile
+def spread_pool(n, heads, dim, block, tables, nb, far, seed, least):
+    """A pool of random codes whose blocks' scales are 2^least and 2^(least - far) in turn."""
+    pool = q8.new_pool(nb, heads, block, dim, seed)
+    codes, scale, mark = q8.views(pool, dim)
+    g = torch.Generator().manual_seed(seed)
+    codes[:] = torch.randint(0, 256, codes.shape, generator=g, dtype=torch.int32).to(torch.uint8)
+    codes[(codes & 0x7f) == 0x7f] = 3
+    scale[:], mark[:] = 2.0 ** least, 0
+    scale[tables[0, 1::2].long()] = 2.0 ** (least - far)
+    return pool
+
+
+def as_staged(x, block, least, far):
+    """Rows [n][Hkv][D] of such a pool as a prefill documents them: multiples of 2^-30 of the
+    largest scale of 64 neighbouring tokens, those of scales more than 2^30 below it zeros."""
+    small = (torch.arange(len(x)) // block % 2 == 1)[:, None, None]
+    step = 2.0 ** (least - 30)
+    return torch.where(small, torch.round(x / step) * step if far <= 30 else torch.zeros_like(x), x)
+
+
+def softmax_rows(q, k, v, scale):
+    """fp64 causal attention of the chunk q [r][Hq][D] at the end of k, v [n][Hkv][D]."""
+    r, n, heads = len(q), len(k), k.shape[1]
+    z = torch.einsum("rhgd,khd->rhgk", q.double().unflatten(1, (heads, -1)), k.double()) * scale
+    seen = torch.arange(n)[None] <= torch.arange(n - r, n)[:, None]
+    w = torch.softmax(z.masked_fill(~seen[:, None, None], -math.inf), -1)
+    return torch.einsum("rhgk,khd->rhgd", w, v.double()).flatten(1, 2)
+
+
+@pytest.mark.parametrize("far", [20, 25, 30, 31, 40, 60])
+@pytest.mark.parametrize("dtype,dim,block", [(F16, 64, 8), (F16, 128, 32), (BF16, 128, 16), (BF16, 64, 8)])
+def test_scales_of_v_far_apart(dtype, dim, block, far):
+    """Rows that attend to the blocks of small values all but alone, and rows that attend to
+    all of them; each row on its own, since their outputs differ by orders of magnitude."""
+    n, chunk, heads, group = 150, 60, 2, 2
+    tables, nb = q8.tables_for([n], block, 4)
+    kc, vc = q8.new_pool(nb, heads, block, dim, 1), spread_pool(n, heads, dim, block, tables, nb, far, 2, 6)
+    k = rows((n, heads, dim), dtype, 3)
+    k[..., 0] = (torch.arange(n) // block % 2)[:, None].to(dtype)          # 1 in the blocks of small values
+    q8.fill(kc, tables[0], k)
+    q = rows((chunk, heads * group, dim), dtype, 5)
+    q[..., 0] = 0
+    q[::2, :, 0] = 2000.0
+    slots = q8.sequence_slots(tables, 0, n, block)
+    kx, vx = q8.read(kc, slots, dim), q8.read(vc, slots, dim)
+    ref = softmax_rows(q, kx, as_staged(vx, block, 6, far), dim ** -0.5)
+    for parts in (1, 32):
+        out = prefill(q, kc, vc, tables, [0, chunk], [n], dim ** -0.5, key_parts=parts)
+        for r in range(chunk):
+            q8.assert_near(out[r], ref[r], dtype, 2, f"parts {parts} row {r}")
+    assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("far", [20, 25, 31, 40, 60])
+@pytest.mark.parametrize("dtype,dim,block", [(F16, 64, 8), (F16, 128, 32), (BF16, 128, 16), (BF16, 64, 8)])
+def test_scales_of_k_far_apart(dtype, dim, block, far):
+    """Keys of small blocks count as documented in fp16, and as they are in bf16."""
+    n, chunk, heads, group, least = 150, 60, 2, 2, 7
+    tables, nb = q8.tables_for([n], block, 4)
+    kc, vc = spread_pool(n, heads, dim, block, tables, nb, far, 2, least), q8.new_pool(nb, heads, block, dim, 1)
+    codes = q8.views(kc, dim)[0]
+    codes[tables[0, ::2].long(), :, 0, :, 8:] = 0         # the large blocks' keys: channels 0 to 7 alone
+    codes[tables[0, ::2].long(), :, 1:] = 0
+    q8.fill(vc, tables[0], rows((n, heads, dim), dtype, 3))
+    # queries that see the small keys alone, as large as a type of 16 bits lets them be
+    size = min(2.0 ** (far - least - 4), 2.0 ** 14) if dtype == F16 else 2.0 ** (far - least - 4)
+    q = (rows((chunk, heads * group, dim), torch.float32, 5) * size / 4).to(dtype)
+    q[..., :8] = 0
+    slots = q8.sequence_slots(tables, 0, n, block)
+    kx, vx = q8.read(kc, slots, dim), q8.read(vc, slots, dim)
+    ref = softmax_rows(q, as_staged(kx, block, least, far) if dtype == F16 else kx, vx, dim ** -0.5)
+    for parts in (1, 32):
+        out = prefill(q, kc, vc, tables, [0, chunk], [n], dim ** -0.5, key_parts=parts)
+        q8.assert_near(out, ref, dtype, 2, f"parts {parts}")
+    assert pk.device_errors() == 0
