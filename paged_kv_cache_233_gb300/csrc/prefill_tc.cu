@@ -141,6 +141,8 @@ constexpr int kTmemTile = 256;   // tensor-memory columns per Q tile: S, S, O
 // small end
 template <int kBits> constexpr float move_past() { return kBits == 8 ? 14.f : 8.f; }
 template <int kBits> constexpr float below_max() { return kBits == 8 ? 6.f : 0.f; }
+// 8-bit pools in bf16: key tiles of scales up to 2^40 are held low (below)
+constexpr int kLowKeysExp = 40;
 
 // mbarrier indices
 constexpr int kKvFull = 0;
@@ -1217,6 +1219,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     most[o] = __reduce_max_sync(kAll, e[o]);
                     any[o] = __any_sync(kAll, there && info[o].y != 0) != 0;
                 }
+                // bf16's K lies lower, at 2^-16: 128 products of 448 * 2^-16 and bf16's largest
+                // query are within fp32. (Not where K is so large itself that its factor would
+                // pass fp32.)
+                const int up = kBf16 && most[0] <= kLowKeysExp ? -16 : 6;
                 const uint32_t scales = base + Ly::kScales + uint32_t(ring * Ly::kScalesTile);
                 if (any[0] || any[1]) {
 #pragma unroll
@@ -1226,9 +1232,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         if (lane == 0) sts16(scales + uint32_t(16 + 8 * o + 2 * w), marked);
                     }
                 }
-                // (a factor of 0 would turn a masked score's -inf into a NaN)
+                // (a factor of 0 would turn a masked score's -inf into a NaN; the smallest number
+                // leaves every score of a scale of 0 below 2^-21)
                 if (w == 0 && lane == 0)
-                    sts128(scales, make_uint4(__float_as_uint(fmaxf(fabsf(p.scale_log2) * q8_power(most[0] - 6), 0x1p-126f)),
+                    sts128(scales, make_uint4(__float_as_uint(fmaxf(fabsf(p.scale_log2) * q8_power(most[0] - up), 0x1p-149f)),
                                               __float_as_uint(float(most[1] - 6)), __float_as_uint(q8_power(6 - most[1])),
                                               any[0] || any[1] ? 1u : 0u));
 #pragma unroll
@@ -1236,7 +1243,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     const bool of_v = o == 1;
                     // (bf16's K leaves its conversion at 2^-120 of the code, and loses nothing)
                     const int down = __shfl_sync(kAll, e[o], blk) - most[o];
-                    const float power = q8_power(kBf16 && !of_v ? down + 126 : max(down, -100) + 6);
+                    const float power = q8_power(kBf16 && !of_v ? down + 120 + up : max(down, -100) + 6);
                     const uint32_t by = kBf16 && !of_v ? Elem<__nv_bfloat16>::pack2(power, power) : pack_half2(power);
                     const uint32_t to = dst + uint32_t(st * Ly::kStage) + (of_v ? uint32_t(Ly::kHalf) : 0u);
                     auto put = [&](int i, const uint32_t (&v)[8]) {

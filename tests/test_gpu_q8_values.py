@@ -157,3 +157,50 @@ def test_scales_of_k_far_apart(dtype, dim, block, far):
         out = prefill(q, kc, vc, tables, [0, chunk], [n], dim ** -0.5, key_parts=parts)
         q8.assert_near(out, ref, dtype, 2, f"parts {parts}")
     assert pk.device_errors() == 0
+
+
+# ------------------------------------------------------- the ends of bf16's range
+@pytest.mark.parametrize("size", [2.0 ** 90, 2.0 ** 108, 2.0 ** 113, 2.0 ** 118, 2.0 ** 124])
+@pytest.mark.parametrize("dim,block", [(64, 16), (128, 8)])
+def test_large_queries(dim, block, size):
+    """Queries of any size, and a scale that brings their scores back to ordinary ones."""
+    n, heads, group = 300, 2, 4
+    k, v = rows((n, heads, dim), BF16, 1, 2.0 ** -10), rows((n, heads, dim), BF16, 2)
+    kc, vc, tables = pools(k, v, block)
+    q = (rows((70, heads * group, dim), torch.float32, 3) * size).to(BF16)
+    scale = dim ** -0.5 * 2.0 ** 10 / size
+    ref = q8.attention(q, (kc, vc), tables, [0, 70], [n], scale, dim)
+    for parts in (1, 32):
+        q8.assert_near(prefill(q, kc, vc, tables, [0, 70], [n], scale, key_parts=parts), ref, BF16, 2, f"parts {parts}")
+    assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** 45, 2.0 ** 111])
+@pytest.mark.parametrize("dim,block", [(64, 16), (128, 8)])
+def test_large_keys(dim, block, size):
+    """Keys of any size, small ones beside them."""
+    n, heads, group = 300, 2, 4
+    k, v = rows((n, heads, dim), torch.float32, 1), rows((n, heads, dim), BF16, 2)
+    k[:200] *= size
+    kc, vc, tables = pools(k.to(BF16), v, block)
+    q = (rows((70, heads * group, dim), torch.float32, 3) / size).to(BF16)
+    scale = dim ** -0.5
+    ref = q8.attention(q, (kc, vc), tables, [0, 70], [n], scale, dim)
+    for parts in (1, 32):
+        q8.assert_near(prefill(q, kc, vc, tables, [0, 70], [n], scale, key_parts=parts), ref, BF16, 2, f"parts {parts}")
+    for part in (0, 64, pk.PARTITION_BALANCED):
+        q8.assert_near(decode(q[-1:], kc, vc, tables, [n], scale, part), ref[-1:], BF16, 2, f"part {part}")
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -126])
+@pytest.mark.parametrize("dim,block", [(64, 16), (128, 8)])
+def test_a_scale_of_none_with_large_queries(dim, block, scale):
+    """Every token the same weight."""
+    n, heads, group = 300, 2, 4
+    kc, vc, tables = pools(rows((n, heads, dim), BF16, 1, 2.0 ** -30), rows((n, heads, dim), BF16, 2), block)
+    q = (rows((70, heads * group, dim), torch.float32, 3) * 2.0 ** 124).to(BF16)
+    ref = q8.attention(q, (kc, vc), tables, [0, 70], [n], scale, dim)
+    for parts in (1, 32):
+        q8.assert_near(prefill(q, kc, vc, tables, [0, 70], [n], scale, key_parts=parts), ref, BF16, 2, f"parts {parts}")
+    for part in (0, 64, pk.PARTITION_BALANCED):
+        q8.assert_near(decode(q[-1:], kc, vc, tables, [n], scale, part), ref[-1:], BF16, 2, f"part {part}")
