@@ -550,7 +550,7 @@ int paged_kv_gather_q4(const void *k_cache, const void *v_cache, const int64_t *
  * Scores, softmax statistics and output sums are fp32 and out is rounded once.
  * Held in fewer bits on the way, each of them rounded once:
  *   - q in fp16, scaled by a power of two per row: exact but for elements below
- *     2^-17 (bf16: 2^-20) of the row's largest;
+ *     2^-17 (bf16: 2^-20) of the row's largest, or of 2^-97 where it is less;
  *   - the sum of a group's 32 channels of q in two parts of dtype (off by
  *     2^-22 of it, bf16: 2^-16);
  *   - a probability times a scale of V in fp16, relative to the largest such
@@ -683,7 +683,7 @@ int paged_kv_gather_q8(const void *k_cache, const void *v_cache, const int64_t *
  * Scores, softmax statistics and output sums are fp32 and out is rounded once.
  * Held in fewer bits on the way, each of them rounded once:
  *   - q in fp16, scaled by a power of two per row: exact but for elements below
- *     2^-24 (bf16: 2^-27) of the row's largest;
+ *     2^-24 (bf16: 2^-27) of the row's largest, or of 2^-97 where it is less;
  *   - a probability times the scale of its token's V, in fp16, relative to the
  *     largest such product so far: what is below 2^-24 of that loses bits.
  * In bf16 caches values of V may be 2^70 at most. A NaN or an infinity in q, or a

@@ -152,7 +152,7 @@ struct Q4Consumer {
         top = fmaxf(top, __shfl_xor_sync(kPackedAll, top, 2));
         // a power of two that brings the row's largest value to [8, 16): 72
         // times a group's sum stays in fp16's range
-        const int ex = min(max(int((__float_as_uint(top) >> 23) & 255u), 30), 240);
+        const int ex = min(max(int((__float_as_uint(top) >> 23) & 255u), 30), 254);
         const float mult = __uint_as_float(uint32_t(3 + 127 + 127 - ex) << 23);
         const float inv = __uint_as_float(uint32_t(ex - 3) << 23);   // 1 / mult
         float sums[G];

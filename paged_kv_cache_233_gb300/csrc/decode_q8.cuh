@@ -94,7 +94,7 @@ struct Q8Consumer {
         top = fmaxf(top, __shfl_xor_sync(kPackedAll, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kPackedAll, top, 2));
         // a power of two that brings the row's largest value to [2^14, 2^15)
-        const int ex = min(max(int(__float_as_uint(top) >> 23), 30), 240);
+        const int ex = min(max(int(__float_as_uint(top) >> 23), 30), 254);
         const float mult = __uint_as_float(uint32_t(14 + 127 + 127 - ex) << 23);
         const float k = scale_log2 * __uint_as_float(uint32_t(ex - 14) << 23);   // with 1 / mult
 #pragma unroll

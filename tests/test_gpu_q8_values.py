@@ -172,6 +172,8 @@ def test_large_queries(dim, block, size):
     ref = q8.attention(q, (kc, vc), tables, [0, 70], [n], scale, dim)
     for parts in (1, 32):
         q8.assert_near(prefill(q, kc, vc, tables, [0, 70], [n], scale, key_parts=parts), ref, BF16, 2, f"parts {parts}")
+    for part in (0, 64, pk.PARTITION_BALANCED):
+        q8.assert_near(decode(q[-1:], kc, vc, tables, [n], scale, part), ref[-1:], BF16, 2, f"part {part}")
     assert pk.device_errors() == 0
 
 
