@@ -194,6 +194,33 @@ def test_large_keys(dim, block, size):
         q8.assert_near(decode(q[-1:], kc, vc, tables, [n], scale, part), ref[-1:], BF16, 2, f"part {part}")
 
 
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("dtype,log2_size", [(F16, 14), (BF16, 14), (BF16, 40)])
+def test_blocks_of_zeros_beside_the_largest_values(dtype, log2_size, first):
+    """Tokens whose values are zeros keep their part of the softmax's sum, although their
+    scale is the least there is: 4000 of them at 2^-8 of the others' weight each."""
+    heads, group, dim, block, few = 2, 2, 64, 16, 64
+    n = 4000 + few
+    large = torch.zeros(n, dtype=torch.bool)
+    large[:few if first else n] = True
+    if not first:
+        large[:n - few] = False
+    k, v = torch.zeros(n, heads, dim), rows((n, heads, dim), torch.float32, 2, 0.25).clamp(-1, 1) * 2.0 ** log2_size
+    k[large, :, 0] = 8 * math.log(2.0)
+    v[~large] = 0
+    kc, vc, tables = pools(k.to(dtype), v.to(dtype), block)
+    q = torch.zeros(few // 2, heads * group, dim, dtype=dtype)
+    q[..., 0] = 1
+    ref = q8.attention(q, (kc, vc), tables, [0, len(q)], [n], 1.0, dim)
+    for parts in (1, 32):
+        out = prefill(q, kc, vc, tables, [0, len(q)], [n], 1.0, key_parts=parts)
+        q8.assert_near(out, ref, dtype, 2, f"parts {parts}")
+    for part in (0, 256, pk.PARTITION_BALANCED):
+        out = decode(q[-1:], kc, vc, tables, [n], 1.0, part)
+        q8.assert_near(out, ref[-1:], dtype, 2, f"part {part}")
+    assert pk.device_errors() == 0
+
+
 @pytest.mark.parametrize("scale", [0.0, 2.0 ** -126])
 @pytest.mark.parametrize("dim,block", [(64, 16), (128, 8)])
 def test_a_scale_of_none_with_large_queries(dim, block, scale):
