@@ -853,7 +853,9 @@ int paged_kv_fork(const int32_t *parents, const int32_t *context_lens, int32_t *
  * PAGEDKV_DEVERR_BLOCK_ID; blocks past the stack's capacity are lost, and a
  * free_count outside [0, free_capacity] is clamped (PAGEDKV_DEVERR_POSITION).
  * num_seqs <= 4096, num_blocks <= 2^24; outputs other than those named must not
- * overlap inputs.
+ * overlap inputs. Pools of more than 2^15 blocks are pushed by 16 SMs of one GPC at
+ * once; in a context without them (one limited to few SMs) by one SM, and from
+ * 1851393 blocks on the call returns PAGEDKV_ERR_CUDA with nothing enqueued.
  */
 int paged_kv_release(const int32_t *keep_lens, const int32_t *context_lens,
                      const int32_t *block_tables, int32_t *shared, int32_t *free_blocks,

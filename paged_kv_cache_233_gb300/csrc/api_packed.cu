@@ -21,7 +21,6 @@ using pkv::api_device_state;
 
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxCount = (1 << 30) - 1;   // free blocks and tokens of a step
-constexpr int kMaxPages = 1 << 24;         // blocks of a pool whose rows fork and are released
 
 int done(cudaError_t e) { return e == cudaSuccess ? PAGEDKV_OK : PAGEDKV_ERR_CUDA; }
 
@@ -96,7 +95,7 @@ template <typename Launch>
 int change_pages(pkv::PagesParams p, bool pairs, Launch launch) {
     if (p.num_seqs < 0 || p.max_blocks < 1 || p.num_blocks < 1 || p.free_capacity < 0 || p.block_size < 1)
         return PAGEDKV_ERR_INVALID_ARG;
-    if (p.num_seqs > kMaxSeqs || p.num_blocks > kMaxPages || p.free_capacity > kMaxCount ||
+    if (p.num_seqs > kMaxSeqs || p.num_blocks > pkv::kMaxPages || p.free_capacity > kMaxCount ||
         (long long)p.max_blocks * p.block_size > INT_MAX / 2)
         return PAGEDKV_ERR_UNSUPPORTED;
     if (!p.free_count || !p.free_count_out || !p.shared || (p.free_capacity > 0 && !p.free_blocks))

@@ -1,7 +1,7 @@
 // launch_cache.h -- per-device host records shared by the kernel launchers:
-// the dynamic shared memory a kernel has been opened up to, and the result of
-// its occupancy query for the last shared-memory size asked about. Both are
-// read and written with atomics, so host threads may launch concurrently.
+// the dynamic shared memory a kernel has been opened up to, the result of
+// its occupancy query for the last shared-memory size asked about, and whether
+// a cluster of it finds room. They are read and written with atomics, so host threads may launch concurrently.
 #pragma once
 
 #include <atomic>
@@ -65,6 +65,27 @@ cudaError_t occupancy_per_sm(std::atomic<long long> *record, int dev, Kernel ker
     if (cached && n > 0)
         record[dev].store((static_cast<long long>(smem) << 32) | n, std::memory_order_release);
     return cudaSuccess;
+}
+
+// Whether the current context has room for a cluster of the launch `cfg` (past the
+// portable size too; `cfg` of the same size and shared memory for a record).
+template <typename Kernel>
+bool cluster_fits(std::atomic<unsigned long long> *record, int dev, Kernel kernel, const cudaLaunchConfig_t &cfg) {
+    const unsigned long long ctx = current_context_id() & 0xffffffffull;
+    const bool cached = ctx != 0 && dev >= 0 && dev < kLaunchCacheDevices;
+    if (cached) {
+        const unsigned long long r = record[dev].load(std::memory_order_acquire);
+        if ((r >> 32) == ctx) return (r & 1) != 0;
+    }
+    int n = 0;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();     // the answer is no
+        return false;
+    }
+    if (cached) record[dev].store((ctx << 32) | (n > 0 ? 1u : 0u), std::memory_order_release);
+    return n > 0;
 }
 
 }  // namespace pkv

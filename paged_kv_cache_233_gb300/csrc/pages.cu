@@ -284,9 +284,6 @@ __device__ __forceinline__ void drop_holders(const PagesParams &p, int *memory, 
 
 // Blocks whose count went below zero, onto the stack in the order of their ids; the
 // lengths and the count after the call. A run of 32-block words per warp.
-constexpr int kPushCtas = 16;
-constexpr int kSmallBlocks = 1 << 15;  // up to as many, one block of threads pushes
-
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -301,10 +298,6 @@ __device__ __forceinline__ int cluster_load(const int *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
-}
-
-__host__ __device__ constexpr int push_words(int num_blocks, int ctas) {   // a warp's words, of 1024 threads
-    return ((num_blocks + 31) / 32 + 32 * ctas - 1) / (32 * ctas);
 }
 
 template <bool kCluster>
@@ -442,42 +435,45 @@ cudaError_t launch_fork(const PagesParams &p, int num_sms, cudaStream_t st) {
 }
 
 cudaError_t launch_release(const PagesParams &p, int num_sms, cudaStream_t st) {
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg;
-    int threads, blocks;
+    int threads, blocks, dev = 0;
     shape(p, num_sms, threads, blocks);
+    // Whatever may refuse a launch comes before the first one: holders that are taken
+    // away and blocks that are not pushed would be lost.
     static std::atomic<unsigned long long> opened_runs[kLaunchCacheDevices];
     cudaError_t e = open_runs(opened_runs, release_kernel, runs_bytes(p.num_seqs));
     if (e != cudaSuccess) return e;
-    cfg = config(attr, blocks, threads, runs_bytes(p.num_seqs), st);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t push;
+    int ctas = 1;
+    if (p.num_blocks > kSmallBlocks) {
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
+        e = open_dynamic_smem(opened, dev, push_kernel<true>, push_smem(kMaxPages, kPushCtas));
+        if (e != cudaSuccess) return e;
+        push = config(attr, kPushCtas, kMaxThreads, push_smem(kMaxPages, kPushCtas), st);
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kPushCtas;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        push.numAttrs = 2;
+        // (a cluster of 16 needs as many SMs of one GPC at once: asked for the largest pool's)
+        static std::atomic<unsigned long long> room[kLaunchCacheDevices];
+        ctas = push_ctas(p.num_blocks, cluster_fits(room, dev, push_kernel<true>, push));
+        if (ctas == 0) return cudaErrorLaunchOutOfResources;
+        push.dynamicSmemBytes = size_t(push_smem(p.num_blocks, kPushCtas));
+    }
+    if (ctas == 1) {
+        const int smem = push_smem(p.num_blocks, 1);
+        static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
+        e = open_runs(opened, push_kernel<false>, smem);
+        if (e != cudaSuccess) return e;
+        push = config(attr, 1, kMaxThreads, smem, st);
+    }
+    cudaLaunchAttribute early[1];
+    const cudaLaunchConfig_t cfg = config(early, blocks, threads, runs_bytes(p.num_seqs), st);
     e = cudaLaunchKernelEx(&cfg, release_kernel, p);
     if (e != cudaSuccess) return e;
-    if (p.num_blocks <= kSmallBlocks) {
-        cfg = config(attr, 1, kMaxThreads, 4 * 32 * push_words(p.num_blocks, 1), st);
-        return cudaLaunchKernelEx(&cfg, push_kernel<false>, p);
-    }
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const int smem = 4 * 32 * push_words(p.num_blocks, kPushCtas);
-    static std::atomic<unsigned long long> opened[kLaunchCacheDevices];
-    e = open_dynamic_smem(opened, dev, push_kernel<true>, smem);
-    if (e != cudaSuccess) return e;
-    // (clusters of more than 8 blocks have to be asked for, once in each context)
-    static std::atomic<unsigned long long> allowed[kLaunchCacheDevices];
-    const unsigned long long ctx = current_context_id();
-    const bool cached = ctx != 0 && dev >= 0 && dev < kLaunchCacheDevices;
-    if (!cached || allowed[dev].load(std::memory_order_acquire) != ctx) {
-        e = cudaFuncSetAttribute(push_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        if (cached) allowed[dev].store(ctx, std::memory_order_release);
-    }
-    cfg = config(attr, kPushCtas, kMaxThreads, smem, st);
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kPushCtas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, push_kernel<true>, p);
+    return ctas == 1 ? cudaLaunchKernelEx(&push, push_kernel<false>, p) : cudaLaunchKernelEx(&push, push_kernel<true>, p);
 }
 
 }  // namespace pkv
