@@ -226,6 +226,7 @@ int prefill_packed(int bits, const void *q, const void *k_cache, const void *v_c
     p.q = q;
     p.k_packed = static_cast<const uint8_t *>(k_cache);
     p.v_packed = static_cast<const uint8_t *>(v_cache);
+    p.no_empty_rows = bits == 8 ? 1 : 0;
     p.block_tables = block_tables;
     p.query_start = query_start;
     p.context_lens = context_lens;

@@ -46,6 +46,7 @@ struct PrefillParams {
     // 4- or 8-bit pools (q4.h, q8.h; launch_prefill_packed_tc alone reads them)
     const uint8_t *k_packed;
     const uint8_t *v_packed;
+    int no_empty_rows;    // 8-bit pools: a row whose weights are all 0 is a NaN (launch_prefill_merge)
     int *ws_plan;
     float *ws_o;
     float *ws_m;

@@ -681,8 +681,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
             if (!__all_sync(kAll, got)) return false;
             tc_fence_after_sync();
             // the row normalised into `out`, or (key split) its part's O as it is
-            // (a row without keys has a sum of 0; a NaN sum goes through)
-            const float inv = prev_l != 0.f ? 1.f / prev_l : 0.f;
+            // (a row without keys has a sum of 0; a NaN sum goes through). 8-bit pools: every row
+            // of an item has met a key, and a sum of 0 says that all its scores were -inf (an
+            // infinite query, or scores past fp32): 0 times infinity, a NaN
+            const float inv = kBits == 8 || prev_l != 0.f ? 1.f / prev_l : 0.f;
             const bool keep = prev_row && (!split || prev_l != 0.f);
             uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.out) + prev_qrow * D);
             float4 *wo = reinterpret_cast<float4 *>(p.ws_o + wrow * D);
@@ -829,9 +831,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 if (lane == 0) mbar_arrive(bar(bar_p(t, b)));
             }
             if (!ok) break;
-            // 8-bit pools: a row that has met a key and has no maximum met -inf alone (an
-            // infinite query, or scores past fp32): no weights, and a sum of NaN
-            if (kBits == 8 && ref == -INFINITY && it.kb * kTcKeys <= pos) l = __int_as_float(0x7fffffff);
             prev_nk = nk;
             prev_jend = jt + nk;
             prev_l = l;
@@ -1584,7 +1583,8 @@ paged_prefill_merge_kernel(const PrefillParams p, int tiles) {
             for (int e = 0; e < E; ++e) acc[e] = use ? fmaf(wq, x[q][e], acc[e]) : acc[e];
         }
     }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
+    // (a sum of 0: as in the kernel's epilogue)
+    const float inv = den != 0.f || p.no_empty_rows ? 1.f / den : 0.f;
     T *dst = reinterpret_cast<T *>(p.out) + qrow * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
