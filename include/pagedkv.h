@@ -688,10 +688,9 @@ int paged_kv_gather_q8(const void *k_cache, const void *v_cache, const int64_t *
  *     largest such product so far: what is below 2^-24 of that loses bits.
  * In bf16 caches values of V may be 2^40 at most: a block of zeros has the least
  * scale there is, and beside larger values its tokens' weights would be lost to the
- * softmax's sum. A NaN or an infinity in q, or a
- * NaN code in K, makes all outputs NaN of the query heads that attend to it, one in
- * V those of its channel. What lies in a block past a sequence's context never
- * matters, but for the block's scale.
+ * softmax's sum. A NaN or an infinity in q, or a NaN code in K, makes all outputs NaN of
+ * the query heads that attend to it, one in V those of its channel. What lies in a block
+ * past a sequence's context never matters, but for the block's scale.
  */
 int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_cache,
                               const int32_t *block_tables, const int32_t *context_lens, float scale,
@@ -710,10 +709,10 @@ int paged_attention_decode_q8(const void *q, const void *k_cache, const void *v_
  * brought to one scale, exactly unless one's scale is more than 2^21 below the largest:
  * its values are then rounded to multiples of 2^-30 of that scale, and count as zeros where
  * it is more than 2^30 below (K of bf16 calls loses nothing within 2^100). Arguments,
- * limits, workspace and key_parts as paged_attention_prefill_q4's. In bf16 caches values of V may be 2^40 at most, as in
- * the decode. A
- * NaN or an infinity in a row of q makes that row's outputs of the head NaN; a token
- * that is marked as holding a NaN, in K or in V, those of the rows that attend to it.
+ * limits, workspace and key_parts as paged_attention_prefill_q4's. In bf16 caches values
+ * of V may be 2^40 at most, as in the decode, and the scale times those of K 2^119. A NaN
+ * or an infinity in a row of q makes that row's outputs of the head NaN; a token that is
+ * marked as holding a NaN, in K or in V, those of the rows that attend to it.
  */
 int paged_attention_prefill_q8(const void *q, const void *k_cache, const void *v_cache,
                                const int32_t *block_tables, const int32_t *query_start,

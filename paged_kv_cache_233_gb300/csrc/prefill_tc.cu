@@ -95,6 +95,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "launch_cache.h"
@@ -141,8 +142,6 @@ constexpr int kTmemTile = 256;   // tensor-memory columns per Q tile: S, S, O
 // small end
 template <int kBits> constexpr float move_past() { return kBits == 8 ? 14.f : 8.f; }
 template <int kBits> constexpr float below_max() { return kBits == 8 ? 6.f : 0.f; }
-// 8-bit pools in bf16: key tiles of scales up to 2^40 are held low (below)
-constexpr int kLowKeysExp = 40;
 
 // mbarrier indices
 constexpr int kKvFull = 0;
@@ -1219,9 +1218,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     any[o] = __any_sync(kAll, there && info[o].y != 0) != 0;
                 }
                 // bf16's K lies lower, at 2^-16: 128 products of 448 * 2^-16 and bf16's largest
-                // query are within fp32. (Not where K is so large itself that its factor would
-                // pass fp32.)
-                const int up = kBf16 && most[0] <= kLowKeysExp ? -16 : 6;
+                // query are within fp32. (Its factor passes fp32 only where the scale times K
+                // does 2^120: it stays finite there. Staged by K's size instead, at 2^6 where
+                // K is that large, the long chunk took 0.5% longer.)
+                constexpr int up = kBf16 ? -16 : 6;
                 const uint32_t scales = base + Ly::kScales + uint32_t(ring * Ly::kScalesTile);
                 if (any[0] || any[1]) {
 #pragma unroll
@@ -1233,10 +1233,12 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 }
                 // (a factor of 0 would turn a masked score's -inf into a NaN; the smallest number
                 // leaves every score of a scale of 0 below 2^-21)
-                if (w == 0 && lane == 0)
-                    sts128(scales, make_uint4(__float_as_uint(fmaxf(fabsf(p.scale_log2) * q8_power(most[0] - up), 0x1p-149f)),
+                if (w == 0 && lane == 0) {
+                    const float factor = fabsf(p.scale_log2) * q8_power(-up) * q8_power(most[0]);
+                    sts128(scales, make_uint4(__float_as_uint(fminf(fmaxf(factor, 0x1p-149f), FLT_MAX)),
                                               __float_as_uint(float(most[1] - 6)), __float_as_uint(q8_power(6 - most[1])),
                                               any[0] || any[1] ? 1u : 0u));
+                }
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const bool of_v = o == 1;

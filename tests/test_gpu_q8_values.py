@@ -233,3 +233,24 @@ def test_a_scale_of_none_with_large_queries(dim, block, scale):
         q8.assert_near(prefill(q, kc, vc, tables, [0, 70], [n], scale, key_parts=parts), ref, BF16, 2, f"parts {parts}")
     for part in (0, 64, pk.PARTITION_BALANCED):
         q8.assert_near(decode(q[-1:], kc, vc, tables, [n], scale, part), ref[-1:], BF16, 2, f"part {part}")
+
+
+# ------------------------------------------------- tables wider than the contexts
+@pytest.mark.parametrize("wider", [4, 32])
+@pytest.mark.parametrize("cached,chunk", [([6001], [33]), ([900, 0, 40, 500], [64] * 4), ([100] * 20, [64] * 20), ([8192], [600])])
+@pytest.mark.parametrize("dtype,dim", [(BF16, 128), (F16, 64)])
+def test_a_split_chosen_by_the_tables_width(dtype, dim, cached, chunk, wider):
+    """key_parts 0 goes by a width that says little about the contexts: the results are the
+    same, whole or split."""
+    heads, group, block = 8, 4, 16
+    lens = [c + n for c, n in zip(cached, chunk)]
+    kc, vc, tables = q8.filled(lens, heads, block, dim, dtype, 5)
+    wide = torch.full((len(lens), wider * tables.shape[1]), -1, dtype=torch.int32)
+    wide[:, :tables.shape[1]] = tables
+    starts = torch.tensor([0] + chunk).cumsum(0)
+    q = rows((int(starts[-1]), heads * group, dim), dtype, 6)
+    ref = q8.attention(q, (kc, vc), tables, starts, lens, dim ** -0.5, dim)
+    for t in (tables, wide):
+        out = prefill(q, kc, vc, t, starts, lens, dim ** -0.5, key_parts=0)
+        q8.assert_near(out, ref, dtype, 2, f"width {t.shape[1]}")
+    assert pk.device_errors() == 0
