@@ -735,7 +735,8 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     if (path == pkv::kPathSimt) gmax = group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
     // ---- split-K
     const bool split = partition_tokens != 0;
-    const int P = partition_tokens > 0 ? partition_tokens
+    // (past 2^30 tokens, which no context reaches, a length plus P would not be an int)
+    const int P = partition_tokens > 0 ? (partition_tokens < 1 << 30 ? partition_tokens : 1 << 30)
                                        : int((cap + pkv::kTile - 1) / pkv::kTile * pkv::kTile);
     const long long max_parts =
         partition_tokens > 0 ? max_parts_for(max_blocks_per_seq, block_size, P) : 1;

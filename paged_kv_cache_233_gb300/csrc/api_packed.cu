@@ -167,8 +167,10 @@ int decode_packed(int bits, const void *q, const void *k_cache, const void *v_ca
     p.max_blocks = max_blocks_per_seq;
     p.balanced = partition_tokens == PAGEDKV_PARTITION_BALANCED ? 1 : 0;
     p.log2_hpu = n_kv_heads % 4 == 0 ? 2 : (n_kv_heads % 2 == 0 ? 1 : 0);
-    // (unsplit: one partition of the tables' whole width)
-    p.part_tokens = partition_tokens > 0 ? partition_tokens : int((cap + 31) / 32 * 32);
+    // (unsplit: one partition of the tables' whole width; nor is a longer one more than that,
+    // and a length plus it stays an int)
+    const int widest = int((cap + 31) / 32 * 32);
+    p.part_tokens = partition_tokens > 0 && partition_tokens < widest ? partition_tokens : widest;
     p.max_parts = int((cap + p.part_tokens - 1) / p.part_tokens);
     p.merged = p.balanced || p.max_parts > 1 ? 1 : 0;
     // the kernel counts units and tiles in ints
