@@ -244,6 +244,9 @@ int prefill_packed(int bits, const void *q, const void *k_cache, const void *v_c
     p.block_size = block_size;
     while ((1 << p.log2_block) < block_size) ++p.log2_block;
     p.max_blocks = max_blocks_per_seq;
+    // (no chunk is longer than all rows: a loose bound costs no items, and its tiles' tokens
+    // stay an int)
+    if (max_query_len > num_tokens) max_query_len = num_tokens;
     // the persistent kernel counts its work items in ints
     const long long per_seq = ((long long)max_query_len + p.tile_tokens - 1) / p.tile_tokens * n_kv_heads;
     if (per_seq > (INT_MAX / 2) / num_seqs) return PAGEDKV_ERR_UNSUPPORTED;

@@ -254,3 +254,19 @@ def test_a_split_chosen_by_the_tables_width(dtype, dim, cached, chunk, wider):
         out = prefill(q, kc, vc, t, starts, lens, dim ** -0.5, key_parts=0)
         q8.assert_near(out, ref, dtype, 2, f"width {t.shape[1]}")
     assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("parts", [1, 0, 32])
+@pytest.mark.parametrize("cached,chunk", [([6001], [33]), ([40, 0, 500], [1, 300, 64])])
+def test_any_bound_of_the_chunks_will_do(cached, chunk, parts):
+    """max_query_len far above every chunk, up to the largest int: the same as the exact one."""
+    heads, group, dim, block = 4, 4, 128, 16
+    lens = [c + n for c, n in zip(cached, chunk)]
+    kc, vc, tables = q8.filled(lens, heads, block, dim, BF16, 5)
+    starts = torch.tensor([0] + chunk).cumsum(0)
+    q = rows((int(starts[-1]), heads * group, dim), BF16, 6)
+    ref = q8.attention(q, (kc, vc), tables, starts, lens, 0.09, dim)
+    for most in (max(chunk), 4096, (1 << 31) - 1):
+        out = prefill(q, kc, vc, tables, starts, lens, 0.09, max_query_len=most, key_parts=parts)
+        q8.assert_near(out, ref, BF16, 2, f"most {most}")
+    assert pk.device_errors() == 0
