@@ -270,3 +270,47 @@ def test_any_bound_of_the_chunks_will_do(cached, chunk, parts):
         out = prefill(q, kc, vc, tables, starts, lens, 0.09, max_query_len=most, key_parts=parts)
         q8.assert_near(out, ref, BF16, 2, f"most {most}")
     assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,dim,block", [(F16, 64, 8), (BF16, 128, 16), (BF16, 64, 32)])
+def test_nan_tokens_taken_back_and_kept_through_growth(dtype, dim, block):
+    """A token with a NaN stays one when later rows make its block's scale grow, and leaves
+    nothing behind when it is taken back, before the next token takes its place or after."""
+    heads, group, n = 2, 2, block + 3
+    tables, nb = q8.tables_for([2 * block], block, 3)
+    kc, vc = (q8.new_pool(nb, heads, block, dim, i).cuda() for i in (1, 2))
+    gt = tables.cuda()
+    k, v = rows((n, heads, dim), dtype, 4), rows((n, heads, dim), dtype, 5)
+    bad = k.clone()
+    bad[block, 1, 7] = math.nan
+    big = rows((1, heads, dim), dtype, 6, 300.0)
+    q = rows((2, heads * group, dim), dtype, 7)
+
+    def append(x, y, L):
+        pk.paged_kv_append_q8(x.cuda(), y.cuda(), gt, i32([0, len(x)]), i32([L]), kc, vc)
+
+    def check(L, what, nan):
+        host = kc.cpu(), vc.cpu()
+        ref = q8.attention(q[:1], host, tables, [0, 1], [L], 0.1, dim)
+        assert bool(ref.isnan().any()) == nan, what
+        for out in (decode(q[:1], kc, vc, gt, [L], 0.1, 0), prefill(q[:1], kc, vc, gt, [0, 1], [L], 0.1),
+                    prefill(q[:1], kc, vc, gt, [0, 1], [L], 0.1, key_parts=32)):
+            out = out.cpu()
+            if nan:
+                assert bool(out[0, group:].isnan().all()) and bool(torch.isfinite(out[0, :group]).all()), what
+                q8.assert_near(out[:, :group], ref[:, :group], dtype, 2, what)
+            else:
+                q8.assert_near(out, ref, dtype, 2, what)
+
+    append(bad[:block + 1], v[:block + 1], block + 1)
+    check(block + 1, "appended", True)
+    check(block, "taken back", False)
+    append(bad[block:block + 1], v[block:block + 1], block + 1)
+    append(big, big, block + 2)                              # its block's scales grow
+    check(block + 2, "kept through growth", True)
+    assert int(q8.views(kc.cpu(), dim)[2][int(tables[0, 1]), 1, 0]) & 3 == 1
+    append(k[block:block + 2], v[block:block + 2], block + 2)    # both taken back, others in their place
+    check(block + 2, "replaced", False)
+    append(k[block + 1:block + 2], v[block + 1:block + 2], block + 2)
+    check(block + 1, "part of it taken back", False)
+    assert pk.device_errors() == 0
