@@ -609,6 +609,10 @@ int paged_attention_prefill_q4(const void *q, const void *k_cache, const void *v
  *     marks  32 bits behind it, bit t set when token t's row holds a NaN; the rest
  *            is not used
  *
+ * paged_kv_append_q8 keeps scale and marks. Anything else that fills blocks has to set
+ * both, the marks of rows without a NaN to 0: the prefill goes by the marks alone (a NaN
+ * code without one counts as +-480 * 2^e, as 0 or reaches rows that do not attend to it).
+ *
  * and tokens, slots and block tables mean what they mean for 16-bit pools. The
  * codes do not depend on the 16-bit type of the rows. Supported: `dtype`
  * PAGEDKV_F16 or PAGEDKV_BF16 (the type of q, k, v and out), head_dim 64 or 128,

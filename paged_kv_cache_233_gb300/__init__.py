@@ -569,7 +569,9 @@ def paged_attention_prefill_q4(q, k_cache, v_cache, block_tables, query_start, c
 
 def new_q8_pool(num_blocks, n_kv_heads, block_size, head_dim, device="cuda"):
     """An empty 8-bit pool: uint8 [num_blocks][n_kv_heads][block_size][head_dim + tail / block_size]
-    (the last two dimensions are one run of bytes, laid out as pagedkv.h says)."""
+    (the last two dimensions are one run of bytes, laid out as pagedkv.h says). Its bytes are
+    whatever they were: paged_kv_append_q8 sets what it fills; a program that writes codes
+    itself has to set each block's scale and marks too."""
     if block_size not in (8, 16, 32):
         raise PagedKVError("an 8-bit pool's block_size must be 8, 16 or 32")
     tail = max(16, block_size) // block_size

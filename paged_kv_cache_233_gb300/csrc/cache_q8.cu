@@ -24,8 +24,13 @@
 //                                                       append        gather
 //     64 rows of 8 heads of 128, blocks of 16            3.2           2.0
 //     12 x 1024 rows, the same                          12.7 (4480)   12.4 (4650)
+//         blocks of 8                                   13.1 (4350)   12.2 (4690)
+//         blocks of 32                                  15.9 (3590)   12.4 (4730)
 //     16,383 rows of 32 heads of 64, blocks of 32       36.6 (5500)   40.4 (4980)
 //     16,383 rows of 8 heads of 128, blocks of 16       20.7 (4870)   20.3 (4980)
+//         blocks of 8                                   22.0 (4570)   20.3 (4960)
+//         blocks of 32                                  21.4 (4710)   20.2 (5000)
+// (A run of 32 rows of 128 takes 121 registers: two CTAs to an SM, where the others have four.)
 // append with three CTAs to an SM, as its registers come out by themselves: 14.8, 38.9
 // and 21.5; with tiles of 16 rows, or CTAs of 128 or 512 threads: up to 20% slower.
 #include <limits.h>
@@ -298,7 +303,7 @@ cudaLaunchConfig_t config(cudaLaunchAttribute *attr, dim3 grid, int threads, int
 
 template <typename T, int D, int B>
 cudaError_t append_sized(Q8AppendParams p, int sms, cudaStream_t st) {
-    // rows of a tile: as many as leave two CTAs for each SM
+    // rows of a tile: as many as leave each SM a CTA for K and one for V
     p.rows = kMaxTile;
     while (p.rows > 1 && (long long)p.num_tokens < (long long)p.rows * sms) p.rows >>= 1;
     const dim3 grid(unsigned((p.num_tokens + p.rows - 1) / p.rows), 2);

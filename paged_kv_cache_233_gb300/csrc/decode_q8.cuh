@@ -33,8 +33,8 @@
 //     8 x 32768-131072 tokens, 8 heads of 128, 64 query heads, fp16   201    98%
 //     64 x 1-2048 tokens, 32 heads of 64, fp16, blocks of 8            48    84%
 //     1 x 1999 tokens, 8 heads of 128, 32 query heads, bf16           7.6     8%
-// The first two are the copies'; the third is launch, ramp, pieces and merge beside
-// them (28% of the issue slots are used); the last two dependent launches. Two CTAs to
+// The first two are the copies' (28% of the issue slots are used); the third is launch,
+// ramp, pieces and merge beside them (37%); the last: two dependent launches. Two CTAs to
 // an SM: three, as the 4-bit cache has, gained nothing, nor did two heads to a unit.
 #pragma once
 

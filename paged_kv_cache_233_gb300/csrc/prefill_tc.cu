@@ -21,8 +21,8 @@
 //              block][64 keys][128 B] with 128-byte swizzle (the canonical
 //              layout the tensor core reads);
 //   warps 1,10 MMA issuers, one per Q tile (warp 1 also allocates tensor
-//              memory): the warp runs the loop and its waits, and lane 0
-//              issues, for its tile, S = Q K^T into one of two S buffers in
+//              memory): the warp runs the loop and its waits, and one
+//              elected lane issues, for its tile, S = Q K^T into one of two S buffers in
 //              tensor memory and, once the softmax has written P, O += P V
 //              with P read from tensor memory, into the O accumulator that
 //              stays in tensor memory for the whole key loop; completions are
@@ -123,8 +123,10 @@ template <int kBits> constexpr int issuer1_warp() { return kBits == 8 ? 2 : 2 + 
 template <int kBits> constexpr int zero_warp() { return issuer1_warp<kBits>() + 1; }
 constexpr int kTcThreads = 32 * (2 + kTcTiles * kTcRows / 32 + 2);
 // 8-bit pools: of the 512 threads' 128 registers each, the softmax's 256 take 40 more,
-// which the other 256 give up: the softmax then holds its row without spilling (2048
-// rows after 16384 tokens, heads of 128, fp16: 527 -> 490 us).
+// which the other 256 give up: the softmax then holds its row (2048 rows after 16384
+// tokens, heads of 128, fp16: 527 -> 490 us). What still spills (heads of 128: 36
+// bytes a thread, 32 with the key split; heads of 64: 8 and none) is the softmax's: the
+// other roles, compiled without it, spill nothing.
 // (setmaxnreg has to be the same instruction in a warpgroup's four warps, and the
 // shares have to come out of what the block was launched with: 256 * 168 + 256 * 88 =
 // 512 * 128.)
@@ -1334,8 +1336,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // every wait of an issuing warp is idle tensor time; with one issuer
         // per tile, one tile's MMAs go in while the other's issuer waits. The
         // whole warp runs the loop and its waits (so that the descriptors and
-        // addresses are warp-uniform values), and lane 0 alone issues each
-        // tcgen05.mma and tcgen05.commit (a commit tracks its own thread's MMAs).
+        // addresses are warp-uniform values), and one elected lane issues
+        // each tcgen05.mma and tcgen05.commit (a commit tracks its own thread's MMAs).
         {
             // (values by a shuffle are the compiler's to keep in uniform registers)
             const int t = __shfl_sync(kAll, warp == 1 ? 0 : 1, 0);
