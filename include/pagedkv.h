@@ -581,9 +581,9 @@ int paged_attention_decode_q4(const void *q, const void *k_cache, const void *v_
  * paged_attention_prefill_split's, and 1 <= key_parts means the same; a split's
  * ranges hold at least 6 key tiles here, not 16. key_parts 0 splits when the
  * workspace holds it and the items (counted from max_query_len, or from num_tokens
- * where that is less) and the tables' width say that the SMs' even share of the key tiles saves more than the extra
- * pieces and the merge cost: with few items, or with one sequence whose items
- * leave SMs without any in their last round. The width stands for the contexts,
+ * where that is less) and the tables' width say that the SMs' even share of the key
+ * tiles saves more than the extra pieces and the merge cost: with few items, or with
+ * one sequence whose items leave SMs without any in their last round. The width stands for the contexts,
  * which the host does not see: with tables several times wider than the contexts
  * of a call, name key_parts (1, or 32) where speed counts; results are right
  * either way.

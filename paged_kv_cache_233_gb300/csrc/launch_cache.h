@@ -1,7 +1,8 @@
 // launch_cache.h -- per-device host records shared by the kernel launchers:
 // the dynamic shared memory a kernel has been opened up to, the result of
 // its occupancy query for the last shared-memory size asked about, and whether
-// a cluster of it finds room. They are read and written with atomics, so host threads may launch concurrently.
+// a cluster of it finds room. They are read and written with atomics, so host
+// threads may launch concurrently.
 #pragma once
 
 #include <atomic>
