@@ -228,12 +228,21 @@ int prefill_packed(int bits, const void *q, const void *k_cache, const void *v_c
     p.q = q;
     p.k_packed = static_cast<const uint8_t *>(k_cache);
     p.v_packed = static_cast<const uint8_t *>(v_cache);
-    p.no_empty_rows = bits == 8 ? 1 : 0;
     p.block_tables = block_tables;
     p.query_start = query_start;
     p.context_lens = context_lens;
     p.out = out;
     p.scale_log2 = scale * pkv::kLog2e;
+    if (bits == 8) {
+        // the scale without its sign times 2^-shift, in two parts that stay within fp32 until
+        // their product passes it, where the scale times K passes 2^120
+        const float size = fabsf(p.scale_log2);
+        const int shift = pkv::q8_key_shift(dtype == PAGEDKV_BF16);
+        const bool large = size > 0x1p100f;
+        p.k_scale = large ? size : ldexpf(size, -shift);
+        p.k_exp = large ? -shift : 0;
+        p.no_empty_rows = 1;
+    }
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
     p.n_q_heads = n_q_heads;

@@ -13,6 +13,12 @@ constexpr int kPfKeys = 64;      // keys per pipeline stage
 constexpr int kPfStages = 3;     // depth of the K/V ring
 constexpr int kPfThreads = 160;  // one producer warp + four consumer warps of 16 rows
 
+// 8-bit pools: a key tile's codes c are staged as c * 2^shift. In bf16 lower than fp16's
+// range takes them: 128 products of 448 * 2^-16 and bf16's largest query are within fp32.
+// (By K's size instead, at 2^6 where K is large, 2048 rows after 16384 tokens took 0.5%
+// longer.)
+constexpr int q8_key_shift(bool bf16) { return bf16 ? -16 : 6; }
+
 struct PrefillParams {
     const void *q;               // [num_tokens][n_q_heads][head_dim]
     void *out;                   // [num_tokens][n_q_heads][head_dim]
@@ -46,7 +52,11 @@ struct PrefillParams {
     // 4- or 8-bit pools (q4.h, q8.h; launch_prefill_packed_tc alone reads them)
     const uint8_t *k_packed;
     const uint8_t *v_packed;
-    int no_empty_rows;    // 8-bit pools: a row whose weights are all 0 is a NaN (launch_prefill_merge)
+    // 8-bit pools: S's factor for a key tile whose largest scale is 2^e is k_scale *
+    // 2^(e + k_exp); a row whose weights are all 0 is a NaN (launch_prefill_merge)
+    float k_scale;
+    int k_exp;
+    int no_empty_rows;
     int *ws_plan;
     float *ws_o;
     float *ws_m;

@@ -1206,9 +1206,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     for (int i = 0; i < D / 32; ++i) cw[o][i] = lds128_u4(from + src + uint32_t(i) * step);
                 }
                 // The tile's keys under one scale, 2^6 below their blocks' largest (448 *
-                // 2^6 is in fp16's range): a power of two takes each code there, exactly
-                // unless its block's scale is more than 2^21 below the largest. (Past 2^30
-                // below it that power is below fp16's smallest number: zeros.)
+                // 2^6 is in fp16's range; bf16's K q8_key_shift): a power of two takes each
+                // code there, exactly unless its block's scale is more than 2^21 below the
+                // largest. (Past 2^30 below it that power is below fp16's smallest number: zeros.)
+                constexpr int up = q8_key_shift(kBf16);
                 const bool there = x > 1 || some * B < past;    // (a block past the context has no scale)
                 const bool live = x > 1 || row < past;
                 int e[2], most[2];
@@ -1219,11 +1220,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                     most[o] = __reduce_max_sync(kAll, e[o]);
                     any[o] = __any_sync(kAll, there && info[o].y != 0) != 0;
                 }
-                // bf16's K lies lower, at 2^-16: 128 products of 448 * 2^-16 and bf16's largest
-                // query are within fp32. (Its factor passes fp32 only where the scale times K
-                // does 2^120: it stays finite there. Staged by K's size instead, at 2^6 where
-                // K is that large, the long chunk took 0.5% longer.)
-                constexpr int up = kBf16 ? -16 : 6;
                 const uint32_t scales = base + Ly::kScales + uint32_t(ring * Ly::kScalesTile);
                 if (any[0] || any[1]) {
 #pragma unroll
@@ -1236,7 +1232,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                 // (a factor of 0 would turn a masked score's -inf into a NaN; the smallest number
                 // leaves every score of a scale of 0 below 2^-21)
                 if (w == 0 && lane == 0) {
-                    const float factor = fabsf(p.scale_log2) * q8_power(-up) * q8_power(most[0]);
+                    const float factor = p.k_scale * q8_power(min(most[0] + p.k_exp, 127));
                     sts128(scales, make_uint4(__float_as_uint(fminf(fmaxf(factor, 0x1p-149f), FLT_MAX)),
                                               __float_as_uint(float(most[1] - 6)), __float_as_uint(q8_power(6 - most[1])),
                                               any[0] || any[1] ? 1u : 0u));

@@ -314,3 +314,20 @@ def test_nan_tokens_taken_back_and_kept_through_growth(dtype, dim, block):
     append(k[block + 1:block + 2], v[block + 1:block + 2], block + 2)
     check(block + 1, "part of it taken back", False)
     assert pk.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,small", [(F16, 2.0 ** -12), (BF16, 2.0 ** -90)])
+@pytest.mark.parametrize("dim,block", [(64, 16), (128, 8)])
+def test_small_queries_under_a_large_scale(dtype, small, dim, block):
+    """Queries and keys as small as they come, and a scale that brings their scores back."""
+    n, heads, group = 300, 2, 4
+    least = 2.0 ** -10 if dtype == F16 else 2.0 ** -30
+    kc, vc, tables = pools(rows((n, heads, dim), dtype, 1, least), rows((n, heads, dim), dtype, 2), block)
+    q = (rows((70, heads * group, dim), torch.float32, 3) * small).to(dtype)
+    scale = dim ** -0.5 / small / least
+    ref = q8.attention(q, (kc, vc), tables, [0, 70], [n], scale, dim)
+    for parts in (1, 32):
+        q8.assert_near(prefill(q, kc, vc, tables, [0, 70], [n], scale, key_parts=parts), ref, dtype, 2, f"parts {parts}")
+    for part in (0, 64, pk.PARTITION_BALANCED):
+        q8.assert_near(decode(q[-1:], kc, vc, tables, [n], scale, part), ref[-1:], dtype, 2, f"part {part}")
+    assert pk.device_errors() == 0
